@@ -26,17 +26,20 @@ __all__ = [
     "RF_DECODE_NOALLOC_SCRATCH_BYTES", "rf_mla_decode", "rf_mla_decode_num_splits",
     "rf_mla_decode_workspace_size", "rf_moe_gate_topk_softmax", "rf_moe_gate_topk_softmax_ex",
     "rf_absmax_fp8_gemm", "rf_absmax_fp8_gemm_workspace_size", "rf_absmax_quant_fp8",
+    "rf_paged_kv", "rf_norm_rope", "rf_qk_norm_rope", "rf_kv_append_paged", "rf_attn_decode_paged",
+    "rf_attn_decode_paged_workspace_size", "rf_selftest_append_plan",
+    "rf_selftest_decode_paged_plan",
     "rf_selftest_wait_timeout", "rf_selftest_bounds", "rf_selftest_decode_plan",
     "rf_selftest_fp8_schedule", "rf_selftest_moe_plan",
     "RF_OK", "RF_ERR_INVALID_ARG", "RF_ERR_UNSUPPORTED", "RF_ERR_WORKSPACE", "RF_ERR_CUDA",
     "RF_ERR_DEVICE_TIMEOUT", "RF_ERR_DEVICE_INPUT", "RF_ERR_DEVICE_LAYOUT", "RF_ERR_DEVICE_BOUNDS",
-    "RF_F32", "RF_BF16",
+    "RF_F32", "RF_BF16", "RF_E4M3",
     "RF_ATTN_AUTO", "RF_ATTN_INCREMENTAL", "RF_ATTN_TWO_PASS", "RF_GATE_W_ED", "RF_GATE_W_DE",
 ]
 
 RF_OK, RF_ERR_INVALID_ARG, RF_ERR_UNSUPPORTED, RF_ERR_WORKSPACE, RF_ERR_CUDA, \
     RF_ERR_DEVICE_TIMEOUT, RF_ERR_DEVICE_INPUT, RF_ERR_DEVICE_LAYOUT, RF_ERR_DEVICE_BOUNDS = range(9)
-RF_F32, RF_BF16 = 0, 1
+RF_F32, RF_BF16, RF_E4M3 = 0, 1, 2
 RF_ATTN_AUTO, RF_ATTN_INCREMENTAL, RF_ATTN_TWO_PASS = 0, 1, 2
 RF_GATE_W_ED, RF_GATE_W_DE = 0, 1                # layouts of W_gate: [E][D], [D][E]
 RF_DECODE_NOALLOC_SCRATCH_BYTES = 16 << 20   # as in rf.h
@@ -54,8 +57,20 @@ _P = _c.c_void_p
 _I = _c.c_int
 _F = _c.c_float
 _Z = _c.c_size_t
+_L = _c.c_int64
 
 lib = _c.CDLL(LIB_PATH)
+
+
+class _PagedKV(_c.Structure):
+    _fields_ = [(n, _P) for n in ("k", "v", "k_scale", "v_scale", "block_table", "seq_lens")] + \
+        [(n, _I) for n in ("dtype", "B", "num_pages", "page_size", "max_pages", "Hkv", "d")]
+
+
+class _NormRope(_c.Structure):
+    _fields_ = [("cos", _P), ("sin", _P), ("max_pos", _I), ("rot_dim", _I), ("interleaved", _I),
+                ("q_weight", _P), ("k_weight", _P), ("eps", _F)]
+
 
 _SIGS = {
     "rf_status_string": (_c.c_char_p, [_I]),
@@ -77,6 +92,14 @@ _SIGS = {
     "rf_absmax_fp8_gemm_workspace_size": (_Z, [_I, _I, _I]),
     "rf_absmax_fp8_gemm": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _Z, _P]),
     "rf_absmax_quant_fp8": (_I, [_P, _I, _I, _P, _P, _P]),
+    "rf_qk_norm_rope": (_I, [_I, _P, _L, _P, _L, _P, _L, _P, _L, _P, _c.POINTER(_NormRope), _I, _I,
+                             _I, _I, _P]),
+    "rf_kv_append_paged": (_I, [_c.POINTER(_PagedKV), _P, _L, _P, _L, _P, _I, _c.POINTER(_NormRope),
+                                _P, _L, _P, _L, _I, _P]),
+    "rf_attn_decode_paged_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
+    "rf_attn_decode_paged": (_I, [_c.POINTER(_PagedKV), _P, _P, _I, _I, _F, _P, _Z, _P]),
+    "rf_selftest_append_plan": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I]),
+    "rf_selftest_decode_paged_plan": (_I, [_P, _I, _I, _I, _I, _I]),
     "rf_selftest_wait_timeout": (_I, [_I, _P]),
     "rf_selftest_bounds": (_I, [_P]),
     "rf_selftest_decode_plan": (_I, [_I, _I, _I, _I, _I]),
@@ -340,6 +363,205 @@ def rf_absmax_quant_fp8(x, sx_out, xq_out, stream=None) -> None:
            "rf_absmax_quant_fp8")
 
 
+# ------------------------------------------------------------------ paged cache
+
+
+def _on_device(name, t):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _rows(t, dtype, T, H, d, name):
+    """Checks a [T, H, d] tensor whose tokens may be any distance apart; returns
+    that distance in elements."""
+    _on_device(name, t)
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != (T, H, d):
+        raise ValueError(f"{name} must have shape {(T, H, d)}, got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s0 if T > 1 else H * d
+
+
+class rf_paged_kv:
+    """A paged key/value cache and the batch that uses it (struct rf_paged_kv).
+    k_pages, v_pages: [num_pages, Hkv, page_size, d], bf16 or uint8 E4M3 codes;
+    k_scale, v_scale: fp32 [num_pages, Hkv] (E4M3 only); block_table: int32
+    [B, max_pages]; seq_lens: int32 [B], the lengths after the call's new
+    tokens.  Holds the tensors; their contents may change between calls."""
+
+    def __init__(self, k_pages, v_pages, block_table, seq_lens, k_scale=None, v_scale=None):
+        _on_device("k_pages", k_pages)
+        if k_pages.dtype not in (torch.bfloat16, torch.uint8):
+            raise ValueError("k_pages must be bfloat16 or uint8 (E4M3 codes)")
+        if k_pages.dim() != 4:
+            raise ValueError("k_pages must be [num_pages, Hkv, page_size, d]")
+        e4m3 = k_pages.dtype == torch.uint8
+        num_pages, Hkv, page_size, d = k_pages.shape
+        _need(k_pages, k_pages.dtype, k_pages.shape, "k_pages")
+        _on_device("v_pages", v_pages)
+        _need(v_pages, k_pages.dtype, k_pages.shape, "v_pages")
+        _on_device("block_table", block_table)
+        _on_device("seq_lens", seq_lens)
+        B = seq_lens.numel()
+        max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
+        _need(block_table, torch.int32, (B, max_pages), "block_table")
+        _need(seq_lens, torch.int32, (B,), "seq_lens")
+        if e4m3:
+            for n, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                _on_device(n, t)
+                _need(t, torch.float32, (num_pages, Hkv), n)
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 cache has no scales")
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.block_table, self.seq_lens = block_table, seq_lens
+        self.B, self.Hkv, self.d, self.device = B, Hkv, d, k_pages.get_device()
+        self._c = _PagedKV(k_pages.data_ptr(), v_pages.data_ptr(),
+                           k_scale.data_ptr() if e4m3 else None,
+                           v_scale.data_ptr() if e4m3 else None, block_table.data_ptr(),
+                           seq_lens.data_ptr(), RF_E4M3 if e4m3 else RF_BF16, B, num_pages,
+                           page_size, max_pages, Hkv, d)
+        self._ref = _c.byref(self._c)
+
+    def _here(self):
+        if self.device != torch.cuda.current_device():
+            raise ValueError("the cache must be on the current CUDA device")
+
+
+class rf_norm_rope:
+    """Norm and rotation of query and key heads (struct rf_norm_rope).  cos, sin:
+    fp32 [max_pos, rot_dim / 2], or None: no rotation; interleaved: rotate pairs
+    (2j, 2j + 1) instead of (j, j + rot_dim / 2); q_weight, k_weight: [d] of the
+    rows' type, or None: no norm.  Holds the tensors."""
+
+    def __init__(self, cos=None, sin=None, interleaved=False, q_weight=None, k_weight=None,
+                 eps: float = 1e-6):
+        if (cos is None) != (sin is None):
+            raise ValueError("cos and sin come together")
+        max_pos = rot_dim = 0
+        if cos is not None:
+            _on_device("cos", cos)
+            _on_device("sin", sin)
+            if cos.dim() != 2:
+                raise ValueError("cos must be [max_pos, rot_dim / 2]")
+            _need(cos, torch.float32, cos.shape, "cos")
+            _need(sin, torch.float32, cos.shape, "sin")
+            max_pos, rot_dim = cos.shape[0], 2 * cos.shape[1]
+        for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                _on_device(n, w)
+                if w.dim() != 1 or not w.is_contiguous():
+                    raise ValueError(f"{n} must be a contiguous [d] tensor")
+        self.cos, self.sin, self.q_weight, self.k_weight = cos, sin, q_weight, k_weight
+        self._c = _NormRope(None if cos is None else cos.data_ptr(),
+                            None if sin is None else sin.data_ptr(), max_pos, rot_dim,
+                            int(interleaved), None if q_weight is None else q_weight.data_ptr(),
+                            None if k_weight is None else k_weight.data_ptr(), float(eps))
+        self._ref = _c.byref(self._c)
+
+    def _need_for(self, dtype, d, has_q, has_k):
+        here = torch.cuda.current_device()
+        for n, w, used in (("q_weight", self.q_weight, has_q), ("k_weight", self.k_weight, has_k)):
+            if used and w is not None and (w.dtype != dtype or w.shape[0] != d or
+                                           w.get_device() != here):
+                raise ValueError(f"{n} must be a {dtype} [{d}] tensor on the current CUDA device")
+        if self.cos is not None and self.cos.get_device() != here:
+            raise ValueError("cos and sin must be on the current CUDA device")
+
+
+def rf_qk_norm_rope(q, k, q_out, k_out, norm_rope, positions=None, stream=None) -> None:
+    """RMS norm and rotation of every query and key head.  q, q_out: [T,Hq,d];
+    k, k_out: [T,Hkv,d], all fp32 or all bf16; the tokens may be strided (views
+    of a fused projection), the heads of a token contiguous; q_out may be q and
+    k_out may be k; q and q_out, or k and k_out, may be None.  norm_rope: an
+    rf_norm_rope, or None: a copy; positions: int32 [T] (needed with a
+    rotation)."""
+    x = q if q is not None else k
+    if not isinstance(x, torch.Tensor) or x.dim() != 3 or \
+            x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("q or k must be given, as [T, heads, d] float32 or bfloat16")
+    T, _, d = x.shape
+    dt = x.dtype
+    Hq = Hkv = ldq = ldqo = ldk = ldko = 0
+    if q is not None:
+        Hq = q.shape[1]
+        ldq, ldqo = _rows(q, dt, T, Hq, d, "q"), _rows(q_out, dt, T, Hq, d, "q_out")
+    if k is not None:
+        Hkv = k.shape[1]
+        ldk, ldko = _rows(k, dt, T, Hkv, d, "k"), _rows(k_out, dt, T, Hkv, d, "k_out")
+    ref = None
+    if norm_rope is not None:
+        norm_rope._need_for(dt, d, q is not None, k is not None)
+        ref = norm_rope._ref
+        if norm_rope.cos is not None:
+            _on_device("positions", positions)
+            _need(positions, torch.int32, (T,), "positions")
+    _check(lib.rf_qk_norm_rope(RF_F32 if dt == torch.float32 else RF_BF16, _ptr(q), ldq, _ptr(k),
+                               ldk, _ptr(q_out), ldqo, _ptr(k_out), ldko, _ptr(positions), ref, T,
+                               Hq, Hkv, d, _stream(stream)), "rf_qk_norm_rope")
+
+
+def rf_kv_append_paged(cache, k, v, norm_rope=None, cu_seqlens=None, q=None, q_out=None,
+                       stream=None) -> None:
+    """Appends new keys and values to a paged cache (an rf_paged_kv), with the
+    keys' norm and rotation (an rf_norm_rope) on the way.  k, v: [total,Hkv,d]
+    bf16, tokens strided as they like; cu_seqlens: int32 [B+1] cumulative new
+    tokens, or None: total / B each; q, q_out: the same tokens' queries
+    [total,Hq,d], normed and rotated in the same launch, or None."""
+    cache._here()
+    total = k.shape[0]
+    Hkv, d = cache.Hkv, cache.d
+    ldk = _rows(k, torch.bfloat16, total, Hkv, d, "k")
+    ldv = _rows(v, torch.bfloat16, total, Hkv, d, "v")
+    Hq = ldq = ldqo = 0
+    if q is not None:
+        Hq = q.shape[1]
+        ldq = _rows(q, torch.bfloat16, total, Hq, d, "q")
+        ldqo = _rows(q_out, torch.bfloat16, total, Hq, d, "q_out")
+    if cu_seqlens is not None:
+        _on_device("cu_seqlens", cu_seqlens)
+        _need(cu_seqlens, torch.int32, (cache.B + 1,), "cu_seqlens")
+    ref = None
+    if norm_rope is not None:
+        norm_rope._need_for(torch.bfloat16, d, q is not None, True)
+        ref = norm_rope._ref
+    _check(lib.rf_kv_append_paged(cache._ref, _ptr(k), ldk, _ptr(v), ldv, _ptr(cu_seqlens), total,
+                                  ref, _ptr(q), ldq, _ptr(q_out) if Hq else None, ldqo, Hq,
+                                  _stream(stream)), "rf_kv_append_paged")
+
+
+def rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq=1, d=128) -> int:
+    return lib.rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq, d)
+
+
+def rf_attn_decode_paged(cache, q, o, scale: float, workspace, stream=None) -> None:
+    """Decode attention over a paged cache (an rf_paged_kv).  q, o:
+    [B,Tq,Hq,d] (or [B,Hq,d]: Tq = 1) bf16, the last Tq tokens of each
+    sequence; workspace: a uint8 CUDA tensor of at least
+    rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq, d) bytes."""
+    cache._here()
+    shape = tuple(q.shape)
+    if len(shape) not in (3, 4) or shape[0] != cache.B or shape[-1] != cache.d:
+        raise ValueError(f"q must be [{cache.B}, Tq, Hq, {cache.d}] or [{cache.B}, Hq, {cache.d}], "
+                         f"got {shape}")
+    Tq, Hq = (1, shape[1]) if len(shape) == 3 else shape[1:3]
+    _on_device("q", q)
+    _need(q, torch.bfloat16, shape, "q")
+    _on_device("o", o)
+    _need(o, torch.bfloat16, shape, "o")
+    ws_bytes = 0
+    if workspace is not None:
+        _on_device("workspace", workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib.rf_attn_decode_paged(cache._ref, _ptr(q), _ptr(o), Hq, Tq, float(scale),
+                                    _ptr(workspace), ws_bytes, _stream(stream)),
+           "rf_attn_decode_paged")
+
+
 def rf_selftest_wait_timeout(timeout_us: int, stream=None) -> None:
     _check(lib.rf_selftest_wait_timeout(int(timeout_us), _stream(stream)),
            "rf_selftest_wait_timeout")
@@ -372,3 +594,33 @@ def rf_selftest_moe_plan(T: int, D: int, E: int, sms: int) -> int:
     is consistent, -1 for refused sizes, else the number of the first failed
     check."""
     return lib.rf_selftest_moe_plan(int(T), int(D), int(E), int(sms))
+
+
+def _host_i32(t, name):
+    if not isinstance(t, torch.Tensor) or t.is_cuda or t.dtype != torch.int32 or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CPU tensor")
+    return _ptr(t)
+
+
+def rf_selftest_append_plan(block_table, seq_lens, cu_seqlens, total: int, num_pages: int,
+                            page_size: int, max_pos: int = 0) -> int:
+    """Host-side check of the append's work items (no GPU needed): int32 CPU
+    tensors block_table [B, max_pages], seq_lens [B], cu_seqlens [B+1] or None.
+    0 when they are consistent, -1 for refused sizes, else the number of the
+    first failed check (see include/rf.h)."""
+    B, max_pages = block_table.shape
+    if seq_lens.numel() != B or (cu_seqlens is not None and cu_seqlens.numel() != B + 1):
+        raise ValueError("block_table, seq_lens and cu_seqlens must agree on B")
+    return lib.rf_selftest_append_plan(
+        _host_i32(block_table, "block_table"), _host_i32(seq_lens, "seq_lens"),
+        None if cu_seqlens is None else _host_i32(cu_seqlens, "cu_seqlens"), B, int(total),
+        int(num_pages), int(page_size), max_pages, int(max_pos))
+
+
+def rf_selftest_decode_paged_plan(seq_lens, tiles: int, max_len: int, warps: int, sms: int) -> int:
+    """Host-side check of the paged decode's partition (no GPU needed):
+    seq_lens an int32 CPU tensor; 0 when it is consistent, -1 for refused
+    sizes, else the number of the first failed check (see include/rf.h)."""
+    return lib.rf_selftest_decode_paged_plan(_host_i32(seq_lens, "seq_lens"), seq_lens.numel(),
+                                             int(tiles), int(max_len), int(warps), int(sms))

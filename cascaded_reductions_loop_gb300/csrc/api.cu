@@ -427,6 +427,169 @@ rf_status rf_absmax_quant_fp8(const void* X, int M, int K, float* sx_out, uint8_
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
+static bool aligned4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static rf_status paged_check(const rf_paged_kv* c) {
+  if (!c || !ptr_ok(c->k) || !ptr_ok(c->v) || !aligned4(c->block_table) || !aligned4(c->seq_lens))
+    return RF_ERR_INVALID_ARG;
+  if (c->dtype != RF_BF16 && c->dtype != RF_E4M3) return RF_ERR_INVALID_ARG;
+  if (c->dtype == RF_E4M3 && (!ptr_ok(c->k_scale) || !ptr_ok(c->v_scale)))
+    return RF_ERR_INVALID_ARG;
+  if (c->B < 1 || c->num_pages < 1 || c->max_pages < 1 || c->Hkv < 1 || c->page_size < 1 ||
+      c->d < 1)
+    return RF_ERR_INVALID_ARG;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return RF_ERR_UNSUPPORTED;
+  if (c->d != 64 && c->d != 128) return RF_ERR_UNSUPPORTED;
+  if ((int64_t)c->num_pages * c->Hkv >= (1ll << 31) / c->page_size ||
+      (int64_t)c->max_pages * c->page_size > (1ll << 30))
+    return RF_ERR_INVALID_ARG;
+  return RF_OK;
+}
+
+// Checks what of `in` applies to heads of d elements and brings it into *out.
+static rf_status norm_rope_check(const rf_norm_rope* in, int d, bool has_q, bool has_k,
+                                 NormRope* out) {
+  *out = NormRope{nullptr, nullptr, 0, 0, 0, nullptr, nullptr, 0.f};
+  if (!in) return RF_OK;
+  if ((in->cos == nullptr) != (in->sin == nullptr)) return RF_ERR_INVALID_ARG;
+  if (in->cos) {
+    if (!aligned16(in->cos) || !aligned16(in->sin)) return RF_ERR_INVALID_ARG;
+    if (in->max_pos < 1 || in->rot_dim < 16 || in->rot_dim > d || in->rot_dim % 16 != 0)
+      return RF_ERR_INVALID_ARG;
+    if (in->interleaved != 0 && in->interleaved != 1) return RF_ERR_INVALID_ARG;
+    out->cos = in->cos;
+    out->sin = in->sin;
+    out->max_pos = in->max_pos;
+    out->rot = in->rot_dim;
+    out->interleaved = in->interleaved;
+  }
+  if (!aligned16(in->q_weight) || !aligned16(in->k_weight)) return RF_ERR_INVALID_ARG;
+  if (has_q) out->wq = in->q_weight;
+  if (has_k) out->wk = in->k_weight;
+  if (in->q_weight || in->k_weight) {
+    if (!(in->eps > 0.f) || !(in->eps < INFINITY)) return RF_ERR_INVALID_ARG;
+    out->eps = in->eps;
+  }
+  return RF_OK;
+}
+
+// A tensor of T rows [H][d], `ld` elements apart: 16-byte aligned rows.
+static bool rows_ok(const void* p, int64_t ld, int T, int H, int d, int elem) {
+  return ptr_ok(p) && ld >= (int64_t)H * d && ld < (1ll << 40) / T && ld * elem % 16 == 0;
+}
+
+rf_status rf_qk_norm_rope(int dtype, const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                          void* Qo, int64_t ldqo, void* Ko, int64_t ldko,
+                          const int32_t* positions, const rf_norm_rope* nr, int T, int Hq, int Hkv,
+                          int d, rf_stream_t stream) {
+  if (dtype != RF_F32 && dtype != RF_BF16) return RF_ERR_INVALID_ARG;
+  if (T < 1 || Hq < 0 || Hkv < 0 || (int64_t)Hq + Hkv < 1 || d < 1) return RF_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return RF_ERR_UNSUPPORTED;
+  if (Hq > (1 << 20) || Hkv > (1 << 20) || (int64_t)T * (Hq + Hkv) >= (1ll << 31))
+    return RF_ERR_INVALID_ARG;
+  const int elem = dtype == RF_F32 ? 4 : 2;
+  if (Hq > 0 && (!rows_ok(Q, ldq, T, Hq, d, elem) || !rows_ok(Qo, ldqo, T, Hq, d, elem)))
+    return RF_ERR_INVALID_ARG;
+  if (Hkv > 0 && (!rows_ok(K, ldk, T, Hkv, d, elem) || !rows_ok(Ko, ldko, T, Hkv, d, elem)))
+    return RF_ERR_INVALID_ARG;
+  NormRope n;
+  const rf_status st = norm_rope_check(nr, d, Hq > 0, Hkv > 0, &n);
+  if (st != RF_OK) return st;
+  if (n.rot > 0 && !aligned4(positions)) return RF_ERR_INVALID_ARG;
+  unsigned* err = device_error_word();
+  if (!err) return RF_ERR_CUDA;
+  return from_cuda(launch_qk_norm_rope(dtype, n, Q, ldq, K, ldk, Qo, ldqo, Ko, ldko, positions, T,
+                                       Hq, Hkv, d, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+rf_status rf_kv_append_paged(const rf_paged_kv* cache, const void* K, int64_t ldk, const void* V,
+                             int64_t ldv, const int32_t* cu_seqlens, int total,
+                             const rf_norm_rope* nr, const void* Q, int64_t ldq, void* Qo,
+                             int64_t ldqo, int Hq, rf_stream_t stream) {
+  rf_status st = paged_check(cache);
+  if (st != RF_OK) return st;
+  const int d = cache->d;
+  if (total < 1 || Hq < 0 || Hq > (1 << 20)) return RF_ERR_INVALID_ARG;
+  if (cu_seqlens ? !aligned4(cu_seqlens) : total % cache->B != 0) return RF_ERR_INVALID_ARG;
+  if (!rows_ok(K, ldk, total, cache->Hkv, d, 2) || !rows_ok(V, ldv, total, cache->Hkv, d, 2))
+    return RF_ERR_INVALID_ARG;
+  if (Hq > 0 && (!rows_ok(Q, ldq, total, Hq, d, 2) || !rows_ok(Qo, ldqo, total, Hq, d, 2)))
+    return RF_ERR_INVALID_ARG;
+  if (append_grid_bound(total, cache->B, cu_seqlens != nullptr, cache->page_size, cache->Hkv,
+                        Hq) >= (1ll << 31))
+    return RF_ERR_INVALID_ARG;
+  NormRope n;
+  st = norm_rope_check(nr, d, Hq > 0, true, &n);
+  if (st != RF_OK) return st;
+  unsigned* err = device_error_word();
+  if (!err) return RF_ERR_CUDA;
+  return from_cuda(launch_kv_append_paged(*cache, n, K, ldk, V, ldv, cu_seqlens, total, Q, ldq, Qo,
+                                          ldqo, Hq, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static rf_status decode_paged_check(int B, int Hq, int Hkv, int Tq, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Tq < 1 || d < 1 || Hq % Hkv != 0) return RF_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return RF_ERR_UNSUPPORTED;
+  if ((int64_t)B * Hq >= (1ll << 31) / Tq) return RF_ERR_INVALID_ARG;
+  return RF_OK;
+}
+
+size_t rf_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Tq, int d) {
+  if (decode_paged_check(B, Hq, Hkv, Tq, d) != RF_OK) return 0;
+  return decode_paged_workspace_bytes(B, Hkv, Hq / Hkv * Tq, d);
+}
+
+rf_status rf_attn_decode_paged(const rf_paged_kv* cache, const void* Q, void* O, int Hq, int Tq,
+                               float scale, void* workspace, size_t workspace_bytes,
+                               rf_stream_t stream) {
+  rf_status st = paged_check(cache);
+  if (st != RF_OK) return st;
+  if (!ptr_ok(Q) || !ptr_ok(O)) return RF_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale < INFINITY)) return RF_ERR_INVALID_ARG;
+  st = decode_paged_check(cache->B, Hq, cache->Hkv, Tq, cache->d);
+  if (st != RF_OK) return st;
+  const int R = Hq / cache->Hkv * Tq;
+  if (decode_paged_max_chunks(cache->B, cache->Hkv, R, cache->max_pages, cache->page_size) >=
+      (1ll << 31))
+    return RF_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace)) return RF_ERR_WORKSPACE;
+  const size_t need = decode_paged_workspace_bytes(cache->B, cache->Hkv, R, cache->d);
+  if (need == 0) return RF_ERR_CUDA;   // the partition needs the device's SM count
+  if (workspace_bytes < need) return RF_ERR_WORKSPACE;
+  unsigned* err = device_error_word();
+  if (!err) return RF_ERR_CUDA;
+  return from_cuda(launch_decode_paged(*cache, Q, O, Hq, Tq, scale, workspace, err,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int rf_selftest_append_plan(const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* cu_seqlens, int B, int total, int num_pages,
+                            int page_size, int max_pages, int max_pos) {
+  if (!block_table || !seq_lens || B < 1 || total < 1 || num_pages < 1 || page_size < 1 ||
+      page_size > 128 || max_pages < 1 || max_pos < 0 || (!cu_seqlens && total % B != 0) ||
+      (int64_t)max_pages * page_size > (1ll << 30))
+    return -1;
+  rf_paged_kv c = {};
+  c.block_table = block_table;
+  c.seq_lens = seq_lens;
+  c.B = B;
+  c.num_pages = num_pages;
+  c.page_size = page_size;
+  c.max_pages = max_pages;
+  c.Hkv = 1;
+  return append_plan_selfcheck(c, cu_seqlens, total, max_pos);
+}
+
+int rf_selftest_decode_paged_plan(const int32_t* seq_lens, int B, int tiles, int max_len,
+                                  int warps, int sms) {
+  if (!seq_lens || B < 1 || tiles < 1 || max_len < 1 || max_len > (1 << 30) ||
+      (warps != 4 && warps != 8) || sms < 1 || sms > (1 << 20) ||
+      (int64_t)B * tiles >= (1ll << 31) || (int64_t)B * tiles * (max_len / 32 + 1) >= (1ll << 31))
+    return -1;
+  return decode_paged_plan_selfcheck(seq_lens, B, tiles, max_len, warps, sms);
+}
+
 rf_status rf_selftest_wait_timeout(int timeout_us, rf_stream_t stream) {
   if (timeout_us < 1 || timeout_us > 1000000) return RF_ERR_INVALID_ARG;
   unsigned* err = device_error_word();

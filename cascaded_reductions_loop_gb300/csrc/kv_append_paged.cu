@@ -1,0 +1,585 @@
+// kv_append_paged.cu -- appends new keys and values to a paged cache, with
+// the keys' norm and rotation on the way, and (optionally) the norm and
+// rotation of the same tokens' queries in the same launch.
+//
+// Layout.  Pages are [num_pages][Hkv][page_size][d]; the token at position p
+// of sequence b lives in page block_table[b][p / page_size], slot
+// p % page_size.  An E4M3 cache has one fp32 scale per (page, kv head) for
+// keys and one for values: a value is code * scale.
+//
+// The 8-bit append is itself a cascade with a running state: the scale of a
+// page's head is the smallest power of two s with absmax <= 448 s, and the
+// absmax of a page that is filled a token at a time is a running maximum.
+// When a new token raises it, the codes that the page holds already are
+// rescaled to the new s.  The scale is a power of two so that this rescaling
+// is exact except where a code falls into E4M3's subnormals (the format's
+// relative step does not depend on the scale, so the choice costs at most one
+// of its 18 binades).
+//
+// Work items: one page of one sequence that receives tokens ("item") and one
+// kv head, so that a scale has one owner and no atomics are needed.
+//  - step kernel (one new token a sequence): one lane group for the key row
+//    and one for the value row of an (item, head); a page that has to be
+//    rescaled is rescaled by the whole warp.
+//  - prompt kernel: one CTA of 256 threads for an (item, head); the new rows
+//    stay in registers between the absmax and the quantisation, so each is
+//    read once.
+// Query rows are further CTAs of the same launch (norm_rope.cuh).
+//
+// What bounds it: memory for prompts, launch latency for a step.
+#include <vector>
+
+#include "norm_rope.cuh"
+
+namespace rf {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------- quantisation
+
+// Exponent field (biased by 127) of the smallest power of two s >= 2^-126
+// with a <= 448 s; a >= 0, finite.  448 = 1.75 * 2^8.
+__device__ __forceinline__ int scale_exp(float a) {
+  const uint32_t u = __float_as_uint(a);
+  const int e = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return e < 1 ? 1 : e;
+}
+
+// Two values (already divided by the scale) -> two E4M3 codes, round to
+// nearest even, saturating; NaN -> 0x7F.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+
+// Two E4M3 codes -> two floats (exact).
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+  float lo, hi;
+  asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(h));
+  return make_float2(lo, hi);
+}
+// Four codes of a page whose scale grows by 1 / ratio.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+  const float2 a = from_e4m3x2(w & 0xFFFFu), b = from_e4m3x2(w >> 16);
+  return e4m3x4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+}
+__device__ __forceinline__ uint4 rescale16(uint4 w, float ratio) {
+  return make_uint4(rescale4(w.x, ratio), rescale4(w.y, ratio), rescale4(w.z, ratio),
+                    rescale4(w.w, ratio));
+}
+
+// Largest finite magnitude of eight values (infinities saturate and NaN keeps
+// its code: neither sets the scale).
+__device__ __forceinline__ float absmax8(const float (&v)[8]) {
+  float a = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float m = fabsf(v[e]);
+    if (m < INFINITY) a = fmaxf(a, m);
+  }
+  return a;
+}
+
+// The scale of a page's head after the append: a = absmax of the new values,
+// s_old the scale of the `off` tokens it holds (not looked at when off = 0).
+__device__ __forceinline__ float new_scale(float a, float s_old, int off) {
+  const float s = __uint_as_float((uint32_t)scale_exp(a) << 23);
+  return off > 0 ? fmaxf(s, s_old) : s;
+}
+
+// ------------------------------------------------------------- the plan
+// The same code on the device and, for the self-check, on the host.
+
+struct Seqs {
+  const int* block_table;
+  const int* seq_lens;
+  const int* cu;          // cumulative new tokens [B + 1], or nullptr: n_uniform each
+  int B, n_uniform, total, num_pages, page_size, max_pages, Hkv;
+  int max_len;            // longest length the rotation's tables and the block table allow
+};
+
+// New tokens of sequence b: token rows [first, first + n), positions
+// [start, start + n).  n = 0 where there is nothing to do.
+struct NewTokens {
+  int first, n, start;
+};
+
+// report: note inconsistent sizes (one caller per sequence is enough).
+__host__ __device__ __forceinline__ NewTokens new_tokens(const Seqs& sq, int b, bool report,
+                                                         unsigned* err) {
+  NewTokens r = {0, 0, 0};
+  int c0, c1;
+  if (sq.cu) {
+    c0 = ld_int(sq.cu, b, sq.B + 1, err);
+    c1 = ld_int(sq.cu, b + 1, sq.B + 1, err);
+    if (c0 < 0 || c1 < c0 || c1 > sq.total) {
+      if (report) note_error(err, kDevErrInput);
+      return r;
+    }
+  } else {
+    c0 = b * sq.n_uniform;
+    c1 = c0 + sq.n_uniform;
+  }
+  const int len = ld_int(sq.seq_lens, b, sq.B, err);
+  if (len == 0 || c1 == c0) return r;        // a padded row of the batch, or no new tokens
+  if (len < c1 - c0 || len > sq.max_len) {
+    if (report) note_error(err, kDevErrInput);
+    return r;
+  }
+  r.first = c0;
+  r.n = c1 - c0;
+  r.start = len - r.n;
+  return r;
+}
+
+// The last b with cu[b] <= t (0 <= t < total); cu[0] = 0.
+__host__ __device__ __forceinline__ int find_seq(const Seqs& sq, int t, unsigned* err) {
+  int lo = 0, hi = sq.B;                     // cu[lo] <= t, and (if in order) cu[hi] > t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (ld_int(sq.cu, mid, sq.B + 1, err) <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Sequence and position of token t; false if there is nothing to do for it.
+__host__ __device__ __forceinline__ bool find_token(const Seqs& sq, int t, int* pos,
+                                                    unsigned* err) {
+  const int b = sq.cu ? find_seq(sq, t, err) : t / sq.n_uniform;
+  const NewTokens nt = new_tokens(sq, b, false, err);
+  *pos = nt.start + (t - nt.first);
+  return nt.n > 0 && t >= nt.first && t < nt.first + nt.n;
+}
+
+// Items.  Sequence b gets the item numbers [f(b), f(b + 1)), as many as its
+// n tokens can touch pages at any offset.  Uniform n: pages_of(n) each.  With
+// cu: f(b) = cu[b] / page_size + 2 b, since n tokens touch at most
+// n / page_size + 2 pages and the floor of a sum is at least the sum of floors.
+__host__ __device__ __forceinline__ int pages_of(int n, int page_size) {
+  return (int)(((int64_t)n + page_size - 2) / page_size) + 1;
+}
+__host__ __device__ __forceinline__ int64_t num_items(int total, int B, int n_uniform, bool has_cu,
+                                                      int page_size) {
+  return has_cu ? (int64_t)total / page_size + 2 * (int64_t)B
+                : (int64_t)B * pages_of(n_uniform, page_size);
+}
+
+// The page that item x stands for: new tokens [t0, t0 + n) at positions pos0
+// onwards go to slots [off, off + n) of page phys.  n = 0: nothing to do.
+struct Item {
+  int t0, n, off, pos0, phys;
+};
+__host__ __device__ __forceinline__ Item find_item(const Seqs& sq, int x, bool report,
+                                                   unsigned* err) {
+  Item it = {0, 0, 0, 0, 0};
+  int b, p;
+  if (sq.cu) {
+    int lo = 0, hi = sq.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((int64_t)(ld_int(sq.cu, mid, sq.B + 1, err) / sq.page_size) + 2 * (int64_t)mid <= x)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    b = lo;
+    const int64_t q =
+        (int64_t)x - (ld_int(sq.cu, b, sq.B + 1, err) / sq.page_size) - 2 * (int64_t)b;
+    if (q < 0 || q > x) return it;
+    p = (int)q;
+  } else {
+    const int m = pages_of(sq.n_uniform, sq.page_size);
+    b = x / m;
+    p = x - b * m;
+  }
+  if (b >= sq.B) return it;
+  const NewTokens nt = new_tokens(sq, b, report && p == 0, err);
+  if (nt.n == 0) return it;
+  const int64_t page = (int64_t)nt.start / sq.page_size + p;
+  const int64_t lo_pos = page * sq.page_size;
+  const int64_t end = (int64_t)nt.start + nt.n;
+  const int64_t a = lo_pos > nt.start ? lo_pos : nt.start;
+  const int64_t z = lo_pos + sq.page_size < end ? lo_pos + sq.page_size : end;
+  if (a >= z) return it;
+  const int phys = ld_int(sq.block_table, (int64_t)b * sq.max_pages + page,
+                          (int64_t)sq.B * sq.max_pages, err);
+  if (phys < 0 || phys >= sq.num_pages) {
+    if (report) note_error(err, kDevErrInput);
+    return it;
+  }
+  it.t0 = nt.first + (int)(a - nt.start);
+  it.n = (int)(z - a);
+  it.off = (int)(a - lo_pos);
+  it.pos0 = (int)a;
+  it.phys = phys;
+  return it;
+}
+
+struct Cache {
+  uint8_t* pages[2];      // K, V
+  float* scale[2];        // E4M3 only
+};
+
+using bf16 = __nv_bfloat16;
+
+// ------------------------------------------------------------- query rows
+
+template <int D>
+__device__ __forceinline__ void query_rows(const Seqs& sq, const NormRope& nr,
+                                           const RowsIn<bf16>& q, const RowsOut<bf16>& qo, int Hq,
+                                           int cta, unsigned* err) {
+  constexpr int LG = D / 8;
+  const int li = threadIdx.x % LG;
+  const int64_t u = (int64_t)cta * (kThreads / LG) + threadIdx.x / LG;
+  const int t = (int)(u / Hq), h = (int)(u % Hq);
+  int pos = 0;
+  const bool active = t < sq.total && find_token(sq, t, &pos, err);
+  norm_rope_heads<bf16, D, 1>(nr, static_cast<const bf16*>(nr.wq), q, qo, sq.total, Hq, t, h, pos,
+                              active, li, err);
+}
+
+// ------------------------------------------------------------- one token a sequence
+
+template <int D, bool kF8>
+__global__ void __launch_bounds__(kThreads)
+    append_step_kernel(const Seqs sq, const NormRope nr, const RowsIn<bf16> k, const RowsIn<bf16> v,
+                       const RowsIn<bf16> q, const RowsOut<bf16> qo, int Hq, const Cache cache,
+                       int kv_ctas, unsigned* err) {
+  if ((int)blockIdx.x >= kv_ctas) {
+    query_rows<D>(sq, nr, q, qo, Hq, (int)blockIdx.x - kv_ctas, err);
+    return;
+  }
+  constexpr int LG = D / 8;                   // lanes of a row
+  constexpr int kPairs = 32 / (2 * LG);       // (item, head) pairs of a warp
+  const int lane = threadIdx.x & 31, li = lane % LG, grp = lane / LG;
+  const bool is_v = grp & 1;
+  const int64_t u =
+      ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kPairs + (grp >> 1);
+  const int b = (int)(u / sq.Hkv), h = (int)(u % sq.Hkv);
+  Item it = {0, 0, 0, 0, 0};
+  if (b < sq.B) it = find_item(sq, b, h == 0 && !is_v && li == 0, err);
+  const bool active = it.n > 0;
+
+  const RowsIn<bf16>& in = is_v ? v : k;
+  Raw8<bf16> x = {};
+  if (active)
+    x = load8<bf16>(in.p, (int64_t)it.t0 * in.ld + (int64_t)h * D + 8 * li,
+                    (int64_t)(sq.total - 1) * in.ld + (int64_t)sq.Hkv * D, err);
+  RopeLane rp = {};
+  if (active && !is_v && 8 * li < nr.rot) rp = load_rope(nr, it.pos0, li, err);
+  WeightLane w = {};
+  if (nr.wk && !is_v) w = load_weight<bf16, D>(nr, static_cast<const bf16*>(nr.wk), li, err);
+  float y[8];
+  norm_rope_row<bf16, D>(nr, x, nr.wk != nullptr, w, rp, li, y);
+  if (is_v) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = x.get(e);
+  }
+
+  const int64_t head = (int64_t)it.phys * sq.Hkv + h;         // (page, head)
+  const int64_t n_pages = (int64_t)sq.num_pages * sq.Hkv * sq.page_size * D;
+  const int64_t row = (head * sq.page_size + it.off) * D + 8 * li;
+  uint8_t* pages = is_v ? cache.pages[1] : cache.pages[0];
+  if (!kF8) {
+    if (active) store8(reinterpret_cast<bf16*>(pages), row, y, n_pages, err);
+    return;
+  }
+  float a = absmax8(y);
+#pragma unroll
+  for (int o = LG / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  float* sc = is_v ? cache.scale[1] : cache.scale[0];
+  const int64_t n_sc = (int64_t)sq.num_pages * sq.Hkv;
+  const float s_old = active && it.off > 0 && RF_IN(err, head, n_sc) ? sc[head] : 0.f;
+  const float s = new_scale(a, s_old, it.off);
+  const bool grow = active && it.off > 0 && s > s_old;
+  const unsigned growing = __ballot_sync(0xffffffffu, grow && li == 0);   // after everyone's load
+  if (active) {
+    const float inv = 1.f / s;                                // exact: a power of two
+    if (RF_IN(err, row + 7, n_pages))
+      *reinterpret_cast<uint2*>(pages + row) =
+          make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                     e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+    if (li == 0 && RF_IN(err, head, n_sc)) sc[head] = s;
+  }
+  // pages whose scale grew: the warp rescales the off * D codes held already
+  for (unsigned m = growing; m; m &= m - 1) {
+    const int src = __ffs(m) - 1;
+    const int64_t at = __shfl_sync(0xffffffffu, head, src) * sq.page_size * D;
+    const int n16 = __shfl_sync(0xffffffffu, it.off, src) * D / 16;
+    const float ratio = __shfl_sync(0xffffffffu, s_old / s, src);
+    uint8_t* pg = ((src / LG) & 1 ? cache.pages[1] : cache.pages[0]) + at;
+    for (int i0 = 0; i0 < n16; i0 += 32 * 8) {
+      uint4 c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + 32 * j + lane;
+        if (i < n16 && RF_IN(err, at + 16 * i + 15, n_pages))
+          c[j] = reinterpret_cast<const uint4*>(pg)[i];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + 32 * j + lane;
+        if (i < n16 && RF_IN(err, at + 16 * i + 15, n_pages))
+          reinterpret_cast<uint4*>(pg)[i] = rescale16(c[j], ratio);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------- prompts
+
+// SW: sweeps of the CTA's 256 / (D / 8) rows that cover a page.
+template <int D, bool kF8, int SW>
+__global__ void __launch_bounds__(kThreads)
+    append_prompt_kernel(const Seqs sq, const NormRope nr, const RowsIn<bf16> k,
+                         const RowsIn<bf16> v, const RowsIn<bf16> q, const RowsOut<bf16> qo, int Hq,
+                         const Cache cache, int kv_ctas, unsigned* err) {
+  if ((int)blockIdx.x >= kv_ctas) {
+    query_rows<D>(sq, nr, q, qo, Hq, (int)blockIdx.x - kv_ctas, err);
+    return;
+  }
+  constexpr int LG = D / 8, kRows = kThreads / LG;
+  const int li = threadIdx.x % LG, r = threadIdx.x / LG;
+  const int x = (int)blockIdx.x / sq.Hkv, h = (int)blockIdx.x % sq.Hkv;
+  const Item it = find_item(sq, x, h == 0 && threadIdx.x == 0, err);
+  if (it.n == 0) return;
+
+  Raw8<bf16> kx[SW], vx[SW];
+  const int64_t n_k = (int64_t)(sq.total - 1) * k.ld + (int64_t)sq.Hkv * D;
+  const int64_t n_v = (int64_t)(sq.total - 1) * v.ld + (int64_t)sq.Hkv * D;
+#pragma unroll
+  for (int i = 0; i < SW; ++i) {
+    const int t = r + i * kRows;
+    kx[i] = {};
+    vx[i] = {};
+    if (t < it.n) {
+      kx[i] = load8<bf16>(k.p, (int64_t)(it.t0 + t) * k.ld + (int64_t)h * D + 8 * li, n_k, err);
+      vx[i] = load8<bf16>(v.p, (int64_t)(it.t0 + t) * v.ld + (int64_t)h * D + 8 * li, n_v, err);
+    }
+  }
+  WeightLane w = {};
+  if (nr.wk) w = load_weight<bf16, D>(nr, static_cast<const bf16*>(nr.wk), li, err);
+
+  const int64_t head = (int64_t)it.phys * sq.Hkv + h;
+  const int64_t n_pages = (int64_t)sq.num_pages * sq.Hkv * sq.page_size * D;
+  const int64_t row0 = (head * sq.page_size + it.off) * D + 8 * li;
+  float ky[kF8 ? SW : 1][8];
+  float ak = 0.f, av = 0.f;
+#pragma unroll
+  for (int i = 0; i < SW; ++i) {
+    const int t = r + i * kRows;
+    if (i * kRows >= it.n) break;                    // the same for the whole CTA
+    RopeLane rp = {};
+    if (t < it.n && 8 * li < nr.rot) rp = load_rope(nr, it.pos0 + t, li, err);
+    float(&y)[8] = ky[kF8 ? i : 0];
+    norm_rope_row<bf16, D>(nr, kx[i], nr.wk != nullptr, w, rp, li, y);
+    float vf[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) vf[e] = vx[i].get(e);
+    if (kF8) {
+      if (t < it.n) {
+        ak = fmaxf(ak, absmax8(y));
+        av = fmaxf(av, absmax8(vf));
+      }
+    } else if (t < it.n) {
+      store8(reinterpret_cast<bf16*>(cache.pages[0]), row0 + (int64_t)t * D, y, n_pages, err);
+      store8(reinterpret_cast<bf16*>(cache.pages[1]), row0 + (int64_t)t * D, vf, n_pages, err);
+    }
+  }
+  if (!kF8) return;
+
+  __shared__ float red[2][kThreads / 32];
+  ak = warp_max(ak);
+  av = warp_max(av);
+  if ((threadIdx.x & 31) == 0) {
+    red[0][threadIdx.x >> 5] = ak;
+    red[1][threadIdx.x >> 5] = av;
+  }
+  const int64_t n_sc = (int64_t)sq.num_pages * sq.Hkv;
+  float s_old[2] = {0.f, 0.f}, s[2];
+  if (it.off > 0 && RF_IN(err, head, n_sc)) {
+    s_old[0] = cache.scale[0][head];
+    s_old[1] = cache.scale[1][head];
+  }
+  __syncthreads();                       // after it: everyone has read the old scales
+#pragma unroll
+  for (int w2 = 0; w2 < 2; ++w2) {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) a = fmaxf(a, red[w2][i]);
+    s[w2] = new_scale(a, s_old[w2], it.off);
+    if (threadIdx.x == 0 && RF_IN(err, head, n_sc)) cache.scale[w2][head] = s[w2];
+    if (it.off > 0 && s[w2] > s_old[w2]) {
+      const float ratio = s_old[w2] / s[w2];
+      const int64_t at = head * sq.page_size * D;
+      uint4* pg = reinterpret_cast<uint4*>(cache.pages[w2] + at);
+      for (int i = threadIdx.x; i < it.off * D / 16; i += kThreads)
+        if (RF_IN(err, at + 16 * i + 15, n_pages)) pg[i] = rescale16(pg[i], ratio);
+    }
+  }
+  const float ik = 1.f / s[0], iv = 1.f / s[1];
+#pragma unroll
+  for (int i = 0; i < SW; ++i) {
+    const int t = r + i * kRows;
+    const int64_t at = row0 + (int64_t)t * D;
+    if (t < it.n && RF_IN(err, at + 7, n_pages)) {
+      const float(&y)[8] = ky[kF8 ? i : 0];
+      *reinterpret_cast<uint2*>(cache.pages[0] + at) =
+          make_uint2(e4m3x4(y[0] * ik, y[1] * ik, y[2] * ik, y[3] * ik),
+                     e4m3x4(y[4] * ik, y[5] * ik, y[6] * ik, y[7] * ik));
+      float z[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = vx[i].get(e) * iv;
+      *reinterpret_cast<uint2*>(cache.pages[1] + at) =
+          make_uint2(e4m3x4(z[0], z[1], z[2], z[3]), e4m3x4(z[4], z[5], z[6], z[7]));
+    }
+  }
+}
+
+template <int D, bool kF8>
+cudaError_t launch(const Seqs& sq, const NormRope& nr, const RowsIn<bf16>& k,
+                   const RowsIn<bf16>& v, const RowsIn<bf16>& q, const RowsOut<bf16>& qo, int Hq,
+                   const Cache& cache, unsigned* err, cudaStream_t s) {
+  constexpr int LG = D / 8, per = kThreads / LG;
+  const int64_t q_ctas = Hq > 0 ? ((int64_t)sq.total * Hq + per - 1) / per : 0;
+  if (!sq.cu && sq.n_uniform == 1) {
+    const int64_t pairs = kThreads / (2 * LG);
+    const int64_t kv = ((int64_t)sq.B * sq.Hkv + pairs - 1) / pairs;
+    append_step_kernel<D, kF8><<<(unsigned)(kv + q_ctas), kThreads, 0, s>>>(
+        sq, nr, k, v, q, qo, Hq, cache, (int)kv, err);
+    return cudaGetLastError();
+  }
+  const int64_t kv =
+      num_items(sq.total, sq.B, sq.n_uniform, sq.cu != nullptr, sq.page_size) * sq.Hkv;
+  const unsigned grid = (unsigned)(kv + q_ctas);
+#define RF_GO(SW)                                                                              \
+  append_prompt_kernel<D, kF8, SW>                                                             \
+      <<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq, cache, (int)kv, err)
+  switch ((sq.page_size + per - 1) / per) {
+    case 1: RF_GO(1); break;
+    case 2: RF_GO(2); break;
+    case 4: RF_GO(4); break;
+    default: RF_GO(8); break;
+  }
+#undef RF_GO
+  return cudaGetLastError();
+}
+
+Seqs make_seqs(const PagedKV& c, const int* cu, int total, int max_pos) {
+  Seqs sq;
+  sq.block_table = c.block_table;
+  sq.seq_lens = c.seq_lens;
+  sq.cu = cu;
+  sq.B = c.B;
+  sq.n_uniform = cu ? 0 : total / c.B;
+  sq.total = total;
+  sq.num_pages = c.num_pages;
+  sq.page_size = c.page_size;
+  sq.max_pages = c.max_pages;
+  sq.Hkv = c.Hkv;
+  sq.max_len = c.max_pages * c.page_size;             // at most 2^30
+  if (max_pos > 0 && max_pos < sq.max_len) sq.max_len = max_pos;
+  return sq;
+}
+
+}  // namespace
+
+int64_t append_grid_bound(int total, int B, bool has_cu, int page_size, int Hkv, int Hq) {
+  return num_items(total, B, has_cu ? 0 : total / B, has_cu, page_size) * Hkv +
+         (int64_t)total * (Hq > 0 ? Hq : 1);
+}
+
+cudaError_t launch_kv_append_paged(const PagedKV& c, const NormRope& nr, const void* K,
+                                   int64_t ldk, const void* V, int64_t ldv, const int* cu,
+                                   int total, const void* Q, int64_t ldq, void* Qo, int64_t ldqo,
+                                   int Hq, unsigned* err, cudaStream_t s) {
+  const Seqs sq = make_seqs(c, cu, total, nr.rot > 0 ? nr.max_pos : 0);
+  Cache cache = {{static_cast<uint8_t*>(c.k), static_cast<uint8_t*>(c.v)}, {c.k_scale, c.v_scale}};
+  const RowsIn<bf16> k = {static_cast<const bf16*>(K), ldk}, v = {static_cast<const bf16*>(V), ldv},
+                     q = {static_cast<const bf16*>(Q), ldq};
+  const RowsOut<bf16> qo = {static_cast<bf16*>(Qo), ldqo};
+  const bool f8 = c.dtype == RF_E4M3;
+  if (c.d == 64)
+    return f8 ? launch<64, true>(sq, nr, k, v, q, qo, Hq, cache, err, s)
+              : launch<64, false>(sq, nr, k, v, q, qo, Hq, cache, err, s);
+  return f8 ? launch<128, true>(sq, nr, k, v, q, qo, Hq, cache, err, s)
+            : launch<128, false>(sq, nr, k, v, q, qo, Hq, cache, err, s);
+}
+
+// Host-side walk of the items (the functions above, shared by host and
+// device).  All arrays are host arrays.  Returns 0 when every invariant
+// holds, else the number of the first that fails:
+//   1 no index leaves its array;
+//   2 an item's page and slots lie in the cache and in one page;
+//   3 every token of a sequence that is not skipped is written once, to the
+//     slot of its position, and no other token is;
+//   4 the query rows' lookup finds the same position for the same tokens;
+//   5 inconsistent sizes, and only those, are noted.
+int append_plan_selfcheck(const PagedKV& c, const int* cu, int total, int max_pos) {
+  const Seqs sq = make_seqs(c, cu, total, max_pos);
+  unsigned err = 0;
+  // tables out of order name tokens twice or not at all: only the bounds
+  // hold then
+  bool order = true;
+  if (cu) {
+    order = cu[0] == 0 && cu[c.B] == total;
+    for (int b = 0; b < c.B; ++b) order = order && cu[b] <= cu[b + 1];
+  }
+  std::vector<int> pos_of((size_t)total, -1);
+  const int64_t n = num_items(total, c.B, sq.n_uniform, cu != nullptr, c.page_size);
+  for (int64_t x = 0; x < n; ++x) {
+    const Item it = find_item(sq, (int)x, true, &err);
+    if (err & kDevErrBounds) return 1;
+    if (it.n == 0) continue;
+    if (it.n < 0 || it.off < 0 || it.off + it.n > c.page_size || it.phys < 0 ||
+        it.phys >= c.num_pages || it.t0 < 0 || it.t0 + it.n > total)
+      return 2;
+    for (int i = 0; i < it.n; ++i) {
+      if (order &&
+          (pos_of[(size_t)it.t0 + i] != -1 || (it.pos0 + i) % c.page_size != it.off + i))
+        return 3;
+      pos_of[(size_t)it.t0 + i] = it.pos0 + i;
+    }
+  }
+  bool bad = false;
+  std::vector<int> want((size_t)total, -1), seen((size_t)total, -1);
+  for (int b = 0; b < c.B; ++b) {
+    const int64_t c0 = cu ? cu[b] : (int64_t)b * sq.n_uniform;
+    const int64_t c1 = cu ? cu[b + 1] : c0 + sq.n_uniform;
+    if (!order) break;
+    const int64_t len = c.seq_lens[b];
+    if (len == 0 || c1 == c0) continue;
+    if (len < c1 - c0 || len > sq.max_len) {
+      bad = true;
+      continue;
+    }
+    for (int64_t t = c0; t < c1; ++t) {
+      const int64_t pos = len - (c1 - c0) + (t - c0);
+      const int page = c.block_table[(int64_t)b * c.max_pages + pos / c.page_size];
+      seen[(size_t)t] = (int)pos;
+      if (page < 0 || page >= c.num_pages) bad = true;
+      else want[(size_t)t] = (int)pos;
+    }
+  }
+  if (order && pos_of != want) return 3;
+  for (int t = 0; t < total; ++t) {
+    int pos = 0;
+    const bool active = find_token(sq, t, &pos, &err);
+    if (err & kDevErrBounds) return 1;
+    if (order && (active ? pos : -1) != seen[(size_t)t]) return 4;
+  }
+  if (order && bad != ((err & kDevErrInput) != 0)) return 5;
+  return 0;
+}
+
+}  // namespace rf

@@ -51,6 +51,26 @@ __device__ __forceinline__ bool bounds_ok(unsigned* err, int64_t i, int64_t n) {
 #define RF_IN(err, i, n) ((void)sizeof((i) + (n)), true)
 #endif
 
+// For plans that run on the device and, in a self-check, on the host (where
+// `err` is a host word and outside accesses are always noted).
+__host__ __device__ __forceinline__ void note_error(unsigned* err, unsigned bits) {
+#ifdef __CUDA_ARCH__
+  raise_error(err, bits);
+#else
+  *err |= bits;
+#endif
+}
+// p[i] of an array of n; 0 where an access outside it was skipped.
+__host__ __device__ __forceinline__ int ld_int(const int* p, int64_t i, int64_t n, unsigned* err) {
+#ifdef __CUDA_ARCH__
+  return RF_IN(err, i, n) ? __ldg(p + i) : 0;
+#else
+  if (i >= 0 && i < n) return p[i];
+  *err |= kDevErrBounds;
+  return 0;
+#endif
+}
+
 // ----------------------------------------------------------------- smem
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

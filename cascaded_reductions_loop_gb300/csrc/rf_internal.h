@@ -100,6 +100,41 @@ cudaError_t launch_absmax_fp8_gemm(const void* X, const uint8_t* Wq, const float
                                    int M, int N, int K, float* sx, uint8_t* xq, void* workspace,
                                    unsigned* err, cudaStream_t s);
 
+// Paged cache: the description of rf.h, validated.
+using PagedKV = ::rf_paged_kv;
+
+// Norm and rotation, validated: rot = 0 for no rotation, null weights for no norm.
+struct NormRope {
+  const float* cos;
+  const float* sin;
+  int max_pos, rot, interleaved;
+  const void* wq;
+  const void* wk;
+  float eps;
+};
+
+cudaError_t launch_qk_norm_rope(int dtype, const NormRope& nr, const void* Q, int64_t ldq,
+                                const void* K, int64_t ldk, void* Qo, int64_t ldqo, void* Ko,
+                                int64_t ldko, const int* positions, int T, int Hq, int Hkv, int d,
+                                unsigned* err, cudaStream_t s);
+
+// An upper bound of the CTAs launch_kv_append_paged starts (must fit a grid).
+int64_t append_grid_bound(int total, int B, bool has_cu, int page_size, int Hkv, int Hq);
+// host only (host arrays): 0 when the append's items are consistent
+int append_plan_selfcheck(const PagedKV& c, const int* cu, int total, int max_pos);
+cudaError_t launch_kv_append_paged(const PagedKV& c, const NormRope& nr, const void* K,
+                                   int64_t ldk, const void* V, int64_t ldv, const int* cu,
+                                   int total, const void* Q, int64_t ldq, void* Qo, int64_t ldqo,
+                                   int Hq, unsigned* err, cudaStream_t s);
+
+// R = Tq * Hq / Hkv query rows of a kv head.
+int64_t decode_paged_max_chunks(int B, int Hkv, int R, int max_pages, int page_size);
+// host only (host array): 0 when the partition over sms CTAs of W warps is consistent
+int decode_paged_plan_selfcheck(const int* seq_lens, int B, int HR, int max_len, int W, int sms);
+size_t decode_paged_workspace_bytes(int B, int Hkv, int R, int d);
+cudaError_t launch_decode_paged(const PagedKV& c, const void* Q, void* O, int Hq, int Tq,
+                                float scale, void* workspace, unsigned* err, cudaStream_t s);
+
 cudaError_t launch_selftest_wait_timeout(int timeout_us, unsigned* err, cudaStream_t s);
 
 }  // namespace rf

@@ -56,7 +56,8 @@ typedef enum {
   RF_ERR_DEVICE_BOUNDS = 8    /* debug build: an access outside its tensor  */
 } rf_status;
 
-typedef enum { RF_F32 = 0, RF_BF16 = 1 } rf_dtype;
+/* RF_E4M3 (OCP 8-bit float, held as uint8 codes) is a cache's type only. */
+typedef enum { RF_F32 = 0, RF_BF16 = 1, RF_E4M3 = 2 } rf_dtype;
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* rf_status_string(int status);
@@ -385,6 +386,161 @@ rf_status rf_absmax_quant_fp8(const void* X, int M, int K, float* sx_out, uint8_
                               rf_stream_t stream);
 
 /*
+ * A paged key/value cache and the batch that uses it (all pointers are device
+ * pointers; the struct itself is read on the host during the call).  The token
+ * at position p of sequence b lives in page block_table[b][p / page_size],
+ * slot p % page_size.
+ *   k, v         pages [num_pages][Hkv][page_size][d], RF_BF16 or RF_E4M3.
+ *   k_scale, v_scale   RF_E4M3: fp32 [num_pages][Hkv]; the value that a code
+ *                stands for is code * scale of its page and head (positive,
+ *                finite, normal).  RF_BF16: ignored.
+ *   block_table  int32 [B][max_pages].  Only the entries of pages that hold
+ *                tokens are used; the others may be anything.  A page may be in
+ *                several rows (a shared prefix), but a page that an append
+ *                writes belongs to one sequence.
+ *   seq_lens     int32 [B]: tokens of each sequence, the call's own new tokens
+ *                included.  0: a padded row of the batch.
+ *   Sizes   B, num_pages, max_pages, Hkv >= 1; page_size 16, 32, 64 or 128;
+ *           d 64 or 128; num_pages * Hkv * page_size < 2^31;
+ *           max_pages * page_size <= 2^30.
+ * block_table and seq_lens need 4-byte alignment.  They are read by the
+ * kernels, so a captured graph follows what a later step writes there (they
+ * must not change while a call runs).  A length outside 0 .. max_pages *
+ * page_size, or a page outside the cache, makes rf_get_device_status report
+ * RF_ERR_DEVICE_INPUT; that sequence (or page) counts as empty, and nothing is
+ * read or written out of bounds.  (The paper has no counterpart.)
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int dtype, B, num_pages, page_size, max_pages, Hkv, d;
+} rf_paged_kv;
+
+/*
+ * Norm of every head and position rotation, as rf_qk_norm_rope and
+ * rf_kv_append_paged apply them to a row x of d elements (fp32 arithmetic):
+ *     y = x * rsqrt(mean(x^2) + eps) * weight         (where weight is given)
+ *     (a, b) <- (a cos - b sin, b cos + a sin)        (where cos, sin are)
+ * for the pairs of y's first rot_dim elements: (j, j + rot_dim / 2), or, with
+ * interleaved = 1, (2j, 2j + 1); j = 0 .. rot_dim / 2 - 1.
+ *   cos, sin   device fp32 [max_pos][rot_dim / 2], or both NULL: no rotation.
+ *   rot_dim    a multiple of 16, 16 .. d.
+ *   q_weight, k_weight   device [d], of the rows' type; NULL: no norm.
+ *   eps        finite, > 0 (looked at where a weight is given).
+ */
+typedef struct {
+  const float* cos;
+  const float* sin;
+  int max_pos, rot_dim, interleaved;
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+} rf_norm_rope;
+
+/*
+ * Norm of every query and key head and position rotation in one pass (what
+ * rf_attn_fwd's inputs need before it; the mean of squares and the scaling
+ * that needs it are a cascade of [E] §2.1's kind).
+ *   dtype   RF_F32 or RF_BF16: type of Q, K, Qo, Ko and the weights; fp32
+ *           arithmetic, rounded once.
+ *   Q, Qo   [T][Hq][d], tokens ldq (ldqo) elements apart; K, Ko [T][Hkv][d],
+ *           ldk (ldko).  Rows of a fused projection's output can be given as
+ *           they are.  Hq or Hkv may be 0 (its pointers are then ignored).
+ *           Qo may be Q and Ko may be K (with equal strides: in place); other
+ *           overlaps are not allowed.
+ *   positions   device int32 [T] (4-byte aligned); not read without rotation.
+ *           A token whose position lies outside 0 .. max_pos - 1 is left
+ *           unwritten and reported as RF_ERR_DEVICE_INPUT.
+ *   nr      norm and rotation (NULL: a copy).
+ *   Sizes   T >= 1; Hq, Hkv <= 2^20, T * (Hq + Hkv) < 2^31; d = 64 or 128;
+ *           strides >= heads * d, a multiple of 16 bytes, and below 2^40 / T.
+ * Errors: RF_ERR_INVALID_ARG, RF_ERR_UNSUPPORTED (d not covered), RF_ERR_CUDA.
+ */
+rf_status rf_qk_norm_rope(int dtype, const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                          void* Qo, int64_t ldqo, void* Ko, int64_t ldko,
+                          const int32_t* positions, const rf_norm_rope* nr, int T, int Hq, int Hkv,
+                          int d, rf_stream_t stream);
+
+/*
+ * Appends new keys and values to a paged cache, with the keys' norm and
+ * rotation on the way and, if Q is given, those of the same tokens' queries
+ * in the same launch.
+ *   K, V    [total][Hkv][d] bf16, tokens ldk (ldv) elements apart.
+ *   cu_seqlens   device int32 [B + 1] of cumulative new tokens, as in
+ *           rf_attn_fwd_varlen (entry 0 is 0, the last is `total`; sequences
+ *           may have none), or NULL: total / B tokens for each sequence.
+ *           The n new tokens of sequence b are its last: positions
+ *           seq_lens[b] - n .. seq_lens[b] - 1.
+ *   nr      norm and rotation (NULL: neither).
+ *   Q, Qo   [total][Hq][d] bf16 (ldq, ldqo), with Hq = 0: no queries.  Qo may
+ *           be Q (with equal strides); other overlaps are not allowed.
+ * RF_BF16 cache: K (after norm and rotation) and V are stored rounded to bf16.
+ * RF_E4M3 cache: per (page, kv head), for keys and values apart, with a the
+ * largest finite magnitude of the page's new values,
+ *     s' = smallest power of two >= 2^-126 with a <= 448 s',
+ *     s  = max(s', the page's scale if it holds earlier tokens of the
+ *              sequence, i.e. if the new tokens do not begin at slot 0),
+ * earlier codes c become E4M3(c * old scale / s) where s grew, new values x
+ * are stored as E4M3(x / s) (round to nearest even, saturating; an infinity
+ * saturates, NaN is stored as NaN), and s as the page's scale.  This is the
+ * running-maximum form of [E] §4.3's row absmax and quantisation: a power of
+ * two makes the rescaling of earlier codes exact but for E4M3's subnormals.
+ * A sequence with seq_lens 0 is a padded row: nothing of it is written, nor
+ * are its rows of Qo.  A sequence whose length is below its new tokens, above
+ * max_pages * page_size, or (with rotation) above max_pos, or whose entries of
+ * cu_seqlens are out of order, is skipped the same way and reported as
+ * RF_ERR_DEVICE_INPUT; so are the new keys and values of a page outside the
+ * cache.  Slots that get no new token keep their contents (but for the
+ * rescaling).
+ * Errors: RF_ERR_INVALID_ARG (null or misaligned pointer or stride, sizes of
+ * rf_paged_kv, total < 1 or not a multiple of B without cu_seqlens, a grid of
+ * 2^31 CTAs or more), RF_ERR_UNSUPPORTED (d or page_size not covered),
+ * RF_ERR_CUDA.
+ */
+rf_status rf_kv_append_paged(const rf_paged_kv* cache, const void* K, int64_t ldk, const void* V,
+                             int64_t ldv, const int32_t* cu_seqlens, int total,
+                             const rf_norm_rope* nr, const void* Q, int64_t ldq, void* Qo,
+                             int64_t ldqo, int Hq, rf_stream_t stream);
+
+/* Workspace bytes rf_attn_decode_paged needs (0 for an invalid shape, or when
+ * no device can be queried: it depends on the current device's SM count, not
+ * on the lengths). */
+size_t rf_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Tq, int d);
+
+/*
+ * Decode attention over a paged cache ([S] Methodologie 3, multi-segment
+ * strategy; the cascade of rf_attn_decode_splitkv with the keys' and values'
+ * scales in it).  Tq query tokens a sequence, its last Tq tokens:
+ *   Q, O    [B][Tq][Hq][d] bf16.  Query head hq reads kv head hq / (Hq / Hkv).
+ *     s_j = scale * q . k_j   for keys j <= seq_lens[b] - Tq + t,
+ *     o   = sum_j softmax(s)_j v_j
+ * (fp32 accumulation and softmax state).  A row that reads no key (a padded
+ * sequence, or one of fewer than Tq tokens) is written as zeros.  What lies
+ * in a page behind the sequence's last token, or behind the last key that a
+ * row reads, has no effect on it, whatever its value.
+ * The lengths are read on the device; the keys of all sequences are shared
+ * out evenly over the SMs, and the partial states of a sequence are merged in
+ * key order, so the bits do not depend on timing.
+ *   Sizes   those of rf_paged_kv; Tq >= 1; Hq a multiple of Hkv, any group
+ *           size (16 query rows Tq * Hq / Hkv of a kv head share one pass over
+ *           its keys); B * Tq * Hq < 2^31 and B * Hkv * ceil(Tq * Hq / Hkv /
+ *           16) * ceil(max_pages * page_size / 32) < 2^31; scale finite, > 0.
+ *   workspace   device buffer of at least rf_attn_decode_paged_workspace_size
+ *           bytes, 16-byte aligned, owned by the caller.  Its contents need
+ *           not be initialised and are unspecified on return.  Calls that may
+ *           overlap on the GPU must not share one.
+ * Errors: RF_ERR_INVALID_ARG, RF_ERR_UNSUPPORTED (d or page_size not covered),
+ * RF_ERR_WORKSPACE, RF_ERR_CUDA.
+ */
+rf_status rf_attn_decode_paged(const rf_paged_kv* cache, const void* Q, void* O, int Hq, int Tq,
+                               float scale, void* workspace, size_t workspace_bytes,
+                               rf_stream_t stream);
+
+/*
  * Failure-detection self-test (no counterpart in the paper).  Launches one
  * CTA that waits on an mbarrier nothing ever completes, with a wait limit of
  * `timeout_us` microseconds (1..1000000).  The kernel gives up, records
@@ -443,6 +599,35 @@ int rf_selftest_fp8_schedule(int M, int N, int clusters);
  * that fails.
  */
 int rf_selftest_moe_plan(int T, int D, int E, int sms);
+
+/*
+ * Host-side check of rf_kv_append_paged's work items (no counterpart in the
+ * paper; no GPU needed, no CUDA call made).  block_table, seq_lens and
+ * cu_seqlens (or NULL) are HOST arrays, otherwise as in that call; max_pos 0
+ * means no rotation.  It walks every item and every query row's lookup and
+ * checks that no index leaves its array, that items lie in one page of the
+ * cache, that every token that is not skipped is written once, to the slot of
+ * its position, that queries get the same positions, and that inconsistent
+ * sizes are noticed.  Returns 0 when all of that holds, -1 for refused sizes,
+ * else the number (1..5) of the first check that fails.
+ */
+int rf_selftest_append_plan(const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* cu_seqlens, int B, int total, int num_pages,
+                            int page_size, int max_pages, int max_pos);
+
+/*
+ * Host-side check of rf_attn_decode_paged's partition (no counterpart in the
+ * paper; no GPU needed, no CUDA call made).  For sequences of the lengths in
+ * the HOST array seq_lens, `tiles` tiles of query rows for each, and a device
+ * of `sms` CTAs of `warps` (4 or 8) warps, it checks that the warps' ranges
+ * are all 32-key chunks of all tiles once, in order, that a warp leaves at most
+ * two unfinished tiles and a CTA at most two cut ones, in workspace slots of
+ * their own, and that the merge reads a tile's parts in key order.  Returns 0
+ * when all of that holds, -1 for refused sizes, else the number (1..5) of the
+ * first check that fails.
+ */
+int rf_selftest_decode_paged_plan(const int32_t* seq_lens, int B, int tiles, int max_len,
+                                  int warps, int sms);
 
 #ifdef __cplusplus
 }

@@ -26,7 +26,8 @@ method's sources define the cascade.  Sources cited in this package:
 Modules: ``attention`` (safe-softmax cascade, its incremental and
 multi-segment forms, the latent-KV decode), ``moe_gate`` (gate scores, top-k, softmax of the
 selected scores), ``fp8_quant_gemm`` (row absmax, E4M3 quantisation, GEMM,
-dequantisation).  Every function is pinned by tests under ``tests/`` against
+dequantisation), ``paged`` (norm and rotation, the paged cache's append and the
+decode attention over it).  Every function is pinned by tests under ``tests/`` against
 closed forms, library routines, brute force or worked examples; none is
 "parity unpinned".
 """
