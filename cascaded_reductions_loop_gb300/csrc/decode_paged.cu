@@ -45,7 +45,8 @@
 // Masked places.  Keys behind a sequence's last may hold anything: scores are
 // selected, not added to, and values are replaced by zero.  Where the last Tq
 // keys hold an infinity or NaN, which rows that may not read them would meet
-// as 0 * inf, the chunk's product is taken token by token.
+// as 0 * inf, the chunk's product is taken token by token, and each row takes
+// the one of its own token.
 #include <math.h>
 
 #include <algorithm>
@@ -318,11 +319,24 @@ struct KFrag {
 // O += V^T P^T for the 16 keys of half mt.  Which dims an m-tile holds is
 // free too.  E4M3: lane (g, c) reads dims [g D/8, (g+1) D/8) of keys 2c, 2c+1,
 // 2c+8, 2c+9; m-tile i's rows g and g + 8 are dims g D/8 + 2i and + 1.
-// bf16: natural order.  lim: keys at or beyond it (counted within the chunk)
-// are replaced by zero (kMask).
-template <bool kF8, int D, int NT, bool kMask>
+// bf16: natural order.  Modes: kAll; kMask, keys at or beyond lim (counted
+// within the chunk) are replaced by zero; kSome, the same, and only the rows
+// whose bit is set in `rows` (bit 2 nt + e for this lane's row 2c + e) take
+// the result.
+enum { kAll, kMasked, kSome };
+template <bool kF8, int D, int NT, int kMode>
 __device__ __forceinline__ void pv16(float (&o)[D / 16][NT][4], uint32_t base, int mt, int lane,
-                                     int lim, const uint32_t (&p)[NT][kF8 ? 1 : 2][2]) {
+                                     int lim, unsigned rows,
+                                     const uint32_t (&p)[NT][kF8 ? 1 : 2][2]) {
+  constexpr bool kMask = kMode != kAll;
+  auto accumulate = [&](float(&acc)[4], const uint32_t(&a)[4], int nt) {
+    float x[4] = {acc[0], acc[1], acc[2], acc[3]};
+    mma16816<kF8>(x, a, p[nt][0][0], p[nt][0][1]);
+    if (!kF8) mma16816<kF8>(x, a, p[nt][kF8 ? 0 : 1][0], p[nt][kF8 ? 0 : 1][1]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc[e] = kMode != kSome || ((rows >> (2 * nt + (e & 1))) & 1u) ? x[e] : acc[e];
+  };
   const int c = lane & 3;
   if (kF8) {
     constexpr int NW = D / 32;                   // words a key
@@ -348,8 +362,8 @@ __device__ __forceinline__ void pv16(float (&o)[D / 16][NT][4], uint32_t base, i
       const uint32_t a1[4] = {widen_lo(x1), widen_hi(x1), widen_lo(y1), widen_hi(y1)};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mma16816<true>(o[2 * j][nt], a0, p[nt][0][0], p[nt][0][1]);
-        mma16816<true>(o[2 * j + 1][nt], a1, p[nt][0][0], p[nt][0][1]);
+        accumulate(o[2 * j][nt], a0, nt);
+        accumulate(o[2 * j + 1][nt], a1, nt);
       }
     }
   } else {
@@ -372,10 +386,7 @@ __device__ __forceinline__ void pv16(float (&o)[D / 16][NT][4], uint32_t base, i
         a[3] &= keep1;
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        mma16816<false>(o[i][nt], a, p[nt][0][0], p[nt][0][1]);
-        mma16816<false>(o[i][nt], a, p[nt][kF8 ? 0 : 1][0], p[nt][kF8 ? 0 : 1][1]);
-      }
+      for (int nt = 0; nt < NT; ++nt) accumulate(o[i][nt], a, nt);
     }
   }
 }
@@ -842,8 +853,8 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
 
     // ---- O^T += V^T P^T
     if (!tail) {
-      pv16<kF8, D, NT, false>(o, vb, 0, lane, 0, pb[0]);
-      pv16<kF8, D, NT, false>(o, vb, 1, lane, 0, pb[1]);
+      pv16<kF8, D, NT, kAll>(o, vb, 0, lane, 0, 0u, pb[0]);
+      pv16<kF8, D, NT, kAll>(o, vb, 1, lane, 0, 0u, pb[1]);
     } else {
       int end[2];                              // keys of each half that exist
 #pragma unroll
@@ -852,24 +863,21 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
       if (p.Tq > 1 && any_nonfinite<kF8, D>(vb, lane, lo, hi)) {
 #pragma unroll 1
         for (int t = 0; t < p.Tq; ++t) {       // the rows of one query token at a time
-          uint32_t pt1[2][NT][kF8 ? 1 : 2][2];
-          const int r_t = (cur_hr % p.tiles) * kTileRows + g;
+          unsigned rows = 0;
 #pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int x = 0; x < (kF8 ? 1 : 2); ++x)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  pt1[h2][nt][x][k] = (r_t + nt * 8) / p.G == t ? pb[h2][nt][x][k] : 0u;
+            for (int e = 0; e < 2; ++e)
+              if (((cur_hr % p.tiles) * kTileRows + nt * 8 + 2 * c + e) / p.G == t)
+                rows |= 1u << (2 * nt + e);
+          if (!__any_sync(0xffffffffu, rows != 0)) continue;
           const int seen = cur_len - p.Tq + t + 1 - key0;
-          pv16<kF8, D, NT, true>(o, vb, 0, lane, min(end[0], seen), pt1[0]);
-          pv16<kF8, D, NT, true>(o, vb, 1, lane, min(end[1], seen), pt1[1]);
+          pv16<kF8, D, NT, kSome>(o, vb, 0, lane, min(end[0], seen), rows, pb[0]);
+          pv16<kF8, D, NT, kSome>(o, vb, 1, lane, min(end[1], seen), rows, pb[1]);
         }
       } else {
-        pv16<kF8, D, NT, true>(o, vb, 0, lane, end[0], pb[0]);
-        pv16<kF8, D, NT, true>(o, vb, 1, lane, end[1], pb[1]);
+        pv16<kF8, D, NT, kMasked>(o, vb, 0, lane, end[0], 0u, pb[0]);
+        pv16<kF8, D, NT, kMasked>(o, vb, 1, lane, end[1], 0u, pb[1]);
       }
     }
 
