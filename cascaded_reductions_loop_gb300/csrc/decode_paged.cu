@@ -69,7 +69,14 @@ struct Cfg {
   static constexpr int kStageBytes = 2 * kTensorBytes;
   static constexpr int kWarps = kStageBytes > 8192 ? 4 : 8;
   static constexpr int kStages = kF8 ? (D == 128 ? 2 : 4) : (D == 64 ? 2 : (NT == 1 ? 3 : 2));
-  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kRings = kWarps / 4;                     // of a producer warp
+  static constexpr int kConsumers = kWarps * 32;
+  static constexpr int kThreads = kConsumers + 128;             // + four producer warps
+  // Registers: 384 threads start with 168 each (64512); the two consumer
+  // warpgroups take 208 (53248) of them and the producers keep 88 (11264).
+  // With four consumer warps everyone has the compiler's 255 at most.
+  static constexpr int kConsumerRegs = kWarps == 8 ? 208 : 0;
+  static constexpr int kProducerRegs = kWarps == 8 ? 88 : 0;
   static constexpr int kRows = 8 * NT;
   static constexpr int kPitch = D + 4;                          // floats of a state's row
   static constexpr int kStateBytes = kRows * kPitch * 4 + kRows * 16;
@@ -123,12 +130,10 @@ __host__ __device__ __forceinline__ unsigned ctas_for(unsigned total, unsigned s
 struct Cursor {
   int b, hr, len;
   unsigned ck, nck;
-  // Chunk `off` of sequence b0's tiles; false if there is none (the lengths
-  // changed under the kernel).
-  __host__ __device__ __forceinline__ bool init(const Lens& p, int b0, unsigned off,
-                                                unsigned* err) {
+  // Chunk `off` of the tiles of sequence b0, of len0 keys; false if there is none.
+  __host__ __device__ __forceinline__ bool init(const Lens& p, int b0, int len0, unsigned off) {
     b = b0;
-    len = seq_len(p, b0, false, err);
+    len = len0;
     nck = num_chunks(len);
     hr = 0;
     ck = 0;
@@ -137,7 +142,8 @@ struct Cursor {
     ck = off % nck;
     return true;
   }
-  // On to the next chunk; false if there is none.
+  // On to the next chunk; false if there is none (on the device: the lengths
+  // changed under the kernel).
   __host__ __device__ __forceinline__ bool next(const Lens& p, unsigned* err) {
     if (++ck < nck) return true;
     ck = 0;
@@ -173,7 +179,7 @@ struct Params {
   unsigned* err;
   Lens lens;
   int Hq, Hkv, G, Tq, R, tiles;            // HR = Hkv * tiles
-  int num_pages, page_size, max_pages;
+  int num_pages, page_size, page_shift, max_pages;      // page_size = 1 << page_shift
   float scale_log2;
 };
 
@@ -191,12 +197,12 @@ struct Seg {              // a state left at the barrier
 
 template <int W, int S>
 struct Shared {
-  uint64_t full[W][S];
+  uint64_t full[W][S], empty[W][S];
   Meta meta[W][S];
   Seg seg[W][2];          // [0] the warp's first state, [1] its last
   int has[W][2];
-  unsigned warp_sum[W];
-  int start_b[W];
+  unsigned warp_sum[W + 4];
+  int start_b[W], start_len[W];
   unsigned start_off[W];
   int fail;
   int last[2];
@@ -212,14 +218,12 @@ template <bool kF8>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
   if (kF8)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -231,26 +235,25 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   return r;
 }
 
+// Volatile, so that they stay between the wait for a stage and its refill, but
+// without a memory clobber: the arithmetic between them may move.
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t* w) {
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 __device__ __forceinline__ void lds64(uint32_t addr, uint32_t* w) {
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
 }
 
 // Two E4M3 codes (the low or high half of a word) -> two f16, exact.
@@ -267,6 +270,28 @@ __device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  if (N > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N > 0 ? N : 24));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  if (N > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N > 0 ? N : 24));
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives on `bar` when this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ unsigned atom_acq_rel_add(unsigned* p, unsigned v) {
+  unsigned r;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(r) : "l"(p), "r"(v) : "memory");
   return r;
 }
 
@@ -433,28 +458,36 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
   const int g = lane >> 2, c = lane & 3;
   const int cta = (int)blockIdx.x;
   const Lens& lens = p.lens;
-  uint8_t* ring = smem + warp * (S * C::kStageBytes);
+  uint8_t* ring = smem + (warp < W ? warp : 0) * (S * C::kStageBytes);     // a consumer's
   const int64_t n_qo = (int64_t)lens.B * p.Tq * p.Hq * D;     // elements of Q and O
 
   // ---- plan: add up all lengths; find where each warp's range begins
   if (threadIdx.x == 0) {
     for (int w = 0; w < W; ++w)
-      for (int i = 0; i < S; ++i) mbar_init(smem_u32(&sh.full[w][i]), 1);
+      for (int i = 0; i < S; ++i) {
+        // the copies' bytes and, for E4M3, the two lanes that fetch scales
+        mbar_init(smem_u32(&sh.full[w][i]), kF8 ? 3 : 1);
+        mbar_init(smem_u32(&sh.empty[w][i]), 1);
+      }
     fence_mbar_init();
     sh.fail = 0;
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  if (lane < 2) sh.has[warp][lane] = 0;
-  if (lane == 0) {
-    sh.start_b[warp] = 0;
-    sh.start_off[warp] = 0;
-  }
+  const bool consumer = warp < W;
+  if (consumer && lane < 2) sh.has[warp][lane] = 0;
+  if (consumer && lane == 0) sh.start_b[warp] = sh.start_len[warp] = 0;
   const int per = (lens.B + C::kThreads - 1) / C::kThreads;
   const int b_lo = min((int)threadIdx.x * per, lens.B), b_hi = min(b_lo + per, lens.B);
   unsigned mine = 0;
-  for (int b = b_lo; b < b_hi; ++b)
-    mine += num_chunks(seq_len(lens, b, cta == 0, p.err)) * (unsigned)lens.HR;
+  int first_len = 0;
+  bool empty = false;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int len = seq_len(lens, b, cta == 0, p.err);
+    if (b == b_lo) first_len = len;
+    empty |= len == 0;
+    mine += num_chunks(len) * (unsigned)lens.HR;
+  }
   unsigned incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -462,99 +495,105 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     if (lane >= o) incl += v;
   }
   if (lane == 31) sh.warp_sum[warp] = incl;
-  __syncthreads();
+  const bool empties = __syncthreads_or(empty);
   unsigned pre = incl - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
+  for (int w = 0; w < W + 4; ++w) {
     if (w < warp) pre += sh.warp_sum[w];
     total += sh.warp_sum[w];
   }
-  // sequences without keys: their rows are zeros
-  for (int b = cta; b < lens.B; b += (int)gridDim.x) {
-    if (seq_len(lens, b, false, p.err) > 0) continue;
-    const int64_t n = (int64_t)p.Tq * p.Hq * D / 8;
-    for (int64_t i = threadIdx.x; i < n; i += C::kThreads)
-      if (RF_IN(p.err, (b * n + i) * 8 + 7, n_qo))
-        reinterpret_cast<uint4*>(p.O)[b * n + i] = make_uint4(0u, 0u, 0u, 0u);
-  }
   const unsigned grid = ctas_for(total, gridDim.x, W);
-  if (total == 0 || (unsigned)cta >= grid) return;
   const Split ctas(total, grid);
-  const unsigned r0 = ctas.start(cta), r1 = ctas.start(cta + 1);
+  const unsigned r0 = ctas.start(cta), r1 = (unsigned)cta < grid ? ctas.start(cta + 1) : r0;
   const Split warps(r1 - r0, W);
   for (int w = 0; w < W; ++w) {
     const unsigned x = r0 + warps.start(w);
     if (x >= pre && x - pre < mine) {            // in this thread's sequences: walk to it
       unsigned at = pre;
-      for (int b = b_lo; b < b_hi; ++b) {
-        const unsigned n = num_chunks(seq_len(lens, b, false, p.err)) * (unsigned)lens.HR;
+      for (int b = b_lo, len = first_len; b < b_hi;) {
+        const unsigned n = num_chunks(len) * (unsigned)lens.HR;
         if (x - at < n) {
           sh.start_b[w] = b;
+          sh.start_len[w] = len;
           sh.start_off[w] = x - at;
           break;
         }
         at += n;
+        if (++b < b_hi) len = seq_len(lens, b, false, p.err);
       }
     }
   }
   __syncthreads();
-  const unsigned x0 = r0 + warps.start(warp);
-  unsigned count = warps.start(warp + 1) - warps.start(warp);         // chunks of this warp
+  // element of Q and O at which row r of kv head h of sequence b begins
+  auto row_at = [&](int b, int h, int r) {
+    const int t = p.Tq == 1 ? 0 : r / p.G;
+    return (((int64_t)b * p.Tq + t) * p.Hq + (int64_t)h * p.G + (r - t * p.G)) * D;
+  };
 
-  // ---- producer (the same in all lanes)
-  Cursor cur = {0, 0, 0, 0, 0};
-  unsigned issued = 0;
-  int pt = -1, pt_b = -1, pt_base = 0;  // 32 entries of a block table row, one a lane
-  if (count > 0 && !cur.init(lens, sh.start_b[warp], sh.start_off[warp], p.err)) count = 0;
-  auto issue = [&]() {
-    if (issued < count) {
+  if (!consumer) {
+    setmaxnreg_dec<C::kProducerRegs>();
+    // ---- producers: half a warp (or a whole one) keeps a consumer's ring full
+    constexpr int kLanes = 32 / C::kRings;
+    const int hl = lane % kLanes;
+    const int w = (warp - W) * C::kRings + lane / kLanes;
+    const unsigned half = C::kRings == 1 ? 0xFFFFFFFFu : (lane < 16 ? 0xFFFFu : 0xFFFF0000u);
+    unsigned count = (unsigned)cta < grid ? warps.start(w + 1) - warps.start(w) : 0u;
+    Cursor cur = {0, 0, 0, 0, 0};
+    if (count > 0 && !cur.init(lens, sh.start_b[w], sh.start_len[w], sh.start_off[w])) count = 0;
+    unsigned issued = 0;
+    int pt = -1, pt_b = -1, pt_base = 0;  // kLanes entries of a block table row, one a lane
+    bool failed = false;
+    uint64_t t0 = 0;                      // since when nothing could be issued
+    while (__any_sync(0xffffffffu, issued < count)) {
       const int slot = (int)(issued % S);
-      Meta& mt = sh.meta[warp][slot];
+      bool go = issued < count &&
+                (issued < S || mbar_test_wait(smem_u32(&sh.empty[w][slot]), (issued / S - 1) & 1));
+      go = __shfl_sync(0xffffffffu, go, 0, kLanes);          // as the ring's first lane saw it
+      if (!__any_sync(0xffffffffu, go)) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        failed = now - t0 > kDefaultWaitNs || *(volatile int*)&sh.fail;
+        failed = __any_sync(0xffffffffu, failed);
+        if (failed) break;
+        __nanosleep(20);
+        continue;
+      }
+      t0 = 0;
+      if (!go) continue;
+      Meta& mt = sh.meta[w][slot];
       const int first = (int)(cur.ck * kChunk);
-      const int pg = first / p.page_size, in_page = first - pg * p.page_size;
+      const int pg = first >> p.page_shift, in_page = first & (p.page_size - 1);
       const int halves = p.page_size < kChunk ? 2 : 1;
-      if (cur.b != pt_b || pg < pt_base || pg + halves > pt_base + 32) {
+      if (cur.b != pt_b || pg < pt_base || pg + halves > pt_base + kLanes) {
         pt_b = cur.b;
         pt_base = pg;
-        const int e = pg + lane;
-        pt = e < (cur.len + p.page_size - 1) / p.page_size
+        const int e = pg + hl;
+        pt = e < (cur.len + p.page_size - 1) >> p.page_shift
                  ? ld_int(p.block_table, (int64_t)cur.b * p.max_pages + e,
                           (int64_t)lens.B * p.max_pages, p.err)
                  : -1;
       }
-      const int h = cur.hr / p.tiles;
-      int valid = 0;
-      int page[2];
+      const int h = p.tiles == 1 ? cur.hr : cur.hr / p.tiles;
+      int page[2], valid = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int e = i < halves ? pg + i : pg;
-        page[i] = __shfl_sync(0xffffffffu, pt, e - pt_base);
+        page[i] = __shfl_sync(half, pt, e - pt_base, kLanes);
         const bool ok = (unsigned)page[i] < (unsigned)p.num_pages;
         if (!ok) {
-          if (lane == 0 && e * p.page_size < cur.len) raise_error(p.err, kDevErrInput);
+          if (hl == 0 && e * p.page_size < cur.len) raise_error(p.err, kDevErrInput);
           page[i] = 0;                             // read something of the cache; masked
         }
         valid |= ok ? 1 << i : 0;
       }
-      if (kF8 && lane < 2) {
-        const int64_t at = (int64_t)(lane ? page[1] : page[0]) * p.Hkv + h;
-        if (RF_IN(p.err, at, (int64_t)p.num_pages * p.Hkv)) {
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&mt.ks[lane])),
-                       "l"(p.k_scale + at)
-                       : "memory");
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&mt.vs[lane])),
-                       "l"(p.v_scale + at)
-                       : "memory");
-        }
-      }
-      if (lane == 0) {
+      const uint32_t bar = smem_u32(&sh.full[w][slot]);
+      if (hl == 0) {
         mt.b = cur.b;
         mt.hr = cur.hr;
         mt.ck = (int)cur.ck;
         mt.len = cur.len;
         mt.valid = valid;
-        const uint32_t bar = smem_u32(&sh.full[warp][slot]);
-        const uint32_t dst = smem_u32(ring + slot * C::kStageBytes);
+        const uint32_t dst = smem_u32(smem + (w * S + slot) * C::kStageBytes);
         mbar_arrive_expect_tx(bar, C::kStageBytes);
         constexpr int kKeysPerRow = kF8 && D == 64 ? 2 : 1;       // of the tensor map
         constexpr int kBoxes = !kF8 && D == 128 ? 2 : 1;
@@ -571,12 +610,47 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
           }
         }
       }
+      if (kF8 && hl < 2) {
+        const int64_t at = (int64_t)(hl ? page[1] : page[0]) * p.Hkv + h;
+        if (RF_IN(p.err, at, (int64_t)p.num_pages * p.Hkv)) {
+          cp_async4(smem_u32(&mt.ks[hl]), p.k_scale + at);
+          cp_async4(smem_u32(&mt.vs[hl]), p.v_scale + at);
+        }
+        cp_async_arrive(bar);
+      }
+      if (issued > 0 && cur.ck == 0) {             // the tile's queries: into L1 meanwhile
+        for (int i = hl; i < C::kRows * (D / 64); i += kLanes) {       // pieces of 128 bytes
+          const int r = (cur.hr - h * p.tiles) * kTileRows + i % C::kRows;
+          if (r < p.R)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(p.Q + row_at(cur.b, h, r) +
+                                                          64 * (i / C::kRows)));
+        }
+      }
       ++issued;
       if (issued < count && !cur.next(lens, p.err)) count = issued;
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");     // empty at the end of the range
-  };
-  for (int i = 0; i < S; ++i) issue();
+    if (failed && hl == 0) {
+      raise_error(p.err, kDevErrTimeout);
+      // copies in flight land before shared memory is released
+      for (unsigned x = issued > S ? issued - S : 0; x < issued; ++x)
+        (void)mbar_wait(smem_u32(&sh.full[w][x % S]), (x / S) & 1, 1000000ull);
+    }
+    return;
+  }
+  setmaxnreg_inc<C::kConsumerRegs>();
+
+  // sequences without keys: their rows are zeros
+  if (empties)
+    for (int b = cta; b < lens.B; b += (int)gridDim.x) {
+      if (seq_len(lens, b, false, p.err) > 0) continue;
+      const int64_t n = (int64_t)p.Tq * p.Hq * D / 8;
+      for (int64_t i = threadIdx.x; i < n; i += C::kConsumers)
+        if (RF_IN(p.err, (b * n + i) * 8 + 7, n_qo))
+          reinterpret_cast<uint4*>(p.O)[b * n + i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  if ((unsigned)cta >= grid || total == 0) return;
+  const unsigned x0 = r0 + warps.start(warp);
+  const unsigned count = warps.start(warp + 1) - warps.start(warp);   // chunks of this warp
 
   // ---- the warp's range
   float o[D / 16][NT][4];
@@ -588,12 +662,12 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
   int cur_b = 0, cur_hr = 0, cur_len = 0;
 
   auto load_q = [&]() {
-    const int h = cur_hr / p.tiles, r0_ = (cur_hr % p.tiles) * kTileRows;
+    const int h = p.tiles == 1 ? cur_hr : cur_hr / p.tiles;
+    const int r0_ = (cur_hr - h * p.tiles) * kTileRows;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = r0_ + nt * 8 + g;
-      const int64_t at =
-          (((int64_t)cur_b * p.Tq + r / p.G) * p.Hq + (int64_t)h * p.G + r % p.G) * D;
+      const int64_t at = row_at(cur_b, h, r);
       const bool ok = r < p.R && RF_IN(p.err, at + D - 1, n_qo);
       if (kF8) {
         uint32_t w[D / 8];                    // bf16 pairs: dims [c D/4, (c+1) D/4)
@@ -634,7 +708,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int t = min((r0_ + nt * 8 + 2 * c + e) / p.G, p.Tq - 1);
+        const int t = p.Tq == 1 ? 0 : min((r0_ + nt * 8 + 2 * c + e) / p.G, p.Tq - 1);
         lim[nt][e] = cur_len - p.Tq + t + 1;             // keys this row reads
       }
     }
@@ -666,10 +740,8 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
 
   // A whole tile's rows, from the registers.
   auto put_rows = [&]() {
-    const int h = cur_hr / p.tiles, r0_ = (cur_hr % p.tiles) * kTileRows;
-    auto row_at = [&](int r) {
-      return (((int64_t)cur_b * p.Tq + r / p.G) * p.Hq + (int64_t)h * p.G + r % p.G) * D;
-    };
+    const int h = p.tiles == 1 ? cur_hr : cur_hr / p.tiles;
+    const int r0_ = (cur_hr - h * p.tiles) * kTileRows;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float w[2];
@@ -680,7 +752,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = r0_ + nt * 8 + 2 * c + e;
-          const int64_t at = row_at(r) + g * (D / 8);
+          const int64_t at = row_at(cur_b, h, r) + g * (D / 8);
           if (r < p.R && RF_IN(p.err, at + D / 8 - 1, n_qo)) {
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
@@ -694,7 +766,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
         }
       } else {
         const int r = r0_ + nt * 8 + g;
-        const int64_t at = row_at(r);
+        const int64_t at = row_at(cur_b, h, r);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -710,22 +782,17 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
 
   for (unsigned it = 0; it < count; ++it) {
     const int slot = (int)(it % S);
-    asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-    bool ok = mbar_wait(smem_u32(&sh.full[warp][slot]), (it / S) & 1);
-    ok = __all_sync(0xffffffffu, ok);
-    __syncwarp();                                // the scales that other lanes fetched
-    if (!ok) {
-      failed = true;
-      break;
-    }
     const Meta& mt = sh.meta[warp][slot];
-    const int ck = mt.ck;
     if (fresh) {
-      fresh = false;
-      cur_b = mt.b;
-      cur_hr = mt.hr;
-      cur_len = mt.len;
-      load_q();
+      // the first tile's queries are fetched while its first chunk is on its way
+      if (it == 0) {
+        Cursor cur;
+        (void)cur.init(lens, sh.start_b[warp], sh.start_len[warp], sh.start_off[warp]);
+        cur_b = cur.b;
+        cur_hr = cur.hr;
+        cur_len = cur.len;
+        load_q();
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -740,6 +807,20 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
     }
+    const bool ok = mbar_wait(smem_u32(&sh.full[warp][slot]), (it / S) & 1);
+    if (!__all_sync(0xffffffffu, ok)) {
+      failed = true;
+      done = it;
+      break;
+    }
+    const int ck = mt.ck;
+    if (fresh && it > 0) {
+      cur_b = mt.b;
+      cur_hr = mt.hr;
+      cur_len = mt.len;
+      load_q();
+    }
+    fresh = false;
     const uint32_t kb = smem_u32(ring + slot * C::kStageBytes), vb = kb + C::kTensorBytes;
     const int key0 = ck * kChunk;
     const int valid = mt.valid;
@@ -752,22 +833,41 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
       lv[i] = kF8 ? (in ? __log2f(mt.vs[i]) : 0.f) : 0.f;
     }
 
-    // ---- S^T = K Q^T
+    // ---- S^T = K Q^T.  An accumulator's products follow one another, so the two
+    // halves (and at NT = 1 the even and odd k-steps) go in parallel chains.
     float s[2][NT][4];
+    {
+      constexpr int kChains = NT == 1 ? 2 : 1;
+      float s2[2][kChains][NT][4];
 #pragma unroll
-    for (int h2 = 0; h2 < 2; ++h2) {
+      for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        s[h2][nt][0] = s[h2][nt][1] = s[h2][nt][2] = s[h2][nt][3] = 0.f;
-      KFrag<kF8, D> kf;
-      kf.load(kb, h2, lane);
+        for (int x = 0; x < kChains; ++x)
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t a[4];
-        kf.get(kb, h2, lane, ks, a);
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816<kF8>(s[h2][nt], a, q[ks][nt][0], q[ks][nt][1]);
-      }
+            for (int e = 0; e < 4; ++e) s2[h2][x][nt][e] = 0.f;
+      KFrag<kF8, D> kf[2];
+      kf[0].load(kb, 0, lane);
+      kf[1].load(kb, 1, lane);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) {
+          uint32_t a[4];
+          kf[h2].get(kb, h2, lane, ks, a);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816<kF8>(s2[h2][ks % kChains][nt], a, q[ks][nt][0], q[ks][nt][1]);
+        }
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[h2][nt][e] = kChains == 2 ? s2[h2][0][nt][e] + s2[h2][kChains - 1][nt][e]
+                                        : s2[h2][0][nt][e];
     }
 
     // ---- running maxima and sums (log2 units); element (k, e): key g + 8 k, row 2c + e
@@ -881,10 +981,9 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
       }
     }
 
-    // ---- refill the stage; end of a tile or of the range
+    // ---- the stage is free; end of a tile or of the range
     __syncwarp();
-    issue();
-    ++done;
+    if (lane == 0) mbar_arrive(smem_u32(&sh.empty[warp][slot]));
     const bool tile_end = (unsigned)ck + 1 == num_chunks(cur_len);
     if (tile_end || it + 1 == count) {
 #pragma unroll
@@ -916,12 +1015,13 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
   }
   if (failed) {
     raise_error(p.err, kDevErrTimeout);
-    sh.fail = 1;
-    // copies in flight land before shared memory is released
-    for (unsigned x = done; x < issued; ++x)
+    sh.fail = 1;                               // ends the producers
+    // copies in flight land before shared memory is released (the producer may
+    // have ended already)
+    for (unsigned x = done; x < count && x < done + S; ++x)
       (void)mbar_wait(smem_u32(&sh.full[warp][x % S]), (x / S) & 1, 1000000ull);
   }
-  __syncthreads();
+  named_bar_sync(1, C::kConsumers);
   if (sh.fail) return;
 
   // ---- merge the states that warps left, in key order
@@ -939,117 +1039,105 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
                    : smem + C::kRingBytes + (e >> 1) * C::kStateBytes;
   };
   constexpr int NV = D / 32;                 // floats a lane holds of a row
-  auto put_row = [&](int b, int hr, int r, float w, const float (&v)[NV]) {
-    const int h = hr / p.tiles, rr = (hr % p.tiles) * kTileRows + r;
-    const int64_t at =
-        (((int64_t)b * p.Tq + rr / p.G) * p.Hq + (int64_t)h * p.G + rr % p.G) * D + NV * lane;
+  auto put_row = [&](const Seg& sg, int r, float w, const float (&v)[NV]) {
+    const int h = p.tiles == 1 ? sg.hr : sg.hr / p.tiles;
+    const int64_t at = row_at(sg.b, h, (sg.hr - h * p.tiles) * kTileRows + r) + NV * lane;
     if (!RF_IN(p.err, at + NV - 1, n_qo)) return;
 #pragma unroll
     for (int i = 0; i < NV; i += 2)
       *reinterpret_cast<uint32_t*>(p.O + at + i) = pack_bf16x2(v[i] * w, v[i + 1] * w);
   };
-  auto rows_of = [&](int hr) { return min(p.R - (hr % p.tiles) * kTileRows, C::kRows); };
+  const int rows = min(p.R, C::kRows);       // of a tile (its last one may have fewer)
+  auto has_row = [&](int hr, int r) { return p.tiles == 1 || hr % p.tiles * kTileRows + r < p.R; };
   const int64_t n_slots = 2 * (int64_t)gridDim.x * kTileRows;
-  bool any_cut = false;
-  for (unsigned left = starts; left; left &= left - 1) {
+  const int n_groups = __popc(starts);
+  // first entries of the (at most two) tiles that are cut between CTAs: the
+  // first and the last group
+  int cut[2] = {-1, -1};
+  {
+    const int ea = __ffs(starts) - 1, eb = 31 - __clz((int)starts);
+    const Seg &sa = sh.seg[ea >> 1][ea & 1], &sb = sh.seg[eb >> 1][eb & 1];
+    if (sa.s0 < r0 || sa.s0 + num_chunks(sa.len) > r1) cut[0] = ea;
+    if (eb != ea && sb.s0 + num_chunks(sb.len) > r1) cut[1] = eb;
+  }
+  for (int i = warp; i < n_groups * rows; i += W) {
+    const int gi = i / rows, r = i - gi * rows;
+    unsigned left = starts;
+    for (int k = 0; k < gi; ++k) left &= left - 1;
     const int e0 = __ffs(left) - 1;
     const unsigned rest = left & (left - 1);
-    const unsigned members =
-        mask & ~((1u << e0) - 1u) & (rest ? (1u << (__ffs(rest) - 1)) - 1u : 0xFFFFFFFFu);
+    const int e1 = rest ? __ffs(rest) - 1 : 2 * W;       // entries e0 .. e1 - 1
     const Seg sg = sh.seg[e0 >> 1][e0 & 1];
-    const bool cut = sg.s0 < r0 || sg.s0 + num_chunks(sg.len) > r1;
-    any_cut |= cut;
-    for (int r = warp; r < rows_of(sg.hr); r += W) {
-      float Mx = -INFINITY, mx = -INFINITY;
-      for (unsigned q2 = members; q2; q2 &= q2 - 1) {
-        const float4 st = reinterpret_cast<const float4*>(state_of(__ffs(q2) - 1) +
-                                                          C::kRows * C::kPitch * 4)[r];
-        Mx = fmaxf(Mx, st.x);
-        mx = fmaxf(mx, st.y);
+    if (!has_row(sg.hr, r)) continue;
+    const bool in = here && lane >= e0 && lane < e1;     // one entry a lane
+    float4 st = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+    if (in) st = reinterpret_cast<const float4*>(state_of(lane) + C::kRows * C::kPitch * 4)[r];
+    const float Mx = warp_max(st.x), mx = warp_max(st.y);
+    const float Mu = Mx == -INFINITY ? 0.f : Mx, mu = mx == -INFINITY ? 0.f : mx;
+    const float wo = ex2(st.x - Mu), L = warp_sum(st.z * ex2(st.y - mu));
+    float v[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) v[k] = 0.f;
+#pragma unroll 4
+    for (int e = e0; e < e1; ++e) {
+      const float we = __shfl_sync(0xffffffffu, wo, e);
+      if ((mask >> e) & 1u) {
+        const float* row = reinterpret_cast<const float*>(state_of(e)) + r * C::kPitch + NV * lane;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) v[k] = fmaf(row[k], we, v[k]);
       }
-      const float Mu = Mx == -INFINITY ? 0.f : Mx, mu = mx == -INFINITY ? 0.f : mx;
-      float L = 0.f, v[NV];
+    }
+    if (e0 != cut[0] && e0 != cut[1]) {
+      put_row(sg, r, L == 0.f ? 0.f : ex2(Mu - mu) / L, v);
+    } else {
+      const int64_t at = slot_of(ctas, sg.s0, cta) * kTileRows + r;
+      if (RF_IN(p.err, at, n_slots)) {
+        float* dst = p.ws_o + at * D + NV * lane;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = 0.f;
-      for (unsigned q2 = members; q2; q2 &= q2 - 1) {
-        const uint8_t* buf = state_of(__ffs(q2) - 1);
-        const float4 st = reinterpret_cast<const float4*>(buf + C::kRows * C::kPitch * 4)[r];
-        const float wo = ex2(st.x - Mu);
-        L = fmaf(st.z, ex2(st.y - mu), L);
-        const float* row = reinterpret_cast<const float*>(buf) + r * C::kPitch + NV * lane;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = fmaf(row[i], wo, v[i]);
-      }
-      if (!cut) {
-        put_row(sg.b, sg.hr, r, L == 0.f ? 0.f : ex2(Mu - mu) / L, v);
-      } else {
-        const int64_t at = slot_of(ctas, sg.s0, cta) * kTileRows + r;
-        if (RF_IN(p.err, at, n_slots)) {
-          float* dst = p.ws_o + at * D + NV * lane;
-#pragma unroll
-          for (int i = 0; i < NV; i += 2)
-            *reinterpret_cast<float2*>(dst + i) = make_float2(v[i], v[i + 1]);
-          if (lane == 0) p.ws_st[at] = make_float4(Mx, mx, L, 0.f);
-        }
+        for (int k = 0; k < NV; k += 2)
+          *reinterpret_cast<float2*>(dst + k) = make_float2(v[k], v[k + 1]);
+        if (lane == 0) p.ws_st[at] = make_float4(Mx, mx, L, 0.f);
       }
     }
   }
-  if (!any_cut) return;
-  // ---- tiles cut between CTAs: the last CTA to arrive merges
-  __threadfence();
-  __syncthreads();
-  int n_cut = 0;
-  for (unsigned left = starts; left; left &= left - 1) {
-    const int e0 = __ffs(left) - 1;
-    const Seg sg = sh.seg[e0 >> 1][e0 & 1];
-    const unsigned s1 = sg.s0 + num_chunks(sg.len);
-    if (sg.s0 >= r0 && s1 <= r1) continue;
-    if (threadIdx.x == 0) {
+  if (cut[0] < 0 && cut[1] < 0) return;
+  // ---- tiles cut between CTAs: the last CTA to arrive merges.  The barrier
+  // orders the CTA's stores before the ticket's release.
+  named_bar_sync(1, C::kConsumers);
+  if (threadIdx.x < 2) {
+    const int e0 = threadIdx.x ? cut[1] : cut[0];
+    unsigned last = 0;
+    if (e0 >= 0) {
+      const Seg& sg = sh.seg[e0 >> 1][e0 & 1];
+      const unsigned s1 = sg.s0 + num_chunks(sg.len);
       const unsigned pieces = ctas.owner(s1 - 1) - ctas.owner(sg.s0) + 1;
       const int64_t tile = (int64_t)sg.b * lens.HR + sg.hr;
-      unsigned t = 0;
-      if (RF_IN(p.err, tile, (int64_t)lens.B * lens.HR)) t = atomicAdd(&p.tickets[tile], 1u);
-      sh.last[n_cut] = t == pieces - 1;
+      if (RF_IN(p.err, tile, (int64_t)lens.B * lens.HR))
+        last = atom_acq_rel_add(&p.tickets[tile], 1u) == pieces - 1;
     }
-    ++n_cut;                                  // at most two: the range's first and last tile
+    sh.last[threadIdx.x] = (int)last;
   }
-  __threadfence();
-  __syncthreads();
-  n_cut = 0;
-  for (unsigned left = starts; left; left &= left - 1) {
-    const int e0 = __ffs(left) - 1;
-    const Seg sg = sh.seg[e0 >> 1][e0 & 1];
+  named_bar_sync(1, C::kConsumers);
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const int ek = k ? cut[1] : cut[0];
+    if (ek < 0 || !sh.last[k]) continue;
+    const Seg sg = sh.seg[ek >> 1][ek & 1];
     const unsigned s1 = sg.s0 + num_chunks(sg.len);
-    if (sg.s0 >= r0 && s1 <= r1) continue;
-    if (!sh.last[n_cut++]) continue;
     const int c0 = (int)ctas.owner(sg.s0), pieces = (int)ctas.owner(s1 - 1) - c0 + 1;
-    for (int r = warp; r < rows_of(sg.hr); r += W) {
+    for (int r = warp; r < rows; r += W) {
+      if (!has_row(sg.hr, r)) continue;
       auto at_piece = [&](int j) { return slot_of(ctas, sg.s0, c0 + j) * kTileRows + r; };
-      float Mx = -INFINITY, mx = -INFINITY;
-      for (int j = lane; j < pieces; j += 32) {
-        if (!RF_IN(p.err, at_piece(j), n_slots)) continue;
-        const float4 st = __ldcg(&p.ws_st[at_piece(j)]);
-        Mx = fmaxf(Mx, st.x);
-        mx = fmaxf(mx, st.y);
-      }
-      Mx = warp_max(Mx);
-      mx = warp_max(mx);
-      const float Mu = Mx == -INFINITY ? 0.f : Mx, mu = mx == -INFINITY ? 0.f : mx;
-      float L = 0.f, v[NV];
+      // 32 pieces at a time, a piece's (M, m, l) a lane, with the running maxima
+      // carried over; the loads of kBatch pieces' rows go together
+      float Mx = -INFINITY, mx = -INFINITY, L = 0.f, v[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] = 0.f;
       for (int j0 = 0; j0 < pieces; j0 += 32) {
-        float wo = 0.f, lj = 0.f;
-        if (j0 + lane < pieces && RF_IN(p.err, at_piece(j0 + lane), n_slots)) {
-          const float4 st = __ldcg(&p.ws_st[at_piece(j0 + lane)]);
-          wo = ex2(st.x - Mu);
-          lj = st.z * ex2(st.y - mu);
-        }
-        L += warp_sum(lj);
-        const int n = min(pieces - j0, 32);
         constexpr int kBatch = 8;
-        for (int j = 0; j < n; j += kBatch) {
-          float x[kBatch][NV];
+        const int n = min(pieces - j0, 32);
+        float x[kBatch][NV];
+        auto load = [&](int j) {
 #pragma unroll
           for (int u = 0; u < kBatch; ++u) {
 #pragma unroll
@@ -1064,6 +1152,21 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
               }
             }
           }
+        };
+        load(0);
+        float4 st = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+        if (lane < n && RF_IN(p.err, at_piece(j0 + lane), n_slots))
+          st = __ldcg(&p.ws_st[at_piece(j0 + lane)]);
+        const float Mn = fmaxf(Mx, warp_max(st.x)), mn = fmaxf(mx, warp_max(st.y));
+        const float Mu = Mn == -INFINITY ? 0.f : Mn, mu = mn == -INFINITY ? 0.f : mn;
+        const float wo = ex2(st.x - Mu), keep = ex2(Mx - Mu);
+        L = fmaf(L, ex2(mx - mu), warp_sum(st.z * ex2(st.y - mu)));
+        Mx = Mn;
+        mx = mn;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] *= keep;
+        for (int j = 0; j < n; j += kBatch) {
+          if (j > 0) load(j);
 #pragma unroll
           for (int u = 0; u < kBatch; ++u) {
             const float wj = __shfl_sync(0xffffffffu, wo, (j + u) & 31);
@@ -1073,7 +1176,8 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
           }
         }
       }
-      put_row(sg.b, sg.hr, r, L == 0.f ? 0.f : ex2(Mu - mu) / L, v);
+      const float Mu = Mx == -INFINITY ? 0.f : Mx, mu = mx == -INFINITY ? 0.f : mx;
+      put_row(sg, r, L == 0.f ? 0.f : ex2(Mu - mu) / L, v);
     }
   }
 }
@@ -1144,6 +1248,7 @@ cudaError_t launch_decode_paged(const PagedKV& c, const void* Q, void* O, int Hq
   p.lens = Lens{c.seq_lens, c.B, c.Hkv * p.tiles, c.max_pages * c.page_size};
   p.num_pages = c.num_pages;
   p.page_size = c.page_size;
+  p.page_shift = c.page_size == 16 ? 4 : (c.page_size == 32 ? 5 : (c.page_size == 64 ? 6 : 7));
   p.max_pages = c.max_pages;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.err = err;
@@ -1201,7 +1306,7 @@ int decode_paged_plan_selfcheck(const int* seq_lens, int B, int HR, int max_len,
       if (x0 != x) return 2;
       const int b = (int)(std::upper_bound(pre.begin(), pre.end(), x0) - pre.begin()) - 1;
       Cursor cur;
-      if (!cur.init(lens, b, x0 - pre[(size_t)b], &err)) return 2;
+      if (!cur.init(lens, b, seq_len(lens, b, false, &err), x0 - pre[(size_t)b])) return 2;
       int left = 0;
       for (unsigned i = 0; i < n; ++i, ++x) {
         if (i > 0 && !cur.next(lens, &err)) return 2;
