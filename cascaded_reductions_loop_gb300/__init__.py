@@ -131,9 +131,9 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return _c.c_void_p(stream.cuda_stream)
+    if stream is None:      # the handle alone: a Stream object costs 3 us to make
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _need(t, dtype, shape, name):
@@ -366,25 +366,39 @@ def rf_absmax_quant_fp8(x, sx_out, xq_out, stream=None) -> None:
 # ------------------------------------------------------------------ paged cache
 
 
-def _on_device(name, t):
+# The checks below run on every call of a decode loop, so the common case is one
+# expression; a tensor that fails it is looked at again for the message.
+
+
+def _on_device(name, t, dev=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != (torch.cuda.current_device() if dev is None else dev):
         raise ValueError(f"{name} must be on the current CUDA device")
 
 
-def _rows(t, dtype, T, H, d, name):
-    """Checks a [T, H, d] tensor whose tokens may be any distance apart; returns
+def _dense(t, dev, dtype, shape, name):
+    """Address of a contiguous tensor of that type and shape on device dev."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype == dtype and
+            t.shape == shape and t.is_contiguous()):
+        _on_device(name, t, dev)
+        _need(t, dtype, shape, name)
+    return t.data_ptr()
+
+
+def _rows(t, dev, dtype, T, H, d, name):
+    """Address of a [T, H, d] tensor whose tokens may be any distance apart, and
     that distance in elements."""
-    _on_device(name, t)
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (T, H, d):
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype == dtype and
+            t.shape == (T, H, d)):
+        _on_device(name, t, dev)
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} must have shape {(T, H, d)}, got {tuple(t.shape)}")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != d and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s0 if T > 1 else H * d
+    return t.data_ptr(), s0 if T > 1 else H * d
 
 
 class rf_paged_kv:
@@ -428,8 +442,11 @@ class rf_paged_kv:
         self._ref = _c.byref(self._c)
 
     def _here(self):
-        if self.device != torch.cuda.current_device():
+        """The current device, which must be the cache's."""
+        dev = torch.cuda.current_device()
+        if self.device != dev:
             raise ValueError("the cache must be on the current CUDA device")
+        return dev
 
 
 class rf_norm_rope:
@@ -457,20 +474,25 @@ class rf_norm_rope:
                 if w.dim() != 1 or not w.is_contiguous():
                     raise ValueError(f"{n} must be a contiguous [d] tensor")
         self.cos, self.sin, self.q_weight, self.k_weight = cos, sin, q_weight, k_weight
+        self._fits = set()          # what _need_for has found to fit
         self._c = _NormRope(None if cos is None else cos.data_ptr(),
                             None if sin is None else sin.data_ptr(), max_pos, rot_dim,
                             int(interleaved), None if q_weight is None else q_weight.data_ptr(),
                             None if k_weight is None else k_weight.data_ptr(), float(eps))
         self._ref = _c.byref(self._c)
 
-    def _need_for(self, dtype, d, has_q, has_k):
-        here = torch.cuda.current_device()
+    def _need_for(self, dev, dtype, d, has_q, has_k):
+        key = (dev, dtype, d, has_q, has_k)
+        if key in self._fits:       # the tensors held do not change their type or place
+            return self._ref
         for n, w, used in (("q_weight", self.q_weight, has_q), ("k_weight", self.k_weight, has_k)):
             if used and w is not None and (w.dtype != dtype or w.shape[0] != d or
-                                           w.get_device() != here):
+                                           w.get_device() != dev):
                 raise ValueError(f"{n} must be a {dtype} [{d}] tensor on the current CUDA device")
-        if self.cos is not None and self.cos.get_device() != here:
+        if self.cos is not None and self.cos.get_device() != dev:
             raise ValueError("cos and sin must be on the current CUDA device")
+        self._fits.add(key)
+        return self._ref
 
 
 def rf_qk_norm_rope(q, k, q_out, k_out, norm_rope, positions=None, stream=None) -> None:
@@ -484,25 +506,27 @@ def rf_qk_norm_rope(q, k, q_out, k_out, norm_rope, positions=None, stream=None) 
     if not isinstance(x, torch.Tensor) or x.dim() != 3 or \
             x.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("q or k must be given, as [T, heads, d] float32 or bfloat16")
+    if not x.is_cuda:
+        raise ValueError("q and k must be CUDA tensors")
     T, _, d = x.shape
-    dt = x.dtype
+    dt, dev = x.dtype, torch.cuda.current_device()
     Hq = Hkv = ldq = ldqo = ldk = ldko = 0
+    qp = qop = kp = kop = pp = ref = None
     if q is not None:
         Hq = q.shape[1]
-        ldq, ldqo = _rows(q, dt, T, Hq, d, "q"), _rows(q_out, dt, T, Hq, d, "q_out")
+        qp, ldq = _rows(q, dev, dt, T, Hq, d, "q")
+        qop, ldqo = _rows(q_out, dev, dt, T, Hq, d, "q_out")
     if k is not None:
         Hkv = k.shape[1]
-        ldk, ldko = _rows(k, dt, T, Hkv, d, "k"), _rows(k_out, dt, T, Hkv, d, "k_out")
-    ref = None
+        kp, ldk = _rows(k, dev, dt, T, Hkv, d, "k")
+        kop, ldko = _rows(k_out, dev, dt, T, Hkv, d, "k_out")
     if norm_rope is not None:
-        norm_rope._need_for(dt, d, q is not None, k is not None)
-        ref = norm_rope._ref
+        ref = norm_rope._need_for(dev, dt, d, q is not None, k is not None)
         if norm_rope.cos is not None:
-            _on_device("positions", positions)
-            _need(positions, torch.int32, (T,), "positions")
-    _check(lib.rf_qk_norm_rope(RF_F32 if dt == torch.float32 else RF_BF16, _ptr(q), ldq, _ptr(k),
-                               ldk, _ptr(q_out), ldqo, _ptr(k_out), ldko, _ptr(positions), ref, T,
-                               Hq, Hkv, d, _stream(stream)), "rf_qk_norm_rope")
+            pp = _dense(positions, dev, torch.int32, (T,), "positions")
+    _check(lib.rf_qk_norm_rope(RF_F32 if dt == torch.float32 else RF_BF16, qp, ldq, kp, ldk, qop,
+                               ldqo, kop, ldko, pp, ref, T, Hq, Hkv, d, _stream(stream)),
+           "rf_qk_norm_rope")
 
 
 def rf_kv_append_paged(cache, k, v, norm_rope=None, cu_seqlens=None, q=None, q_out=None,
@@ -512,26 +536,23 @@ def rf_kv_append_paged(cache, k, v, norm_rope=None, cu_seqlens=None, q=None, q_o
     bf16, tokens strided as they like; cu_seqlens: int32 [B+1] cumulative new
     tokens, or None: total / B each; q, q_out: the same tokens' queries
     [total,Hq,d], normed and rotated in the same launch, or None."""
-    cache._here()
+    dev, bf16 = cache._here(), torch.bfloat16
     total = k.shape[0]
     Hkv, d = cache.Hkv, cache.d
-    ldk = _rows(k, torch.bfloat16, total, Hkv, d, "k")
-    ldv = _rows(v, torch.bfloat16, total, Hkv, d, "v")
+    kp, ldk = _rows(k, dev, bf16, total, Hkv, d, "k")
+    vp, ldv = _rows(v, dev, bf16, total, Hkv, d, "v")
     Hq = ldq = ldqo = 0
+    qp = qop = cup = ref = None
     if q is not None:
         Hq = q.shape[1]
-        ldq = _rows(q, torch.bfloat16, total, Hq, d, "q")
-        ldqo = _rows(q_out, torch.bfloat16, total, Hq, d, "q_out")
+        qp, ldq = _rows(q, dev, bf16, total, Hq, d, "q")
+        qop, ldqo = _rows(q_out, dev, bf16, total, Hq, d, "q_out")
     if cu_seqlens is not None:
-        _on_device("cu_seqlens", cu_seqlens)
-        _need(cu_seqlens, torch.int32, (cache.B + 1,), "cu_seqlens")
-    ref = None
+        cup = _dense(cu_seqlens, dev, torch.int32, (cache.B + 1,), "cu_seqlens")
     if norm_rope is not None:
-        norm_rope._need_for(torch.bfloat16, d, q is not None, True)
-        ref = norm_rope._ref
-    _check(lib.rf_kv_append_paged(cache._ref, _ptr(k), ldk, _ptr(v), ldv, _ptr(cu_seqlens), total,
-                                  ref, _ptr(q), ldq, _ptr(q_out) if Hq else None, ldqo, Hq,
-                                  _stream(stream)), "rf_kv_append_paged")
+        ref = norm_rope._need_for(dev, bf16, d, q is not None, True)
+    _check(lib.rf_kv_append_paged(cache._ref, kp, ldk, vp, ldv, cup, total, ref, qp, ldq, qop, ldqo,
+                                  Hq, _stream(stream)), "rf_kv_append_paged")
 
 
 def rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq=1, d=128) -> int:
@@ -543,23 +564,20 @@ def rf_attn_decode_paged(cache, q, o, scale: float, workspace, stream=None) -> N
     [B,Tq,Hq,d] (or [B,Hq,d]: Tq = 1) bf16, the last Tq tokens of each
     sequence; workspace: a uint8 CUDA tensor of at least
     rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq, d) bytes."""
-    cache._here()
-    shape = tuple(q.shape)
-    if len(shape) not in (3, 4) or shape[0] != cache.B or shape[-1] != cache.d:
+    dev = cache._here()
+    shape = q.shape
+    n = len(shape)
+    if (n != 3 and n != 4) or shape[0] != cache.B or shape[-1] != cache.d:
         raise ValueError(f"q must be [{cache.B}, Tq, Hq, {cache.d}] or [{cache.B}, Hq, {cache.d}], "
-                         f"got {shape}")
-    Tq, Hq = (1, shape[1]) if len(shape) == 3 else shape[1:3]
-    _on_device("q", q)
-    _need(q, torch.bfloat16, shape, "q")
-    _on_device("o", o)
-    _need(o, torch.bfloat16, shape, "o")
-    ws_bytes = 0
+                         f"got {tuple(shape)}")
+    qp = _dense(q, dev, torch.bfloat16, shape, "q")
+    op = _dense(o, dev, torch.bfloat16, shape, "o")
+    wp, ws_bytes = None, 0
     if workspace is not None:
-        _on_device("workspace", workspace)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _check(lib.rf_attn_decode_paged(cache._ref, _ptr(q), _ptr(o), Hq, Tq, float(scale),
-                                    _ptr(workspace), ws_bytes, _stream(stream)),
-           "rf_attn_decode_paged")
+        _on_device("workspace", workspace, dev)
+        wp, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    _check(lib.rf_attn_decode_paged(cache._ref, qp, op, shape[-2], shape[1] if n == 4 else 1, scale,
+                                    wp, ws_bytes, _stream(stream)), "rf_attn_decode_paged")
 
 
 def rf_selftest_wait_timeout(timeout_us: int, stream=None) -> None:
