@@ -16,17 +16,21 @@
 // relative step does not depend on the scale, so the choice costs at most one
 // of its 18 binades).
 //
-// Work items: one page of one sequence that receives tokens ("item") and one
-// kv head, so that a scale has one owner and no atomics are needed.
+// Work.  A bf16 cache needs nothing but the rows: a lane group takes a few
+// heads of one token (rows kernel).  For E4M3 a scale must have one owner, so
+// that no atomics are needed: a work item is one page of one sequence that
+// receives tokens.
 //  - step kernel (one new token a sequence): one lane group for the key row
 //    and one for the value row of an (item, head); a page that has to be
 //    rescaled is rescaled by the whole warp.
-//  - prompt kernel: one CTA of 256 threads for an (item, head); the new rows
-//    stay in registers between the absmax and the quantisation, so each is
-//    read once.
+//  - prompt kernel: a CTA takes a few heads of an item, one after the other,
+//    each thread four 16-byte pieces of the page's keys and values; they stay
+//    in registers between the absmax and the quantisation, so each is read
+//    once, and the next head's are on their way meanwhile.
 // Query rows are further CTAs of the same launch (norm_rope.cuh).
 //
 // What bounds it: memory for prompts, launch latency for a step.
+#include <stdlib.h>
 #include <vector>
 
 #include "norm_rope.cuh"
@@ -78,15 +82,38 @@ __device__ __forceinline__ uint4 rescale16(uint4 w, float ratio) {
 }
 
 // Largest finite magnitude of eight values (infinities saturate and NaN keeps
-// its code: neither sets the scale).
-__device__ __forceinline__ float absmax8(const float (&v)[8]) {
-  float a = 0.f;
+// its code: neither sets the scale).  fmaxf passes over NaN; where an infinity
+// is the largest, the others are looked at again.
+__device__ __forceinline__ float absmax8(const Row8& y) {
+  float v[8], a = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float m = fabsf(v[e]);
-    if (m < INFINITY) a = fmaxf(a, m);
+  for (int k = 0; k < 4; ++k) f2_split(y.v[k], v[2 * k], v[2 * k + 1]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(v[e]));
+  if (a == INFINITY) {
+    a = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = fabsf(v[e]) < INFINITY ? fmaxf(a, fabsf(v[e])) : a;
   }
   return a;
+}
+__device__ __forceinline__ Row8 as_row(const Raw8<__nv_bfloat16>& x) {
+  Row8 y;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) y.v[k] = x.pair(k);
+  return y;
+}
+// Eight values times 1 / scale as codes.
+__device__ __forceinline__ uint2 quantise8(const Row8& y, float inv) {
+  const uint64_t i2 = f2(inv, inv);
+  uint32_t c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float lo, hi;
+    f2_split(fmul2(y.v[k], i2), lo, hi);
+    c[k] = e4m3x2(lo, hi);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 // The scale of a page's head after the append: a = absmax of the new values,
@@ -153,12 +180,32 @@ __host__ __device__ __forceinline__ int find_seq(const Seqs& sq, int t, unsigned
 }
 
 // Sequence and position of token t; false if there is nothing to do for it.
-__host__ __device__ __forceinline__ bool find_token(const Seqs& sq, int t, int* pos,
+__host__ __device__ __forceinline__ bool find_token(const Seqs& sq, int t, int* seq, int* pos,
                                                     unsigned* err) {
   const int b = sq.cu ? find_seq(sq, t, err) : t / sq.n_uniform;
   const NewTokens nt = new_tokens(sq, b, false, err);
+  *seq = b;
   *pos = nt.start + (t - nt.first);
   return nt.n > 0 && t >= nt.first && t < nt.first + nt.n;
+}
+
+// The page of that number of sequence b, or -1 (noted) if it is none of the
+// cache's.
+__host__ __device__ __forceinline__ int find_page(const Seqs& sq, int b, int64_t page, bool report,
+                                                  unsigned* err) {
+  const int phys = ld_int(sq.block_table, (int64_t)b * sq.max_pages + page,
+                          (int64_t)sq.B * sq.max_pages, err);
+  if (phys >= 0 && phys < sq.num_pages) return phys;
+  if (report) note_error(err, kDevErrInput);
+  return -1;
+}
+
+// Notes sequences whose sizes do not fit (thread i of n; a few loads each).
+__host__ __device__ __forceinline__ void check_seqs(const Seqs& sq, int i, int n, unsigned* err) {
+  for (int b = i; b < sq.B; b += n) (void)new_tokens(sq, b, true, err);
+  if (sq.cu && i == 0 &&
+      (ld_int(sq.cu, 0, sq.B + 1, err) != 0 || ld_int(sq.cu, sq.B, sq.B + 1, err) != sq.total))
+    note_error(err, kDevErrInput);
 }
 
 // Items.  Sequence b gets the item numbers [f(b), f(b + 1)), as many as its
@@ -179,31 +226,11 @@ __host__ __device__ __forceinline__ int64_t num_items(int total, int B, int n_un
 struct Item {
   int t0, n, off, pos0, phys;
 };
-__host__ __device__ __forceinline__ Item find_item(const Seqs& sq, int x, bool report,
-                                                   unsigned* err) {
+// Page p (0, 1, ..) of those that the new tokens of sequence b touch.
+__host__ __device__ __forceinline__ Item item_of(const Seqs& sq, int b, int p, bool report,
+                                                 unsigned* err) {
   Item it = {0, 0, 0, 0, 0};
-  int b, p;
-  if (sq.cu) {
-    int lo = 0, hi = sq.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((int64_t)(ld_int(sq.cu, mid, sq.B + 1, err) / sq.page_size) + 2 * (int64_t)mid <= x)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    b = lo;
-    const int64_t q =
-        (int64_t)x - (ld_int(sq.cu, b, sq.B + 1, err) / sq.page_size) - 2 * (int64_t)b;
-    if (q < 0 || q > x) return it;
-    p = (int)q;
-  } else {
-    const int m = pages_of(sq.n_uniform, sq.page_size);
-    b = x / m;
-    p = x - b * m;
-  }
-  if (b >= sq.B) return it;
-  const NewTokens nt = new_tokens(sq, b, report && p == 0, err);
+  const NewTokens nt = new_tokens(sq, b, false, err);
   if (nt.n == 0) return it;
   const int64_t page = (int64_t)nt.start / sq.page_size + p;
   const int64_t lo_pos = page * sq.page_size;
@@ -211,18 +238,31 @@ __host__ __device__ __forceinline__ Item find_item(const Seqs& sq, int x, bool r
   const int64_t a = lo_pos > nt.start ? lo_pos : nt.start;
   const int64_t z = lo_pos + sq.page_size < end ? lo_pos + sq.page_size : end;
   if (a >= z) return it;
-  const int phys = ld_int(sq.block_table, (int64_t)b * sq.max_pages + page,
-                          (int64_t)sq.B * sq.max_pages, err);
-  if (phys < 0 || phys >= sq.num_pages) {
-    if (report) note_error(err, kDevErrInput);
-    return it;
-  }
+  const int phys = find_page(sq, b, page, report, err);
+  if (phys < 0) return it;
   it.t0 = nt.first + (int)(a - nt.start);
   it.n = (int)(z - a);
   it.off = (int)(a - lo_pos);
   it.pos0 = (int)a;
   it.phys = phys;
   return it;
+}
+
+// Whether item x is one of sequence b's, and which of its pages.
+__host__ __device__ __forceinline__ bool item_is_of(const Seqs& sq, int x, int b, int* p,
+                                                    unsigned* err) {
+  int64_t lo, n;
+  if (sq.cu) {
+    const int c0 = ld_int(sq.cu, b, sq.B + 1, err), c1 = ld_int(sq.cu, b + 1, sq.B + 1, err);
+    lo = c0 / sq.page_size + 2 * (int64_t)b;
+    n = (int64_t)(c1 / sq.page_size) - c0 / sq.page_size + 2;
+  } else {
+    n = pages_of(sq.n_uniform, sq.page_size);
+    lo = b * n;
+  }
+  const int64_t q = x - lo;
+  *p = (int)q;
+  return q >= 0 && q < n && q <= x;
 }
 
 struct Cache {
@@ -232,31 +272,80 @@ struct Cache {
 
 using bf16 = __nv_bfloat16;
 
-// ------------------------------------------------------------- query rows
+// ------------------------------------------------------------- rows
 
-template <int D>
+// HB query heads of a token by a lane group of CTA `cta` of the query CTAs.
+template <int D, int HB>
 __device__ __forceinline__ void query_rows(const Seqs& sq, const NormRope& nr,
                                            const RowsIn<bf16>& q, const RowsOut<bf16>& qo, int Hq,
                                            int cta, unsigned* err) {
   constexpr int LG = D / 8;
-  const int li = threadIdx.x % LG;
-  const int64_t u = (int64_t)cta * (kThreads / LG) + threadIdx.x / LG;
-  const int t = (int)(u / Hq), h = (int)(u % Hq);
-  int pos = 0;
-  const bool active = t < sq.total && find_token(sq, t, &pos, err);
-  norm_rope_heads<bf16, D, 1>(nr, static_cast<const bf16*>(nr.wq), q, qo, sq.total, Hq, t, h, pos,
-                              active, li, err);
+  const int li = threadIdx.x % LG, nblk = (Hq + HB - 1) / HB;
+  const int64_t u = (int64_t)cta * (blockDim.x / LG) + threadIdx.x / LG;
+  const int t = (int)(u / nblk), h0 = (int)(u % nblk) * HB;
+  int b = 0, pos = 0;
+  const bool active = t < sq.total && find_token(sq, t, &b, &pos, err);
+  norm_rope_heads<bf16, D, HB>(nr, static_cast<const bf16*>(nr.wq), q, qo, sq.total, Hq, t, h0,
+                               pos, active, li, err);
+}
+
+// bf16 cache: HB kv heads of a token by a lane group.
+template <int D, int HB>
+__global__ void __launch_bounds__(kThreads)
+    append_rows_kernel(const Seqs sq, const NormRope nr, const RowsIn<bf16> k, const RowsIn<bf16> v,
+                       const RowsIn<bf16> q, const RowsOut<bf16> qo, int Hq, const Cache cache,
+                       int kv_ctas, unsigned* err) {
+  if ((int)blockIdx.x >= kv_ctas) {
+    query_rows<D, HB>(sq, nr, q, qo, Hq, (int)blockIdx.x - kv_ctas, err);
+    return;
+  }
+  constexpr int LG = D / 8;
+  const int li = threadIdx.x % LG, nblk = (sq.Hkv + HB - 1) / HB;
+  const int64_t u = (int64_t)blockIdx.x * (kThreads / LG) + threadIdx.x / LG;
+  const int t = (int)(u / nblk), h0 = (int)(u % nblk) * HB;
+  int b = 0, pos = 0, phys = -1;
+  bool active = t < sq.total && find_token(sq, t, &b, &pos, err);
+  if (active) phys = find_page(sq, b, pos / sq.page_size, li == 0, err);
+  active = phys >= 0;
+  const int64_t n_k = (int64_t)(sq.total - 1) * k.ld + (int64_t)sq.Hkv * D;
+  const int64_t n_v = (int64_t)(sq.total - 1) * v.ld + (int64_t)sq.Hkv * D;
+  const int64_t n_pages = (int64_t)sq.num_pages * sq.Hkv * sq.page_size * D;
+  Raw8<bf16> kx[HB], vx[HB];
+#pragma unroll
+  for (int j = 0; j < HB; ++j) {
+    kx[j] = {};
+    vx[j] = {};
+    if (active && h0 + j < sq.Hkv) {
+      kx[j] = load8<bf16>(k.p, (int64_t)t * k.ld + (int64_t)(h0 + j) * D + 8 * li, n_k, err);
+      vx[j] = load8<bf16>(v.p, (int64_t)t * v.ld + (int64_t)(h0 + j) * D + 8 * li, n_v, err);
+    }
+  }
+  const bf16* wk = static_cast<const bf16*>(nr.wk);
+  const Coef cf = load_coef<bf16, D>(nr, wk, pos, li, active, err);
+#pragma unroll
+  for (int j = 0; j < HB; ++j) {
+    const Row8 y = norm_rope_row<bf16, D>(nr, kx[j], wk != nullptr, cf, li);
+    if (active && h0 + j < sq.Hkv) {
+      const int64_t at =
+          (((int64_t)phys * sq.Hkv + h0 + j) * sq.page_size + pos % sq.page_size) * D + 8 * li;
+      store8(reinterpret_cast<bf16*>(cache.pages[0]), at, y, n_pages, err);
+      if (RF_IN(err, at + 7, n_pages))
+        *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(cache.pages[1]) + at) =
+            make_uint4(vx[j].w[0], vx[j].w[1], vx[j].w[2], vx[j].w[3]);
+    }
+  }
+  if (blockIdx.x == 0) check_seqs(sq, (int)threadIdx.x, kThreads, err);
 }
 
 // ------------------------------------------------------------- one token a sequence
 
-template <int D, bool kF8>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
     append_step_kernel(const Seqs sq, const NormRope nr, const RowsIn<bf16> k, const RowsIn<bf16> v,
                        const RowsIn<bf16> q, const RowsOut<bf16> qo, int Hq, const Cache cache,
                        int kv_ctas, unsigned* err) {
   if ((int)blockIdx.x >= kv_ctas) {
-    query_rows<D>(sq, nr, q, qo, Hq, (int)blockIdx.x - kv_ctas, err);
+    query_rows<D, 1>(sq, nr, q, qo, Hq, (int)blockIdx.x - kv_ctas, err);
     return;
   }
   constexpr int LG = D / 8;                   // lanes of a row
@@ -267,7 +356,7 @@ __global__ void __launch_bounds__(kThreads)
       ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kPairs + (grp >> 1);
   const int b = (int)(u / sq.Hkv), h = (int)(u % sq.Hkv);
   Item it = {0, 0, 0, 0, 0};
-  if (b < sq.B) it = find_item(sq, b, h == 0 && !is_v && li == 0, err);
+  if (b < sq.B) it = item_of(sq, b, 0, h == 0 && !is_v && li == 0, err);
   const bool active = it.n > 0;
 
   const RowsIn<bf16>& in = is_v ? v : k;
@@ -275,25 +364,15 @@ __global__ void __launch_bounds__(kThreads)
   if (active)
     x = load8<bf16>(in.p, (int64_t)it.t0 * in.ld + (int64_t)h * D + 8 * li,
                     (int64_t)(sq.total - 1) * in.ld + (int64_t)sq.Hkv * D, err);
-  RopeLane rp = {};
-  if (active && !is_v && 8 * li < nr.rot) rp = load_rope(nr, it.pos0, li, err);
-  WeightLane w = {};
-  if (nr.wk && !is_v) w = load_weight<bf16, D>(nr, static_cast<const bf16*>(nr.wk), li, err);
-  float y[8];
-  norm_rope_row<bf16, D>(nr, x, nr.wk != nullptr, w, rp, li, y);
-  if (is_v) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = x.get(e);
-  }
+  const bf16* wk = static_cast<const bf16*>(nr.wk);
+  const Coef cf = load_coef<bf16, D>(nr, wk, it.pos0, li, active && !is_v, err);
+  Row8 y = norm_rope_row<bf16, D>(nr, x, wk != nullptr, cf, li);
+  if (is_v) y = as_row(x);
 
   const int64_t head = (int64_t)it.phys * sq.Hkv + h;         // (page, head)
   const int64_t n_pages = (int64_t)sq.num_pages * sq.Hkv * sq.page_size * D;
   const int64_t row = (head * sq.page_size + it.off) * D + 8 * li;
   uint8_t* pages = is_v ? cache.pages[1] : cache.pages[0];
-  if (!kF8) {
-    if (active) store8(reinterpret_cast<bf16*>(pages), row, y, n_pages, err);
-    return;
-  }
   float a = absmax8(y);
 #pragma unroll
   for (int o = LG / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
@@ -306,9 +385,7 @@ __global__ void __launch_bounds__(kThreads)
   if (active) {
     const float inv = 1.f / s;                                // exact: a power of two
     if (RF_IN(err, row + 7, n_pages))
-      *reinterpret_cast<uint2*>(pages + row) =
-          make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                     e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+      *reinterpret_cast<uint2*>(pages + row) = quantise8(y, inv);
     if (li == 0 && RF_IN(err, head, n_sc)) sc[head] = s;
   }
   // pages whose scale grew: the warp rescales the off * D codes held already
@@ -334,142 +411,143 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   }
+  if (blockIdx.x == 0) check_seqs(sq, (int)threadIdx.x, kThreads, err);
 }
 
 // ------------------------------------------------------------- prompts
 
-// SW: sweeps of the CTA's 256 / (D / 8) rows that cover a page.
-template <int D, bool kF8, int SW>
+// A CTA takes the keys or the values of one (item, head): its threads cover
+// the page's rows in SW sweeps.
+template <int D, int SW>
 __global__ void __launch_bounds__(kThreads)
     append_prompt_kernel(const Seqs sq, const NormRope nr, const RowsIn<bf16> k,
                          const RowsIn<bf16> v, const RowsIn<bf16> q, const RowsOut<bf16> qo, int Hq,
                          const Cache cache, int kv_ctas, unsigned* err) {
   if ((int)blockIdx.x >= kv_ctas) {
-    query_rows<D>(sq, nr, q, qo, Hq, (int)blockIdx.x - kv_ctas, err);
+    query_rows<D, 4>(sq, nr, q, qo, Hq, (int)blockIdx.x - kv_ctas, err);
     return;
   }
-  constexpr int LG = D / 8, kRows = kThreads / LG;
+  constexpr int LG = D / 8;
+  const int rows = (int)blockDim.x / LG;             // of a sweep
   const int li = threadIdx.x % LG, r = threadIdx.x / LG;
-  const int x = (int)blockIdx.x / sq.Hkv, h = (int)blockIdx.x % sq.Hkv;
-  const Item it = find_item(sq, x, h == 0 && threadIdx.x == 0, err);
+  const int x = (int)blockIdx.x / (2 * sq.Hkv), y_ = (int)blockIdx.x - x * 2 * sq.Hkv;
+  const int h = y_ >> 1;
+  const bool is_v = y_ & 1;
+  // the sequences are looked through in parallel; one thread finds the item
+  __shared__ Item found;
+  if (threadIdx.x == 0) found.n = 0;
+  __syncthreads();
+  for (int b = threadIdx.x; b < sq.B; b += blockDim.x) {
+    int pg;
+    if (item_is_of(sq, x, b, &pg, err)) {
+      const Item i = item_of(sq, b, pg, y_ == 0, err);
+      if (i.n > 0) found = i;
+    }
+  }
+  if (blockIdx.x == 0) check_seqs(sq, (int)threadIdx.x, (int)blockDim.x, err);
+  __syncthreads();
+  const Item it = found;
   if (it.n == 0) return;
 
-  Raw8<bf16> kx[SW], vx[SW];
-  const int64_t n_k = (int64_t)(sq.total - 1) * k.ld + (int64_t)sq.Hkv * D;
-  const int64_t n_v = (int64_t)(sq.total - 1) * v.ld + (int64_t)sq.Hkv * D;
-#pragma unroll
-  for (int i = 0; i < SW; ++i) {
-    const int t = r + i * kRows;
-    kx[i] = {};
-    vx[i] = {};
-    if (t < it.n) {
-      kx[i] = load8<bf16>(k.p, (int64_t)(it.t0 + t) * k.ld + (int64_t)h * D + 8 * li, n_k, err);
-      vx[i] = load8<bf16>(v.p, (int64_t)(it.t0 + t) * v.ld + (int64_t)h * D + 8 * li, n_v, err);
-    }
-  }
-  WeightLane w = {};
-  if (nr.wk) w = load_weight<bf16, D>(nr, static_cast<const bf16*>(nr.wk), li, err);
-
-  const int64_t head = (int64_t)it.phys * sq.Hkv + h;
+  const RowsIn<bf16>& in = is_v ? v : k;
+  const int64_t n_in = (int64_t)(sq.total - 1) * in.ld + (int64_t)sq.Hkv * D;
   const int64_t n_pages = (int64_t)sq.num_pages * sq.Hkv * sq.page_size * D;
-  const int64_t row0 = (head * sq.page_size + it.off) * D + 8 * li;
-  float ky[kF8 ? SW : 1][8];
-  float ak = 0.f, av = 0.f;
-#pragma unroll
-  for (int i = 0; i < SW; ++i) {
-    const int t = r + i * kRows;
-    if (i * kRows >= it.n) break;                    // the same for the whole CTA
-    RopeLane rp = {};
-    if (t < it.n && 8 * li < nr.rot) rp = load_rope(nr, it.pos0 + t, li, err);
-    float(&y)[8] = ky[kF8 ? i : 0];
-    norm_rope_row<bf16, D>(nr, kx[i], nr.wk != nullptr, w, rp, li, y);
-    float vf[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) vf[e] = vx[i].get(e);
-    if (kF8) {
-      if (t < it.n) {
-        ak = fmaxf(ak, absmax8(y));
-        av = fmaxf(av, absmax8(vf));
-      }
-    } else if (t < it.n) {
-      store8(reinterpret_cast<bf16*>(cache.pages[0]), row0 + (int64_t)t * D, y, n_pages, err);
-      store8(reinterpret_cast<bf16*>(cache.pages[1]), row0 + (int64_t)t * D, vf, n_pages, err);
-    }
-  }
-  if (!kF8) return;
-
-  __shared__ float red[2][kThreads / 32];
-  ak = warp_max(ak);
-  av = warp_max(av);
-  if ((threadIdx.x & 31) == 0) {
-    red[0][threadIdx.x >> 5] = ak;
-    red[1][threadIdx.x >> 5] = av;
-  }
   const int64_t n_sc = (int64_t)sq.num_pages * sq.Hkv;
-  float s_old[2] = {0.f, 0.f}, s[2];
-  if (it.off > 0 && RF_IN(err, head, n_sc)) {
-    s_old[0] = cache.scale[0][head];
-    s_old[1] = cache.scale[1][head];
-  }
-  __syncthreads();                       // after it: everyone has read the old scales
-#pragma unroll
-  for (int w2 = 0; w2 < 2; ++w2) {
-    float a = 0.f;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) a = fmaxf(a, red[w2][i]);
-    s[w2] = new_scale(a, s_old[w2], it.off);
-    if (threadIdx.x == 0 && RF_IN(err, head, n_sc)) cache.scale[w2][head] = s[w2];
-    if (it.off > 0 && s[w2] > s_old[w2]) {
-      const float ratio = s_old[w2] / s[w2];
-      const int64_t at = head * sq.page_size * D;
-      uint4* pg = reinterpret_cast<uint4*>(cache.pages[w2] + at);
-      for (int i = threadIdx.x; i < it.off * D / 16; i += kThreads)
-        if (RF_IN(err, at + 16 * i + 15, n_pages)) pg[i] = rescale16(pg[i], ratio);
-    }
-  }
-  const float ik = 1.f / s[0], iv = 1.f / s[1];
+  Raw8<bf16> raw[SW];
 #pragma unroll
   for (int i = 0; i < SW; ++i) {
-    const int t = r + i * kRows;
-    const int64_t at = row0 + (int64_t)t * D;
-    if (t < it.n && RF_IN(err, at + 7, n_pages)) {
-      const float(&y)[8] = ky[kF8 ? i : 0];
-      *reinterpret_cast<uint2*>(cache.pages[0] + at) =
-          make_uint2(e4m3x4(y[0] * ik, y[1] * ik, y[2] * ik, y[3] * ik),
-                     e4m3x4(y[4] * ik, y[5] * ik, y[6] * ik, y[7] * ik));
-      float z[8];
+    const int t = r + i * rows;
+    raw[i] = {};
+    if (t < it.n)
+      raw[i] = load8<bf16>(in.p, (int64_t)(it.t0 + t) * in.ld + (int64_t)h * D + 8 * li, n_in, err);
+  }
+  float* sc = is_v ? cache.scale[1] : cache.scale[0];
+  uint8_t* pages = is_v ? cache.pages[1] : cache.pages[0];
+  const int64_t head = (int64_t)it.phys * sq.Hkv + h;
+  const float s_old = it.off > 0 && RF_IN(err, head, n_sc) ? sc[head] : 0.f;
+
+  Row8 y[SW];
+  float a = 0.f;
+  if (is_v) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = vx[i].get(e) * iv;
-      *reinterpret_cast<uint2*>(cache.pages[1] + at) =
-          make_uint2(e4m3x4(z[0], z[1], z[2], z[3]), e4m3x4(z[4], z[5], z[6], z[7]));
+    for (int i = 0; i < SW; ++i) {
+      y[i] = as_row(raw[i]);                         // rows beyond the item's are zeros
+      a = fmaxf(a, absmax8(y[i]));
     }
+  } else {
+    const bf16* wk = static_cast<const bf16*>(nr.wk);
+#pragma unroll
+    for (int i = 0; i < SW; ++i) {
+      const int t = r + i * rows;
+      const Coef cf = load_coef<bf16, D>(nr, wk, it.pos0 + t, li, t < it.n, err);
+      y[i] = norm_rope_row<bf16, D>(nr, raw[i], wk != nullptr, cf, li);
+      if (t < it.n) a = fmaxf(a, absmax8(y[i]));
+    }
+  }
+  __shared__ float red[kThreads / 32];
+  a = warp_max(a);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+  __syncthreads();                       // after it, too: everyone has read the old scale
+  const int lane = threadIdx.x & 31;
+  a = warp_max(lane < (int)blockDim.x / 32 ? red[lane] : 0.f);
+  const float s = new_scale(a, s_old, it.off);
+  if (threadIdx.x == 0 && RF_IN(err, head, n_sc)) sc[head] = s;
+  const int64_t base = head * sq.page_size * D;
+  if (it.off > 0 && s > s_old) {
+    const float ratio = s_old / s;
+    uint4* pg = reinterpret_cast<uint4*>(pages + base);
+    for (int i = threadIdx.x; i < it.off * D / 16; i += blockDim.x)
+      if (RF_IN(err, base + 16 * i + 15, n_pages)) pg[i] = rescale16(pg[i], ratio);
+  }
+  const float inv = 1.f / s;
+#pragma unroll
+  for (int i = 0; i < SW; ++i) {
+    const int t = r + i * rows;
+    const int64_t at = base + (int64_t)(it.off + t) * D + 8 * li;
+    if (t < it.n && RF_IN(err, at + 7, n_pages))
+      *reinterpret_cast<uint2*>(pages + at) = quantise8(y[i], inv);
   }
 }
 
-template <int D, bool kF8>
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int D>
 cudaError_t launch(const Seqs& sq, const NormRope& nr, const RowsIn<bf16>& k,
                    const RowsIn<bf16>& v, const RowsIn<bf16>& q, const RowsOut<bf16>& qo, int Hq,
-                   const Cache& cache, unsigned* err, cudaStream_t s) {
-  constexpr int LG = D / 8, per = kThreads / LG;
-  const int64_t q_ctas = Hq > 0 ? ((int64_t)sq.total * Hq + per - 1) / per : 0;
+                   const Cache& cache, bool f8, int sms, unsigned* err, cudaStream_t s) {
+  constexpr int LG = D / 8, per = kThreads / LG;      // lane groups of a CTA
+  if (!f8) {
+    // four heads a lane group where that still fills the device
+    const bool many = (int64_t)sq.total * sq.Hkv >= (int64_t)sms * 64 * per;
+    const int hb = many ? 4 : 1;
+    const int64_t kv = ceil_div((int64_t)sq.total * ceil_div(sq.Hkv, hb), per);
+    const int64_t q_ctas = ceil_div((int64_t)sq.total * ceil_div(Hq, hb), per);
+    const unsigned grid = (unsigned)(kv + q_ctas);
+    if (many)
+      append_rows_kernel<D, 4><<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq, cache, (int)kv, err);
+    else
+      append_rows_kernel<D, 1><<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq, cache, (int)kv, err);
+    return cudaGetLastError();
+  }
   if (!sq.cu && sq.n_uniform == 1) {
-    const int64_t pairs = kThreads / (2 * LG);
-    const int64_t kv = ((int64_t)sq.B * sq.Hkv + pairs - 1) / pairs;
-    append_step_kernel<D, kF8><<<(unsigned)(kv + q_ctas), kThreads, 0, s>>>(
+    const int64_t kv = ceil_div((int64_t)sq.B * sq.Hkv, kThreads / (2 * LG));
+    const int64_t q_ctas = ceil_div((int64_t)sq.total * Hq, per);
+    append_step_kernel<D><<<(unsigned)(kv + q_ctas), kThreads, 0, s>>>(
         sq, nr, k, v, q, qo, Hq, cache, (int)kv, err);
     return cudaGetLastError();
   }
-  const int64_t kv =
-      num_items(sq.total, sq.B, sq.n_uniform, sq.cu != nullptr, sq.page_size) * sq.Hkv;
+  const int pieces = sq.page_size * D / 8, threads = pieces < kThreads ? pieces : kThreads;
+  const int64_t items = num_items(sq.total, sq.B, sq.n_uniform, sq.cu != nullptr, sq.page_size);
+  const int64_t kv = items * sq.Hkv * 2;
+  const int64_t q_ctas = ceil_div((int64_t)sq.total * ceil_div(Hq, 4), threads / LG);
   const unsigned grid = (unsigned)(kv + q_ctas);
-#define RF_GO(SW)                                                                              \
-  append_prompt_kernel<D, kF8, SW>                                                             \
-      <<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq, cache, (int)kv, err)
-  switch ((sq.page_size + per - 1) / per) {
+#define RF_GO(SW) \
+  append_prompt_kernel<D, SW><<<grid, threads, 0, s>>>(sq, nr, k, v, q, qo, Hq, cache, (int)kv, err)
+  switch (pieces / threads) {
     case 1: RF_GO(1); break;
     case 2: RF_GO(2); break;
     case 4: RF_GO(4); break;
-    default: RF_GO(8); break;
+    default: RF_GO(D / 16); break;       // 8 at D = 128; at D = 64 four are the most
   }
 #undef RF_GO
   return cudaGetLastError();
@@ -495,8 +573,8 @@ Seqs make_seqs(const PagedKV& c, const int* cu, int total, int max_pos) {
 }  // namespace
 
 int64_t append_grid_bound(int total, int B, bool has_cu, int page_size, int Hkv, int Hq) {
-  return num_items(total, B, has_cu ? 0 : total / B, has_cu, page_size) * Hkv +
-         (int64_t)total * (Hq > 0 ? Hq : 1);
+  return num_items(total, B, has_cu ? 0 : total / B, has_cu, page_size) * Hkv * 2 +
+         (int64_t)total * ((int64_t)Hkv + Hq);
 }
 
 cudaError_t launch_kv_append_paged(const PagedKV& c, const NormRope& nr, const void* K,
@@ -509,21 +587,20 @@ cudaError_t launch_kv_append_paged(const PagedKV& c, const NormRope& nr, const v
                      q = {static_cast<const bf16*>(Q), ldq};
   const RowsOut<bf16> qo = {static_cast<bf16*>(Qo), ldqo};
   const bool f8 = c.dtype == RF_E4M3;
-  if (c.d == 64)
-    return f8 ? launch<64, true>(sq, nr, k, v, q, qo, Hq, cache, err, s)
-              : launch<64, false>(sq, nr, k, v, q, qo, Hq, cache, err, s);
-  return f8 ? launch<128, true>(sq, nr, k, v, q, qo, Hq, cache, err, s)
-            : launch<128, false>(sq, nr, k, v, q, qo, Hq, cache, err, s);
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidValue;
+  return c.d == 64 ? launch<64>(sq, nr, k, v, q, qo, Hq, cache, f8, sms, err, s)
+                   : launch<128>(sq, nr, k, v, q, qo, Hq, cache, f8, sms, err, s);
 }
 
 // Host-side walk of the items (the functions above, shared by host and
 // device).  All arrays are host arrays.  Returns 0 when every invariant
 // holds, else the number of the first that fails:
 //   1 no index leaves its array;
-//   2 an item's page and slots lie in the cache and in one page;
+//   2 an item is of one sequence, its page and slots in the cache and in one page;
 //   3 every token of a sequence that is not skipped is written once, to the
 //     slot of its position, and no other token is;
-//   4 the query rows' lookup finds the same position for the same tokens;
+//   4 the rows' lookup finds the same position and page for the same tokens;
 //   5 inconsistent sizes, and only those, are noted.
 int append_plan_selfcheck(const PagedKV& c, const int* cu, int total, int max_pos) {
   const Seqs sq = make_seqs(c, cu, total, max_pos);
@@ -538,7 +615,15 @@ int append_plan_selfcheck(const PagedKV& c, const int* cu, int total, int max_po
   std::vector<int> pos_of((size_t)total, -1);
   const int64_t n = num_items(total, c.B, sq.n_uniform, cu != nullptr, c.page_size);
   for (int64_t x = 0; x < n; ++x) {
-    const Item it = find_item(sq, (int)x, true, &err);
+    Item it = {0, 0, 0, 0, 0};
+    for (int b = 0; b < c.B; ++b) {
+      int p;
+      if (!item_is_of(sq, (int)x, b, &p, &err)) continue;
+      const Item i = item_of(sq, b, p, true, &err);
+      if (i.n == 0) continue;
+      if (order && it.n != 0) return 2;
+      it = i;
+    }
     if (err & kDevErrBounds) return 1;
     if (it.n == 0) continue;
     if (it.n < 0 || it.off < 0 || it.off + it.n > c.page_size || it.phys < 0 ||
@@ -573,11 +658,17 @@ int append_plan_selfcheck(const PagedKV& c, const int* cu, int total, int max_po
   }
   if (order && pos_of != want) return 3;
   for (int t = 0; t < total; ++t) {
-    int pos = 0;
-    const bool active = find_token(sq, t, &pos, &err);
+    int b = 0, pos = 0;
+    const bool active = find_token(sq, t, &b, &pos, &err);
+    const int phys = active ? find_page(sq, b, pos / c.page_size, true, &err) : -1;
     if (err & kDevErrBounds) return 1;
-    if (order && (active ? pos : -1) != seen[(size_t)t]) return 4;
+    if (order && ((active ? pos : -1) != seen[(size_t)t] ||
+                  (phys >= 0 ? pos : -1) != want[(size_t)t]))
+      return 4;
   }
+  check_seqs(sq, 0, 1, &err);
+  if (err & kDevErrBounds) return 1;
+  if (!order && !(err & kDevErrInput)) return 5;
   if (order && bad != ((err & kDevErrInput) != 0)) return 5;
   return 0;
 }

@@ -3,16 +3,18 @@
 //
 // A row of D elements is held by a group of D / 8 neighbouring lanes, eight
 // consecutive elements a lane (one 16-byte load in bf16).  With x the row,
-//     y_i = x_i * rsqrt(mean(x^2) + eps) * w_i        (where there is a weight)
+//     y_i = x_i * rstd * w_i,   rstd = rsqrt(mean(x^2) + eps)   (where there is a weight)
 // and, for the first rot elements, a rotation of pairs by the token's angles:
 //     (a, b) -> (a cos - b sin, b cos + a sin),
 // the pair j being elements (j, j + rot / 2) (half-split) or (2j, 2j + 1)
-// (interleaved).  Both forms are one formula per element,
-//     out_i = y_i c_i + y_partner(i) s_i,   s_i = -sin for a, +sin for b,
-// with the partner in the lane rot / 16 away or in the same lane.  Everything
-// is fp32 (one warp-shuffle reduction for the sum of squares); the caller
-// rounds once.  rot % 16 == 0, so a lane's eight elements are all rotated or
-// none, and all in the same half.
+// (interleaved).  Both forms, and unrotated elements, are one formula,
+//     out_i = rstd * (x_i A_i + x_partner(i) B_i),
+//     A_i = w_i cos,   B_i = -+ w_partner(i) sin   (a: -, b: +),
+// with the partner in the lane rot / 16 away or in the same lane.  A and B
+// depend on the token and on queries or keys only, so a lane group makes them
+// once for all heads it takes; a head then costs two packed multiply-adds for
+// two elements.  Everything is fp32; the caller rounds once.  rot % 16 == 0, so
+// a lane's eight elements are all rotated or none, and all in the same half.
 #pragma once
 
 #include "rf_device.cuh"
@@ -30,12 +32,21 @@ struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ float get(int e) const {
     return (e & 1) ? bf16hi(w[e >> 1]) : bf16lo(w[e >> 1]);
   }
+  // elements 2 i and 2 i + 1 as packed fp32
+  __device__ __forceinline__ uint64_t pair(int i) const { return f2(bf16lo(w[i]), bf16hi(w[i])); }
+  __device__ __forceinline__ uint64_t swapped(int i) const {
+    return f2(bf16hi(w[i]), bf16lo(w[i]));
+  }
 };
 template <>
 struct Raw8<float> {
   static constexpr int kWords = 8;
   uint32_t w[8];
   __device__ __forceinline__ float get(int e) const { return __uint_as_float(w[e]); }
+  __device__ __forceinline__ uint64_t pair(int i) const { return f2(get(2 * i), get(2 * i + 1)); }
+  __device__ __forceinline__ uint64_t swapped(int i) const {
+    return f2(get(2 * i + 1), get(2 * i));
+  }
 };
 
 // Loads elements [i, i + 8) of a tensor of n elements (zeros outside it, in
@@ -60,75 +71,38 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int64_t i, int64_t n, unsig
   return r;
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, int64_t i, const float (&v)[8], int64_t n,
-                                       unsigned* err) {
-  if (!RF_IN(err, i + 7, n) || !RF_IN(err, i, n)) return;
-  *reinterpret_cast<uint4*>(p + i) =
-      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                 pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(float* p, int64_t i, const float (&v)[8], int64_t n,
-                                       unsigned* err) {
-  if (!RF_IN(err, i + 7, n) || !RF_IN(err, i, n)) return;
-  reinterpret_cast<float4*>(p + i)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p + i)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-
-// This lane's part of the tables' row of one position: c and signed s of its
-// eight elements.  Only called where the lane's elements are rotated.
-struct RopeLane {
-  float c[8], s[8];
+// Eight results, in packed fp32 pairs.
+struct Row8 {
+  uint64_t v[4];
 };
 
-__device__ __forceinline__ RopeLane load_rope(const NormRope& nr, int pos, int li, unsigned* err) {
-  RopeLane r;
-  const int half = nr.rot >> 1;
-  const int64_t n = (int64_t)nr.max_pos * half;
-  if (nr.interleaved) {
-    const int64_t at = (int64_t)pos * half + 4 * li;
-    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (RF_IN(err, at + 3, n)) {
-      c = __ldg(reinterpret_cast<const float4*>(nr.cos + at));
-      s = __ldg(reinterpret_cast<const float4*>(nr.sin + at));
-    }
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+__device__ __forceinline__ void store8(__nv_bfloat16* p, int64_t i, const Row8& y, int64_t n,
+                                       unsigned* err) {
+  if (!RF_IN(err, i + 7, n) || !RF_IN(err, i, n)) return;
+  uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      r.c[e] = cc[e >> 1];
-      r.s[e] = (e & 1) ? ss[e >> 1] : -ss[e >> 1];
-    }
-    return r;
+  for (int k = 0; k < 4; ++k) {
+    float lo, hi;
+    f2_split(y.v[k], lo, hi);
+    w[k] = pack_bf16x2(lo, hi);
   }
-  const bool second = 8 * li >= half;
-  const int64_t at = (int64_t)pos * half + 8 * li - (second ? half : 0);
-  if (RF_IN(err, at + 7, n)) {
+  *reinterpret_cast<uint4*>(p + i) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, int64_t i, const Row8& y, int64_t n,
+                                       unsigned* err) {
+  if (!RF_IN(err, i + 7, n) || !RF_IN(err, i, n)) return;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(nr.cos + at) + k);
-      const float4 s = __ldg(reinterpret_cast<const float4*>(nr.sin + at) + k);
-      r.c[4 * k] = c.x;
-      r.c[4 * k + 1] = c.y;
-      r.c[4 * k + 2] = c.z;
-      r.c[4 * k + 3] = c.w;
-      r.s[4 * k] = second ? s.x : -s.x;
-      r.s[4 * k + 1] = second ? s.y : -s.y;
-      r.s[4 * k + 2] = second ? s.z : -s.z;
-      r.s[4 * k + 3] = second ? s.w : -s.w;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      r.c[e] = 1.f;
-      r.s[e] = 0.f;
-    }
+  for (int k = 0; k < 2; ++k) {
+    float4 f;
+    f2_split(y.v[2 * k], f.x, f.y);
+    f2_split(y.v[2 * k + 1], f.z, f.w);
+    reinterpret_cast<float4*>(p + i)[k] = f;
   }
-  return r;
 }
 
-// Norm weights of a lane's elements and, for the half-split rotation, of its
-// partner lane's.
-struct WeightLane {
-  float own[8], other[8];
+// A and B of a lane's eight elements.
+struct Coef {
+  uint64_t a[4], b[4];
 };
 
 // Lane of the group that holds the half-split partners of lane li's elements.
@@ -137,61 +111,106 @@ __device__ __forceinline__ int partner_lane(const NormRope& nr, int li) {
   return li < h ? li + h : li - h;
 }
 
+// weight: of queries or keys, or null.  active = false: nothing is loaded from
+// the tables.
 template <typename T, int D>
-__device__ __forceinline__ WeightLane load_weight(const NormRope& nr, const T* w, int li,
-                                                  unsigned* err) {
-  WeightLane r;
-  const Raw8<T> a = load8<T>(w, 8 * li, D, err);
+__device__ __forceinline__ Coef load_coef(const NormRope& nr, const T* weight, int pos, int li,
+                                          bool active, unsigned* err) {
+  float a[8], b[8];
+  const bool rotated = 8 * li < nr.rot;
+  const bool split = rotated && !nr.interleaved;
+  if (weight) {
+    const Raw8<T> own = load8<T>(weight, 8 * li, D, err);
+    const Raw8<T> other = load8<T>(weight, 8 * (split ? partner_lane(nr, li) : li), D, err);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r.own[e] = a.get(e);
-  if (!nr.interleaved && 8 * li < nr.rot) {
-    const Raw8<T> b = load8<T>(w, 8 * partner_lane(nr, li), D, err);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r.other[e] = b.get(e);
+    for (int e = 0; e < 8; ++e) {
+      a[e] = own.get(e);
+      b[e] = nr.interleaved ? own.get(e ^ 1) : other.get(e);
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r.other[e] = 0.f;
+    for (int e = 0; e < 8; ++e) a[e] = b[e] = 1.f;
+  }
+  float4 c[2], s[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {                    // unrotated: cos = 1, sin = 0
+    c[k] = make_float4(1.f, 1.f, 1.f, 1.f);
+    s[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const int half = nr.rot >> 1;
+  const int64_t n = (int64_t)nr.max_pos * half;
+  const bool second = split && 8 * li >= half;
+  if (rotated && active) {
+    const int64_t at =
+        (int64_t)pos * half + (nr.interleaved ? 4 * li : 8 * li - (second ? half : 0));
+    const int words = nr.interleaved ? 1 : 2;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (k < words && RF_IN(err, at + 4 * k + 3, n)) {
+        c[k] = __ldg(reinterpret_cast<const float4*>(nr.cos + at) + k);
+        s[k] = __ldg(reinterpret_cast<const float4*>(nr.sin + at) + k);
+      }
+  }
+  const float cc[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
+  const float ss[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool plus = nr.interleaved ? (e & 1) : second;
+    const float cv = nr.interleaved ? cc[e >> 1] : cc[e], sv = nr.interleaved ? ss[e >> 1] : ss[e];
+    a[e] *= cv;
+    b[e] *= plus ? sv : -sv;
+  }
+  Coef r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    r.a[k] = f2(a[2 * k], a[2 * k + 1]);
+    r.b[k] = f2(b[2 * k], b[2 * k + 1]);
   }
   return r;
 }
 
-// Norm (has_w) and rotation (nr.rot > 0) of a group's row.  Called by all 32
-// lanes of a warp together; has_w may differ between the warp's groups.
+// Norm (has_w) and rotation of a group's row.  Called by all 32 lanes of a
+// warp together; has_w may differ between the warp's groups.
 template <typename T, int D>
-__device__ __forceinline__ void norm_rope_row(const NormRope& nr, const Raw8<T>& x, bool has_w,
-                                              const WeightLane& w, const RopeLane& rp, int li,
-                                              float (&out)[8]) {
+__device__ __forceinline__ Row8 norm_rope_row(const NormRope& nr, const Raw8<T>& x, bool has_w,
+                                              const Coef& cf, int li) {
   constexpr int LG = D / 8;
   float rstd = 1.f;
   if (nr.wq || nr.wk) {                 // the same for every lane: the shuffles need all of them
-    float ss = 0.f;
+    uint64_t sq = fmul2(x.pair(0), x.pair(0));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x.get(e), x.get(e), ss);
+    for (int k = 1; k < 4; ++k) sq = ffma2(x.pair(k), x.pair(k), sq);
+    float lo, hi;
+    f2_split(sq, lo, hi);
+    float ss = lo + hi;
 #pragma unroll
     for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    rstd = rsqrtf(fmaf(ss, 1.f / D, nr.eps));
+    if (has_w) rstd = rsqrtf(fmaf(ss, 1.f / D, nr.eps));
   }
-  float y[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = has_w ? x.get(e) * rstd * w.own[e] : x.get(e);
+  // partners; zeros where nothing is rotated, since their B is 0 and x may be
+  // an infinity
   const bool rotated = 8 * li < nr.rot;
-  if (nr.rot == 0) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] = y[e];
-  } else if (nr.interleaved) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] = rotated ? fmaf(y[e ^ 1], rp.s[e], y[e] * rp.c[e]) : y[e];
-  } else {
-    Raw8<T> p;
+  Raw8<T> p;
+  if (nr.rot > 0 && !nr.interleaved) {
     const int src = rotated ? partner_lane(nr, li) : li;
 #pragma unroll
-    for (int k = 0; k < Raw8<T>::kWords; ++k) p.w[k] = __shfl_sync(0xffffffffu, x.w[k], src, LG);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float yp = has_w ? p.get(e) * rstd * w.other[e] : p.get(e);
-      out[e] = rotated ? fmaf(yp, rp.s[e], y[e] * rp.c[e]) : y[e];
+    for (int k = 0; k < Raw8<T>::kWords; ++k) {
+      const uint32_t v = __shfl_sync(0xffffffffu, x.w[k], src, LG);
+      p.w[k] = rotated ? v : 0u;
     }
+  } else {
+#pragma unroll
+    for (int k = 0; k < Raw8<T>::kWords; ++k) p.w[k] = rotated ? x.w[k] : 0u;
   }
+  const uint64_t r2 = f2(rstd, rstd);
+  Row8 y;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint64_t t = ffma2(nr.interleaved ? p.swapped(k) : p.pair(k), cf.b[k],
+                             fmul2(x.pair(k), cf.a[k]));
+    y.v[k] = fmul2(t, r2);
+  }
+  return y;
 }
 
 // Tensors of rows [T][H][D] whose tokens are ld elements apart.
@@ -225,14 +244,10 @@ __device__ __forceinline__ void norm_rope_heads(const NormRope& nr, const T* wei
       for (int k = 0; k < Raw8<T>::kWords; ++k) x[j].w[k] = 0u;
     }
   }
-  RopeLane rp = {};
-  if (active && 8 * li < nr.rot) rp = load_rope(nr, pos, li, err);
-  WeightLane w = {};
-  if (weight) w = load_weight<T, D>(nr, weight, li, err);
+  const Coef cf = load_coef<T, D>(nr, weight, pos, li, active, err);
 #pragma unroll
   for (int j = 0; j < HB; ++j) {
-    float y[8];
-    norm_rope_row<T, D>(nr, x[j], weight != nullptr, w, rp, li, y);
+    const Row8 y = norm_rope_row<T, D>(nr, x[j], weight != nullptr, cf, li);
     if (active && h0 + j < H)
       store8(out.p, (int64_t)t * out.ld + (int64_t)(h0 + j) * D + 8 * li, y, n_out, err);
   }

@@ -58,8 +58,17 @@ cudaError_t launch_qk_norm_rope(int dtype, const NormRope& nr, const void* Q, in
                                 const void* K, int64_t ldk, void* Qo, int64_t ldqo, void* Ko,
                                 int64_t ldko, const int* positions, int T, int Hq, int Hkv, int d,
                                 unsigned* err, cudaStream_t s) {
-#define RF_GO(TY, DD) \
-  return launch<TY, DD, 1>(nr, Q, ldq, K, ldk, Qo, ldqo, Ko, ldko, positions, T, Hq, Hkv, err, s)
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidValue;
+  // Four heads a lane group where that still fills the device (64 rows of heads
+  // for each group of a CTA an SM); one where it would leave SMs idle.
+  const bool many = (int64_t)T * (Hq + Hkv) >= (int64_t)sms * 64 * (kThreads * 8 / d);
+#define RF_GO(TY, DD)                                                                             \
+  return many                                                                                     \
+             ? launch<TY, DD, 4>(nr, Q, ldq, K, ldk, Qo, ldqo, Ko, ldko, positions, T, Hq, Hkv,   \
+                                 err, s)                                                          \
+             : launch<TY, DD, 1>(nr, Q, ldq, K, ldk, Qo, ldqo, Ko, ldko, positions, T, Hq, Hkv,   \
+                                 err, s)
   if (dtype == RF_BF16) {
     if (d == 64) RF_GO(__nv_bfloat16, 64);
     RF_GO(__nv_bfloat16, 128);
