@@ -30,7 +30,7 @@
 // Query rows are further CTAs of the same launch (norm_rope.cuh).
 //
 // What bounds it: memory for prompts, launch latency for a step.
-#include <stdlib.h>
+#include <algorithm>
 #include <vector>
 
 #include "norm_rope.cuh"
@@ -274,64 +274,82 @@ using bf16 = __nv_bfloat16;
 
 // ------------------------------------------------------------- rows
 
-// HB query heads of a token by a lane group of CTA `cta` of the query CTAs.
-template <int D, int HB>
+// nh query heads of a token by a lane group of CTA `cta` of the query CTAs.
+template <int D, int HB, bool kSplit>
 __device__ __forceinline__ void query_rows(const Seqs& sq, const NormRope& nr,
                                            const RowsIn<bf16>& q, const RowsOut<bf16>& qo, int Hq,
-                                           int cta, unsigned* err) {
+                                           int nh, int cta, unsigned* err) {
   constexpr int LG = D / 8;
-  const int li = threadIdx.x % LG, nblk = (Hq + HB - 1) / HB;
+  const int li = threadIdx.x % LG, nblk = (Hq + nh - 1) / nh;
   const int64_t u = (int64_t)cta * (blockDim.x / LG) + threadIdx.x / LG;
-  const int t = (int)(u / nblk), h0 = (int)(u % nblk) * HB;
+  // a warp's groups: neighbouring tokens of one block of heads
+  const int blk = (int)(u / sq.total), t = (int)(u - (int64_t)blk * sq.total), h0 = blk * nh;
   int b = 0, pos = 0;
-  const bool active = t < sq.total && find_token(sq, t, &b, &pos, err);
-  norm_rope_heads<bf16, D, HB>(nr, static_cast<const bf16*>(nr.wq), q, qo, sq.total, Hq, t, h0,
-                               pos, active, li, err);
+  const bool active = blk < nblk && find_token(sq, t, &b, &pos, err);
+  norm_rope_heads<bf16, D, HB, kSplit>(nr, static_cast<const bf16*>(nr.wq), q, qo, sq.total, Hq, t,
+                                       h0, nh, pos, active, li, err);
 }
 
-// bf16 cache: HB kv heads of a token by a lane group.
-template <int D, int HB>
+// bf16 cache: nh kv heads of a token by a lane group, HB at a time.
+template <int D, int HB, bool kSplit>
 __global__ void __launch_bounds__(kThreads)
     append_rows_kernel(const Seqs sq, const NormRope nr, const RowsIn<bf16> k, const RowsIn<bf16> v,
-                       const RowsIn<bf16> q, const RowsOut<bf16> qo, int Hq, const Cache cache,
-                       int kv_ctas, unsigned* err) {
+                       const RowsIn<bf16> q, const RowsOut<bf16> qo, int Hq, int nh, int nhq,
+                       const Cache cache, int kv_ctas, unsigned* err) {
   if ((int)blockIdx.x >= kv_ctas) {
-    query_rows<D, HB>(sq, nr, q, qo, Hq, (int)blockIdx.x - kv_ctas, err);
+    query_rows<D, HB, kSplit>(sq, nr, q, qo, Hq, nhq, (int)blockIdx.x - kv_ctas, err);
     return;
   }
   constexpr int LG = D / 8;
-  const int li = threadIdx.x % LG, nblk = (sq.Hkv + HB - 1) / HB;
+  const int li = threadIdx.x % LG, nblk = (sq.Hkv + nh - 1) / nh;
   const int64_t u = (int64_t)blockIdx.x * (kThreads / LG) + threadIdx.x / LG;
-  const int t = (int)(u / nblk), h0 = (int)(u % nblk) * HB;
+  const int blk = (int)(u / sq.total), t = (int)(u - (int64_t)blk * sq.total), h0 = blk * nh;
   int b = 0, pos = 0, phys = -1;
-  bool active = t < sq.total && find_token(sq, t, &b, &pos, err);
-  if (active) phys = find_page(sq, b, pos / sq.page_size, li == 0, err);
-  active = phys >= 0;
+  const bool known = blk < nblk && find_token(sq, t, &b, &pos, err);
+  if (known) phys = find_page(sq, b, pos / sq.page_size, li == 0, err);
+  const bool active = phys >= 0;
   const int64_t n_k = (int64_t)(sq.total - 1) * k.ld + (int64_t)sq.Hkv * D;
   const int64_t n_v = (int64_t)(sq.total - 1) * v.ld + (int64_t)sq.Hkv * D;
   const int64_t n_pages = (int64_t)sq.num_pages * sq.Hkv * sq.page_size * D;
+  const int64_t src_k = (int64_t)t * k.ld + 8 * li, src_v = (int64_t)t * v.ld + 8 * li;
+  const int64_t head = (int64_t)sq.page_size * D;              // elements of a page's head
+  const int64_t dst = (int64_t)phys * sq.Hkv * head + pos % sq.page_size * D + 8 * li;
+  const int h1 = active ? min(h0 + nh, sq.Hkv) : h0;
   Raw8<bf16> kx[HB], vx[HB];
+  auto load = [&](int h) {
 #pragma unroll
-  for (int j = 0; j < HB; ++j) {
-    kx[j] = {};
-    vx[j] = {};
-    if (active && h0 + j < sq.Hkv) {
-      kx[j] = load8<bf16>(k.p, (int64_t)t * k.ld + (int64_t)(h0 + j) * D + 8 * li, n_k, err);
-      vx[j] = load8<bf16>(v.p, (int64_t)t * v.ld + (int64_t)(h0 + j) * D + 8 * li, n_v, err);
+    for (int j = 0; j < HB; ++j) {
+      kx[j] = {};
+      vx[j] = {};
+      if (h + j < h1) {
+        kx[j] = load8<bf16>(k.p, src_k + (int64_t)(h + j) * D, n_k, err);
+        vx[j] = load8<bf16>(v.p, src_v + (int64_t)(h + j) * D, n_v, err);
+      }
     }
-  }
+  };
+  load(h0);
   const bf16* wk = static_cast<const bf16*>(nr.wk);
-  const Coef cf = load_coef<bf16, D>(nr, wk, pos, li, active, err);
+  const Coef cf = load_coef<bf16, D, kSplit>(nr, wk, pos, li, active, err);
+  const int batches = (int)__reduce_max_sync(0xffffffffu, (unsigned)(h1 - h0 + HB - 1) / HB);
+  for (int i = 0; i < batches; ++i) {
+    const int h = h0 + i * HB;
+    Raw8<bf16> kc[HB], vc[HB];
 #pragma unroll
-  for (int j = 0; j < HB; ++j) {
-    const Row8 y = norm_rope_row<bf16, D>(nr, kx[j], wk != nullptr, cf, li);
-    if (active && h0 + j < sq.Hkv) {
-      const int64_t at =
-          (((int64_t)phys * sq.Hkv + h0 + j) * sq.page_size + pos % sq.page_size) * D + 8 * li;
-      store8(reinterpret_cast<bf16*>(cache.pages[0]), at, y, n_pages, err);
-      if (RF_IN(err, at + 7, n_pages))
-        *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(cache.pages[1]) + at) =
-            make_uint4(vx[j].w[0], vx[j].w[1], vx[j].w[2], vx[j].w[3]);
+    for (int j = 0; j < HB; ++j) {
+      kc[j] = kx[j];
+      vc[j] = vx[j];
+    }
+    if (i + 1 < batches) load(h + HB);
+#pragma unroll
+    for (int j = 0; j < HB; ++j) {
+      const Row8 y = norm_rope_row<bf16, D, kSplit>(nr, kc[j], wk != nullptr, cf, li);
+      const int64_t at = dst + (h + j) * head;
+      if (h + j < h1) {
+        store8(reinterpret_cast<bf16*>(cache.pages[0]), at, y, n_pages, err);
+        if (RF_IN(err, at + 7, n_pages))
+          *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(cache.pages[1]) + at) =
+              make_uint4(vc[j].w[0], vc[j].w[1], vc[j].w[2], vc[j].w[3]);
+      }
     }
   }
   if (blockIdx.x == 0) check_seqs(sq, (int)threadIdx.x, kThreads, err);
@@ -339,13 +357,13 @@ __global__ void __launch_bounds__(kThreads)
 
 // ------------------------------------------------------------- one token a sequence
 
-template <int D>
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads)
     append_step_kernel(const Seqs sq, const NormRope nr, const RowsIn<bf16> k, const RowsIn<bf16> v,
                        const RowsIn<bf16> q, const RowsOut<bf16> qo, int Hq, const Cache cache,
                        int kv_ctas, unsigned* err) {
   if ((int)blockIdx.x >= kv_ctas) {
-    query_rows<D, 1>(sq, nr, q, qo, Hq, (int)blockIdx.x - kv_ctas, err);
+    query_rows<D, 1, kSplit>(sq, nr, q, qo, Hq, 1, (int)blockIdx.x - kv_ctas, err);
     return;
   }
   constexpr int LG = D / 8;                   // lanes of a row
@@ -365,8 +383,8 @@ __global__ void __launch_bounds__(kThreads)
     x = load8<bf16>(in.p, (int64_t)it.t0 * in.ld + (int64_t)h * D + 8 * li,
                     (int64_t)(sq.total - 1) * in.ld + (int64_t)sq.Hkv * D, err);
   const bf16* wk = static_cast<const bf16*>(nr.wk);
-  const Coef cf = load_coef<bf16, D>(nr, wk, it.pos0, li, active && !is_v, err);
-  Row8 y = norm_rope_row<bf16, D>(nr, x, wk != nullptr, cf, li);
+  const Coef cf = load_coef<bf16, D, kSplit>(nr, wk, it.pos0, li, active && !is_v, err);
+  Row8 y = norm_rope_row<bf16, D, kSplit>(nr, x, wk != nullptr, cf, li);
   if (is_v) y = as_row(x);
 
   const int64_t head = (int64_t)it.phys * sq.Hkv + h;         // (page, head)
@@ -418,13 +436,13 @@ __global__ void __launch_bounds__(kThreads)
 
 // A CTA takes the keys or the values of one (item, head): its threads cover
 // the page's rows in SW sweeps.
-template <int D, int SW>
+template <int D, int SW, bool kSplit>
 __global__ void __launch_bounds__(kThreads)
     append_prompt_kernel(const Seqs sq, const NormRope nr, const RowsIn<bf16> k,
                          const RowsIn<bf16> v, const RowsIn<bf16> q, const RowsOut<bf16> qo, int Hq,
-                         const Cache cache, int kv_ctas, unsigned* err) {
+                         int nhq, const Cache cache, int kv_ctas, unsigned* err) {
   if ((int)blockIdx.x >= kv_ctas) {
-    query_rows<D, 4>(sq, nr, q, qo, Hq, (int)blockIdx.x - kv_ctas, err);
+    query_rows<D, 4, kSplit>(sq, nr, q, qo, Hq, nhq, (int)blockIdx.x - kv_ctas, err);
     return;
   }
   constexpr int LG = D / 8;
@@ -479,8 +497,8 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < SW; ++i) {
       const int t = r + i * rows;
-      const Coef cf = load_coef<bf16, D>(nr, wk, it.pos0 + t, li, t < it.n, err);
-      y[i] = norm_rope_row<bf16, D>(nr, raw[i], wk != nullptr, cf, li);
+      const Coef cf = load_coef<bf16, D, kSplit>(nr, wk, it.pos0 + t, li, t < it.n, err);
+      y[i] = norm_rope_row<bf16, D, kSplit>(nr, raw[i], wk != nullptr, cf, li);
       if (t < it.n) a = fmaxf(a, absmax8(y[i]));
     }
   }
@@ -511,38 +529,42 @@ __global__ void __launch_bounds__(kThreads)
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <int D>
+template <int D, bool kSplit>
 cudaError_t launch(const Seqs& sq, const NormRope& nr, const RowsIn<bf16>& k,
                    const RowsIn<bf16>& v, const RowsIn<bf16>& q, const RowsOut<bf16>& qo, int Hq,
                    const Cache& cache, bool f8, int sms, unsigned* err, cudaStream_t s) {
   constexpr int LG = D / 8, per = kThreads / LG;      // lane groups of a CTA
   if (!f8) {
-    // four heads a lane group where that still fills the device
-    const bool many = (int64_t)sq.total * sq.Hkv >= (int64_t)sms * 64 * per;
-    const int hb = many ? 4 : 1;
-    const int64_t kv = ceil_div((int64_t)sq.total * ceil_div(sq.Hkv, hb), per);
-    const int64_t q_ctas = ceil_div((int64_t)sq.total * ceil_div(Hq, hb), per);
+    // keys and values count twice, since a row of both is worked on together
+    const int nh = heads_per_group((int64_t)sq.total * sq.Hkv * 2, sq.Hkv, D, sms);
+    const int nhq = nh == 1 ? 1 : std::max(4, heads_per_group((int64_t)sq.total * Hq, Hq, D, sms));
+    const int64_t kv = ceil_div((int64_t)sq.total * ceil_div(sq.Hkv, nh), per);
+    const int64_t q_ctas = ceil_div((int64_t)sq.total * ceil_div(Hq, nhq), per);
     const unsigned grid = (unsigned)(kv + q_ctas);
-    if (many)
-      append_rows_kernel<D, 4><<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq, cache, (int)kv, err);
+    if (nh > 1)
+      append_rows_kernel<D, 4, kSplit><<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq, nh, nhq,
+                                                                 cache, (int)kv, err);
     else
-      append_rows_kernel<D, 1><<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq, cache, (int)kv, err);
+      append_rows_kernel<D, 1, kSplit><<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq, nh, nhq,
+                                                                 cache, (int)kv, err);
     return cudaGetLastError();
   }
   if (!sq.cu && sq.n_uniform == 1) {
     const int64_t kv = ceil_div((int64_t)sq.B * sq.Hkv, kThreads / (2 * LG));
     const int64_t q_ctas = ceil_div((int64_t)sq.total * Hq, per);
-    append_step_kernel<D><<<(unsigned)(kv + q_ctas), kThreads, 0, s>>>(
+    append_step_kernel<D, kSplit><<<(unsigned)(kv + q_ctas), kThreads, 0, s>>>(
         sq, nr, k, v, q, qo, Hq, cache, (int)kv, err);
     return cudaGetLastError();
   }
   const int pieces = sq.page_size * D / 8, threads = pieces < kThreads ? pieces : kThreads;
   const int64_t items = num_items(sq.total, sq.B, sq.n_uniform, sq.cu != nullptr, sq.page_size);
+  const int nhq = std::max(4, heads_per_group((int64_t)sq.total * Hq, Hq, D, sms));
   const int64_t kv = items * sq.Hkv * 2;
-  const int64_t q_ctas = ceil_div((int64_t)sq.total * ceil_div(Hq, 4), threads / LG);
+  const int64_t q_ctas = ceil_div((int64_t)sq.total * ceil_div(Hq, nhq), threads / LG);
   const unsigned grid = (unsigned)(kv + q_ctas);
-#define RF_GO(SW) \
-  append_prompt_kernel<D, SW><<<grid, threads, 0, s>>>(sq, nr, k, v, q, qo, Hq, cache, (int)kv, err)
+#define RF_GO(SW)                                                                                 \
+  append_prompt_kernel<D, SW, kSplit><<<grid, threads, 0, s>>>(sq, nr, k, v, q, qo, Hq, nhq, cache, \
+                                                               (int)kv, err)
   switch (pieces / threads) {
     case 1: RF_GO(1); break;
     case 2: RF_GO(2); break;
@@ -589,8 +611,12 @@ cudaError_t launch_kv_append_paged(const PagedKV& c, const NormRope& nr, const v
   const bool f8 = c.dtype == RF_E4M3;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidValue;
-  return c.d == 64 ? launch<64>(sq, nr, k, v, q, qo, Hq, cache, f8, sms, err, s)
-                   : launch<128>(sq, nr, k, v, q, qo, Hq, cache, f8, sms, err, s);
+  const bool split = is_split(nr);
+  if (c.d == 64)
+    return split ? launch<64, true>(sq, nr, k, v, q, qo, Hq, cache, f8, sms, err, s)
+                 : launch<64, false>(sq, nr, k, v, q, qo, Hq, cache, f8, sms, err, s);
+  return split ? launch<128, true>(sq, nr, k, v, q, qo, Hq, cache, f8, sms, err, s)
+               : launch<128, false>(sq, nr, k, v, q, qo, Hq, cache, f8, sms, err, s);
 }
 
 // Host-side walk of the items (the functions above, shared by host and

@@ -100,7 +100,7 @@ __device__ __forceinline__ void store8(float* p, int64_t i, const Row8& y, int64
   }
 }
 
-// A and B of a lane's eight elements.
+// A and B of a lane's eight elements, in packed pairs.
 struct Coef {
   uint64_t a[4], b[4];
 };
@@ -111,67 +111,60 @@ __device__ __forceinline__ int partner_lane(const NormRope& nr, int li) {
   return li < h ? li + h : li - h;
 }
 
+// kSplit: half-split rotation (partners in another lane); else interleaved, or
+// no rotation at all.
+__host__ __forceinline__ bool is_split(const NormRope& nr) { return nr.rot > 0 && !nr.interleaved; }
+
 // weight: of queries or keys, or null.  active = false: nothing is loaded from
 // the tables.
-template <typename T, int D>
+template <typename T, int D, bool kSplit>
 __device__ __forceinline__ Coef load_coef(const NormRope& nr, const T* weight, int pos, int li,
                                           bool active, unsigned* err) {
-  float a[8], b[8];
   const bool rotated = 8 * li < nr.rot;
-  const bool split = rotated && !nr.interleaved;
-  if (weight) {
-    const Raw8<T> own = load8<T>(weight, 8 * li, D, err);
-    const Raw8<T> other = load8<T>(weight, 8 * (split ? partner_lane(nr, li) : li), D, err);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      a[e] = own.get(e);
-      b[e] = nr.interleaved ? own.get(e ^ 1) : other.get(e);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = b[e] = 1.f;
-  }
+  const int half = nr.rot >> 1;
+  const int64_t n = (int64_t)nr.max_pos * half;
+  const bool second = kSplit && 8 * li >= half;
   float4 c[2], s[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {                    // unrotated: cos = 1, sin = 0
     c[k] = make_float4(1.f, 1.f, 1.f, 1.f);
     s[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const int half = nr.rot >> 1;
-  const int64_t n = (int64_t)nr.max_pos * half;
-  const bool second = split && 8 * li >= half;
   if (rotated && active) {
-    const int64_t at =
-        (int64_t)pos * half + (nr.interleaved ? 4 * li : 8 * li - (second ? half : 0));
-    const int words = nr.interleaved ? 1 : 2;
+    const int64_t at = (int64_t)pos * half + (kSplit ? 8 * li - (second ? half : 0) : 4 * li);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (k < words && RF_IN(err, at + 4 * k + 3, n)) {
+    for (int k = 0; k < (kSplit ? 2 : 1); ++k)
+      if (RF_IN(err, at + 4 * k + 3, n)) {
         c[k] = __ldg(reinterpret_cast<const float4*>(nr.cos + at) + k);
         s[k] = __ldg(reinterpret_cast<const float4*>(nr.sin + at) + k);
       }
   }
   const float cc[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
   const float ss[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const bool plus = nr.interleaved ? (e & 1) : second;
-    const float cv = nr.interleaved ? cc[e >> 1] : cc[e], sv = nr.interleaved ? ss[e >> 1] : ss[e];
-    a[e] *= cv;
-    b[e] *= plus ? sv : -sv;
-  }
+  const float sign = second ? 1.f : -1.f;
+  const uint64_t sign2 = f2(sign, sign);
   Coef r;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    r.a[k] = f2(a[2 * k], a[2 * k + 1]);
-    r.b[k] = f2(b[2 * k], b[2 * k + 1]);
+    r.a[k] = kSplit ? f2(cc[2 * k], cc[2 * k + 1]) : f2(cc[k], cc[k]);
+    r.b[k] = kSplit ? fmul2(f2(ss[2 * k], ss[2 * k + 1]), sign2) : f2(-ss[k], ss[k]);
+  }
+  if (weight) {
+    const Raw8<T> own = load8<T>(weight, 8 * li, D, err);
+    const Raw8<T> other =
+        kSplit ? load8<T>(weight, 8 * (rotated ? partner_lane(nr, li) : li), D, err) : own;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      r.a[k] = fmul2(r.a[k], own.pair(k));
+      r.b[k] = fmul2(r.b[k], kSplit ? other.pair(k) : own.swapped(k));
+    }
   }
   return r;
 }
 
 // Norm (has_w) and rotation of a group's row.  Called by all 32 lanes of a
 // warp together; has_w may differ between the warp's groups.
-template <typename T, int D>
+template <typename T, int D, bool kSplit>
 __device__ __forceinline__ Row8 norm_rope_row(const NormRope& nr, const Raw8<T>& x, bool has_w,
                                               const Coef& cf, int li) {
   constexpr int LG = D / 8;
@@ -190,24 +183,19 @@ __device__ __forceinline__ Row8 norm_rope_row(const NormRope& nr, const Raw8<T>&
   // partners; zeros where nothing is rotated, since their B is 0 and x may be
   // an infinity
   const bool rotated = 8 * li < nr.rot;
+  const int src = kSplit && rotated ? partner_lane(nr, li) : li;
   Raw8<T> p;
-  if (nr.rot > 0 && !nr.interleaved) {
-    const int src = rotated ? partner_lane(nr, li) : li;
 #pragma unroll
-    for (int k = 0; k < Raw8<T>::kWords; ++k) {
-      const uint32_t v = __shfl_sync(0xffffffffu, x.w[k], src, LG);
-      p.w[k] = rotated ? v : 0u;
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < Raw8<T>::kWords; ++k) p.w[k] = rotated ? x.w[k] : 0u;
+  for (int k = 0; k < Raw8<T>::kWords; ++k) {
+    const uint32_t v = kSplit ? __shfl_sync(0xffffffffu, x.w[k], src, LG) : x.w[k];
+    p.w[k] = rotated ? v : 0u;
   }
   const uint64_t r2 = f2(rstd, rstd);
   Row8 y;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint64_t t = ffma2(nr.interleaved ? p.swapped(k) : p.pair(k), cf.b[k],
-                             fmul2(x.pair(k), cf.a[k]));
+    const uint64_t t =
+        ffma2(kSplit ? p.pair(k) : p.swapped(k), cf.b[k], fmul2(x.pair(k), cf.a[k]));
     y.v[k] = fmul2(t, r2);
   }
   return y;
@@ -225,31 +213,51 @@ struct RowsOut {
   int64_t ld;
 };
 
-// Heads [h0, h0 + HB) (those below H) of token t at position pos, by one lane
-// group: loads of all HB heads first, so that each lane has HB loads in flight.
-template <typename T, int D, int HB>
+// How many heads a lane group takes one after the other: as many of 4, 8, 16
+// ... as leave 1024 threads an SM (more heads share a token's A and B, but a
+// device must be full), one where even four would not.  `rows`: tokens x heads.
+inline int heads_per_group(int64_t rows, int heads, int d, int sms) {
+  const int64_t threads = rows * (d / 8);
+  int h = 1;
+  for (int k = 4; k < 2 * heads && threads / k >= 1024 * (int64_t)sms; k *= 2) h = k;
+  return h;
+}
+
+// Heads [h0, min(h0 + nh, H)) of token t at position pos, by one lane group, in
+// batches of HB: a batch's loads go together, and the next batch's before the
+// present one is worked on.  nh: the same for the whole launch, HB divides it.
+template <typename T, int D, int HB, bool kSplit>
 __device__ __forceinline__ void norm_rope_heads(const NormRope& nr, const T* weight,
                                                 const RowsIn<T>& in, const RowsOut<T>& out, int T_,
-                                                int H, int t, int h0, int pos, bool active,
+                                                int H, int t, int h0, int nh, int pos, bool active,
                                                 int li, unsigned* err) {
   const int64_t n_in = (int64_t)(T_ - 1) * in.ld + (int64_t)H * D;
   const int64_t n_out = (int64_t)(T_ - 1) * out.ld + (int64_t)H * D;
+  const int64_t src = (int64_t)t * in.ld + 8 * li, dst = (int64_t)t * out.ld + 8 * li;
+  const int h1 = active ? min(h0 + nh, H) : h0;
   Raw8<T> x[HB];
+  auto load = [&](int h) {
 #pragma unroll
-  for (int j = 0; j < HB; ++j) {
-    if (active && h0 + j < H) {
-      x[j] = load8<T>(in.p, (int64_t)t * in.ld + (int64_t)(h0 + j) * D + 8 * li, n_in, err);
-    } else {
-#pragma unroll
-      for (int k = 0; k < Raw8<T>::kWords; ++k) x[j].w[k] = 0u;
+    for (int j = 0; j < HB; ++j) {
+      x[j] = {};
+      if (h + j < h1) x[j] = load8<T>(in.p, src + (int64_t)(h + j) * D, n_in, err);
     }
-  }
-  const Coef cf = load_coef<T, D>(nr, weight, pos, li, active, err);
+  };
+  load(h0);
+  const Coef cf = load_coef<T, D, kSplit>(nr, weight, pos, li, active, err);
+  // groups of a warp may have fewer heads than others: the shuffles need all
+  const int batches = (int)__reduce_max_sync(0xffffffffu, (unsigned)(h1 - h0 + HB - 1) / HB);
+  for (int i = 0; i < batches; ++i) {
+    const int h = h0 + i * HB;
+    Raw8<T> now[HB];
 #pragma unroll
-  for (int j = 0; j < HB; ++j) {
-    const Row8 y = norm_rope_row<T, D>(nr, x[j], weight != nullptr, cf, li);
-    if (active && h0 + j < H)
-      store8(out.p, (int64_t)t * out.ld + (int64_t)(h0 + j) * D + 8 * li, y, n_out, err);
+    for (int j = 0; j < HB; ++j) now[j] = x[j];
+    if (i + 1 < batches) load(h + HB);
+#pragma unroll
+    for (int j = 0; j < HB; ++j) {
+      const Row8 y = norm_rope_row<T, D, kSplit>(nr, now[j], weight != nullptr, cf, li);
+      if (h + j < h1) store8(out.p, dst + (int64_t)(h + j) * D, y, n_out, err);
+    }
   }
 }
 
