@@ -23,10 +23,9 @@
 //  - step kernel (one new token a sequence): one lane group for the key row
 //    and one for the value row of an (item, head); a page that has to be
 //    rescaled is rescaled by the whole warp.
-//  - prompt kernel: a CTA takes a few heads of an item, one after the other,
-//    each thread four 16-byte pieces of the page's keys and values; they stay
-//    in registers between the absmax and the quantisation, so each is read
-//    once, and the next head's are on their way meanwhile.
+//  - prompt kernel: CTAs that stay, each with an equal share of the (item, head)
+//    pairs; a head's new rows are held in registers between the absmax and the
+//    quantisation, so each is read once.
 // Query rows are further CTAs of the same launch (norm_rope.cuh).
 //
 // What bounds it: memory for prompts, launch latency for a step.
@@ -82,20 +81,40 @@ __device__ __forceinline__ uint4 rescale16(uint4 w, float ratio) {
 }
 
 // Largest finite magnitude of eight values (infinities saturate and NaN keeps
-// its code: neither sets the scale).  fmaxf passes over NaN; where an infinity
-// is the largest, the others are looked at again.
+// its code: neither sets the scale).  max passes over NaN; where an infinity is
+// the largest, the others are looked at again.
 __device__ __forceinline__ float absmax8(const Row8& y) {
   float v[8], a = 0.f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) f2_split(y.v[k], v[2 * k], v[2 * k + 1]);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(v[e]));
+  for (int k = 0; k < 4; ++k) a = fmax3(a, fabsf(v[2 * k]), fabsf(v[2 * k + 1]));
   if (a == INFINITY) {
     a = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) a = fabsf(v[e]) < INFINITY ? fmaxf(a, fabsf(v[e])) : a;
   }
   return a;
+}
+// The same of eight bf16 as loaded: magnitudes compare as whole numbers.
+__device__ __forceinline__ float absmax8(const Raw8<__nv_bfloat16>& x) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = x.w[k] & 0x7FFF7FFFu;
+    asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
+  }
+  uint32_t a = max(m & 0xFFFFu, m >> 16);
+  if (a >= 0x7F80u) {
+    a = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t lo = x.w[k] & 0x7FFFu, hi = (x.w[k] >> 16) & 0x7FFFu;
+      if (lo < 0x7F80u) a = max(a, lo);
+      if (hi < 0x7F80u) a = max(a, hi);
+    }
+  }
+  return __uint_as_float(a << 16);
 }
 __device__ __forceinline__ Row8 as_row(const Raw8<__nv_bfloat16>& x) {
   Row8 y;
@@ -434,96 +453,148 @@ __global__ void __launch_bounds__(kThreads)
 
 // ------------------------------------------------------------- prompts
 
-// A CTA takes the keys or the values of one (item, head): its threads cover
-// the page's rows in SW sweeps.
-template <int D, int SW, bool kSplit>
-__global__ void __launch_bounds__(kThreads)
+// The units (item, head), items outermost, are shared out evenly over the kv
+// CTAs, as many as run at once.  A CTA's threads cover the page's rows in SW
+// sweeps, keys and values together.  An item is looked up once, and its tokens'
+// A and B are made once and kept in shared memory, a place of its own for each
+// thread (page_size * D * 8 bytes).  TH, the most threads, is 512 with 64
+// registers, so that two CTAs share an SM: one works while the other waits.
+// Pages of 128 x 128 take 1024 threads, since four sweeps of 512 spill (45
+// against 24 us for 8192 tokens of 8 heads).  The next head's keys are fetched
+// as soon as the present ones are in their final form, its values when the
+// present ones are stored.
+template <int D, int SW, int TH, bool kSplit>
+__global__ void __launch_bounds__(TH, 1024 / TH)
     append_prompt_kernel(const Seqs sq, const NormRope nr, const RowsIn<bf16> k,
                          const RowsIn<bf16> v, const RowsIn<bf16> q, const RowsOut<bf16> qo, int Hq,
-                         int nhq, const Cache cache, int kv_ctas, unsigned* err) {
+                         int nhq, const Cache cache, int units, int kv_ctas, unsigned* err) {
   if ((int)blockIdx.x >= kv_ctas) {
-    query_rows<D, 4, kSplit>(sq, nr, q, qo, Hq, nhq, (int)blockIdx.x - kv_ctas, err);
+    query_rows<D, 2, kSplit>(sq, nr, q, qo, Hq, nhq, (int)blockIdx.x - kv_ctas, err);
     return;
   }
   constexpr int LG = D / 8;
+  extern __shared__ uint4 coefs[];                   // [SW][4][threads]
   const int rows = (int)blockDim.x / LG;             // of a sweep
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int li = threadIdx.x % LG, r = threadIdx.x / LG;
-  const int x = (int)blockIdx.x / (2 * sq.Hkv), y_ = (int)blockIdx.x - x * 2 * sq.Hkv;
-  const int h = y_ >> 1;
-  const bool is_v = y_ & 1;
-  // the sequences are looked through in parallel; one thread finds the item
-  __shared__ Item found;
-  if (threadIdx.x == 0) found.n = 0;
-  __syncthreads();
-  for (int b = threadIdx.x; b < sq.B; b += blockDim.x) {
-    int pg;
-    if (item_is_of(sq, x, b, &pg, err)) {
-      const Item i = item_of(sq, b, pg, y_ == 0, err);
-      if (i.n > 0) found = i;
-    }
-  }
-  if (blockIdx.x == 0) check_seqs(sq, (int)threadIdx.x, (int)blockDim.x, err);
-  __syncthreads();
-  const Item it = found;
-  if (it.n == 0) return;
-
-  const RowsIn<bf16>& in = is_v ? v : k;
-  const int64_t n_in = (int64_t)(sq.total - 1) * in.ld + (int64_t)sq.Hkv * D;
+  const int u0 = (int)((int64_t)blockIdx.x * units / kv_ctas);
+  const int u1 = (int)((int64_t)(blockIdx.x + 1) * units / kv_ctas);
+  const int64_t n_k = (int64_t)(sq.total - 1) * k.ld + (int64_t)sq.Hkv * D;
+  const int64_t n_v = (int64_t)(sq.total - 1) * v.ld + (int64_t)sq.Hkv * D;
   const int64_t n_pages = (int64_t)sq.num_pages * sq.Hkv * sq.page_size * D;
   const int64_t n_sc = (int64_t)sq.num_pages * sq.Hkv;
-  Raw8<bf16> raw[SW];
-#pragma unroll
-  for (int i = 0; i < SW; ++i) {
-    const int t = r + i * rows;
-    raw[i] = {};
-    if (t < it.n)
-      raw[i] = load8<bf16>(in.p, (int64_t)(it.t0 + t) * in.ld + (int64_t)h * D + 8 * li, n_in, err);
-  }
-  float* sc = is_v ? cache.scale[1] : cache.scale[0];
-  uint8_t* pages = is_v ? cache.pages[1] : cache.pages[0];
-  const int64_t head = (int64_t)it.phys * sq.Hkv + h;
-  const float s_old = it.off > 0 && RF_IN(err, head, n_sc) ? sc[head] : 0.f;
+  const bool has_w = nr.wk != nullptr;
+  __shared__ Item found;
+  __shared__ float red[2][2][TH / 32];               // of two heads in turn: one barrier a head
+  if (blockIdx.x == 0) check_seqs(sq, (int)threadIdx.x, (int)blockDim.x, err);
 
-  Row8 y[SW];
-  float a = 0.f;
-  if (is_v) {
-#pragma unroll
-    for (int i = 0; i < SW; ++i) {
-      y[i] = as_row(raw[i]);                         // rows beyond the item's are zeros
-      a = fmaxf(a, absmax8(y[i]));
+  int x = u0 / sq.Hkv, h = u0 - x * sq.Hkv, turn = 0;
+  for (int u = u0; u < u1; ++x, h = 0) {             // items
+    const int h_end = min(sq.Hkv, h + (u1 - u));
+    u += h_end - h;
+    // the sequences are looked through in parallel; one thread finds the item
+    if (threadIdx.x == 0) found.n = 0;
+    __syncthreads();
+    for (int b = threadIdx.x; b < sq.B; b += blockDim.x) {
+      int pg;
+      if (item_is_of(sq, x, b, &pg, err)) {
+        const Item i = item_of(sq, b, pg, h == 0, err);
+        if (i.n > 0) found = i;
+      }
     }
-  } else {
-    const bf16* wk = static_cast<const bf16*>(nr.wk);
+    __syncthreads();
+    const Item it = found;
+    __syncthreads();                                 // before the next item's search
+    if (it.n == 0) continue;
+
+    int64_t at_k = (int64_t)(it.t0 + r) * k.ld + (int64_t)h * D + 8 * li;
+    int64_t at_v = (int64_t)(it.t0 + r) * v.ld + (int64_t)h * D + 8 * li;
+    Raw8<bf16> kx[SW], vx[SW];                       // rows beyond the item's are zeros
+    auto load = [&](Raw8<bf16>(&to)[SW], const RowsIn<bf16>& in, int64_t& at, int64_t n) {
 #pragma unroll
-    for (int i = 0; i < SW; ++i) {
-      const int t = r + i * rows;
-      const Coef cf = load_coef<bf16, D, kSplit>(nr, wk, it.pos0 + t, li, t < it.n, err);
-      y[i] = norm_rope_row<bf16, D, kSplit>(nr, raw[i], wk != nullptr, cf, li);
-      if (t < it.n) a = fmaxf(a, absmax8(y[i]));
+      for (int i = 0; i < SW; ++i) {
+        to[i] = {};
+        if (r + i * rows < it.n) to[i] = load8<bf16>(in.p, at + i * rows * in.ld, n, err);
+      }
+      at += D;
+    };
+    load(kx, k, at_k, n_k);
+    load(vx, v, at_v, n_v);
+    {
+      const CoefSource<bf16, D, kSplit> source(nr, static_cast<const bf16*>(nr.wk), li, err);
+#pragma unroll
+      for (int i = 0; i < SW; ++i) {
+        const int t = r + i * rows;
+        const Coef cf = source.get(nr, it.pos0 + t, li, t < it.n, err);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          ulonglong2* at =
+              reinterpret_cast<ulonglong2*>(coefs + (4 * i + j) * blockDim.x + threadIdx.x);
+          at[0] = make_ulonglong2(cf.a[2 * j], cf.a[2 * j + 1]);
+          at[2 * blockDim.x] = make_ulonglong2(cf.b[2 * j], cf.b[2 * j + 1]);
+        }
+      }
     }
-  }
-  __shared__ float red[kThreads / 32];
-  a = warp_max(a);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
-  __syncthreads();                       // after it, too: everyone has read the old scale
-  const int lane = threadIdx.x & 31;
-  a = warp_max(lane < (int)blockDim.x / 32 ? red[lane] : 0.f);
-  const float s = new_scale(a, s_old, it.off);
-  if (threadIdx.x == 0 && RF_IN(err, head, n_sc)) sc[head] = s;
-  const int64_t base = head * sq.page_size * D;
-  if (it.off > 0 && s > s_old) {
-    const float ratio = s_old / s;
-    uint4* pg = reinterpret_cast<uint4*>(pages + base);
-    for (int i = threadIdx.x; i < it.off * D / 16; i += blockDim.x)
-      if (RF_IN(err, base + 16 * i + 15, n_pages)) pg[i] = rescale16(pg[i], ratio);
-  }
-  const float inv = 1.f / s;
+    int64_t head = (int64_t)it.phys * sq.Hkv + h;
+    for (; h < h_end; ++h, ++head, turn ^= 1) {
+      float s_old[2] = {0.f, 0.f};
+      if (it.off > 0 && RF_IN(err, head, n_sc)) {
+        s_old[0] = cache.scale[0][head];
+        s_old[1] = cache.scale[1][head];
+      }
+      Row8 ky[SW];
+      float a[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < SW; ++i) {
-    const int t = r + i * rows;
-    const int64_t at = base + (int64_t)(it.off + t) * D + 8 * li;
-    if (t < it.n && RF_IN(err, at + 7, n_pages))
-      *reinterpret_cast<uint2*>(pages + at) = quantise8(y[i], inv);
+      for (int i = 0; i < SW; ++i) {
+        Coef cf;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const ulonglong2* at =
+              reinterpret_cast<const ulonglong2*>(coefs + (4 * i + j) * blockDim.x + threadIdx.x);
+          const ulonglong2 ca = at[0], cb = at[2 * blockDim.x];
+          cf.a[2 * j] = ca.x;
+          cf.a[2 * j + 1] = ca.y;
+          cf.b[2 * j] = cb.x;
+          cf.b[2 * j + 1] = cb.y;
+        }
+        ky[i] = norm_rope_row<bf16, D, kSplit>(nr, kx[i], has_w, cf, li);
+        if (r + i * rows < it.n) a[0] = fmaxf(a[0], absmax8(ky[i]));
+      }
+      if (h + 1 < h_end) load(kx, k, at_k, n_k);
+#pragma unroll
+      for (int i = 0; i < SW; ++i) a[1] = fmaxf(a[1], absmax8(vx[i]));
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        a[w] = warp_max(a[w]);
+        if (lane == 0) red[turn][w][warp] = a[w];
+      }
+      __syncthreads();                   // after it, too: everyone has read the old scales
+      const int64_t base = head * sq.page_size * D;
+      float inv[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const float m = warp_max(lane < (int)blockDim.x / 32 ? red[turn][w][lane] : 0.f);
+        const float s = new_scale(m, s_old[w], it.off);
+        inv[w] = 1.f / s;
+        if (threadIdx.x == 0 && RF_IN(err, head, n_sc)) cache.scale[w][head] = s;
+        if (it.off > 0 && s > s_old[w]) {
+          const float ratio = s_old[w] / s;
+          uint4* pg = reinterpret_cast<uint4*>(cache.pages[w] + base);
+          for (int i = threadIdx.x; i < it.off * D / 16; i += blockDim.x)
+            if (RF_IN(err, base + 16 * i + 15, n_pages)) pg[i] = rescale16(pg[i], ratio);
+        }
+      }
+      const int64_t at0 = base + (int64_t)(it.off + r) * D + 8 * li;
+#pragma unroll
+      for (int i = 0; i < SW; ++i) {
+        const int64_t at = at0 + i * rows * D;
+        if (r + i * rows < it.n && RF_IN(err, at + 7, n_pages)) {
+          *reinterpret_cast<uint2*>(cache.pages[0] + at) = quantise8(ky[i], inv[0]);
+          *reinterpret_cast<uint2*>(cache.pages[1] + at) = quantise8(as_row(vx[i]), inv[1]);
+        }
+      }
+      if (h + 1 < h_end) load(vx, v, at_v, n_v);
+    }
   }
 }
 
@@ -556,21 +627,27 @@ cudaError_t launch(const Seqs& sq, const NormRope& nr, const RowsIn<bf16>& k,
         sq, nr, k, v, q, qo, Hq, cache, (int)kv, err);
     return cudaGetLastError();
   }
-  const int pieces = sq.page_size * D / 8, threads = pieces < kThreads ? pieces : kThreads;
+  const int pieces = sq.page_size * D / 8;
+  const int threads = pieces <= 512 ? pieces : (pieces <= 1024 ? 512 : 1024);
   const int64_t items = num_items(sq.total, sq.B, sq.n_uniform, sq.cu != nullptr, sq.page_size);
   const int nhq = std::max(4, heads_per_group((int64_t)sq.total * Hq, Hq, D, sms));
-  const int64_t kv = items * sq.Hkv * 2;
+  const int64_t units = items * sq.Hkv;
+  const int64_t kv = std::min(units, (int64_t)sms * 1024 / threads);
   const int64_t q_ctas = ceil_div((int64_t)sq.total * ceil_div(Hq, nhq), threads / LG);
   const unsigned grid = (unsigned)(kv + q_ctas);
-#define RF_GO(SW)                                                                                 \
-  append_prompt_kernel<D, SW, kSplit><<<grid, threads, 0, s>>>(sq, nr, k, v, q, qo, Hq, nhq, cache, \
-                                                               (int)kv, err)
-  switch (pieces / threads) {
-    case 1: RF_GO(1); break;
-    case 2: RF_GO(2); break;
-    case 4: RF_GO(4); break;
-    default: RF_GO(D / 16); break;       // 8 at D = 128; at D = 64 four are the most
-  }
+  const int smem = pieces * 64;
+#define RF_GO(SW, TH)                                                                              \
+  do {                                                                                             \
+    auto kern = append_prompt_kernel<D, SW, TH, kSplit>;                                           \
+    const cudaError_t e =                                                                          \
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);             \
+    if (e != cudaSuccess) return e;                                                                \
+    kern<<<grid, threads, smem, s>>>(sq, nr, k, v, q, qo, Hq, nhq, cache, (int)units, (int)kv,     \
+                                   err);                                                           \
+  } while (0)
+  if (pieces <= 512) RF_GO(1, 512);
+  else if (pieces <= 1024) RF_GO(2, 512);
+  else RF_GO(2, (D == 128 ? 1024 : 512));          // 128 x 128
 #undef RF_GO
   return cudaGetLastError();
 }
@@ -595,7 +672,7 @@ Seqs make_seqs(const PagedKV& c, const int* cu, int total, int max_pos) {
 }  // namespace
 
 int64_t append_grid_bound(int total, int B, bool has_cu, int page_size, int Hkv, int Hq) {
-  return num_items(total, B, has_cu ? 0 : total / B, has_cu, page_size) * Hkv * 2 +
+  return num_items(total, B, has_cu ? 0 : total / B, has_cu, page_size) * Hkv +
          (int64_t)total * ((int64_t)Hkv + Hq);
 }
 

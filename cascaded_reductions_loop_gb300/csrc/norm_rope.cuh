@@ -115,51 +115,62 @@ __device__ __forceinline__ int partner_lane(const NormRope& nr, int li) {
 // no rotation at all.
 __host__ __forceinline__ bool is_split(const NormRope& nr) { return nr.rot > 0 && !nr.interleaved; }
 
-// weight: of queries or keys, or null.  active = false: nothing is loaded from
-// the tables.
+// Where a lane's coefficients come from: the weights of queries or of keys (or
+// null), held as loaded, and the tables.
+template <typename T, int D, bool kSplit>
+struct CoefSource {
+  Raw8<T> own, other;
+  bool has_w;
+  __device__ __forceinline__ CoefSource(const NormRope& nr, const T* weight, int li, unsigned* err)
+      : own{}, other{}, has_w(weight != nullptr) {
+    if (!weight) return;
+    own = load8<T>(weight, 8 * li, D, err);
+    other = own;
+    if (kSplit && 8 * li < nr.rot) other = load8<T>(weight, 8 * partner_lane(nr, li), D, err);
+  }
+  // active = false: nothing is loaded from the tables.
+  __device__ __forceinline__ Coef get(const NormRope& nr, int pos, int li, bool active,
+                                      unsigned* err) const {
+    const int half = nr.rot >> 1;
+    const int64_t n = (int64_t)nr.max_pos * half;
+    const bool second = kSplit && 8 * li >= half;
+    float4 c[2], s[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {                  // unrotated: cos = 1, sin = 0
+      c[k] = make_float4(1.f, 1.f, 1.f, 1.f);
+      s[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (8 * li < nr.rot && active) {
+      const int64_t at = (int64_t)pos * half + (kSplit ? 8 * li - (second ? half : 0) : 4 * li);
+#pragma unroll
+      for (int k = 0; k < (kSplit ? 2 : 1); ++k)
+        if (RF_IN(err, at + 4 * k + 3, n)) {
+          c[k] = __ldg(reinterpret_cast<const float4*>(nr.cos + at) + k);
+          s[k] = __ldg(reinterpret_cast<const float4*>(nr.sin + at) + k);
+        }
+    }
+    const float cc[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
+    const float ss[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
+    const float sign = second ? 1.f : -1.f;
+    const uint64_t sign2 = f2(sign, sign);
+    Coef r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      r.a[k] = kSplit ? f2(cc[2 * k], cc[2 * k + 1]) : f2(cc[k], cc[k]);
+      r.b[k] = kSplit ? fmul2(f2(ss[2 * k], ss[2 * k + 1]), sign2) : f2(-ss[k], ss[k]);
+      if (has_w) {
+        r.a[k] = fmul2(r.a[k], own.pair(k));
+        r.b[k] = fmul2(r.b[k], kSplit ? other.pair(k) : own.swapped(k));
+      }
+    }
+    return r;
+  }
+};
+
 template <typename T, int D, bool kSplit>
 __device__ __forceinline__ Coef load_coef(const NormRope& nr, const T* weight, int pos, int li,
                                           bool active, unsigned* err) {
-  const bool rotated = 8 * li < nr.rot;
-  const int half = nr.rot >> 1;
-  const int64_t n = (int64_t)nr.max_pos * half;
-  const bool second = kSplit && 8 * li >= half;
-  float4 c[2], s[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {                    // unrotated: cos = 1, sin = 0
-    c[k] = make_float4(1.f, 1.f, 1.f, 1.f);
-    s[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  if (rotated && active) {
-    const int64_t at = (int64_t)pos * half + (kSplit ? 8 * li - (second ? half : 0) : 4 * li);
-#pragma unroll
-    for (int k = 0; k < (kSplit ? 2 : 1); ++k)
-      if (RF_IN(err, at + 4 * k + 3, n)) {
-        c[k] = __ldg(reinterpret_cast<const float4*>(nr.cos + at) + k);
-        s[k] = __ldg(reinterpret_cast<const float4*>(nr.sin + at) + k);
-      }
-  }
-  const float cc[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
-  const float ss[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
-  const float sign = second ? 1.f : -1.f;
-  const uint64_t sign2 = f2(sign, sign);
-  Coef r;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    r.a[k] = kSplit ? f2(cc[2 * k], cc[2 * k + 1]) : f2(cc[k], cc[k]);
-    r.b[k] = kSplit ? fmul2(f2(ss[2 * k], ss[2 * k + 1]), sign2) : f2(-ss[k], ss[k]);
-  }
-  if (weight) {
-    const Raw8<T> own = load8<T>(weight, 8 * li, D, err);
-    const Raw8<T> other =
-        kSplit ? load8<T>(weight, 8 * (rotated ? partner_lane(nr, li) : li), D, err) : own;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      r.a[k] = fmul2(r.a[k], own.pair(k));
-      r.b[k] = fmul2(r.b[k], kSplit ? other.pair(k) : own.swapped(k));
-    }
-  }
-  return r;
+  return CoefSource<T, D, kSplit>(nr, weight, li, err).get(nr, pos, li, active, err);
 }
 
 // Norm (has_w) and rotation of a group's row.  Called by all 32 lanes of a
