@@ -40,7 +40,9 @@
 // those cut between CTAs through the workspace by the CTA that draws the
 // tile's last ticket, always in key order, so the bits do not depend on the
 // order of arrival.  Lengths are read on the device: every CTA adds up all
-// B lengths itself, so a captured graph follows lengths that change.
+// B lengths itself, so a captured graph follows lengths that change.  The
+// tickets are zeroed by a small kernel before, whose programmatic dependent
+// this one is.
 //
 // Masked places.  Keys behind a sequence's last may hold anything: scores are
 // selected, not added to, and values are replaced by zero.  Where the last Tq
@@ -206,6 +208,8 @@ struct Shared {
   unsigned start_off[W];
   int fail;
   int last[2];
+  float weight[2 * W][kTileRows], factor[2 * W][kTileRows];     // of states and rows
+  int group[2 * W];       // first entry and end of a tile's states
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -287,6 +291,12 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 // Arrives on `bar` when this thread's cp.async copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Waits until the kernel before this one (a programmatic dependent of it) has
+// completed and its writes are visible.
+__device__ __forceinline__ void griddep_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 __device__ __forceinline__ unsigned atom_acq_rel_add(unsigned* p, unsigned v) {
@@ -648,7 +658,10 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
         if (RF_IN(p.err, (b * n + i) * 8 + 7, n_qo))
           reinterpret_cast<uint4*>(p.O)[b * n + i] = make_uint4(0u, 0u, 0u, 0u);
     }
-  if ((unsigned)cta >= grid || total == 0) return;
+  if ((unsigned)cta >= grid || total == 0) {
+    griddep_wait();
+    return;
+  }
   const unsigned x0 = r0 + warps.start(warp);
   const unsigned count = warps.start(warp + 1) - warps.start(warp);   // chunks of this warp
 
@@ -1021,12 +1034,15 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     for (unsigned x = done; x < count && x < done + S; ++x)
       (void)mbar_wait(smem_u32(&sh.full[warp][x % S]), (x / S) & 1, 1000000ull);
   }
+  griddep_wait();                              // the tickets are zero
   named_bar_sync(1, C::kConsumers);
   if (sh.fail) return;
 
   // ---- merge the states that warps left, in key order
-  // entry e = (warp e / 2, state e % 2); groups of entries of one tile
-  const bool here = lane < 2 * W && sh.has[(lane >> 1) % W][lane & 1] != 0;
+  // entry e = (warp e / 2, state e % 2); groups of neighbouring entries belong to
+  // one tile
+  constexpr int E = 2 * W;
+  const bool here = lane < E && sh.has[(lane >> 1) % W][lane & 1] != 0;
   const unsigned mask = __ballot_sync(0xffffffffu, here);
   if (mask == 0) return;
   const unsigned my_s0 = sh.seg[(lane >> 1) % W][lane & 1].s0;
@@ -1034,78 +1050,112 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
   const int prev = below ? 31 - __clz((int)below) : lane;
   const unsigned prev_s0 = __shfl_sync(0xffffffffu, my_s0, prev);
   const unsigned starts = __ballot_sync(0xffffffffu, here && (below == 0 || prev_s0 != my_s0));
+  const int n_groups = __popc(starts);
   auto state_of = [&](int e) {
     return (e & 1) ? smem + (e >> 1) * (S * C::kStageBytes)
                    : smem + C::kRingBytes + (e >> 1) * C::kStateBytes;
   };
-  constexpr int NV = D / 32;                 // floats a lane holds of a row
-  auto put_row = [&](const Seg& sg, int r, float w, const float (&v)[NV]) {
-    const int h = p.tiles == 1 ? sg.hr : sg.hr / p.tiles;
-    const int64_t at = row_at(sg.b, h, (sg.hr - h * p.tiles) * kTileRows + r) + NV * lane;
-    if (!RF_IN(p.err, at + NV - 1, n_qo)) return;
-#pragma unroll
-    for (int i = 0; i < NV; i += 2)
-      *reinterpret_cast<uint32_t*>(p.O + at + i) = pack_bf16x2(v[i] * w, v[i + 1] * w);
-  };
   const int rows = min(p.R, C::kRows);       // of a tile (its last one may have fewer)
   auto has_row = [&](int hr, int r) { return p.tiles == 1 || hr % p.tiles * kTileRows + r < p.R; };
   const int64_t n_slots = 2 * (int64_t)gridDim.x * kTileRows;
-  const int n_groups = __popc(starts);
   // first entries of the (at most two) tiles that are cut between CTAs: the
   // first and the last group
-  int cut[2] = {-1, -1};
+  int cut0 = -1, cut1 = -1;
   {
     const int ea = __ffs(starts) - 1, eb = 31 - __clz((int)starts);
     const Seg &sa = sh.seg[ea >> 1][ea & 1], &sb = sh.seg[eb >> 1][eb & 1];
-    if (sa.s0 < r0 || sa.s0 + num_chunks(sa.len) > r1) cut[0] = ea;
-    if (eb != ea && sb.s0 + num_chunks(sb.len) > r1) cut[1] = eb;
+    if (sa.s0 < r0 || sa.s0 + num_chunks(sa.len) > r1) cut0 = ea;
+    if (eb != ea && sb.s0 + num_chunks(sb.len) > r1) cut1 = eb;
   }
-  for (int i = warp; i < n_groups * rows; i += W) {
+  // weights: a thread for every entry and row
+  for (int i = threadIdx.x; i < E * rows; i += C::kConsumers) {
+    const int e = i / rows, r = i - e * rows;
+    if (!((mask >> e) & 1u)) continue;
+    const int e0 = 31 - __clz((int)(starts & ((2u << e) - 1u)));
+    const unsigned later = starts & ~((2u << e) - 1u);
+    const int e1 = later ? __ffs(later) - 1 : E;
+    float Mx = -INFINITY, mx = -INFINITY;
+    for (int x = e0; x < e1; ++x)
+      if ((mask >> x) & 1u) {
+        const float4 st = reinterpret_cast<const float4*>(state_of(x) + C::kRows * C::kPitch * 4)[r];
+        Mx = fmaxf(Mx, st.x);
+        mx = fmaxf(mx, st.y);
+      }
+    const float Mu = Mx == -INFINITY ? 0.f : Mx, mu = mx == -INFINITY ? 0.f : mx;
+    const float4 own = reinterpret_cast<const float4*>(state_of(e) + C::kRows * C::kPitch * 4)[r];
+    sh.weight[e][r] = ex2(own.x - Mu);
+    if (e != e0) continue;
+    if (r == 0) sh.group[__popc(starts & ((1u << e) - 1u))] = e0 | e1 << 8;
+    float L = 0.f;
+    for (int x = e0; x < e1; ++x)
+      if ((mask >> x) & 1u) {
+        const float4 st = reinterpret_cast<const float4*>(state_of(x) + C::kRows * C::kPitch * 4)[r];
+        L = fmaf(st.z, ex2(st.y - mu), L);
+      }
+    if (e != cut0 && e != cut1) {
+      sh.factor[e][r] = L == 0.f ? 0.f : ex2(Mu - mu) / L;
+    } else {
+      const int64_t at = slot_of(ctas, sh.seg[e >> 1][e & 1].s0, cta) * kTileRows + r;
+      if (RF_IN(p.err, at, n_slots)) p.ws_st[at] = make_float4(Mx, mx, L, 0.f);
+    }
+  }
+  named_bar_sync(1, C::kConsumers);
+  // rows: half a warp for every group and row
+  constexpr int NV = D / 16;                 // dims a lane holds of a row
+  const int hw = threadIdx.x >> 4, l16 = lane & 15;
+  auto put_row = [&](const Seg& sg, int r, float w, const float (&v)[NV]) {
+    const int h = p.tiles == 1 ? sg.hr : sg.hr / p.tiles;
+    const int64_t at = row_at(sg.b, h, (sg.hr - h * p.tiles) * kTileRows + r) + NV * l16;
+    if (!RF_IN(p.err, at + NV - 1, n_qo)) return;
+    uint32_t u[NV / 2];
+#pragma unroll
+    for (int i = 0; i < NV / 2; ++i) u[i] = pack_bf16x2(v[2 * i] * w, v[2 * i + 1] * w);
+    if (NV == 8)
+      *reinterpret_cast<uint4*>(p.O + at) = make_uint4(u[0], u[1], u[NV / 2 - 2], u[NV / 2 - 1]);
+    else
+      *reinterpret_cast<uint2*>(p.O + at) = make_uint2(u[0], u[1]);
+  };
+  for (int i = hw; i < n_groups * rows; i += 2 * W) {
     const int gi = i / rows, r = i - gi * rows;
-    unsigned left = starts;
-    for (int k = 0; k < gi; ++k) left &= left - 1;
-    const int e0 = __ffs(left) - 1;
-    const unsigned rest = left & (left - 1);
-    const int e1 = rest ? __ffs(rest) - 1 : 2 * W;       // entries e0 .. e1 - 1
+    const int e0 = sh.group[gi] & 255, e1 = sh.group[gi] >> 8;
     const Seg sg = sh.seg[e0 >> 1][e0 & 1];
     if (!has_row(sg.hr, r)) continue;
-    const bool in = here && lane >= e0 && lane < e1;     // one entry a lane
-    float4 st = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
-    if (in) st = reinterpret_cast<const float4*>(state_of(lane) + C::kRows * C::kPitch * 4)[r];
-    const float Mx = warp_max(st.x), mx = warp_max(st.y);
-    const float Mu = Mx == -INFINITY ? 0.f : Mx, mu = mx == -INFINITY ? 0.f : mx;
-    const float wo = ex2(st.x - Mu), L = warp_sum(st.z * ex2(st.y - mu));
     float v[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) v[k] = 0.f;
-#pragma unroll 4
-    for (int e = e0; e < e1; ++e) {
-      const float we = __shfl_sync(0xffffffffu, wo, e);
+#pragma unroll 2
+    for (int e = e0; e < e1; ++e)
       if ((mask >> e) & 1u) {
-        const float* row = reinterpret_cast<const float*>(state_of(e)) + r * C::kPitch + NV * lane;
+        const float we = sh.weight[e][r];
+        const float4* row = reinterpret_cast<const float4*>(
+            reinterpret_cast<const float*>(state_of(e)) + r * C::kPitch + NV * l16);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) v[k] = fmaf(row[k], we, v[k]);
+        for (int k = 0; k < NV / 4; ++k) {
+          const float4 x = row[k];
+          v[4 * k] = fmaf(x.x, we, v[4 * k]);
+          v[4 * k + 1] = fmaf(x.y, we, v[4 * k + 1]);
+          v[4 * k + 2] = fmaf(x.z, we, v[4 * k + 2]);
+          v[4 * k + 3] = fmaf(x.w, we, v[4 * k + 3]);
+        }
       }
-    }
-    if (e0 != cut[0] && e0 != cut[1]) {
-      put_row(sg, r, L == 0.f ? 0.f : ex2(Mu - mu) / L, v);
+    if (e0 != cut0 && e0 != cut1) {
+      put_row(sg, r, sh.factor[e0][r], v);
     } else {
       const int64_t at = slot_of(ctas, sg.s0, cta) * kTileRows + r;
       if (RF_IN(p.err, at, n_slots)) {
-        float* dst = p.ws_o + at * D + NV * lane;
+        float4* dst = reinterpret_cast<float4*>(p.ws_o + at * D + NV * l16);
 #pragma unroll
-        for (int k = 0; k < NV; k += 2)
-          *reinterpret_cast<float2*>(dst + k) = make_float2(v[k], v[k + 1]);
-        if (lane == 0) p.ws_st[at] = make_float4(Mx, mx, L, 0.f);
+        for (int k = 0; k < NV / 4; ++k)
+          dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
       }
     }
   }
-  if (cut[0] < 0 && cut[1] < 0) return;
+  if (cut0 < 0 && cut1 < 0) return;
   // ---- tiles cut between CTAs: the last CTA to arrive merges.  The barrier
   // orders the CTA's stores before the ticket's release.
   named_bar_sync(1, C::kConsumers);
   if (threadIdx.x < 2) {
-    const int e0 = threadIdx.x ? cut[1] : cut[0];
+    const int e0 = threadIdx.x ? cut1 : cut0;
     unsigned last = 0;
     if (e0 >= 0) {
       const Seg& sg = sh.seg[e0 >> 1][e0 & 1];
@@ -1118,68 +1168,89 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     sh.last[threadIdx.x] = (int)last;
   }
   named_bar_sync(1, C::kConsumers);
-#pragma unroll 1
-  for (int k = 0; k < 2; ++k) {
-    const int ek = k ? cut[1] : cut[0];
-    if (ek < 0 || !sh.last[k]) continue;
+  const unsigned half = lane < 16 ? 0xFFFFu : 0xFFFF0000u;
+  for (int i = hw; i < 2 * rows; i += 2 * W) {
+    const int k2 = i / rows, r = i - k2 * rows;
+    const int ek = k2 ? cut1 : cut0;
+    if (ek < 0 || !sh.last[k2]) continue;
     const Seg sg = sh.seg[ek >> 1][ek & 1];
+    if (!has_row(sg.hr, r)) continue;
     const unsigned s1 = sg.s0 + num_chunks(sg.len);
     const int c0 = (int)ctas.owner(sg.s0), pieces = (int)ctas.owner(s1 - 1) - c0 + 1;
-    for (int r = warp; r < rows; r += W) {
-      if (!has_row(sg.hr, r)) continue;
-      auto at_piece = [&](int j) { return slot_of(ctas, sg.s0, c0 + j) * kTileRows + r; };
-      // 32 pieces at a time, a piece's (M, m, l) a lane, with the running maxima
-      // carried over; the loads of kBatch pieces' rows go together
-      float Mx = -INFINITY, mx = -INFINITY, L = 0.f, v[NV];
+    auto at_piece = [&](int j) { return slot_of(ctas, sg.s0, c0 + j) * kTileRows + r; };
+    // 16 pieces at a time, a piece's (M, m, l) a lane, with the running maxima
+    // carried over; the loads of kBatch pieces' rows go together
+    float Mx = -INFINITY, mx = -INFINITY, L = 0.f, v[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = 0.f;
-      for (int j0 = 0; j0 < pieces; j0 += 32) {
-        constexpr int kBatch = 8;
-        const int n = min(pieces - j0, 32);
-        float x[kBatch][NV];
-        auto load = [&](int j) {
+    for (int k = 0; k < NV; ++k) v[k] = 0.f;
+    for (int j0 = 0; j0 < pieces; j0 += 16) {
+      constexpr int kBatch = 4;
+      const int n = min(pieces - j0, 16);
+      float4 x[kBatch][NV / 4];
+      auto load = [&](int j) {
 #pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
+        for (int u = 0; u < kBatch; ++u)
 #pragma unroll
-            for (int i = 0; i < NV; ++i) x[u][i] = 0.f;
-            if (j + u < n && RF_IN(p.err, at_piece(j0 + j + u), n_slots)) {
-              const float* src = p.ws_o + at_piece(j0 + j + u) * D + NV * lane;
+          for (int k = 0; k < NV / 4; ++k) {
+            x[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j + u < n && RF_IN(p.err, at_piece(j0 + j + u), n_slots))
+              x[u][k] = __ldcg(reinterpret_cast<const float4*>(
+                                   p.ws_o + at_piece(j0 + j + u) * D + NV * l16) + k);
+          }
+      };
+      load(0);
+      float4 st = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+      if (l16 < n && RF_IN(p.err, at_piece(j0 + l16), n_slots))
+        st = __ldcg(&p.ws_st[at_piece(j0 + l16)]);
+      float Mn = st.x, mn = st.y;
 #pragma unroll
-              for (int i = 0; i < NV; i += 2) {
-                const float2 y = __ldcg(reinterpret_cast<const float2*>(src + i));
-                x[u][i] = y.x;
-                x[u][i + 1] = y.y;
-              }
+      for (int o = 8; o > 0; o >>= 1) {
+        Mn = fmaxf(Mn, __shfl_xor_sync(half, Mn, o));
+        mn = fmaxf(mn, __shfl_xor_sync(half, mn, o));
+      }
+      Mn = fmaxf(Mn, Mx);
+      mn = fmaxf(mn, mx);
+      const float Mu = Mn == -INFINITY ? 0.f : Mn, mu = mn == -INFINITY ? 0.f : mn;
+      const float wo = ex2(st.x - Mu), keep = ex2(Mx - Mu);
+      float l_new = st.z * ex2(st.y - mu);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) l_new += __shfl_xor_sync(half, l_new, o);
+      L = fmaf(L, ex2(mx - mu), l_new);
+      Mx = Mn;
+      mx = mn;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) v[k] *= keep;
+      for (int j = 0; j < n; j += kBatch) {
+        if (j > 0) load(j);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const float wj = __shfl_sync(half, wo, (j + u) & 15, 16);
+          if (j + u < n)
+#pragma unroll
+            for (int k = 0; k < NV / 4; ++k) {
+              v[4 * k] = fmaf(x[u][k].x, wj, v[4 * k]);
+              v[4 * k + 1] = fmaf(x[u][k].y, wj, v[4 * k + 1]);
+              v[4 * k + 2] = fmaf(x[u][k].z, wj, v[4 * k + 2]);
+              v[4 * k + 3] = fmaf(x[u][k].w, wj, v[4 * k + 3]);
             }
-          }
-        };
-        load(0);
-        float4 st = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
-        if (lane < n && RF_IN(p.err, at_piece(j0 + lane), n_slots))
-          st = __ldcg(&p.ws_st[at_piece(j0 + lane)]);
-        const float Mn = fmaxf(Mx, warp_max(st.x)), mn = fmaxf(mx, warp_max(st.y));
-        const float Mu = Mn == -INFINITY ? 0.f : Mn, mu = mn == -INFINITY ? 0.f : mn;
-        const float wo = ex2(st.x - Mu), keep = ex2(Mx - Mu);
-        L = fmaf(L, ex2(mx - mu), warp_sum(st.z * ex2(st.y - mu)));
-        Mx = Mn;
-        mx = mn;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] *= keep;
-        for (int j = 0; j < n; j += kBatch) {
-          if (j > 0) load(j);
-#pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            const float wj = __shfl_sync(0xffffffffu, wo, (j + u) & 31);
-            if (j + u < n)
-#pragma unroll
-              for (int i = 0; i < NV; ++i) v[i] = fmaf(x[u][i], wj, v[i]);
-          }
         }
       }
-      const float Mu = Mx == -INFINITY ? 0.f : Mx, mu = mx == -INFINITY ? 0.f : mx;
-      put_row(sg, r, L == 0.f ? 0.f : ex2(Mu - mu) / L, v);
     }
+    const float Mu = Mx == -INFINITY ? 0.f : Mx, mu = mx == -INFINITY ? 0.f : mx;
+    put_row(sg, r, L == 0.f ? 0.f : ex2(Mu - mu) / L, v);
   }
+}
+
+// Zeroes the tickets.  The decode kernel is its programmatic dependent: it may
+// start as soon as this one has, and waits for it just before its tickets.
+// What it reads until then was written before this kernel began, which is
+// launched the ordinary way.  (A memset in its place has to end before the
+// decode kernel starts.)
+__global__ void __launch_bounds__(1024) zero_tickets_kernel(unsigned* tickets, int64_t n,
+                                                            unsigned* err) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 1024)
+    if (RF_IN(err, i, n)) tickets[i] = 0u;
 }
 
 template <bool kF8, int D, int NT>
@@ -1202,10 +1273,23 @@ cudaError_t launch(const PagedKV& c, const Params& p, int sms, cudaStream_t s) {
   auto kern = decode_paged_kernel<kF8, D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  e = cudaMemsetAsync(p.tickets, 0, (size_t)p.lens.B * p.lens.HR * sizeof(unsigned), s);
+  const int64_t tickets = (int64_t)p.lens.B * p.lens.HR;
+  const int64_t ctas = (tickets + 1023) / 1024;
+  zero_tickets_kernel<<<(unsigned)(ctas < sms ? ctas : sms), 1024, 0, s>>>(p.tickets, tickets,
+                                                                          p.err);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  kern<<<sms, C::kThreads, C::kSmem, s>>>(tm[0], tm[1], p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms, 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], p);
 }
 
 int tiles_of(int R) { return (R + kTileRows - 1) / kTileRows; }
