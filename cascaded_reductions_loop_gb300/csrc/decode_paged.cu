@@ -208,8 +208,6 @@ struct Shared {
   unsigned start_off[W];
   int fail;
   int last[2];
-  float weight[2 * W][kTileRows], factor[2 * W][kTileRows];     // of states and rows
-  int group[2 * W];       // first entry and end of a tile's states
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -1067,42 +1065,20 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     if (sa.s0 < r0 || sa.s0 + num_chunks(sa.len) > r1) cut0 = ea;
     if (eb != ea && sb.s0 + num_chunks(sb.len) > r1) cut1 = eb;
   }
-  // weights: a thread for every entry and row
-  for (int i = threadIdx.x; i < E * rows; i += C::kConsumers) {
-    const int e = i / rows, r = i - e * rows;
-    if (!((mask >> e) & 1u)) continue;
-    const int e0 = 31 - __clz((int)(starts & ((2u << e) - 1u)));
-    const unsigned later = starts & ~((2u << e) - 1u);
-    const int e1 = later ? __ffs(later) - 1 : E;
-    float Mx = -INFINITY, mx = -INFINITY;
-    for (int x = e0; x < e1; ++x)
-      if ((mask >> x) & 1u) {
-        const float4 st = reinterpret_cast<const float4*>(state_of(x) + C::kRows * C::kPitch * 4)[r];
-        Mx = fmaxf(Mx, st.x);
-        mx = fmaxf(mx, st.y);
-      }
-    const float Mu = Mx == -INFINITY ? 0.f : Mx, mu = mx == -INFINITY ? 0.f : mx;
-    const float4 own = reinterpret_cast<const float4*>(state_of(e) + C::kRows * C::kPitch * 4)[r];
-    sh.weight[e][r] = ex2(own.x - Mu);
-    if (e != e0) continue;
-    if (r == 0) sh.group[__popc(starts & ((1u << e) - 1u))] = e0 | e1 << 8;
-    float L = 0.f;
-    for (int x = e0; x < e1; ++x)
-      if ((mask >> x) & 1u) {
-        const float4 st = reinterpret_cast<const float4*>(state_of(x) + C::kRows * C::kPitch * 4)[r];
-        L = fmaf(st.z, ex2(st.y - mu), L);
-      }
-    if (e != cut0 && e != cut1) {
-      sh.factor[e][r] = L == 0.f ? 0.f : ex2(Mu - mu) / L;
-    } else {
-      const int64_t at = slot_of(ctas, sh.seg[e >> 1][e & 1].s0, cta) * kTileRows + r;
-      if (RF_IN(p.err, at, n_slots)) p.ws_st[at] = make_float4(Mx, mx, L, 0.f);
-    }
-  }
-  named_bar_sync(1, C::kConsumers);
-  // rows: half a warp for every group and row
+  // half a warp for every group and row, an entry's (M, m, l) a lane
   constexpr int NV = D / 16;                 // dims a lane holds of a row
   const int hw = threadIdx.x >> 4, l16 = lane & 15;
+  const unsigned half = lane < 16 ? 0xFFFFu : 0xFFFF0000u;
+  auto max16 = [&](float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(half, v, o));
+    return v;
+  };
+  auto sum16 = [&](float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(half, v, o);
+    return v;
+  };
   auto put_row = [&](const Seg& sg, int r, float w, const float (&v)[NV]) {
     const int h = p.tiles == 1 ? sg.hr : sg.hr / p.tiles;
     const int64_t at = row_at(sg.b, h, (sg.hr - h * p.tiles) * kTileRows + r) + NV * l16;
@@ -1115,18 +1091,30 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     else
       *reinterpret_cast<uint2*>(p.O + at) = make_uint2(u[0], u[1]);
   };
+#pragma unroll 1
   for (int i = hw; i < n_groups * rows; i += 2 * W) {
-    const int gi = i / rows, r = i - gi * rows;
-    const int e0 = sh.group[gi] & 255, e1 = sh.group[gi] >> 8;
+    int gi = i / rows;
+    const int r = i - gi * rows;
+    unsigned left = starts;
+    for (; gi > 0; --gi) left &= left - 1;
+    const int e0 = __ffs(left) - 1;
+    const unsigned rest = left & (left - 1);
+    const int e1 = rest ? __ffs(rest) - 1 : E;           // entries e0 .. e1 - 1
     const Seg sg = sh.seg[e0 >> 1][e0 & 1];
     if (!has_row(sg.hr, r)) continue;
+    float4 st = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+    if (l16 >= e0 && l16 < e1 && ((mask >> l16) & 1u))
+      st = reinterpret_cast<const float4*>(state_of(l16) + C::kRows * C::kPitch * 4)[r];
+    const float Mx = max16(st.x), mx = max16(st.y);
+    const float Mu = Mx == -INFINITY ? 0.f : Mx, mu = mx == -INFINITY ? 0.f : mx;
+    const float wo = ex2(st.x - Mu), L = sum16(st.z * ex2(st.y - mu));
     float v[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) v[k] = 0.f;
 #pragma unroll 2
-    for (int e = e0; e < e1; ++e)
+    for (int e = e0; e < e1; ++e) {
+      const float we = __shfl_sync(half, wo, e, 16);
       if ((mask >> e) & 1u) {
-        const float we = sh.weight[e][r];
         const float4* row = reinterpret_cast<const float4*>(
             reinterpret_cast<const float*>(state_of(e)) + r * C::kPitch + NV * l16);
 #pragma unroll
@@ -1138,8 +1126,9 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
           v[4 * k + 3] = fmaf(x.w, we, v[4 * k + 3]);
         }
       }
+    }
     if (e0 != cut0 && e0 != cut1) {
-      put_row(sg, r, sh.factor[e0][r], v);
+      put_row(sg, r, L == 0.f ? 0.f : ex2(Mu - mu) / L, v);
     } else {
       const int64_t at = slot_of(ctas, sg.s0, cta) * kTileRows + r;
       if (RF_IN(p.err, at, n_slots)) {
@@ -1147,6 +1136,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < NV / 4; ++k)
           dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        if (l16 == 0) p.ws_st[at] = make_float4(Mx, mx, L, 0.f);
       }
     }
   }
@@ -1168,7 +1158,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     sh.last[threadIdx.x] = (int)last;
   }
   named_bar_sync(1, C::kConsumers);
-  const unsigned half = lane < 16 ? 0xFFFFu : 0xFFFF0000u;
+#pragma unroll 1
   for (int i = hw; i < 2 * rows; i += 2 * W) {
     const int k2 = i / rows, r = i - k2 * rows;
     const int ek = k2 ? cut1 : cut0;
@@ -1202,19 +1192,12 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
       float4 st = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
       if (l16 < n && RF_IN(p.err, at_piece(j0 + l16), n_slots))
         st = __ldcg(&p.ws_st[at_piece(j0 + l16)]);
-      float Mn = st.x, mn = st.y;
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) {
-        Mn = fmaxf(Mn, __shfl_xor_sync(half, Mn, o));
-        mn = fmaxf(mn, __shfl_xor_sync(half, mn, o));
-      }
+      float Mn = max16(st.x), mn = max16(st.y);
       Mn = fmaxf(Mn, Mx);
       mn = fmaxf(mn, mx);
       const float Mu = Mn == -INFINITY ? 0.f : Mn, mu = mn == -INFINITY ? 0.f : mn;
       const float wo = ex2(st.x - Mu), keep = ex2(Mx - Mu);
-      float l_new = st.z * ex2(st.y - mu);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) l_new += __shfl_xor_sync(half, l_new, o);
+      const float l_new = sum16(st.z * ex2(st.y - mu));
       L = fmaf(L, ex2(mx - mu), l_new);
       Mx = Mn;
       mx = mn;
