@@ -233,7 +233,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 
@@ -882,83 +882,98 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     }
 
     // ---- running maxima and sums (log2 units); element (k, e): key g + 8 k, row 2c + e
+    // (step by step for all rows together, so that their chains overlap)
     uint32_t pb[2][NT][kF8 ? 1 : 2][2];
     const bool two = kF8 && lv[0] != lv[1];
+    float cm[NT][2], cM[NT][2], mu[NT][2], Mu[NT][2], a_o[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float a_o[2];
-      bool moved = false;
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2)
+        for (int h2 = 0; h2 < 2; ++h2) {
+          const float sc = f[nt][e] * kscale[h2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float v = s[h2][nt][2 * k + e] * (f[nt][e] * kscale[h2]);
+            float v = s[h2][nt][2 * k + e] * sc;
             if (tail && (key0 + 16 * h2 + g + 8 * k >= lim[nt][e] || !((valid >> h2) & 1)))
               v = -INFINITY;
             s[h2][nt][2 * k + e] = v;
             mx[h2] = fmaxf(mx[h2], v);
           }
-        float cm = fmaxf(mx[0], mx[1]);
-        float cM = two ? fmaxf(mx[0] + lv[0], mx[1] + lv[1]) : 0.f;
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) {
-          cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, x));
-          if (two) cM = fmaxf(cM, __shfl_xor_sync(0xffffffffu, cM, x));
         }
-        if (!two) cM = cm + lv[0];
-        const float mn = fmaxf(m[nt][e], cm);
-        const float mu = mn == -INFINITY ? 0.f : mn;
-        const float a_l = ex2(m[nt][e] - mu);
+        cm[nt][e] = fmaxf(mx[0], mx[1]);
+        cM[nt][e] = fmaxf(mx[0] + lv[0], mx[1] + lv[1]);
+      }
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          cm[nt][e] = fmaxf(cm[nt][e], __shfl_xor_sync(0xffffffffu, cm[nt][e], x));
+    if (two) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            cM[nt][e] = fmaxf(cM[nt][e], __shfl_xor_sync(0xffffffffu, cM[nt][e], x));
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) cM[nt][e] = cm[nt][e] + lv[0];
+    }
+    bool moved = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mn = fmaxf(m[nt][e], cm[nt][e]);
+        mu[nt][e] = mn == -INFINITY ? 0.f : mn;
+        l[nt][e] *= ex2(m[nt][e] - mu[nt][e]);
         m[nt][e] = mn;
-        float Mu = mu;
-        a_o[e] = a_l;
-        if (kF8) {
-          const float Mn = fmaxf(M[nt][e], cM);
-          Mu = Mn == -INFINITY ? 0.f : Mn;
-          a_o[e] = ex2(M[nt][e] - Mu);
-          moved |= Mn != M[nt][e];
-          M[nt][e] = Mn;
-        } else {
-          moved |= mn != M[nt][e];
-          M[nt][e] = mn;
-        }
-        float sum = 0.f;
-#pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float v = s[h2][nt][2 * k + e];
-            const float pr = ex2(v - mu);
-            sum += pr;
-            s[h2][nt][2 * k + e] = kF8 ? ex2(v + lv[h2] - Mu) : pr;
-          }
-        l[nt][e] = fmaf(l[nt][e], a_l, sum);
+        const float Mn = kF8 ? fmaxf(M[nt][e], cM[nt][e]) : mn;
+        Mu[nt][e] = Mn == -INFINITY ? 0.f : Mn;
+        a_o[nt][e] = ex2(M[nt][e] - Mu[nt][e]);
+        moved |= Mn != M[nt][e];
+        M[nt][e] = Mn;
       }
-      if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          o[i][nt][0] *= a_o[0];
-          o[i][nt][1] *= a_o[1];
-          o[i][nt][2] *= a_o[0];
-          o[i][nt][3] *= a_o[1];
-        }
-      }
-      // P^T as B fragments
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float x = s[h2][nt][2 * k], y = s[h2][nt][2 * k + 1];
-          if (kF8) {
-            pb[h2][nt][0][k] = movmatrix(pack_f16x2(x, y));
-          } else {
-            const uint32_t hi = pack_bf16x2(x, y);
-            pb[h2][nt][0][k] = movmatrix(hi);
-            pb[h2][nt][kF8 ? 0 : 1][k] = movmatrix(pack_bf16x2(x - bf16lo(hi), y - bf16hi(hi)));
+          float w[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float v = s[h2][nt][2 * k + e], pr = ex2(v - mu[nt][e]);
+            l[nt][e] += pr;
+            w[e] = kF8 ? ex2(v + lv[h2] - Mu[nt][e]) : pr;
           }
+          // P^T as B fragments
+          if (kF8) {
+            pb[h2][nt][0][k] = movmatrix(pack_f16x2(w[0], w[1]));
+          } else {
+            const uint32_t hi = pack_bf16x2(w[0], w[1]);
+            pb[h2][nt][0][k] = movmatrix(hi);
+            pb[h2][nt][kF8 ? 0 : 1][k] =
+                movmatrix(pack_bf16x2(w[0] - bf16lo(hi), w[1] - bf16hi(hi)));
+          }
+        }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          o[i][nt][0] *= a_o[nt][0];
+          o[i][nt][1] *= a_o[nt][1];
+          o[i][nt][2] *= a_o[nt][0];
+          o[i][nt][3] *= a_o[nt][1];
         }
     }
 
