@@ -32,8 +32,8 @@
 // values may be anything bf16 holds; M = m.
 //
 // Partition.  The 32-key chunks of all tiles, end to end in the order (b, hr,
-// chunk), are cut into one equal range per CTA and each of these into one per
-// warp.  A warp streams its range through a private ring of TMA stages and
+// chunk), are cut into one equal range per CTA (at tile borders where all tiles
+// are short) and each of these into one per warp.  A warp streams its range through a private ring of TMA stages and
 // keeps the running state; where a tile begins and ends in a warp's range the
 // warp writes its output itself.  At the end of the kernel one CTA barrier
 // follows: the states of tiles cut between warps are merged by the CTA, and
@@ -127,6 +127,18 @@ __host__ __device__ __forceinline__ unsigned ctas_for(unsigned total, unsigned s
   return want < 1u ? 1u : (want < sms ? want : sms);
 }
 
+// Short tiles are not cut between CTAs: merging through the workspace costs
+// about 3.5 us, three or four chunks' time.  Where no tile has more than 2 W
+// chunks (two a warp), the CTAs' ranges therefore begin at the tile border that
+// is next to the even cut.
+__host__ __device__ __forceinline__ bool keeps_tiles(unsigned max_chunks, unsigned W) {
+  return max_chunks <= 2 * W;
+}
+// The border next to chunk x, the off-th of a tile of nck.
+__host__ __device__ __forceinline__ unsigned snap(unsigned x, unsigned off, unsigned nck) {
+  return 2 * off < nck ? x - off : x - off + nck;
+}
+
 // Where the chunks of all tiles stand in one order: chunk ck of tile hr of
 // sequence b (of len keys, nck chunks a tile).
 struct Cursor {
@@ -203,7 +215,7 @@ struct Shared {
   Meta meta[W][S];
   Seg seg[W][2];          // [0] the warp's first state, [1] its last
   int has[W][2];
-  unsigned warp_sum[W + 4];
+  unsigned warp_sum[W + 4], warp_most[W + 4], border[2];
   int start_b[W], start_len[W];
   unsigned start_off[W];
   int fail;
@@ -487,13 +499,14 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
   if (consumer && lane == 0) sh.start_b[warp] = sh.start_len[warp] = 0;
   const int per = (lens.B + C::kThreads - 1) / C::kThreads;
   const int b_lo = min((int)threadIdx.x * per, lens.B), b_hi = min(b_lo + per, lens.B);
-  unsigned mine = 0;
+  unsigned mine = 0, most = 0;
   int first_len = 0;
   bool empty = false;
   for (int b = b_lo; b < b_hi; ++b) {
     const int len = seq_len(lens, b, cta == 0, p.err);
     if (b == b_lo) first_len = len;
     empty |= len == 0;
+    most = max(most, num_chunks(len));
     mine += num_chunks(len) * (unsigned)lens.HR;
   }
   unsigned incl = mine;
@@ -502,17 +515,45 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) sh.warp_sum[warp] = incl;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    sh.warp_sum[warp] = incl;
+    sh.warp_most[warp] = most;
+  }
   const bool empties = __syncthreads_or(empty);
   unsigned pre = incl - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < W + 4; ++w) {
     if (w < warp) pre += sh.warp_sum[w];
     total += sh.warp_sum[w];
+    most = max(most, sh.warp_most[w]);
   }
   const unsigned grid = ctas_for(total, gridDim.x, W);
   const Split ctas(total, grid);
-  const unsigned r0 = ctas.start(cta), r1 = (unsigned)cta < grid ? ctas.start(cta + 1) : r0;
+  unsigned r0 = ctas.start(cta), r1 = (unsigned)cta < grid ? ctas.start(cta + 1) : r0;
+  if (keeps_tiles(most, W)) {
+    for (int i = 0; i < 2; ++i) {
+      const unsigned x = i ? r1 : r0;
+      if (threadIdx.x == 0 && x >= total) sh.border[i] = total;
+      if (x >= pre && x - pre < mine) {
+        unsigned at = pre;
+        for (int b = b_lo, len = first_len; b < b_hi;) {
+          const unsigned nck = num_chunks(len), n = nck * (unsigned)lens.HR;
+          if (x - at < n) {
+            sh.border[i] = snap(x, (x - at) % nck, nck);
+            break;
+          }
+          at += n;
+          if (++b < b_hi) len = seq_len(lens, b, false, p.err);
+        }
+      }
+    }
+    __syncthreads();
+    if ((unsigned)cta < grid) {
+      r0 = sh.border[0];
+      r1 = sh.border[1];
+    }
+  }
   const Split warps(r1 - r0, W);
   for (int w = 0; w < W; ++w) {
     const unsigned x = r0 + warps.start(w);
@@ -1364,12 +1405,23 @@ cudaError_t launch_decode_paged(const PagedKV& c, const void* Q, void* O, int Hq
 //     slots that it reads, in key order.
 int decode_paged_plan_selfcheck(const int* seq_lens, int B, int HR, int max_len, int W, int sms) {
   const Lens lens = {seq_lens, B, HR, max_len};
-  unsigned err = 0, total = 0;
+  unsigned err = 0, total = 0, most = 0;
   std::vector<unsigned> pre((size_t)B + 1, 0);
   for (int b = 0; b < B; ++b) {
-    total += num_chunks(seq_len(lens, b, true, &err)) * (unsigned)HR;
+    const unsigned nck = num_chunks(seq_len(lens, b, true, &err));
+    most = std::max(most, nck);
+    total += nck * (unsigned)HR;
     pre[(size_t)b + 1] = total;
   }
+  auto seq_of = [&](unsigned x) {
+    return (int)(std::upper_bound(pre.begin(), pre.end(), x) - pre.begin()) - 1;
+  };
+  auto border = [&](unsigned x) {
+    if (x == total) return total;
+    const int b = seq_of(x);
+    const unsigned nck = num_chunks(seq_len(lens, b, false, &err));
+    return snap(x, (x - pre[(size_t)b]) % nck, nck);
+  };
   if (total == 0) return 0;
   const unsigned grid = ctas_for(total, (unsigned)sms, (unsigned)W);
   const Split ctas(total, grid);
@@ -1378,7 +1430,11 @@ int decode_paged_plan_selfcheck(const int* seq_lens, int B, int HR, int max_len,
   std::vector<std::vector<int64_t>> parts((size_t)B * HR);
   std::vector<unsigned char> used((size_t)2 * sms, 0);
   for (unsigned c = 0; c < grid; ++c) {
-    const unsigned r0 = ctas.start(c), r1 = ctas.start(c + 1);
+    unsigned r0 = ctas.start(c), r1 = ctas.start(c + 1);
+    if (keeps_tiles(most, (unsigned)W)) {
+      r0 = border(r0);
+      r1 = border(r1);
+    }
     const Split warps(r1 - r0, (unsigned)W);
     int cut_tiles = 0;
     int64_t last_cut = -1;
@@ -1386,7 +1442,7 @@ int decode_paged_plan_selfcheck(const int* seq_lens, int B, int HR, int max_len,
       const unsigned x0 = r0 + warps.start(w), n = warps.start(w + 1) - warps.start(w);
       if (n == 0) continue;
       if (x0 != x) return 2;
-      const int b = (int)(std::upper_bound(pre.begin(), pre.end(), x0) - pre.begin()) - 1;
+      const int b = seq_of(x0);
       Cursor cur;
       if (!cur.init(lens, b, seq_len(lens, b, false, &err), x0 - pre[(size_t)b])) return 2;
       int left = 0;
@@ -1404,6 +1460,7 @@ int decode_paged_plan_selfcheck(const int* seq_lens, int B, int HR, int max_len,
         if (++left > 2) return 3;
         const int64_t tile = (int64_t)cur.b * HR + cur.hr;
         if ((s0 < r0 || s1 > r1) && tile != last_cut) {
+          if (keeps_tiles(most, (unsigned)W)) return 4;
           last_cut = tile;
           if (++cut_tiles > 2) return 4;
           const int64_t slot = slot_of(ctas, s0, c);
