@@ -70,7 +70,7 @@ struct Cfg {
   static constexpr int kTensorBytes = kChunk * kRowBytes;       // K or V of a stage
   static constexpr int kStageBytes = 2 * kTensorBytes;
   static constexpr int kWarps = kStageBytes > 8192 ? 4 : 8;
-  static constexpr int kStages = kF8 ? (D == 128 ? 2 : 4) : (D == 64 ? 2 : (NT == 1 ? 3 : 2));
+  static constexpr int kStages = kF8 ? (D == 128 ? 2 : 4) : (NT == 1 ? 3 : 2);
   static constexpr int kRings = kWarps / 4;                     // of a producer warp
   static constexpr int kConsumers = kWarps * 32;
   static constexpr int kThreads = kConsumers + 128;             // + four producer warps
@@ -590,6 +590,9 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     Cursor cur = {0, 0, 0, 0, 0};
     if (count > 0 && !cur.init(lens, sh.start_b[w], sh.start_len[w], sh.start_off[w])) count = 0;
     unsigned issued = 0;
+    // the cache streams through L2 once; queries, tables and states stay (32 x 2k
+    // keys 31.6 us without, 30.2 with)
+    const uint64_t policy = policy_evict_first();
     int pt = -1, pt_b = -1, pt_base = 0;  // kLanes entries of a block table row, one a lane
     bool failed = false;
     uint64_t t0 = 0;                      // since when nothing could be issued
@@ -654,8 +657,9 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
           const uint32_t at = dst + i * (16 / kKeysPerRow) * 128;
 #pragma unroll
           for (int x = 0; x < kBoxes; ++x) {
-            tma_load_2d(at + x * (kChunk * 128), &tmK, bar, 64 * x, y);
-            tma_load_2d(at + x * (kChunk * 128) + C::kTensorBytes, &tmV, bar, 64 * x, y);
+            tma_load_2d_hint(at + x * (kChunk * 128), &tmK, bar, 64 * x, y, policy);
+            tma_load_2d_hint(at + x * (kChunk * 128) + C::kTensorBytes, &tmV, bar, 64 * x, y,
+                             policy);
           }
         }
       }
