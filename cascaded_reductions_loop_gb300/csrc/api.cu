@@ -566,9 +566,9 @@ rf_status rf_attn_decode_paged(const rf_paged_kv* cache, const void* Q, void* O,
 int rf_selftest_append_plan(const int32_t* block_table, const int32_t* seq_lens,
                             const int32_t* cu_seqlens, int B, int total, int num_pages,
                             int page_size, int max_pages, int max_pos) {
-  if (!block_table || !seq_lens || B < 1 || total < 1 || num_pages < 1 || page_size < 1 ||
-      page_size > 128 || max_pages < 1 || max_pos < 0 || (!cu_seqlens && total % B != 0) ||
-      (int64_t)max_pages * page_size > (1ll << 30))
+  if (!block_table || !seq_lens || B < 1 || B > (1 << 20) || total < 1 || total > (1 << 24) ||
+      num_pages < 1 || page_size < 1 || page_size > 128 || max_pages < 1 || max_pos < 0 ||
+      (!cu_seqlens && total % B != 0) || (int64_t)max_pages * page_size > (1ll << 30))
     return -1;
   rf_paged_kv c = {};
   c.block_table = block_table;
@@ -578,16 +578,24 @@ int rf_selftest_append_plan(const int32_t* block_table, const int32_t* seq_lens,
   c.page_size = page_size;
   c.max_pages = max_pages;
   c.Hkv = 1;
-  return append_plan_selfcheck(c, cu_seqlens, total, max_pos);
+  try {
+    return append_plan_selfcheck(c, cu_seqlens, total, max_pos);
+  } catch (...) {                              // no memory for the walk
+    return -1;
+  }
 }
 
 int rf_selftest_decode_paged_plan(const int32_t* seq_lens, int B, int tiles, int max_len,
                                   int warps, int sms) {
   if (!seq_lens || B < 1 || tiles < 1 || max_len < 1 || max_len > (1 << 30) ||
       (warps != 4 && warps != 8) || sms < 1 || sms > (1 << 20) ||
-      (int64_t)B * tiles >= (1ll << 31) || (int64_t)B * tiles * (max_len / 32 + 1) >= (1ll << 31))
+      (int64_t)B * tiles > (1ll << 24) || (int64_t)B * tiles * (max_len / 32 + 1) >= (1ll << 31))
     return -1;
-  return decode_paged_plan_selfcheck(seq_lens, B, tiles, max_len, warps, sms);
+  try {
+    return decode_paged_plan_selfcheck(seq_lens, B, tiles, max_len, warps, sms);
+  } catch (...) {                              // no memory for the walk
+    return -1;
+  }
 }
 
 rf_status rf_selftest_wait_timeout(int timeout_us, rf_stream_t stream) {

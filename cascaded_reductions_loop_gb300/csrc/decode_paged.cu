@@ -885,7 +885,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const bool in = ((valid >> i) & 1) && key0 + 16 * i < cur_len;
-      kscale[i] = kF8 ? (in ? mt.ks[i] : 0.f) : 1.f;
+      kscale[i] = kF8 && in ? mt.ks[i] : 1.f;
       lv[i] = kF8 ? (in ? __log2f(mt.vs[i]) : 0.f) : 0.f;
     }
 
@@ -931,22 +931,31 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     uint32_t pb[2][NT][kF8 ? 1 : 2][2];
     const bool two = kF8 && lv[0] != lv[1];
     float cm[NT][2], cM[NT][2], mu[NT][2], Mu[NT][2], a_o[NT][2];
+    if (tail) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int h2 = 0; h2 < 2; ++h2)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (key0 + 16 * h2 + g + 8 * k >= lim[nt][e] || !((valid >> h2) & 1))
+                s[h2][nt][2 * k + e] = -INFINITY;
+    }
+    // the factors are positive, so the largest product has the largest score; one
+    // that underflows (queries and a page of zeros, whose products are 0 either
+    // way) must not turn a masked -inf into NaN
+    float sc[2][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx[2] = {-INFINITY, -INFINITY};
+        float mx[2];
 #pragma unroll
         for (int h2 = 0; h2 < 2; ++h2) {
-          const float sc = f[nt][e] * kscale[h2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float v = s[h2][nt][2 * k + e] * sc;
-            if (tail && (key0 + 16 * h2 + g + 8 * k >= lim[nt][e] || !((valid >> h2) & 1)))
-              v = -INFINITY;
-            s[h2][nt][2 * k + e] = v;
-            mx[h2] = fmaxf(mx[h2], v);
-          }
+          sc[h2][nt][e] = fmaxf(f[nt][e] * kscale[h2], 1.17549435e-38f);
+          mx[h2] = fmaxf(s[h2][nt][e], s[h2][nt][2 + e]) * sc[h2][nt][e];
         }
         cm[nt][e] = fmaxf(mx[0], mx[1]);
         cM[nt][e] = fmaxf(mx[0] + lv[0], mx[1] + lv[1]);
@@ -996,9 +1005,10 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
           float w[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float v = s[h2][nt][2 * k + e], pr = ex2(v - mu[nt][e]);
+            const float v = s[h2][nt][2 * k + e], x = sc[h2][nt][e];
+            const float pr = ex2(fmaf(v, x, -mu[nt][e]));
             l[nt][e] += pr;
-            w[e] = kF8 ? ex2(v + lv[h2] - Mu[nt][e]) : pr;
+            w[e] = kF8 ? ex2(fmaf(v, x, lv[h2] - Mu[nt][e])) : pr;
           }
           // P^T as B fragments
           if (kF8) {

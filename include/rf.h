@@ -608,8 +608,9 @@ int rf_selftest_moe_plan(int T, int D, int E, int sms);
  * checks that no index leaves its array, that items lie in one page of the
  * cache, that every token that is not skipped is written once, to the slot of
  * its position, that queries get the same positions, and that inconsistent
- * sizes are noticed.  Returns 0 when all of that holds, -1 for refused sizes,
- * else the number (1..5) of the first check that fails.
+ * sizes are noticed.  Returns 0 when all of that holds, -1 for refused sizes
+ * (beside those of that call: B > 2^20, total > 2^24, or no memory for the
+ * walk), else the number (1..5) of the first check that fails.
  */
 int rf_selftest_append_plan(const int32_t* block_table, const int32_t* seq_lens,
                             const int32_t* cu_seqlens, int B, int total, int num_pages,
@@ -623,8 +624,9 @@ int rf_selftest_append_plan(const int32_t* block_table, const int32_t* seq_lens,
  * are all 32-key chunks of all tiles once, in order, that a warp leaves at most
  * two unfinished tiles and a CTA at most two cut ones, in workspace slots of
  * their own, and that the merge reads a tile's parts in key order.  Returns 0
- * when all of that holds, -1 for refused sizes, else the number (1..5) of the
- * first check that fails.
+ * when all of that holds, -1 for refused sizes (B * tiles > 2^24, 2^31 chunks or
+ * more, or no memory for the walk), else the number (1..5) of the first check
+ * that fails.
  */
 int rf_selftest_decode_paged_plan(const int32_t* seq_lens, int B, int tiles, int max_len,
                                   int warps, int sms);

@@ -534,6 +534,22 @@ def test_attn_pages_of_very_different_value_scales(rf):
     check_attn(rf, bt, q, 0.125, "value scales")
 
 
+@pytest.mark.parametrize("q_exp", [0, -12, -60, -126])
+def test_attn_pages_of_zeros(rf, q_exp):
+    """Zero keys (the smallest scale), zero values, and queries so small that the
+    product of all factors underflows; the last page is cut short."""
+    for Tq in (1, 3):
+        bt = Batch("e4m3", [5, 37, 64], 1, 64, 16, seed=256).garbage()
+        for b, n in enumerate(bt.lens):
+            page = int(bt.table[b, (n - 1) // 16])
+            bt.pages[0][page, 0, :(n - 1) % 16 + 1] = 0
+            bt.scale[0][page] = np.float32(2.0 ** -126)
+        bt.pages[1][int(bt.table[1, 0])] = 0
+        bt.scale[1][int(bt.table[1, 0])] = np.float32(2.0 ** -126)
+        q = (torch.randn(3, Tq, 4, 64, generator=_gen(257)) * 2.0 ** q_exp).to(BF16)
+        check_attn(rf, bt, q, 0.125, f"zeros, queries of 2^{q_exp}")
+
+
 def test_attn_scales_that_are_no_powers_of_two(rf):
     bt = Batch("e4m3", [300], 2, 128, 64, seed=254)
     bt.scale *= np.float32(1.2345)
