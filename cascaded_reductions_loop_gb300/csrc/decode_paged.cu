@@ -482,17 +482,18 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
   const int64_t n_qo = (int64_t)lens.B * p.Tq * p.Hq * D;     // elements of Q and O
 
   // ---- plan: add up all lengths; find where each warp's range begins
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < W; ++w)
-      for (int i = 0; i < S; ++i) {
-        // the copies' bytes and, for E4M3, the two lanes that fetch scales
-        mbar_init(smem_u32(&sh.full[w][i]), kF8 ? 3 : 1);
-        mbar_init(smem_u32(&sh.empty[w][i]), 1);
-      }
+  if (warp == W + 3) {                 // while the first warps fetch their lengths
+    for (int i = lane; i < W * S; i += 32) {
+      // the copies' bytes and, for E4M3, the two lanes that fetch scales
+      mbar_init(smem_u32(&sh.full[i / S][i % S]), kF8 ? 3 : 1);
+      mbar_init(smem_u32(&sh.empty[i / S][i % S]), 1);
+    }
     fence_mbar_init();
-    sh.fail = 0;
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
+    if (lane == 0) {
+      sh.fail = 0;
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+    }
   }
   const bool consumer = warp < W;
   if (consumer && lane < 2) sh.has[warp][lane] = 0;
