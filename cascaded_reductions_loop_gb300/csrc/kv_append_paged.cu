@@ -20,9 +20,9 @@
 // heads of one token (rows kernel).  For E4M3 a scale must have one owner, so
 // that no atomics are needed: a work item is one page of one sequence that
 // receives tokens.
-//  - step kernel (one new token a sequence): one lane group for the key row
-//    and one for the value row of an (item, head); a page that has to be
-//    rescaled is rescaled by the whole warp.
+//  - step kernel (one new token a sequence, or up to 8, the same for all): one
+//    lane group for the key rows and one for the value rows of an (item, head);
+//    a page that has to be rescaled is rescaled by the whole warp.
 //  - prompt kernel: CTAs that stay, each with an equal share of the (item, head)
 //    pairs; a head's new rows are held in registers between the absmax and the
 //    quantisation, so each is read once.
@@ -115,6 +115,11 @@ __device__ __forceinline__ float absmax8(const Raw8<__nv_bfloat16>& x) {
     }
   }
   return __uint_as_float(a << 16);
+}
+// Largest of the lanes' magnitudes (>= 0, so their bits compare as they do): one
+// instruction where a butterfly takes five shuffles.
+__device__ __forceinline__ float group_max(unsigned lanes, float a) {
+  return __uint_as_float(__reduce_max_sync(lanes, __float_as_uint(a)));
 }
 __device__ __forceinline__ Row8 as_row(const Raw8<__nv_bfloat16>& x) {
   Row8 y;
@@ -374,9 +379,11 @@ __global__ void __launch_bounds__(kThreads)
   if (blockIdx.x == 0) check_seqs(sq, (int)threadIdx.x, kThreads, err);
 }
 
-// ------------------------------------------------------------- one token a sequence
+// ------------------------------------------------------------- a few tokens a sequence
 
-template <int D, bool kSplit>
+constexpr int kStepTokens = 8;
+
+template <int D, int TOK, bool kSplit>
 __global__ void __launch_bounds__(kThreads)
     append_step_kernel(const Seqs sq, const NormRope nr, const RowsIn<bf16> k, const RowsIn<bf16> v,
                        const RowsIn<bf16> q, const RowsOut<bf16> qo, int Hq, const Cache cache,
@@ -391,40 +398,52 @@ __global__ void __launch_bounds__(kThreads)
   const bool is_v = grp & 1;
   const int64_t u =
       ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kPairs + (grp >> 1);
-  const int b = (int)(u / sq.Hkv), h = (int)(u % sq.Hkv);
+  const int pages_each = pages_of(sq.n_uniform, sq.page_size);
+  const int x = (int)(u / sq.Hkv), h = (int)(u % sq.Hkv);
+  const int b = TOK == 1 ? x : x / pages_each;
   Item it = {0, 0, 0, 0, 0};
-  if (b < sq.B) it = item_of(sq, b, 0, h == 0 && !is_v && li == 0, err);
-  const bool active = it.n > 0;
+  if (b < sq.B) it = item_of(sq, b, x - b * pages_each, h == 0 && !is_v && li == 0, err);
 
   const RowsIn<bf16>& in = is_v ? v : k;
-  Raw8<bf16> x = {};
-  if (active)
-    x = load8<bf16>(in.p, (int64_t)it.t0 * in.ld + (int64_t)h * D + 8 * li,
-                    (int64_t)(sq.total - 1) * in.ld + (int64_t)sq.Hkv * D, err);
-  const bf16* wk = static_cast<const bf16*>(nr.wk);
-  const Coef cf = load_coef<bf16, D, kSplit>(nr, wk, it.pos0, li, active && !is_v, err);
-  Row8 y = norm_rope_row<bf16, D, kSplit>(nr, x, wk != nullptr, cf, li);
-  if (is_v) y = as_row(x);
-
-  const int64_t head = (int64_t)it.phys * sq.Hkv + h;         // (page, head)
-  const int64_t n_pages = (int64_t)sq.num_pages * sq.Hkv * sq.page_size * D;
-  const int64_t row = (head * sq.page_size + it.off) * D + 8 * li;
-  uint8_t* pages = is_v ? cache.pages[1] : cache.pages[0];
-  float a = absmax8(y);
+  const int64_t n_in = (int64_t)(sq.total - 1) * in.ld + (int64_t)sq.Hkv * D;
+  Raw8<bf16> raw[TOK];
 #pragma unroll
-  for (int o = LG / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  for (int i = 0; i < TOK; ++i) {
+    raw[i] = {};
+    if (i < it.n)
+      raw[i] = load8<bf16>(in.p, (int64_t)(it.t0 + i) * in.ld + (int64_t)h * D + 8 * li, n_in, err);
+  }
+  const int64_t head = (int64_t)it.phys * sq.Hkv + h;         // (page, head)
   float* sc = is_v ? cache.scale[1] : cache.scale[0];
   const int64_t n_sc = (int64_t)sq.num_pages * sq.Hkv;
-  const float s_old = active && it.off > 0 && RF_IN(err, head, n_sc) ? sc[head] : 0.f;
-  const float s = new_scale(a, s_old, it.off);
-  const bool grow = active && it.off > 0 && s > s_old;
-  const unsigned growing = __ballot_sync(0xffffffffu, grow && li == 0);   // after everyone's load
-  if (active) {
-    const float inv = 1.f / s;                                // exact: a power of two
-    if (RF_IN(err, row + 7, n_pages))
-      *reinterpret_cast<uint2*>(pages + row) = quantise8(y, inv);
-    if (li == 0 && RF_IN(err, head, n_sc)) sc[head] = s;
+  const float s_old = it.n > 0 && it.off > 0 && RF_IN(err, head, n_sc) ? sc[head] : 0.f;
+  const bf16* wk = static_cast<const bf16*>(nr.wk);
+  const CoefSource<bf16, D, kSplit> source(nr, wk, li, err);
+  Row8 y[TOK];
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < TOK; ++i) {
+    const Coef cf = source.get(nr, it.pos0 + i, li, i < it.n && !is_v, err);
+    y[i] = norm_rope_row<bf16, D, kSplit>(nr, raw[i], wk != nullptr, cf, li);
+    if (is_v) y[i] = as_row(raw[i]);
+    if (i < it.n) a = fmaxf(a, absmax8(y[i]));
   }
+  constexpr unsigned kGroup = (1u << LG) - 1u;
+  a = group_max(kGroup << (grp * LG), a);
+  const float s = new_scale(a, s_old, it.off);
+  const bool grow = it.n > 0 && it.off > 0 && s > s_old;
+  const unsigned growing = __ballot_sync(0xffffffffu, grow && li == 0);   // after everyone's load
+
+  const int64_t n_pages = (int64_t)sq.num_pages * sq.Hkv * sq.page_size * D;
+  uint8_t* pages = is_v ? cache.pages[1] : cache.pages[0];
+  const float inv = 1.f / s;                                  // exact: a power of two
+#pragma unroll
+  for (int i = 0; i < TOK; ++i) {
+    const int64_t row = (head * sq.page_size + it.off + i) * D + 8 * li;
+    if (i < it.n && RF_IN(err, row + 7, n_pages))
+      *reinterpret_cast<uint2*>(pages + row) = quantise8(y[i], inv);
+  }
+  if (it.n > 0 && li == 0 && RF_IN(err, head, n_sc)) sc[head] = s;
   // pages whose scale grew: the warp rescales the off * D codes held already
   for (unsigned m = growing; m; m &= m - 1) {
     const int src = __ffs(m) - 1;
@@ -565,7 +584,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH)
       for (int i = 0; i < SW; ++i) a[1] = fmaxf(a[1], absmax8(vx[i]));
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        a[w] = warp_max(a[w]);
+        a[w] = group_max(0xffffffffu, a[w]);
         if (lane == 0) red[turn][w][warp] = a[w];
       }
       __syncthreads();                   // after it, too: everyone has read the old scales
@@ -573,7 +592,8 @@ __global__ void __launch_bounds__(TH, 1024 / TH)
       float inv[2];
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const float m = warp_max(lane < (int)blockDim.x / 32 ? red[turn][w][lane] : 0.f);
+        const float m =
+            group_max(0xffffffffu, lane < (int)blockDim.x / 32 ? red[turn][w][lane] : 0.f);
         const float s = new_scale(m, s_old[w], it.off);
         inv[w] = 1.f / s;
         if (threadIdx.x == 0 && RF_IN(err, head, n_sc)) cache.scale[w][head] = s;
@@ -612,19 +632,28 @@ cudaError_t launch(const Seqs& sq, const NormRope& nr, const RowsIn<bf16>& k,
     const int64_t kv = ceil_div((int64_t)sq.total * ceil_div(sq.Hkv, nh), per);
     const int64_t q_ctas = ceil_div((int64_t)sq.total * ceil_div(Hq, nhq), per);
     const unsigned grid = (unsigned)(kv + q_ctas);
+    // batches of two heads of 64 (19.5 against 21.5 us with four for 6.6k tokens of
+    // 16 heads) and of four of 128 (15.7 against 16.9 with two for 8192 of 8)
     if (nh > 1)
-      append_rows_kernel<D, 4, kSplit><<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq, nh, nhq,
+      append_rows_kernel<D, D / 32, kSplit><<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq, nh, nhq,
                                                                  cache, (int)kv, err);
     else
       append_rows_kernel<D, 1, kSplit><<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq, nh, nhq,
                                                                  cache, (int)kv, err);
     return cudaGetLastError();
   }
-  if (!sq.cu && sq.n_uniform == 1) {
-    const int64_t kv = ceil_div((int64_t)sq.B * sq.Hkv, kThreads / (2 * LG));
+  if (!sq.cu && sq.n_uniform <= kStepTokens) {
+    // 32 sequences of 4 tokens and 8 heads: 8.9 us in the prompt kernel
+    const int64_t items = num_items(sq.total, sq.B, sq.n_uniform, false, sq.page_size);
+    const int64_t kv = ceil_div(items * sq.Hkv, kThreads / (2 * LG));
     const int64_t q_ctas = ceil_div((int64_t)sq.total * Hq, per);
-    append_step_kernel<D, kSplit><<<(unsigned)(kv + q_ctas), kThreads, 0, s>>>(
-        sq, nr, k, v, q, qo, Hq, cache, (int)kv, err);
+    const unsigned grid = (unsigned)(kv + q_ctas);
+    if (sq.n_uniform == 1)
+      append_step_kernel<D, 1, kSplit><<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq, cache,
+                                                                 (int)kv, err);
+    else
+      append_step_kernel<D, kStepTokens, kSplit><<<grid, kThreads, 0, s>>>(sq, nr, k, v, q, qo, Hq,
+                                                                           cache, (int)kv, err);
     return cudaGetLastError();
   }
   const int pieces = sq.page_size * D / 8;

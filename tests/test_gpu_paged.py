@@ -293,6 +293,10 @@ APPENDS = [
     ("bf16", 16, 128, 1, [45, 18, 0], [20, 18, 2], True, (96, False, False)),
     ("e4m3", 64, 128, 2, [90, 64, 7, 0], [5] * 4, False, (128, False, True)),
     ("bf16", 32, 64, 2, [33, 66], [33] * 2, False, (64, False, True)),
+    ("e4m3", 16, 128, 3, [8, 19, 40, 0, 16, 17, 24], [8] * 7, False, (128, False, True)),
+    ("e4m3", 64, 64, 5, [3, 66, 65, 0, 64, 67], [3] * 6, False, (32, True, False)),
+    ("e4m3", 32, 128, 2, [9, 40, 33, 32], [9] * 4, False, (128, False, True)),
+    ("e4m3", 128, 64, 2, [2, 129], [2] * 2, False, (64, False, True)),
 ]
 
 
