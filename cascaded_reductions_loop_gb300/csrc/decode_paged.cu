@@ -44,6 +44,28 @@
 // tickets are zeroed by a small kernel before, whose programmatic dependent
 // this one is.
 //
+// Inside a CTA: eight consumer warps (four where a stage is 16 KB), each with a
+// ring of two to four stages of 32 keys, and four producer warps, half a warp a
+// ring, that look pages up, issue the copies and fetch the scales.  With the
+// copies issued by the consumers themselves a chunk took 1.7 us of a warp's
+// time, 0.65 of it for the issue; now 1.05, and eight warps outrun memory.
+//
+// Measured (GB300, CUDA graph, inputs larger than L2; copy rate 6788 GB/s):
+//   32 x 24-32k keys, 8 kv heads of 4, E4M3   275 us   1.86 GB   6.8 TB/s
+//   32 x 2048 keys, the same                  30 us    0.13 GB   4.4 TB/s
+//   9 x 3-20k keys, 7 kv heads of 5, bf16     60 us    0.37 GB   6.2 TB/s
+//   48 x 1-4k keys, 16 heads of 64, bf16      67 us    0.39 GB   5.8 TB/s
+//   16 x 0.5-8k keys, 4 kv heads of 8, four query tokens, E4M3   43 us (32 rows
+//     are two tiles; a warp's chunk of 16 rows takes 2.1 us, latency of the
+//     softmax and MMA chains, so memory waits)
+//   1 x 1000 keys, 8 kv heads of 4, E4M3      10.8 us, all latency: launch 2, the
+//     plan 2, page and first chunk 1.5, the chunk 1, merges 3.
+// Of the 10 us that a mid-sized call takes above its bytes, about 3.5 pass before
+// the first copy, 1.5 until the first burst is in, and 5 from the median warp's
+// end to the last merge.  Tried and left out: 32-row tiles with four warps (63
+// against 43 us for the four query tokens: one warp a scheduler does not hide
+// its own latency); values fetched during the softmax at eight rows (275 -> 280).
+//
 // Masked places.  Keys behind a sequence's last may hold anything: scores are
 // selected, not added to, and values are replaced by zero.  Where the last Tq
 // keys hold an infinity or NaN, which rows that may not read them would meet

@@ -5,6 +5,15 @@
 // lane group of d / 8 lanes takes nh heads of one token, in batches of HB whose
 // 16-byte loads are in flight together while the batch before is worked on;
 // the token's angles and the weights are loaded once for all of them.
+//
+// Measured (GB300, CUDA graph, inputs larger than L2; copy rate 6788 GB/s):
+//   8191 tokens, 32 + 8 heads of 128, bf16, norm, half-split    31 us, 5.5 TB/s
+//   32768 tokens, the same                                     107 us, 6.4 TB/s
+//   4096 tokens, 16 + 16 heads of 64, fp32, half rotated        14 us, 4.8 TB/s
+//   32 tokens, 32 + 8 heads of 128                             2.3 us: launch
+// One head a lane group, everything made anew for it, took 65 us for the first:
+// 186 instructions for 32 lanes' loads of 16 bytes, and the issue slots bound it.
+// About 6 us of a call do not depend on its size (launch, first and last wave).
 #include "norm_rope.cuh"
 
 namespace rf {
