@@ -518,6 +518,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH)
   const int64_t n_sc = (int64_t)sq.num_pages * sq.Hkv;
   const bool has_w = nr.wk != nullptr;
   __shared__ Item found;
+  __shared__ int taken;
   __shared__ float red[2][2][TH / 32];               // of two heads in turn: one barrier a head
   if (blockIdx.x == 0) check_seqs(sq, (int)threadIdx.x, (int)blockDim.x, err);
 
@@ -525,14 +526,16 @@ __global__ void __launch_bounds__(TH, 1024 / TH)
   for (int u = u0; u < u1; ++x, h = 0) {             // items
     const int h_end = min(sq.Hkv, h + (u1 - u));
     u += h_end - h;
-    // the sequences are looked through in parallel; one thread finds the item
-    if (threadIdx.x == 0) found.n = 0;
+    // the sequences are looked through in parallel; one thread finds the item.
+    // With cu_seqlens out of order several may: the first takes it, since words
+    // from two of them would make an item of no sequence's, out of all bounds
+    if (threadIdx.x == 0) found.n = taken = 0;
     __syncthreads();
     for (int b = threadIdx.x; b < sq.B; b += blockDim.x) {
       int pg;
       if (item_is_of(sq, x, b, &pg, err)) {
         const Item i = item_of(sq, b, pg, h == 0, err);
-        if (i.n > 0) found = i;
+        if (i.n > 0 && atomicExch(&taken, 1) == 0) found = i;
       }
     }
     __syncthreads();
@@ -768,13 +771,13 @@ int append_plan_selfcheck(const PagedKV& c, const int* cu, int total, int max_po
       const Item i = item_of(sq, b, p, true, &err);
       if (i.n == 0) continue;
       if (order && it.n != 0) return 2;
-      it = i;
+      it = i;                                  // any of them may be the one that is taken
+      if (it.n < 0 || it.off < 0 || it.off + it.n > c.page_size || it.phys < 0 ||
+          it.phys >= c.num_pages || it.t0 < 0 || it.t0 + it.n > total)
+        return 2;
     }
     if (err & kDevErrBounds) return 1;
     if (it.n == 0) continue;
-    if (it.n < 0 || it.off < 0 || it.off + it.n > c.page_size || it.phys < 0 ||
-        it.phys >= c.num_pages || it.t0 < 0 || it.t0 + it.n > total)
-      return 2;
     for (int i = 0; i < it.n; ++i) {
       if (order &&
           (pos_of[(size_t)it.t0 + i] != -1 || (it.pos0 + i) % c.page_size != it.off + i))

@@ -40,6 +40,9 @@ def main():
     for case in range(len(T.APPENDS)):
         T.test_append(rf, case)
         ok(f"append {T.APPENDS[case][:4]}")
+    for between, tokens in [(1, 100), (41, 2000)]:
+        T.test_append_of_tokens_that_several_sequences_claim(rf, between, tokens)
+        ok(f"append, {tokens} tokens claimed twice")
     for case in range(len(T.ATTNS)):
         if sum(T.ATTNS[case][6]) < 30000:
             T.test_attn_decode_paged(rf, case)

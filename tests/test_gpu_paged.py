@@ -405,6 +405,43 @@ def test_append_inconsistent_sequences_are_skipped(rf, use_cu):
     assert torch.equal(q_out[[0, 1, 6, 7]].cpu(), q[[0, 1, 6, 7]])
 
 
+@pytest.mark.parametrize("between,tokens", [(1, 100), (41, 2000)])
+def test_append_of_tokens_that_several_sequences_claim(rf, between, tokens):
+    """cu_seqlens that fall back to 0: the first and the last sequence claim the
+    same tokens, and (in one warp, and in two) some of the same items.  Reported;
+    a page is left alone or gets what one of them appends, never a mixture."""
+    B = between + 2
+    lens = [tokens] + [0] * between + [tokens]
+    bt = Batch("e4m3", lens, 2, 64, 16, seed=59)
+    cache = bt.device(rf, lens)
+    cu = [0] + [tokens] * between + [0, tokens]
+    claims = [set(range(c // 16 + 2 * b, c // 16 + 2 * b + -(-tokens // 16)))
+              for b, c in ((0, 0), (B - 1, 0))]
+    assert claims[0] & claims[1]
+    g = _gen(60)
+    k, v = (torch.randn(tokens, 2, 64, generator=g).to(BF16) for _ in range(2))
+    rf.rf_kv_append_paged(cache, k.cuda(), v.cuda(), None,
+                          torch.tensor(cu, dtype=torch.int32).cuda())
+    assert rf.rf_get_device_status() == rf.RF_ERR_DEVICE_INPUT
+    before = (bt.pages[0], bt.pages[1], bt.scale[0], bt.scale[1])
+    after = before
+    for b in (0, B - 1):
+        after = G.append(*after, bt.table.numpy()[b:b + 1], [tokens], [tokens], k, v)
+    got = [t.cpu().numpy() for t in (bt.k.t, bt.v.t, bt.ks, bt.vs)]
+    n = bt.num_pages
+    same = [[(x[i] == y[i].astype(x.dtype)).all() for i in range(n)] for ref in (before, after)
+            for x, y in zip(got, ref)]
+    left, done = np.array(same[:4]).all(0), np.array(same[4:]).all(0)
+    assert (left | done).all()
+    own = [bt.table.numpy()[b, :-(-tokens // 16)] for b in (0, B - 1)]
+    first = sorted(claims[0] - claims[1])            # items of the first sequence alone
+    assert done[own[0][first]].all()
+    last = sorted(x - min(claims[1]) for x in claims[1] - claims[0])
+    assert done[own[1][last]].all()
+    bt.k.check("k")
+    bt.v.check("v")
+
+
 # ------------------------------------------------------------------ attention
 
 

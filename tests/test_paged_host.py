@@ -165,6 +165,16 @@ def test_append_plan_stays_in_bounds_with_disordered_cu_seqlens(rf, seed):
     assert rf.rf_selftest_append_plan(table, lens, cu, total, 20, ps, 0) == 0
 
 
+@pytest.mark.parametrize("between,tokens", [(1, 100), (41, 2000)])
+def test_append_plan_with_items_of_several_sequences(rf, between, tokens):
+    """Two sequences claim the same items: each claim stays in bounds."""
+    cu = torch.tensor([0] + [tokens] * between + [0, tokens], dtype=torch.int32)
+    B, pages = between + 2, -(-tokens // 16)
+    lens = torch.tensor([tokens] + [0] * between + [tokens], dtype=torch.int32)
+    table = torch.arange(B * pages, dtype=torch.int32).view(B, pages)
+    assert rf.rf_selftest_append_plan(table, lens, cu, tokens, B * pages, 16, 0) == 0
+
+
 @pytest.mark.parametrize("seed", range(80))
 def test_decode_plan(rf, seed):
     rng = random.Random(seed)
