@@ -517,30 +517,36 @@ __global__ void __launch_bounds__(TH, 1024 / TH)
   const int64_t n_pages = (int64_t)sq.num_pages * sq.Hkv * sq.page_size * D;
   const int64_t n_sc = (int64_t)sq.num_pages * sq.Hkv;
   const bool has_w = nr.wk != nullptr;
-  __shared__ Item found;
-  __shared__ int taken;
+  __shared__ Item found[2];                          // of two items in turn
+  __shared__ int owner[2];
   __shared__ float red[2][2][TH / 32];               // of two heads in turn: one barrier a head
   if (blockIdx.x == 0) check_seqs(sq, (int)threadIdx.x, (int)blockDim.x, err);
 
-  int x = u0 / sq.Hkv, h = u0 - x * sq.Hkv, turn = 0;
-  for (int u = u0; u < u1; ++x, h = 0) {             // items
+  int x = u0 / sq.Hkv, h = u0 - x * sq.Hkv, turn = 0, now = 0;
+  if (threadIdx.x == 0) found[0].n = 0, owner[0] = sq.B;
+  __syncthreads();
+  for (int u = u0; u < u1; ++x, h = 0, now ^= 1) {   // items
     const int h_end = min(sq.Hkv, h + (u1 - u));
     u += h_end - h;
-    // the sequences are looked through in parallel; one thread finds the item.
-    // With cu_seqlens out of order several may: the first takes it, since words
-    // from two of them would make an item of no sequence's, out of all bounds
-    if (threadIdx.x == 0) found.n = taken = 0;
-    __syncthreads();
-    for (int b = threadIdx.x; b < sq.B; b += blockDim.x) {
+    // the sequences are looked through in parallel, and one thread finds the item.
+    // With cu_seqlens out of order several may: the lowest sequence has it, in
+    // every CTA that takes heads of it (words from two would make an item of no
+    // sequence's, out of all bounds)
+    Item mine = {0, 0, 0, 0, 0};
+    int mine_of = sq.B;
+    for (int b = threadIdx.x; b < sq.B && mine.n == 0; b += blockDim.x) {
       int pg;
       if (item_is_of(sq, x, b, &pg, err)) {
-        const Item i = item_of(sq, b, pg, h == 0, err);
-        if (i.n > 0 && atomicExch(&taken, 1) == 0) found = i;
+        mine = item_of(sq, b, pg, h == 0, err);
+        mine_of = b;
       }
     }
+    if (mine.n > 0) atomicMin(&owner[now], mine_of);
     __syncthreads();
-    const Item it = found;
-    __syncthreads();                                 // before the next item's search
+    if (mine.n > 0 && owner[now] == mine_of) found[now] = mine;
+    if (threadIdx.x == 0) found[now ^ 1].n = 0, owner[now ^ 1] = sq.B;   // read before the barrier
+    __syncthreads();
+    const Item it = found[now];
     if (it.n == 0) continue;
 
     int64_t at_k = (int64_t)(it.t0 + r) * k.ld + (int64_t)h * D + 8 * li;

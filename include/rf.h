@@ -493,10 +493,10 @@ rf_status rf_qk_norm_rope(int dtype, const void* Q, int64_t ldq, const void* K, 
  * are its rows of Qo.  A sequence whose length is below its new tokens, above
  * max_pages * page_size, or (with rotation) above max_pos, or whose entries of
  * cu_seqlens are out of order, is skipped the same way and reported as
- * RF_ERR_DEVICE_INPUT (where the entries that are out of order give tokens to
- * several sequences, an E4M3 cache's pages may each get one sequence's or none);
- * so are the new keys and values of a page outside the cache.  Slots that get no new token keep their contents (but for the
- * rescaling).
+ * RF_ERR_DEVICE_INPUT (entries out of order may give tokens to several
+ * sequences; an E4M3 cache's page then gets its new tokens whole or not at all);
+ * so are the new keys and values of a page outside the cache.  Slots that get
+ * no new token keep their contents (but for the rescaling).
  * Errors: RF_ERR_INVALID_ARG (null or misaligned pointer or stride, sizes of
  * rf_paged_kv, total < 1 or not a multiple of B without cu_seqlens, a grid of
  * 2^31 CTAs or more), RF_ERR_UNSUPPORTED (d or page_size not covered),
