@@ -406,7 +406,8 @@ class rf_paged_kv:
     k_pages, v_pages: [num_pages, Hkv, page_size, d], bf16 or uint8 E4M3 codes;
     k_scale, v_scale: fp32 [num_pages, Hkv] (E4M3 only); block_table: int32
     [B, max_pages]; seq_lens: int32 [B], the lengths after the call's new
-    tokens.  Holds the tensors; their contents may change between calls."""
+    tokens.  Holds the tensors and their addresses: their contents may change
+    between calls, their storage may not (no resize_, set_ or .data = ...)."""
 
     def __init__(self, k_pages, v_pages, block_table, seq_lens, k_scale=None, v_scale=None):
         _on_device("k_pages", k_pages)
@@ -453,7 +454,8 @@ class rf_norm_rope:
     """Norm and rotation of query and key heads (struct rf_norm_rope).  cos, sin:
     fp32 [max_pos, rot_dim / 2], or None: no rotation; interleaved: rotate pairs
     (2j, 2j + 1) instead of (j, j + rot_dim / 2); q_weight, k_weight: [d] of the
-    rows' type, or None: no norm.  Holds the tensors."""
+    rows' type, or None: no norm.  Holds the tensors and their addresses, as
+    rf_paged_kv does."""
 
     def __init__(self, cos=None, sin=None, interleaved=False, q_weight=None, k_weight=None,
                  eps: float = 1e-6):
@@ -575,6 +577,8 @@ def rf_attn_decode_paged(cache, q, o, scale: float, workspace, stream=None) -> N
     wp, ws_bytes = None, 0
     if workspace is not None:
         _on_device("workspace", workspace, dev)
+        if not workspace.is_contiguous():       # an expanded tensor has less storage than bytes
+            raise ValueError("workspace must be contiguous")
         wp, ws_bytes = workspace.data_ptr(), workspace.nbytes
     _check(lib.rf_attn_decode_paged(cache._ref, qp, op, shape[-2], shape[1] if n == 4 else 1, scale,
                                     wp, ws_bytes, _stream(stream)), "rf_attn_decode_paged")

@@ -58,11 +58,11 @@
 //   16 x 0.5-8k keys, 4 kv heads of 8, four query tokens, E4M3   43 us (32 rows
 //     are two tiles; a warp's chunk of 16 rows takes 2.1 us, latency of the
 //     softmax and MMA chains, so memory waits)
-//   1 x 1000 keys, 8 kv heads of 4, E4M3      10.8 us, all latency: launch 2, the
-//     plan 2, page and first chunk 1.5, the chunk 1, merges 3.
-// Of the 10 us that a mid-sized call takes above its bytes, about 3.5 pass before
-// the first copy, 1.5 until the first burst is in, and 5 from the median warp's
-// end to the last merge.  Tried and left out: 32-row tiles with four warps (63
+//   1 x 1000 keys, 8 kv heads of 4, E4M3      10.8 us, all latency: the plan 2,
+//     page and first chunk 1.5, the chunk 1 (clock stamps); launch and merges.
+// Of what a mid-sized call takes above its bytes (10 us for 32 x 2048 keys), 3.6
+// pass before the first copy and 1.5 until it is in; the rest is the spread of the
+// warps' ends and the merges.  Tried and left out: 32-row tiles with four warps (63
 // against 43 us for the four query tokens: one warp a scheduler does not hide
 // its own latency); values fetched during the softmax at eight rows (275 -> 280).
 //

@@ -33,9 +33,9 @@
 //   bf16 cache, 32768 tokens of 8 heads of 128   47 us, 6.1 TB/s: memory
 //   bf16 cache, 11 prompts, 6.6k tokens of 16 heads of 64   19.6 us, 5.5 TB/s
 //   E4M3 cache, 32768 tokens of 8 heads of 128   62 us, 3.5 TB/s: instructions
-//     (some 300 for 32 lanes' eight keys and eight values: norm, rotation, two
-//     maxima, two quantisations; issue slots 55 % full) and the barrier between a
-//     head's absmax and its quantisation
+//     (norm, rotation, two maxima and two quantisations for eight keys and eight
+//     values a lane; issue slots 55 % full) and the barrier between a head's
+//     absmax and its quantisation
 //   E4M3 cache, 7 prompts, 10.7k tokens of 8 heads of 128   26 us
 //   E4M3 step, 32 sequences, 8 kv and 32 query heads   3.2 us: launch latency
 // Steps of the E4M3 prompt kernel, for the 7 prompts: one CTA an (item, head) with

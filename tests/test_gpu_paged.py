@@ -809,6 +809,16 @@ def test_attn_is_deterministic_and_ignores_the_workspace(rf):
     assert rf.rf_get_device_status() == rf.RF_OK
 
 
+def test_attn_refuses_an_expanded_workspace(rf):
+    bt = Batch("bf16", [5], 1, 64, 16, seed=3)
+    cache = bt.device(rf)
+    q = torch.zeros(1, 1, 64, dtype=BF16, device="cuda")
+    n = rf.rf_attn_decode_paged_workspace_size(1, 1, 1, 1, 64)
+    with pytest.raises(ValueError, match="workspace"):
+        rf.rf_attn_decode_paged(cache, q, torch.empty_like(q), 1.0,
+                                torch.zeros(1, dtype=torch.uint8, device="cuda").expand(n))
+
+
 def test_two_streams_with_workspaces_of_their_own(rf):
     """Two caches at once on two streams, outputs as when run one by one."""
     sets = []
