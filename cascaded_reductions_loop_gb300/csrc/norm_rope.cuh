@@ -162,6 +162,9 @@ struct CoefSource {
         r.a[k] = fmul2(r.a[k], own.pair(k));
         r.b[k] = fmul2(r.b[k], kSplit ? other.pair(k) : own.swapped(k));
       }
+      // unrotated: the partner's term is +0 * -0 = -0, which changes neither zero's
+      // sign (and is not made from weights, one of which may be infinite)
+      if (8 * li >= nr.rot) r.b[k] = f2(-0.f, -0.f);
     }
     return r;
   }
@@ -191,8 +194,8 @@ __device__ __forceinline__ Row8 norm_rope_row(const NormRope& nr, const Raw8<T>&
     for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if (has_w) rstd = rsqrtf(fmaf(ss, 1.f / D, nr.eps));
   }
-  // partners; zeros where nothing is rotated, since their B is 0 and x may be
-  // an infinity
+  // partners; +0 where nothing is rotated, since their B is -0 and x may be an
+  // infinity
   const bool rotated = 8 * li < nr.rot;
   const int src = kSplit && rotated ? partner_lane(nr, li) : li;
   Raw8<T> p;
