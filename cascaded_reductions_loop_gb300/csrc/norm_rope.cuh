@@ -8,7 +8,7 @@
 //     (a, b) -> (a cos - b sin, b cos + a sin),
 // the pair j being elements (j, j + rot / 2) (half-split) or (2j, 2j + 1)
 // (interleaved).  Both forms, and unrotated elements, are one formula,
-//     out_i = rstd * (x_i A_i + x_partner(i) B_i),
+//     out_i = (x_i rstd) A_i + (x_partner(i) rstd) B_i,
 //     A_i = w_i cos,   B_i = -+ w_partner(i) sin   (a: -, b: +),
 // with the partner in the lane rot / 16 away or in the same lane.  A and B
 // depend on the token and on queries or keys only, so a lane group makes them
@@ -208,9 +208,8 @@ __device__ __forceinline__ Row8 norm_rope_row(const NormRope& nr, const Raw8<T>&
   Row8 y;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint64_t t =
-        ffma2(kSplit ? p.pair(k) : p.swapped(k), cf.b[k], fmul2(x.pair(k), cf.a[k]));
-    y.v[k] = fmul2(t, r2);
+    const uint64_t t = fmul2(fmul2(x.pair(k), r2), cf.a[k]);
+    y.v[k] = ffma2(fmul2(kSplit ? p.pair(k) : p.swapped(k), r2), cf.b[k], t);
   }
   return y;
 }

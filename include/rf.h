@@ -426,7 +426,9 @@ typedef struct {
  *     y = x * rsqrt(mean(x^2) + eps) * weight         (where weight is given)
  *     (a, b) <- (a cos - b sin, b cos + a sin)        (where cos, sin are)
  * for the pairs of y's first rot_dim elements: (j, j + rot_dim / 2), or, with
- * interleaved = 1, (2j, 2j + 1); j = 0 .. rot_dim / 2 - 1.
+ * interleaved = 1, (2j, 2j + 1); j = 0 .. rot_dim / 2 - 1.  A finite row whose
+ * mean of squares is beyond fp32's range (elements above 1e18 or so) becomes
+ * zeros.
  *   cos, sin   device fp32 [max_pos][rot_dim / 2], or both NULL: no rotation.
  *   rot_dim    a multiple of 16, 16 .. d.
  *   q_weight, k_weight   device [d], of the rows' type; NULL: no norm.

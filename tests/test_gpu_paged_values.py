@@ -86,3 +86,32 @@ def test_an_infinite_weight_spoils_its_own_element_only(rf):
         ref = G.norm_rope(x, pos, cos, sin, inter, torch.ones(128, dtype=BF16))
         assert_rows(got[..., finite], ref[..., finite], BF16, "finite elements")
         assert np.isinf(got[..., 100]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("x_exp,w_exp", [(50, 100), (-50, -100), (60, 120)])
+def test_norm_comes_before_the_weight(rf, dtype, inter, x_exp, w_exp):
+    """x * w leaves fp32's range where the normed row times w does not."""
+    cos, sin = _tables(40, 32)
+    w = ((1 + 0.3 * torch.rand(64, generator=_gen(10))) * 2.0 ** w_exp).to(dtype)
+    x = (torch.randn(33, 3, 64, generator=_gen(11)) * 2.0 ** x_exp).to(dtype)
+    pos = torch.arange(33, dtype=torch.int32)
+    nr = rf.rf_norm_rope(cos.cuda(), sin.cuda(), inter, w.cuda(), None, 2.0 ** -120)
+    o = torch.empty_like(x, device="cuda")
+    rf.rf_qk_norm_rope(x.cuda(), None, o, None, nr, pos.cuda())
+    ref = G.norm_rope(x, pos, cos, sin, inter, w, 2.0 ** -120)
+    assert_rows(to64(o) * 2.0 ** -w_exp, ref * 2.0 ** -w_exp, dtype, "normed rows")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_whose_mean_of_squares_is_infinite_become_zeros(rf, dtype):
+    nr = NR(rf, 64, 64, False, True, dtype)
+    x = (torch.randn(5, 2, 64, generator=_gen(12)) * 2.0 ** 70).to(dtype)
+    x[3] = torch.finfo(dtype).max
+    x[4] = torch.randn(2, 64, generator=_gen(13)).to(dtype)
+    pos = torch.arange(5, dtype=torch.int32)
+    o = torch.empty_like(x, device="cuda")
+    rf.rf_qk_norm_rope(x.cuda(), None, o, None, nr.dev, pos.cuda())
+    assert (o[:4] == 0).all()
+    assert_rows(o[4:], nr.ref(x[4:], pos[4:], "q"), dtype, "the other rows")
