@@ -23,11 +23,15 @@
 // of two to a largest element in [2^14, 2^15), so its bf16 elements are exact
 // in f16 down to 2^-28 of the row's largest; products are summed in fp32.
 // The value scales enter the exponent: with e_j = log2 of the unnormalised
-// weight, the kernel keeps two running maxima,
-//     m = max_j e_j                 for the sum   l = sum_j 2^(e_j - m),
-//     M = max_j (e_j + log2 vs_j)   for           o = sum_j 2^(e_j + log2 vs_j - M) vc_j,
-// and out = o 2^(M - m) / l.  So P is at most 1 for whatever scales the pages
-// have, and is rounded to f16 (2^-11), finer than the bf16 output.  bf16: P is
+// weight, the kernel keeps a running maximum and a reference,
+//     m = max_j e_j   for the sum   l = sum_j 2^(e_j - m),
+//     M               for           o = sum_j 2^(e_j + log2 vs_j - M) vc_j,
+// and out = o 2^(M - m) / l.  P = 2^(e_j + log2 vs_j - M) is rounded to f16
+// (2^-11), finer than the bf16 output, and f16 keeps that for 29 binades, 2^-14
+// to 2^15.  So M puts the largest P so far at 2^15; and since a key whose weight
+// dwarfs all others' may have a value of zero, M comes down again where a whole
+// chunk lies more than 16 binades below it: to the chunk's own largest, at most
+// 48 binades, which o in fp32 holds (2^15 448 2^30 2^48 < 2^103).  bf16: P is
 // split in two bf16 parts (hi + lo, 2^-17 together) for two MMAs, since
 // values may be anything bf16 holds; M = m.
 //
@@ -307,6 +311,26 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// The same for weights, whose largest is 2^15 but for the rounding of its
+// exponent: not above f16's largest value.
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// E4M3's M (see the file's head): log2 of the largest P, and by how many binades
+// a chunk may lie below M before M comes down, and how far it may.
+constexpr float kTopP = 15.f, kLag = 16.f, kDrop = 48.f;
+__device__ __forceinline__ float next_ref(float M, float chunk, float top) {
+  return chunk < M - kLag ? fmaxf(chunk, top - kDrop) : fmaxf(M, chunk);
+}
+// out = o x y: 2^(M - m) / l in two factors, since 2^(M - m) itself may underflow.
+// (0, 0) for a row without keys.
+__device__ __forceinline__ float2 out_factors(float M, float m, float l) {
+  const float y = ex2(0.5f * (M - m));
+  return l == 0.f ? make_float2(0.f, 0.f) : make_float2(y / l, y);
 }
 
 template <int N>
@@ -733,7 +757,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
 
   // ---- the warp's range
   float o[D / 16][NT][4];
-  float m[NT][2], M[NT][2], l[NT][2], f[NT][2];
+  float m[NT][2], M[NT][2], top[NT][2], l[NT][2], f[NT][2];    // top: M's largest
   int lim[NT][2];
   uint32_t q[D / 16][NT][2];
   unsigned done = 0;
@@ -823,10 +847,11 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     const int r0_ = (cur_hr - h * p.tiles) * kTileRows;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float w[2];
+      float2 w[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        w[e] = l[nt][e] == 0.f ? 0.f : (kF8 ? ex2(M[nt][e] - m[nt][e]) : 1.f) / l[nt][e];
+        w[e] = kF8 ? out_factors(M[nt][e], m[nt][e], l[nt][e])
+                   : make_float2(l[nt][e] == 0.f ? 0.f : 1.f / l[nt][e], 1.f);
       if (kF8) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -838,7 +863,8 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
               uint32_t u[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                u[k] = pack_bf16x2(o[4 * i + k][nt][e] * w[e], o[4 * i + k][nt][e + 2] * w[e]);
+                u[k] = pack_bf16x2(o[4 * i + k][nt][e] * w[e].x * w[e].y,
+                                   o[4 * i + k][nt][e + 2] * w[e].x * w[e].y);
               reinterpret_cast<uint4*>(p.O + at)[i] = make_uint4(u[0], u[1], u[2], u[3]);
             }
           }
@@ -851,7 +877,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t u =
-                movmatrix(pack_bf16x2(o[i][nt][2 * k] * w[0], o[i][nt][2 * k + 1] * w[1]));
+                movmatrix(pack_bf16x2(o[i][nt][2 * k] * w[0].x, o[i][nt][2 * k + 1] * w[1].x));
             if (r < p.R && RF_IN(p.err, at + 16 * i + 8 * k + 2 * c + 1, n_qo))
               reinterpret_cast<uint32_t*>(p.O + at)[8 * i + 4 * k + c] = u;
           }
@@ -876,7 +902,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          m[nt][e] = M[nt][e] = -INFINITY;
+          m[nt][e] = M[nt][e] = top[nt][e] = -INFINITY;
           l[nt][e] = 0.f;
         }
 #pragma unroll
@@ -981,7 +1007,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
           mx[h2] = fmaxf(s[h2][nt][e], s[h2][nt][2 + e]) * sc[h2][nt][e];
         }
         cm[nt][e] = fmaxf(mx[0], mx[1]);
-        cM[nt][e] = fmaxf(mx[0] + lv[0], mx[1] + lv[1]);
+        cM[nt][e] = fmaxf(mx[0] + (lv[0] - kTopP), mx[1] + (lv[1] - kTopP));
       }
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1)
@@ -1002,7 +1028,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) cM[nt][e] = cm[nt][e] + lv[0];
+        for (int e = 0; e < 2; ++e) cM[nt][e] = cm[nt][e] + (lv[0] - kTopP);
     }
     bool moved = false;
 #pragma unroll
@@ -1013,7 +1039,8 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
         mu[nt][e] = mn == -INFINITY ? 0.f : mn;
         l[nt][e] *= ex2(m[nt][e] - mu[nt][e]);
         m[nt][e] = mn;
-        const float Mn = kF8 ? fmaxf(M[nt][e], cM[nt][e]) : mn;
+        if (kF8) top[nt][e] = fmaxf(top[nt][e], cM[nt][e]);
+        const float Mn = kF8 ? next_ref(M[nt][e], cM[nt][e], top[nt][e]) : mn;
         Mu[nt][e] = Mn == -INFINITY ? 0.f : Mn;
         a_o[nt][e] = ex2(M[nt][e] - Mu[nt][e]);
         moved |= Mn != M[nt][e];
@@ -1035,7 +1062,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
           }
           // P^T as B fragments
           if (kF8) {
-            pb[h2][nt][0][k] = movmatrix(pack_f16x2(w[0], w[1]));
+            pb[h2][nt][0][k] = movmatrix(pack_weights(w[0], w[1]));
           } else {
             const uint32_t hi = pack_bf16x2(w[0], w[1]);
             pb[h2][nt][0][k] = movmatrix(hi);
@@ -1172,13 +1199,14 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(half, v, o);
     return v;
   };
-  auto put_row = [&](const Seg& sg, int r, float w, const float (&v)[NV]) {
+  auto put_row = [&](const Seg& sg, int r, float2 w, const float (&v)[NV]) {
     const int h = p.tiles == 1 ? sg.hr : sg.hr / p.tiles;
     const int64_t at = row_at(sg.b, h, (sg.hr - h * p.tiles) * kTileRows + r) + NV * l16;
     if (!RF_IN(p.err, at + NV - 1, n_qo)) return;
     uint32_t u[NV / 2];
 #pragma unroll
-    for (int i = 0; i < NV / 2; ++i) u[i] = pack_bf16x2(v[2 * i] * w, v[2 * i + 1] * w);
+    for (int i = 0; i < NV / 2; ++i)
+      u[i] = pack_bf16x2(v[2 * i] * w.x * w.y, v[2 * i + 1] * w.x * w.y);
     if (NV == 8)
       *reinterpret_cast<uint4*>(p.O + at) = make_uint4(u[0], u[1], u[NV / 2 - 2], u[NV / 2 - 1]);
     else
@@ -1221,7 +1249,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
       }
     }
     if (e0 != cut0 && e0 != cut1) {
-      put_row(sg, r, L == 0.f ? 0.f : ex2(Mu - mu) / L, v);
+      put_row(sg, r, out_factors(Mu, mu, L), v);
     } else {
       const int64_t at = slot_of(ctas, sg.s0, cta) * kTileRows + r;
       if (RF_IN(p.err, at, n_slots)) {
@@ -1313,7 +1341,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
       }
     }
     const float Mu = Mx == -INFINITY ? 0.f : Mx, mu = mx == -INFINITY ? 0.f : mx;
-    put_row(sg, r, L == 0.f ? 0.f : ex2(Mu - mu) / L, v);
+    put_row(sg, r, out_factors(Mu, mu, L), v);
   }
 }
 

@@ -521,8 +521,12 @@ size_t rf_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Tq, int d
  *   Q, O    [B][Tq][Hq][d] bf16.  Query head hq reads kv head hq / (Hq / Hkv).
  *     s_j = scale * q . k_j   for keys j <= seq_lens[b] - Tq + t,
  *     o   = sum_j softmax(s)_j v_j
- * (fp32 accumulation and softmax state).  A row that reads no key (a padded
- * sequence, or one of fewer than Tq tokens) is written as zeros.  What lies
+ * with fp32 sums and softmax state.  A weight softmax(s)_j (times its v_scale) is
+ * multiplied with the stored values as two bf16 parts (RF_BF16: 16 bits) or as f16
+ * (RF_E4M3: off by at most 2^-11 of itself, or 2^-24 of the largest among 32
+ * consecutive keys where that is more, down to 2^-64 of the row's largest).
+ * A row that reads no key (a padded sequence, or one of fewer than Tq tokens), or
+ * whose scores are all -infinity, is written as zeros.  What lies
  * in a page behind the sequence's last token, or behind the last key that a
  * row reads, has no effect on it, whatever its value.
  * The lengths are read on the device; the keys of all sequences are shared

@@ -6,8 +6,10 @@ import pytest
 import torch
 
 from oracle import paged as G
+from oracle.fp8_quant_gemm import e4m3_encode
 from tests.helpers import to64
-from tests.test_gpu_paged import BF16, F32, NR, Batch, _gen, _tables, assert_rows
+from tests.test_gpu_paged import BF16, F32, NR, Batch, _gen, _tables, assert_rows, attn_reference, \
+    check_attn, run_attn
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +117,99 @@ def test_rows_whose_mean_of_squares_is_infinite_become_zeros(rf, dtype):
     rf.rf_qk_norm_rope(x.cuda(), None, o, None, nr.dev, pos.cuda())
     assert (o[:4] == 0).all()
     assert_rows(o[4:], nr.ref(x[4:], pos[4:], "q"), dtype, "the other rows")
+
+
+# ------------------------------------------------------------------ weights of many binades
+
+
+def _sink(kind, n, d, gap, first, seed, G_, Tq):
+    """Sequences of the same n keys, more of them than the device has warps, so that
+    a warp streams whole ones: the first key's score is `gap` nats above every
+    other one's (to within the others' own spread, about 0.05 sqrt(d)), and the
+    values of its chunk of 32 keys are `first` times the others'."""
+    bt = Batch(kind, [n], 1, d, 64, seed=seed, loud=0.0)
+    g = _gen(seed + 1)
+    x = 0.05 * torch.randn(2, bt.num_pages, 1, 64, d, generator=g)
+    x[1] *= 20
+    x[0, ..., 0] = 0
+    p0 = int(bt.table[0, 0])
+    x[0, p0, 0, 0] = 0
+    x[0, p0, 0, 0, 0] = 0.25
+    x[1, p0, 0, :32] *= first
+    if kind == "e4m3":
+        bt.scale[0], bt.scale[1] = 2.0 ** -10, 2.0 ** -7
+        bt.pages = e4m3_encode(x.numpy() / bt.scale[..., None, None])
+    else:
+        bt.pages = x.to(BF16)
+    q = torch.randn(1, Tq, G_, d, generator=g).to(BF16)
+    q[..., 0] = 4 * gap
+    return bt, q
+
+
+def _weighted(bt, q, scale):
+    """(o, tolerance) of one sequence and kv head: fp64, and the half steps of the
+    output (2^-8), of a weight (2^-11 relative in f16) and of the scores (d products
+    and sums in fp32, the exponential's argument and result).  A weight below f16's
+    normal numbers is off by 2^-25 of what is 2^15 for the sequence's first chunk's
+    largest, and 2^-1 at least for a later chunk's."""
+    qq = to64(q)[0]
+    n, ps, d = bt.lens[0], bt.ps, bt.d
+    pages = bt.table[0, :-(-n // ps)].numpy()
+    K, V = (G.values(*bt.host(i))[pages, 0].reshape(-1, d)[:n] for i in (0, 1))
+    Tq = len(qq)
+    o, tol = np.zeros_like(qq), np.zeros_like(qq)
+    for t in range(Tq):
+        m = n - Tq + t + 1
+        s = scale * qq[t] @ K[:m].T
+        p = np.exp(s - s.max(1, keepdims=True))
+        p /= p.sum(1, keepdims=True)
+        size = scale * np.abs(qq[t]) @ np.abs(K[:m]).T
+        u = 2.0 ** -23
+        per = 2 * ((d + 8) * u * size.max(1) + 4 * u * np.abs(s).max(1) + 8 * u) + \
+            2.0 ** -11 + (m / 8 + 64) * u
+        small = np.repeat(np.stack([p[:, i:i + 32].max(1) * 2.0 ** (-24 if i else -40)
+                                    for i in range(0, m, 32)], 1), 32, 1)[:, :m]
+        o[t] = p @ V[:m]
+        tol[t] = per[:, None] * (p @ np.abs(V[:m])) + small @ np.abs(V[:m])
+    return o, tol + 2.0 ** -8 * (np.abs(o) + tol) + 1e-37
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "bf16"])
+@pytest.mark.parametrize("gap", [4, 10, 14, 16, 18, 22, 26, 30, 36])
+@pytest.mark.parametrize("first", [0.0, 2.0 ** -7, 1.0])
+@pytest.mark.parametrize("n,d,G_,Tq", [(2048, 128, 4, 1), (700, 64, 3, 4), (1000, 128, 12, 1)])
+def test_a_dominant_key_does_not_drown_the_others(rf, kind, gap, first, n, d, G_, Tq):
+    """The others' weights are e^-gap of the first key's, whose value is zero or
+    small: their sum is all, or most, of the output."""
+    bt, q = _sink(kind, n, d, gap, first, 800 + gap, G_, Tq)
+    ref, tol = _weighted(bt, q, 1.0)
+    warps = 8 * torch.cuda.get_device_properties(0).multi_processor_count
+    B = warps + warps // 16                   # the sequences' borders fall anywhere in a warp's range
+    bt.lens, bt.table, bt.B = [n] * B, bt.table.expand(B, -1).contiguous(), B
+    got, status = run_attn(rf, bt, q.expand(B, -1, -1, -1).contiguous(), 1.0)
+    assert status == rf.RF_OK
+    err = np.abs(to64(got) - ref)
+    assert (err <= tol).all(), f"worst {(err / tol).max():.2f} of the tolerance, " \
+        f"{(np.linalg.norm(err, axis=(1, 2, 3)) / np.linalg.norm(ref)).max():.2e} relative"
+
+
+@pytest.mark.parametrize("v_exp", [-114, -105, 112])
+@pytest.mark.parametrize("lens", [[70, 5], [9000, 3]])
+def test_value_scales_next_to_fp32s_ends(rf, v_exp, lens):
+    """2^(M - m) alone, or its product with o, would leave fp32's range."""
+    bt = Batch("e4m3", lens, 1, 128, 32, seed=830, loud=0.0)
+    bt.scale[1] *= np.float32(2.0 ** v_exp)
+    q = torch.randn(2, 1, 4, 128, generator=_gen(831)).to(BF16)
+    check_attn(rf, bt, q, 128 ** -0.5, f"value scales of 2^{v_exp}")
+
+
+@pytest.mark.parametrize("Tq,G_", [(1, 4), (4, 3)])
+@pytest.mark.parametrize("exp", [4, 10, 16])
+def test_scores_up_to_a_million(rf, Tq, G_, exp):
+    """The largest weight's exponent is rounded by more than f16 has left above it."""
+    bt = Batch("e4m3", [500, 33], 1, 64, 16, seed=832)
+    q = (torch.randn(2, Tq, G_, 64, generator=_gen(833)) * 2.0 ** exp).to(BF16)
+    got, status = run_attn(rf, bt, q, 1.0)
+    assert status == rf.RF_OK
+    ref, tol = attn_reference(q, bt, 1.0)
+    assert (np.abs(to64(got) - ref) <= tol).all()
