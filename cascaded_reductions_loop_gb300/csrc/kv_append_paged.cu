@@ -286,18 +286,23 @@ __host__ __device__ __forceinline__ Item item_of(const Seqs& sq, int b, int p, b
   return it;
 }
 
+// Sequence b's items [lo, lo + n); none where lo < 0 or n <= 0 (tables out of order).
+__host__ __device__ __forceinline__ void items_of(const Seqs& sq, int b, int64_t* lo, int64_t* n,
+                                                  unsigned* err) {
+  if (sq.cu) {
+    const int c0 = ld_int(sq.cu, b, sq.B + 1, err), c1 = ld_int(sq.cu, b + 1, sq.B + 1, err);
+    *lo = c0 / sq.page_size + 2 * (int64_t)b;
+    *n = (int64_t)(c1 / sq.page_size) - c0 / sq.page_size + 2;
+  } else {
+    *n = pages_of(sq.n_uniform, sq.page_size);
+    *lo = b * *n;
+  }
+}
 // Whether item x is one of sequence b's, and which of its pages.
 __host__ __device__ __forceinline__ bool item_is_of(const Seqs& sq, int x, int b, int* p,
                                                     unsigned* err) {
   int64_t lo, n;
-  if (sq.cu) {
-    const int c0 = ld_int(sq.cu, b, sq.B + 1, err), c1 = ld_int(sq.cu, b + 1, sq.B + 1, err);
-    lo = c0 / sq.page_size + 2 * (int64_t)b;
-    n = (int64_t)(c1 / sq.page_size) - c0 / sq.page_size + 2;
-  } else {
-    n = pages_of(sq.n_uniform, sq.page_size);
-    lo = b * n;
-  }
+  items_of(sq, b, &lo, &n, err);
   const int64_t q = x - lo;
   *p = (int)q;
   return q >= 0 && q < n && q <= x;
@@ -757,6 +762,8 @@ cudaError_t launch_kv_append_paged(const PagedKV& c, const NormRope& nr, const v
 //     slot of its position, and no other token is;
 //   4 the rows' lookup finds the same position and page for the same tokens;
 //   5 inconsistent sizes, and only those, are noted.
+// -1 where tables out of order would make the walk too long.
+constexpr int64_t kMostWalked = 1ll << 28;
 int append_plan_selfcheck(const PagedKV& c, const int* cu, int total, int max_pos) {
   const Seqs sq = make_seqs(c, cu, total, max_pos);
   unsigned err = 0;
@@ -769,26 +776,34 @@ int append_plan_selfcheck(const PagedKV& c, const int* cu, int total, int max_po
   }
   std::vector<int> pos_of((size_t)total, -1);
   const int64_t n = num_items(total, c.B, sq.n_uniform, cu != nullptr, c.page_size);
-  for (int64_t x = 0; x < n; ++x) {
-    Item it = {0, 0, 0, 0, 0};
-    for (int b = 0; b < c.B; ++b) {
+  // each sequence's items (in order, all of them together are n; out of order they
+  // may be any number of times that, and are walked as long as that takes seconds)
+  std::vector<unsigned char> taken((size_t)n, 0);
+  int64_t walked = 0;
+  for (int b = 0; b < c.B; ++b) {
+    int64_t lo, count;
+    items_of(sq, b, &lo, &count, &err);
+    if (err & kDevErrBounds) return 1;
+    if (lo < 0) continue;
+    const int64_t end = std::min(n, lo + count);
+    walked += std::max<int64_t>(end - lo, 0);
+    if (walked > kMostWalked) return -1;
+    for (int64_t x = lo; x < end; ++x) {
       int p;
-      if (!item_is_of(sq, (int)x, b, &p, &err)) continue;
-      const Item i = item_of(sq, b, p, true, &err);
-      if (i.n == 0) continue;
-      if (order && it.n != 0) return 2;
-      it = i;                                  // any of them may be the one that is taken
+      if (!item_is_of(sq, (int)x, b, &p, &err)) return 2;
+      const Item it = item_of(sq, b, p, true, &err);
+      if (err & kDevErrBounds) return 1;
+      if (it.n == 0) continue;
+      if (order && taken[(size_t)x]++) return 2;
       if (it.n < 0 || it.off < 0 || it.off + it.n > c.page_size || it.phys < 0 ||
           it.phys >= c.num_pages || it.t0 < 0 || it.t0 + it.n > total)
         return 2;
-    }
-    if (err & kDevErrBounds) return 1;
-    if (it.n == 0) continue;
-    for (int i = 0; i < it.n; ++i) {
-      if (order &&
-          (pos_of[(size_t)it.t0 + i] != -1 || (it.pos0 + i) % c.page_size != it.off + i))
-        return 3;
-      pos_of[(size_t)it.t0 + i] = it.pos0 + i;
+      for (int i = 0; i < it.n; ++i) {
+        if (order &&
+            (pos_of[(size_t)it.t0 + i] != -1 || (it.pos0 + i) % c.page_size != it.off + i))
+          return 3;
+        pos_of[(size_t)it.t0 + i] = it.pos0 + i;
+      }
     }
   }
   bool bad = false;

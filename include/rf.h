@@ -616,8 +616,9 @@ int rf_selftest_moe_plan(int T, int D, int E, int sms);
  * cache, that every token that is not skipped is written once, to the slot of
  * its position, that queries get the same positions, and that inconsistent
  * sizes are noticed.  Returns 0 when all of that holds, -1 for refused sizes
- * (beside those of that call: B > 2^20, total > 2^24, or no memory for the
- * walk), else the number (1..5) of the first check that fails.
+ * (beside those of that call: B > 2^20, total > 2^24, no memory for the walk,
+ * or entries of cu_seqlens out of order that give the sequences 2^28 items or
+ * more together), else the number (1..5) of the first check that fails.
  */
 int rf_selftest_append_plan(const int32_t* block_table, const int32_t* seq_lens,
                             const int32_t* cu_seqlens, int B, int total, int num_pages,
