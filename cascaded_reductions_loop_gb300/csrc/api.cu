@@ -531,7 +531,7 @@ rf_status rf_kv_append_paged(const rf_paged_kv* cache, const void* K, int64_t ld
 static rf_status decode_paged_check(int B, int Hq, int Hkv, int Tq, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Tq < 1 || d < 1 || Hq % Hkv != 0) return RF_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return RF_ERR_UNSUPPORTED;
-  if ((int64_t)B * Hq >= (1ll << 31) / Tq) return RF_ERR_INVALID_ARG;
+  if ((int64_t)B * Hq > ((1ll << 31) - 1) / Tq) return RF_ERR_INVALID_ARG;
   return RF_OK;
 }
 

@@ -1396,7 +1396,7 @@ cudaError_t launch(const PagedKV& c, const Params& p, int sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], p);
 }
 
-int tiles_of(int R) { return (R + kTileRows - 1) / kTileRows; }
+int tiles_of(int R) { return R / kTileRows + (R % kTileRows != 0); }   // R up to 2^31 - 1
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
