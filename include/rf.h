@@ -397,7 +397,7 @@ rf_status rf_absmax_quant_fp8(const void* X, int M, int K, float* sx_out, uint8_
  *   block_table  int32 [B][max_pages].  Only the entries of pages that hold
  *                tokens are used; the others may be anything.  A page may be in
  *                several rows (a shared prefix), but a page that an append
- *                writes belongs to one sequence.
+ *                writes belongs to one sequence, and once.
  *   seq_lens     int32 [B]: tokens of each sequence, the call's own new tokens
  *                included.  0: a padded row of the batch.
  *   Sizes   B, num_pages, max_pages, Hkv >= 1; page_size 16, 32, 64 or 128;
@@ -491,6 +491,11 @@ rf_status rf_qk_norm_rope(int dtype, const void* Q, int64_t ldq, const void* K, 
  * saturates, NaN is stored as NaN), and s as the page's scale.  This is the
  * running-maximum form of [E] §4.3's row absmax and quantisation: a power of
  * two makes the rescaling of earlier codes exact but for E4M3's subnormals.
+ * (Where a page comes with a scale that is no power of two, x / s is x times
+ * the rounded 1 / s.)  A scale never shrinks while its page holds earlier
+ * tokens: tokens that are taken back (a rejected draft) and overwritten behind
+ * others leave theirs, and what is stored then keeps its coarser steps, until
+ * the page is filled from slot 0 again.
  * A sequence with seq_lens 0 is a padded row: nothing of it is written, nor
  * are its rows of Qo.  A sequence whose length is below its new tokens, above
  * max_pages * page_size, or (with rotation) above max_pos, or whose entries of
@@ -519,6 +524,7 @@ size_t rf_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Tq, int d
  * strategy; the cascade of rf_attn_decode_splitkv with the keys' and values'
  * scales in it).  Tq query tokens a sequence, its last Tq tokens:
  *   Q, O    [B][Tq][Hq][d] bf16.  Query head hq reads kv head hq / (Hq / Hkv).
+ *           O may be Q; other overlaps are not allowed.
  *     s_j = scale * q . k_j   for keys j <= seq_lens[b] - Tq + t,
  *     o   = sum_j softmax(s)_j v_j
  * with fp32 sums and softmax state.  A weight softmax(s)_j (times its v_scale) is
