@@ -9,13 +9,13 @@
 // j's page.  Tiles hold 8 or 16 rows; more rows make more tiles (a tile is
 // named by b and hr = h * tiles + tile).
 //
-// What bounds it: memory.  Every cached byte is read once from HBM, and the
-// arithmetic per byte is small (16 flop at G = 8 in E4M3).  mma.sync keeps
-// the operands in registers, which is what an 8-bit cache needs: codes are
+// What bounds it, up to 16 rows: memory.  Every cached byte is read once for each
+// tile of its kv head, and the arithmetic per byte is small (16 flop at G = 8 in
+// E4M3).  mma.sync keeps the operands in registers, which is what an 8-bit cache needs: codes are
 // widened on their way into the fragments and never go back to shared memory.
 // The cache is the A operand (16 keys or 16 dims by 16) and the few query
-// rows are the B operand (n = 8), so a fragment is widened once for all rows
-// and no MMA row is padding:
+// rows are the B operand (n = 8), so a fragment is widened once for all rows of
+// a tile and no MMA row is padding:
 //     S^T = K Q^T    (keys x rows),      O^T += V^T P^T   (dims x rows).
 // S^T's accumulators become P^T's fragments by one movmatrix each.
 //
@@ -54,15 +54,18 @@
 // copies issued by the consumers themselves a chunk took 1.7 us of a warp's
 // time, 0.65 of it for the issue; now 1.05, and eight warps outrun memory.
 //
-// Measured (GB300, CUDA graph, inputs larger than L2; copy rate 6788 GB/s):
-//   32 x 24-32k keys, 8 kv heads of 4, E4M3   275 us   1.86 GB   6.8 TB/s
-//   32 x 2048 keys, the same                  30 us    0.13 GB   4.4 TB/s
-//   9 x 3-20k keys, 7 kv heads of 5, bf16     60 us    0.37 GB   6.2 TB/s
-//   48 x 1-4k keys, 16 heads of 64, bf16      67 us    0.39 GB   5.8 TB/s
-//   16 x 0.5-8k keys, 4 kv heads of 8, four query tokens, E4M3   43 us (32 rows
-//     are two tiles; a warp's chunk of 16 rows takes 2.1 us, latency of the
-//     softmax and MMA chains, so memory waits)
-//   1 x 1000 keys, 8 kv heads of 4, E4M3      10.8 us, all latency: the plan 2,
+// Measured (GB300, CUDA graph, inputs larger than L2; copy rate 6683 GB/s; bytes
+// of the lengths that were timed, a mean of three batches):
+//   32 x 24-32k keys, 8 kv heads of 4, E4M3   276 us   1.84 GB   6.7 TB/s
+//   32 x 2048 keys, the same                  30.5 us  0.13 GB   4.4 TB/s
+//   32 x 24-32k keys, 2 kv heads of 16, E4M3  92 us    0.46 GB   5.0 TB/s
+//   9 x 3-20k keys, 7 kv heads of 5, bf16     60 us    0.36 GB   5.9 TB/s
+//   48 x 1-4k keys, 16 heads of 64, bf16      68 us    0.41 GB   6.0 TB/s
+//   16 x 0.5-8k keys, 4 kv heads of 8, four query tokens   0.07 GB in E4M3, 43 us;
+//     0.14 GB in bf16, 55 us (32 rows are two tiles; a warp's chunk of 16 rows in
+//     E4M3 takes 2.1 us, latency of the softmax and MMA chains, so memory waits;
+//     that instance spills 32 bytes, too)
+//   1 x 1000 keys, 8 kv heads of 4, E4M3      10.9 us, all latency: the plan 2,
 //     page and first chunk 1.5, the chunk 1 (clock stamps); launch and merges.
 // Of what a mid-sized call takes above its bytes (10 us for 32 x 2048 keys), 3.6
 // pass before the first copy and 1.5 until it is in; the rest is the spread of the
@@ -637,8 +640,9 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     Cursor cur = {0, 0, 0, 0, 0};
     if (count > 0 && !cur.init(lens, sh.start_b[w], sh.start_len[w], sh.start_off[w])) count = 0;
     unsigned issued = 0;
-    // the cache streams through L2 once; queries, tables and states stay (32 x 2k
-    // keys 31.6 us without, 30.2 with)
+    // evict first, so that queries, tables and states stay in L2 (32 x 2k keys 31.6 us
+    // without, 30.2 with).  A cache that one tile a kv head reads passes through once;
+    // several tiles read it once each
     const uint64_t policy = policy_evict_first();
     int pt = -1, pt_b = -1, pt_base = 0;  // kLanes entries of a block table row, one a lane
     bool failed = false;

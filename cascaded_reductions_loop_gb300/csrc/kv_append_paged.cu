@@ -29,15 +29,20 @@
 // Query rows are further CTAs of the same launch (norm_rope.cuh).
 //
 // What bounds it, measured (GB300, CUDA graph, inputs larger than L2; copy rate
-// 6788 GB/s):
+// 6683 GB/s):
 //   bf16 cache, 32768 tokens of 8 heads of 128   47 us, 6.1 TB/s: memory
-//   bf16 cache, 11 prompts, 6.6k tokens of 16 heads of 64   19.6 us, 5.5 TB/s
+//   bf16 cache, 8192 tokens of the same   15.7 us, 4.5 TB/s
+//   bf16 cache, 11 prompts, 6.6k tokens of 16 heads of 64   19.8 us, 5.5 TB/s
 //   E4M3 cache, 32768 tokens of 8 heads of 128   62 us, 3.5 TB/s: instructions
 //     (norm, rotation, two maxima and two quantisations for eight keys and eight
-//     values a lane; issue slots 55 % full) and the barrier between a head's
+//     values a lane; issue slots 57 % full) and the barrier between a head's
 //     absmax and its quantisation
+//   E4M3 cache, 8192 tokens of the same   22.7 us in pages of 64 tokens, 24.4 in
+//     pages of 128; with 32 query heads 42.7: the kv CTAs that stay fill the SMs,
+//     and the query CTAs begin where they end
 //   E4M3 cache, 7 prompts, 10.7k tokens of 8 heads of 128   26 us
-//   E4M3 step, 32 sequences, 8 kv and 32 query heads   3.2 us: launch latency
+//   steps, 32 sequences, 8 kv and 32 query heads   3.5 us in E4M3, 3.2 in bf16:
+//     launch latency
 // Steps of the E4M3 prompt kernel, for the 7 prompts: one CTA an (item, head) with
 // a serial search 36 us; several heads a CTA of 1024 threads, one an SM, 45-58;
 // keys and values in CTAs of their own 33; packed arithmetic on shared
@@ -498,7 +503,8 @@ __global__ void __launch_bounds__(kThreads)
 // thread (page_size * D * 8 bytes).  TH, the most threads, is 512 with 64
 // registers, so that two CTAs share an SM: one works while the other waits.
 // Pages of 128 x 128 take 1024 threads, since four sweeps of 512 spill (45
-// against 24 us for 8192 tokens of 8 heads).  The next head's keys are fetched
+// against 24 us for 8192 tokens of 8 heads); two sweeps spill 32 or 36 bytes.
+// The next head's keys are fetched
 // as soon as the present ones are in their final form, its values when the
 // present ones are stored.
 template <int D, int SW, int TH, bool kSplit>

@@ -227,8 +227,11 @@ struct RowsOut {
 };
 
 // How many heads a lane group takes one after the other: as many of 4, 8, 16
-// ... as leave 1024 threads an SM (more heads share a token's A and B, but a
-// device must be full), one where even four would not.  `rows`: tokens x heads.
+// ... as leave 1024 threads for each SM (more heads share a token's A and B, but a
+// device must be full), one where even four would not.  By their registers 768
+// threads of the bf16 kernels run on an SM at once, and 512 of the fp32 ones and of
+// the bf16 append's for heads of 128, so that a grid has 1.3 to 2.7 waves, or 2 to
+// 4, or more; the last is a part of one.  `rows`: tokens x heads.
 inline int heads_per_group(int64_t rows, int heads, int d, int sms) {
   const int64_t threads = rows * (d / 8);
   int h = 1;

@@ -6,14 +6,17 @@
 // 16-byte loads are in flight together while the batch before is worked on;
 // the token's angles and the weights are loaded once for all of them.
 //
-// Measured (GB300, CUDA graph, inputs larger than L2; copy rate 6788 GB/s):
+// Measured (GB300, CUDA graph, inputs larger than L2; copy rate 6683 GB/s):
 //   8191 tokens, 32 + 8 heads of 128, bf16, norm, half-split    31 us, 5.5 TB/s
-//   32768 tokens, the same                                     107 us, 6.4 TB/s
-//   4096 tokens, 16 + 16 heads of 64, fp32, half rotated        14 us, 4.8 TB/s
+//   32768 and 131072 tokens, the same               108 and 416 us, 6.4 and 6.6 TB/s
+//   4096 tokens, 16 + 16 heads of 64, fp32, half rotated        14 us, 4.9 TB/s
+//   16384 and 65536 tokens, the same                 46 and 161 us, 5.9 and 6.7 TB/s
 //   32 tokens, 32 + 8 heads of 128                             2.3 us: launch
 // One head a lane group, everything made anew for it, took 65 us for the first:
 // 186 instructions for 32 lanes' loads of 16 bytes, and the issue slots bound it.
-// About 6 us of a call do not depend on its size (launch, first and last wave).
+// The bf16 sizes lie 5.7 to 5.9 us above 3.13 ns a token (launch, first and last
+// wave).  The fp32 ones make 3.4, 3.4 and 13.5 waves of CTAs, two an SM by their
+// registers, and the part of a wave counts.
 #include "norm_rope.cuh"
 
 namespace rf {
