@@ -537,7 +537,9 @@ def rf_kv_append_paged(cache, k, v, norm_rope=None, cu_seqlens=None, q=None, q_o
     keys' norm and rotation (an rf_norm_rope) on the way.  k, v: [total,Hkv,d]
     bf16, tokens strided as they like; cu_seqlens: int32 [B+1] cumulative new
     tokens, or None: total / B each; q, q_out: the same tokens' queries
-    [total,Hq,d], normed and rotated in the same launch, or None."""
+    [total,Hq,d], normed and rotated in the same launch, or None; q_out may be
+    q.  A page's E4M3 scale does not shrink while the page holds earlier
+    tokens (include/rf.h)."""
     dev, bf16 = cache._here(), torch.bfloat16
     total = k.shape[0]
     Hkv, d = cache.Hkv, cache.d
@@ -564,7 +566,7 @@ def rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq=1, d=128) -> int:
 def rf_attn_decode_paged(cache, q, o, scale: float, workspace, stream=None) -> None:
     """Decode attention over a paged cache (an rf_paged_kv).  q, o:
     [B,Tq,Hq,d] (or [B,Hq,d]: Tq = 1) bf16, the last Tq tokens of each
-    sequence; workspace: a uint8 CUDA tensor of at least
+    sequence; o may be q; workspace: a uint8 CUDA tensor of at least
     rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq, d) bytes."""
     dev = cache._here()
     shape = q.shape
