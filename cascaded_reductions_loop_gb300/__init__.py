@@ -27,8 +27,9 @@ __all__ = [
     "rf_mla_decode_workspace_size", "rf_moe_gate_topk_softmax", "rf_moe_gate_topk_softmax_ex",
     "rf_absmax_fp8_gemm", "rf_absmax_fp8_gemm_workspace_size", "rf_absmax_quant_fp8",
     "rf_paged_kv", "rf_norm_rope", "rf_qk_norm_rope", "rf_kv_append_paged", "rf_attn_decode_paged",
-    "rf_attn_decode_paged_workspace_size", "rf_selftest_append_plan",
-    "rf_selftest_decode_paged_plan",
+    "rf_attn_decode_paged_workspace_size", "rf_attn_mask", "rf_attn_decode_paged_ex",
+    "rf_attn_decode_paged_ex_workspace_size", "rf_selftest_append_plan",
+    "rf_selftest_decode_paged_plan", "rf_selftest_decode_paged_ex_plan",
     "rf_selftest_wait_timeout", "rf_selftest_bounds", "rf_selftest_decode_plan",
     "rf_selftest_fp8_schedule", "rf_selftest_moe_plan",
     "RF_OK", "RF_ERR_INVALID_ARG", "RF_ERR_UNSUPPORTED", "RF_ERR_WORKSPACE", "RF_ERR_CUDA",
@@ -72,6 +73,10 @@ class _NormRope(_c.Structure):
                 ("q_weight", _P), ("k_weight", _P), ("eps", _F)]
 
 
+class _AttnMask(_c.Structure):
+    _fields_ = [("window", _I), ("sinks", _I), ("parents", _P)]
+
+
 _SIGS = {
     "rf_status_string": (_c.c_char_p, [_I]),
     "rf_last_cuda_error": (_c.c_char_p, []),
@@ -98,8 +103,12 @@ _SIGS = {
                                 _P, _L, _P, _L, _I, _P]),
     "rf_attn_decode_paged_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "rf_attn_decode_paged": (_I, [_c.POINTER(_PagedKV), _P, _P, _I, _I, _F, _P, _Z, _P]),
+    "rf_attn_decode_paged_ex_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
+    "rf_attn_decode_paged_ex": (_I, [_c.POINTER(_PagedKV), _P, _P, _I, _I, _F,
+                                     _c.POINTER(_AttnMask), _P, _Z, _P]),
     "rf_selftest_append_plan": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I]),
     "rf_selftest_decode_paged_plan": (_I, [_P, _I, _I, _I, _I, _I]),
+    "rf_selftest_decode_paged_ex_plan": (_I, [_P, _I, _I, _I, _I, _I, _I, _I, _I]),
     "rf_selftest_wait_timeout": (_I, [_I, _P]),
     "rf_selftest_bounds": (_I, [_P]),
     "rf_selftest_decode_plan": (_I, [_I, _I, _I, _I, _I]),
@@ -568,6 +577,43 @@ def rf_attn_decode_paged(cache, q, o, scale: float, workspace, stream=None) -> N
     [B,Tq,Hq,d] (or [B,Hq,d]: Tq = 1) bf16, the last Tq tokens of each
     sequence; o may be q; workspace: a uint8 CUDA tensor of at least
     rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq, d) bytes."""
+    _decode_paged(cache, q, o, scale, None, workspace, stream)
+
+
+class rf_attn_mask:
+    """Which keys the rows of rf_attn_decode_paged_ex read (struct rf_attn_mask).
+    window: 0: every key up to the row's position, else the last `window` of them
+    and the first `sinks` keys; parents: int32 [B, Tq] of a tree of drafted tokens
+    (the node each follows, an earlier one, or -1), or None: a chain.  Holds the
+    tensor and its address, as rf_paged_kv does."""
+
+    def __init__(self, window: int = 0, sinks: int = 0, parents=None):
+        self.window, self.sinks, self.parents, self._shape = int(window), int(sinks), parents, None
+        for n, x in (("window", self.window), ("sinks", self.sinks)):
+            if not 0 <= x <= 1 << 30:
+                raise ValueError(f"{n} must be in 0 .. 2^30")
+        if parents is not None:
+            _on_device("parents", parents)
+            if parents.dim() != 2:
+                raise ValueError("parents must be [B, Tq]")
+            _need(parents, torch.int32, parents.shape, "parents")
+            self._shape = (parents.get_device(), parents.shape[0], parents.shape[1])
+        self._c = _AttnMask(self.window, self.sinks, None if parents is None else parents.data_ptr())
+        self._ref = _c.byref(self._c)
+
+
+def rf_attn_decode_paged_ex_workspace_size(B, Hq, Hkv, Tq=1, d=128) -> int:
+    return lib.rf_attn_decode_paged_ex_workspace_size(B, Hq, Hkv, Tq, d)
+
+
+def rf_attn_decode_paged_ex(cache, q, o, scale: float, mask, workspace, stream=None) -> None:
+    """rf_attn_decode_paged with an rf_attn_mask (or None): a window with sinks, a
+    tree of drafted tokens.  workspace: a uint8 CUDA tensor of at least
+    rf_attn_decode_paged_ex_workspace_size(B, Hq, Hkv, Tq, d) bytes."""
+    _decode_paged(cache, q, o, scale, mask, workspace, stream)
+
+
+def _decode_paged(cache, q, o, scale, mask, workspace, stream):
     dev = cache._here()
     shape = q.shape
     n = len(shape)
@@ -582,8 +628,15 @@ def rf_attn_decode_paged(cache, q, o, scale: float, workspace, stream=None) -> N
         if not workspace.is_contiguous():       # an expanded tensor has less storage than bytes
             raise ValueError("workspace must be contiguous")
         wp, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    _check(lib.rf_attn_decode_paged(cache._ref, qp, op, shape[-2], shape[1] if n == 4 else 1, scale,
-                                    wp, ws_bytes, _stream(stream)), "rf_attn_decode_paged")
+    Tq = shape[1] if n == 4 else 1
+    if mask is None:
+        _check(lib.rf_attn_decode_paged(cache._ref, qp, op, shape[-2], Tq, scale, wp, ws_bytes,
+                                        _stream(stream)), "rf_attn_decode_paged")
+        return
+    if mask._shape is not None and mask._shape != (dev, cache.B, Tq):
+        raise ValueError(f"parents must be [{cache.B}, {Tq}] on the current CUDA device")
+    _check(lib.rf_attn_decode_paged_ex(cache._ref, qp, op, shape[-2], Tq, scale, mask._ref, wp,
+                                       ws_bytes, _stream(stream)), "rf_attn_decode_paged_ex")
 
 
 def rf_selftest_wait_timeout(timeout_us: int, stream=None) -> None:
@@ -640,6 +693,14 @@ def rf_selftest_append_plan(block_table, seq_lens, cu_seqlens, total: int, num_p
         _host_i32(block_table, "block_table"), _host_i32(seq_lens, "seq_lens"),
         None if cu_seqlens is None else _host_i32(cu_seqlens, "cu_seqlens"), B, int(total),
         int(num_pages), int(page_size), max_pages, int(max_pos))
+
+
+def rf_selftest_decode_paged_ex_plan(seq_lens, tiles: int, max_len: int, Tq: int, window: int,
+                                     sinks: int, warps: int, sms: int) -> int:
+    """The same for rf_attn_decode_paged_ex with Tq query tokens, a window and sinks."""
+    return lib.rf_selftest_decode_paged_ex_plan(
+        _host_i32(seq_lens, "seq_lens"), seq_lens.numel(), int(tiles), int(max_len), int(Tq),
+        int(window), int(sinks), int(warps), int(sms))
 
 
 def rf_selftest_decode_paged_plan(seq_lens, tiles: int, max_len: int, warps: int, sms: int) -> int:

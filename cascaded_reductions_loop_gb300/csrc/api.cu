@@ -540,15 +540,33 @@ size_t rf_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Tq, int d
   return decode_paged_workspace_bytes(B, Hkv, Hq / Hkv * Tq, d);
 }
 
+size_t rf_attn_decode_paged_ex_workspace_size(int B, int Hq, int Hkv, int Tq, int d) {
+  return rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq, d);
+}
+
 rf_status rf_attn_decode_paged(const rf_paged_kv* cache, const void* Q, void* O, int Hq, int Tq,
                                float scale, void* workspace, size_t workspace_bytes,
                                rf_stream_t stream) {
+  return rf_attn_decode_paged_ex(cache, Q, O, Hq, Tq, scale, nullptr, workspace, workspace_bytes,
+                                 stream);
+}
+
+static bool window_ok(int window, int sinks) {
+  return window >= 0 && window <= (1 << 30) && sinks >= 0 && sinks <= (1 << 30);
+}
+
+rf_status rf_attn_decode_paged_ex(const rf_paged_kv* cache, const void* Q, void* O, int Hq, int Tq,
+                                  float scale, const rf_attn_mask* mask, void* workspace,
+                                  size_t workspace_bytes, rf_stream_t stream) {
   rf_status st = paged_check(cache);
   if (st != RF_OK) return st;
   if (!ptr_ok(Q) || !ptr_ok(O)) return RF_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !(scale < INFINITY)) return RF_ERR_INVALID_ARG;
   st = decode_paged_check(cache->B, Hq, cache->Hkv, Tq, cache->d);
   if (st != RF_OK) return st;
+  if (mask && (!window_ok(mask->window, mask->sinks) ||
+               (reinterpret_cast<uintptr_t>(mask->parents) & 3u)))
+    return RF_ERR_INVALID_ARG;
   const int R = Hq / cache->Hkv * Tq;
   if (decode_paged_max_chunks(cache->B, cache->Hkv, R, cache->max_pages, cache->page_size) >=
       (1ll << 31))
@@ -559,8 +577,11 @@ rf_status rf_attn_decode_paged(const rf_paged_kv* cache, const void* Q, void* O,
   if (workspace_bytes < need) return RF_ERR_WORKSPACE;
   unsigned* err = device_error_word();
   if (!err) return RF_ERR_CUDA;
-  return from_cuda(launch_decode_paged(*cache, Q, O, Hq, Tq, scale, workspace, err,
-                                       reinterpret_cast<cudaStream_t>(stream)));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool masked = mask && (mask->window != 0 || mask->parents);
+  return from_cuda(masked ? launch_decode_paged_masked(*cache, *mask, Q, O, Hq, Tq, scale,
+                                                       workspace, err, s)
+                          : launch_decode_paged(*cache, Q, O, Hq, Tq, scale, workspace, err, s));
 }
 
 int rf_selftest_append_plan(const int32_t* block_table, const int32_t* seq_lens,
@@ -585,17 +606,28 @@ int rf_selftest_append_plan(const int32_t* block_table, const int32_t* seq_lens,
   }
 }
 
-int rf_selftest_decode_paged_plan(const int32_t* seq_lens, int B, int tiles, int max_len,
-                                  int warps, int sms) {
-  if (!seq_lens || B < 1 || tiles < 1 || max_len < 1 || max_len > (1 << 30) ||
+static int decode_paged_plan(const int32_t* seq_lens, int B, int tiles, int max_len, int Tq,
+                             int window, int sinks, int warps, int sms) {
+  if (!seq_lens || Tq < 1 || !window_ok(window, sinks) || B < 1 || tiles < 1 || max_len < 1 || max_len > (1 << 30) ||
       (warps != 4 && warps != 8) || sms < 1 || sms > (1 << 20) ||
       (int64_t)B * tiles > (1ll << 24) || (int64_t)B * tiles * (max_len / 32 + 1) >= (1ll << 31))
     return -1;
   try {
-    return decode_paged_plan_selfcheck(seq_lens, B, tiles, max_len, warps, sms);
+    return decode_paged_plan_selfcheck(seq_lens, B, tiles, max_len, Tq, window, sinks, warps, sms);
   } catch (...) {                              // no memory for the walk
     return -1;
   }
+}
+
+int rf_selftest_decode_paged_plan(const int32_t* seq_lens, int B, int tiles, int max_len,
+                                  int warps, int sms) {
+  return decode_paged_plan(seq_lens, B, tiles, max_len, 1, 0, 0, warps, sms);
+}
+
+int rf_selftest_decode_paged_ex_plan(const int32_t* seq_lens, int B, int tiles, int max_len, int Tq,
+                                     int window, int sinks, int warps, int sms) {
+  return window < 1 ? -1 : decode_paged_plan(seq_lens, B, tiles, max_len, Tq, window, sinks, warps,
+                                             sms);
 }
 
 rf_status rf_selftest_wait_timeout(int timeout_us, rf_stream_t stream) {

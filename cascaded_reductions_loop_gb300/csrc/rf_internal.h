@@ -129,11 +129,21 @@ cudaError_t launch_kv_append_paged(const PagedKV& c, const NormRope& nr, const v
 
 // R = Tq * Hq / Hkv query rows of a kv head.
 int64_t decode_paged_max_chunks(int B, int Hkv, int R, int max_pages, int page_size);
-// host only (host array): 0 when the partition over sms CTAs of W warps is consistent
-int decode_paged_plan_selfcheck(const int* seq_lens, int B, int HR, int max_len, int W, int sms);
+// host only (host array): 0 when the partition over sms CTAs of W warps is consistent;
+// window 0: no masks
+int decode_paged_plan_selfcheck(const int* seq_lens, int B, int HR, int max_len, int Tq, int window,
+                                int sinks, int W, int sms);
 size_t decode_paged_workspace_bytes(int B, int Hkv, int R, int d);
 cudaError_t launch_decode_paged(const PagedKV& c, const void* Q, void* O, int Hq, int Tq,
                                 float scale, void* workspace, unsigned* err, cudaStream_t s);
+
+
+// What rf.h's rf_attn_mask holds, validated.
+using Mask = ::rf_attn_mask;
+
+cudaError_t launch_decode_paged_masked(const PagedKV& c, const Mask& mask, const void* Q, void* O,
+                                       int Hq, int Tq, float scale, void* workspace, unsigned* err,
+                                       cudaStream_t s);
 
 cudaError_t launch_selftest_wait_timeout(int timeout_us, unsigned* err, cudaStream_t s);
 

@@ -554,6 +554,52 @@ rf_status rf_attn_decode_paged(const rf_paged_kv* cache, const void* Q, void* O,
                                rf_stream_t stream);
 
 /*
+ * Which keys the query rows of rf_attn_decode_paged_ex read (host struct, read
+ * during the call).
+ *   window   0: every key up to the row's own position p.  W > 0: the last W of
+ *            them (p - W + 1 .. p) and
+ *   sinks    the first `sinks` keys of the sequence (looked at with a window).
+ *   parents  NULL: the Tq query tokens are a chain, the sequence's last Tq
+ *            tokens.  Else device int32 [B][Tq], 4-byte aligned: the last Tq
+ *            tokens are the nodes of a tree of drafted tokens, parents[b][t] the
+ *            node that t follows (an earlier one: < t), or -1 where it follows
+ *            the last token before the nodes.  A node reads the tokens before the
+ *            nodes, its line of parents, and itself; its position (which `window`
+ *            and `sinks` go by, for it and for the nodes it reads) is that of the
+ *            last token before the nodes, plus its depth, 1 for a node with
+ *            parent -1.  Several nodes may have parent -1 (a batch's smaller trees
+ *            are filled up with such nodes).
+ *   0 <= window, sinks <= 2^30.
+ */
+typedef struct {
+  int window, sinks;
+  const int32_t* parents;
+} rf_attn_mask;
+
+/* Workspace bytes rf_attn_decode_paged_ex needs, whatever the mask (0 for an
+ * invalid shape, or when no device can be queried). */
+size_t rf_attn_decode_paged_ex_workspace_size(int B, int Hq, int Hkv, int Tq, int d);
+
+/*
+ * rf_attn_decode_paged with a mask: the same cascade, arguments, layouts, limits
+ * and errors, over the keys that `mask` gives each row (NULL: the same call as
+ * rf_attn_decode_paged).  Pages in which no row reads a key (between the sinks and
+ * the window of the first of the Tq tokens) are not looked at: their entries of
+ * block_table may be anything, and a page may have gone to another sequence.  A
+ * value that a row does not read has no effect on it, whatever it is.
+ * A row that reads no key is written as zeros.  With a tree, a sequence of 1 ..
+ * Tq - 1 tokens, and a node whose line of parents meets an entry that is neither
+ * -1 nor that of an earlier node, are reported as RF_ERR_DEVICE_INPUT and their
+ * rows written as zeros.
+ *   workspace   as there, of rf_attn_decode_paged_ex_workspace_size bytes.
+ * Errors: those of rf_attn_decode_paged, and RF_ERR_INVALID_ARG for window or
+ * sinks outside 0 .. 2^30 and a misaligned `parents`.
+ */
+rf_status rf_attn_decode_paged_ex(const rf_paged_kv* cache, const void* Q, void* O, int Hq, int Tq,
+                                  float scale, const rf_attn_mask* mask, void* workspace,
+                                  size_t workspace_bytes, rf_stream_t stream);
+
+/*
  * Failure-detection self-test (no counterpart in the paper).  Launches one
  * CTA that waits on an mbarrier nothing ever completes, with a wait limit of
  * `timeout_us` microseconds (1..1000000).  The kernel gives up, records
@@ -644,6 +690,14 @@ int rf_selftest_append_plan(const int32_t* block_table, const int32_t* seq_lens,
  */
 int rf_selftest_decode_paged_plan(const int32_t* seq_lens, int B, int tiles, int max_len,
                                   int warps, int sms);
+
+/*
+ * The same for rf_attn_decode_paged_ex with Tq query tokens, a window (> 0) and
+ * sinks: also checks (number 6) that the chunks are the ones that hold a key
+ * which some of the Tq tokens reads.
+ */
+int rf_selftest_decode_paged_ex_plan(const int32_t* seq_lens, int B, int tiles, int max_len, int Tq,
+                                     int window, int sinks, int warps, int sms);
 
 #ifdef __cplusplus
 }

@@ -16,7 +16,10 @@ operations are used):
   page holds takes the larger of the old and the new one and re-encodes the
   old codes' values;
 * attention: every row is a three-pass softmax over the values that the cache
-  stands for.
+  stands for;
+* masks: the row at position p reads the keys at positions up to p, with a window
+  of W only those less than W before it and the first S (sinks); a node of a tree
+  of drafted tokens reads the tokens before the nodes and its line of parents.
 """
 from __future__ import annotations
 
@@ -124,4 +127,74 @@ def decode(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, scale: 
                 for g in range(Hq // Hkv):
                     hq = h * (Hq // Hkv) + g
                     o[b, t, hq] = row(q[b, t, hq], kb[:seen], vb[:seen], scale)
+    return o
+
+
+def line_of(parents, t: int):
+    """Node t of a tree and those it descends from, up to the root; None where an
+    entry is neither -1 nor that of an earlier node."""
+    line = [t]
+    while True:
+        up = int(parents[t])
+        if up == -1:
+            return line
+        if not 0 <= up < t:
+            return None
+        line.append(up)
+        t = up
+
+
+def seen_keys(n: int, Tq: int, t: int, window: int = 0, sinks: int = 0, parents=None):
+    """The keys that query token t of the last Tq of a sequence of n tokens reads,
+    ascending.  A chain's token is at its own place; a tree's node at the place of
+    its depth behind the n - Tq tokens before the nodes."""
+    first = n - Tq
+    if parents is None:
+        places = {j: j for j in range(max(0, first + t + 1))}          # key -> position
+        pos = first + t
+    else:
+        line = line_of(parents, t)
+        if line is None or first < 0:
+            return []
+        pos = first + len(line) - 1
+        places = {j: j for j in range(first)}
+        places.update({first + u: pos - i for i, u in enumerate(line)})
+    return sorted(j for j, at in places.items() if window == 0 or pos - at < window or at < sinks)
+
+
+def decode_masked(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, scale: float,
+                  window: int = 0, sinks: int = 0, parents=None, row=three_pass_row) -> np.ndarray:
+    """``decode`` over the keys of ``seen_keys``; parents [B, Tq] or None."""
+    q = _f64(q)
+    B, Tq, Hq, d = q.shape
+    K, V = values(k_pages, k_scale), values(v_pages, v_scale)
+    Hkv, ps = K.shape[1], K.shape[2]
+    o = np.zeros_like(q)
+    for b in range(B):
+        n = int(seq_lens[b])
+        for t in range(Tq if n else 0):
+            keys = seen_keys(n, Tq, t, window, sinks, None if parents is None else parents[b])
+            at = [(int(block_table[b][j // ps]), j % ps) for j in keys]
+            for hq in range(Hq):
+                h = hq // (Hq // Hkv)
+                kb = np.array([K[x, h, i] for x, i in at]).reshape(-1, d)
+                vb = np.array([V[x, h, i] for x, i in at]).reshape(-1, d)
+                o[b, t, hq] = row(q[b, t, hq], kb, vb, scale)
+    return o
+
+
+def window_prompt(q, k, v, new, keys, scale: float, window: int = 0, sinks: int = 0,
+                  row=three_pass_row) -> np.ndarray:
+    """Prompts: q [sum(new), Hq, d], k and v [sum(keys), Hkv, d]; the new tokens of
+    a sequence are the last of its keys'.  Returns o fp64 of q's shape."""
+    q, k, v = _f64(q), _f64(k), _f64(v)
+    o = np.zeros_like(q)
+    q0 = k0 = 0
+    for n, nk in zip(new, keys):
+        for t in range(n):
+            seen = [k0 + j for j in seen_keys(nk, n, t, window, sinks)]
+            for hq in range(q.shape[1]):
+                h = hq // (q.shape[1] // k.shape[1])
+                o[q0 + t, hq] = row(q[q0 + t, hq], k[seen, h], v[seen, h], scale)
+        q0, k0 = q0 + n, k0 + nk
     return o
