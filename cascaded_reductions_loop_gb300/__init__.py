@@ -27,7 +27,8 @@ __all__ = [
     "rf_mla_decode_workspace_size", "rf_moe_gate_topk_softmax", "rf_moe_gate_topk_softmax_ex",
     "rf_absmax_fp8_gemm", "rf_absmax_fp8_gemm_workspace_size", "rf_absmax_quant_fp8",
     "rf_paged_kv", "rf_norm_rope", "rf_qk_norm_rope", "rf_kv_append_paged", "rf_attn_decode_paged",
-    "rf_attn_decode_paged_workspace_size", "rf_attn_mask", "rf_attn_decode_paged_ex",
+    "rf_attn_decode_paged_workspace_size", "rf_attn_fwd_window", "rf_selftest_masked_plan",
+    "rf_attn_mask", "rf_attn_decode_paged_ex",
     "rf_attn_decode_paged_ex_workspace_size", "rf_selftest_append_plan",
     "rf_selftest_decode_paged_plan", "rf_selftest_decode_paged_ex_plan",
     "rf_selftest_wait_timeout", "rf_selftest_bounds", "rf_selftest_decode_plan",
@@ -106,6 +107,9 @@ _SIGS = {
     "rf_attn_decode_paged_ex_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "rf_attn_decode_paged_ex": (_I, [_c.POINTER(_PagedKV), _P, _P, _I, _I, _F,
                                      _c.POINTER(_AttnMask), _P, _Z, _P]),
+    "rf_attn_fwd_window": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _P, _P, _I, _I, _I, _I, _I, _I, _I,
+                                _F, _I, _I, _P]),
+    "rf_selftest_masked_plan": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I]),
     "rf_selftest_append_plan": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I]),
     "rf_selftest_decode_paged_plan": (_I, [_P, _I, _I, _I, _I, _I]),
     "rf_selftest_decode_paged_ex_plan": (_I, [_P, _I, _I, _I, _I, _I, _I, _I, _I]),
@@ -568,6 +572,43 @@ def rf_kv_append_paged(cache, k, v, norm_rope=None, cu_seqlens=None, q=None, q_o
                                   Hq, _stream(stream)), "rf_kv_append_paged")
 
 
+def rf_attn_fwd_window(q, k, v, o, scale: float, window: int, sinks: int = 0, cu_seqlens_q=None,
+                       cu_seqlens_k=None, max_seqlen_q=None, batch: int = 1, stream=None) -> None:
+    """Attention of prompts with a sliding window of `window` keys (0: none) and
+    the first `sinks` keys.  q, o: [total_q,Hq,d]; k, v: [total_k,Hkv,d], all
+    bf16, tokens strided as they like (views of a fused projection), the heads of
+    a token contiguous; cu_seqlens_q/k: int32 [B+1] cumulative lengths (not read
+    on the host; max_seqlen_q is then needed with cu_seqlens_q), or None: `batch`
+    sequences of equal lengths."""
+    dev, bf16 = torch.cuda.current_device(), torch.bfloat16
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(k, torch.Tensor) or \
+            k.dim() != 3:
+        raise ValueError("q and k must be [tokens, heads, d] tensors")
+    total_q, Hq, d = q.shape
+    total_k, Hkv, _ = k.shape
+    qp, ldq = _rows(q, dev, bf16, total_q, Hq, d, "q")
+    kp, ldk = _rows(k, dev, bf16, total_k, Hkv, d, "k")
+    vp, ldv = _rows(v, dev, bf16, total_k, Hkv, d, "v")
+    op, ldo = _rows(o, dev, bf16, total_q, Hq, d, "o")
+    B, cq, ck = int(batch), None, None
+    for cu in (cu_seqlens_q, cu_seqlens_k):
+        if cu is not None:
+            if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.numel() < 2:
+                raise ValueError("cu_seqlens must be an int32 [B + 1] tensor")
+            B = cu.numel() - 1
+    if cu_seqlens_q is not None:
+        cq = _dense(cu_seqlens_q, dev, torch.int32, (B + 1,), "cu_seqlens_q")
+        if max_seqlen_q is None:
+            raise ValueError("max_seqlen_q is needed with cu_seqlens_q")
+    if cu_seqlens_k is not None:
+        ck = _dense(cu_seqlens_k, dev, torch.int32, (B + 1,), "cu_seqlens_k")
+    if max_seqlen_q is None:
+        max_seqlen_q = -(-total_q // B) if B > 0 else 0
+    _check(lib.rf_attn_fwd_window(qp, ldq, kp, ldk, vp, ldv, op, ldo, cq, ck, B, Hq, Hkv,
+                                  int(max_seqlen_q), total_q, total_k, d, scale, int(window),
+                                  int(sinks), _stream(stream)), "rf_attn_fwd_window")
+
+
 def rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq=1, d=128) -> int:
     return lib.rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq, d)
 
@@ -693,6 +734,23 @@ def rf_selftest_append_plan(block_table, seq_lens, cu_seqlens, total: int, num_p
         _host_i32(block_table, "block_table"), _host_i32(seq_lens, "seq_lens"),
         None if cu_seqlens is None else _host_i32(cu_seqlens, "cu_seqlens"), B, int(total),
         int(num_pages), int(page_size), max_pages, int(max_pos))
+
+
+def rf_selftest_masked_plan(seq_lens, cu_seqlens_q, cu_seqlens_k, B: int, Hkv: int, G: int,
+                            max_q: int, total_q: int, total_k: int, window: int, sinks: int,
+                            tree: int, sms: int) -> int:
+    """Host-side check of the plan of rf_attn_fwd_window (seq_lens None) and of
+    rf_attn_decode_paged_ex with many query rows (no GPU needed): int32 CPU
+    tensors or None; 0 when it is consistent, -1 for refused sizes, else the number
+    of the first failed check (see include/rf.h)."""
+    at = []
+    for t, n, name in ((seq_lens, B, "seq_lens"), (cu_seqlens_q, B + 1, "cu_seqlens_q"),
+                       (cu_seqlens_k, B + 1, "cu_seqlens_k")):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} must have {n} entries")
+        at.append(None if t is None else _host_i32(t, name))
+    return lib.rf_selftest_masked_plan(*at, int(B), int(Hkv), int(G), int(max_q), int(total_q),
+                                       int(total_k), int(window), int(sinks), int(tree), int(sms))
 
 
 def rf_selftest_decode_paged_ex_plan(seq_lens, tiles: int, max_len: int, Tq: int, window: int,

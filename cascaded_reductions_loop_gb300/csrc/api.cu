@@ -540,8 +540,18 @@ size_t rf_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Tq, int d
   return decode_paged_workspace_bytes(B, Hkv, Hq / Hkv * Tq, d);
 }
 
+// With a mask, a bf16 cache and more query rows a kv head than this, the tensor-core
+// kernel with tiles of 128 rows takes the call.
+static constexpr int kFewRows = 16;
+static bool many_rows(int dtype, int R, int G) {
+  return dtype == RF_BF16 && R > kFewRows && G <= 128;
+}
+
 size_t rf_attn_decode_paged_ex_workspace_size(int B, int Hq, int Hkv, int Tq, int d) {
-  return rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq, d);
+  const size_t few = rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq, d);
+  if (few == 0 || !many_rows(RF_BF16, Hq / Hkv * Tq, Hq / Hkv)) return few;
+  const size_t many = masked_rows_workspace_bytes(d);
+  return many > few ? many : few;
 }
 
 rf_status rf_attn_decode_paged(const rf_paged_kv* cache, const void* Q, void* O, int Hq, int Tq,
@@ -567,21 +577,77 @@ rf_status rf_attn_decode_paged_ex(const rf_paged_kv* cache, const void* Q, void*
   if (mask && (!window_ok(mask->window, mask->sinks) ||
                (reinterpret_cast<uintptr_t>(mask->parents) & 3u)))
     return RF_ERR_INVALID_ARG;
+  const bool masked = mask && (mask->window != 0 || mask->parents);
+  if (masked && Tq > (1 << 30)) return RF_ERR_INVALID_ARG;
   const int R = Hq / cache->Hkv * Tq;
+  const bool many = masked && many_rows(cache->dtype, R, Hq / cache->Hkv);
   if (decode_paged_max_chunks(cache->B, cache->Hkv, R, cache->max_pages, cache->page_size) >=
       (1ll << 31))
     return RF_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace)) return RF_ERR_WORKSPACE;
-  const size_t need = decode_paged_workspace_bytes(cache->B, cache->Hkv, R, cache->d);
+  const size_t need = many ? masked_rows_workspace_bytes(cache->d)
+                           : decode_paged_workspace_bytes(cache->B, cache->Hkv, R, cache->d);
   if (need == 0) return RF_ERR_CUDA;   // the partition needs the device's SM count
   if (workspace_bytes < need) return RF_ERR_WORKSPACE;
   unsigned* err = device_error_word();
   if (!err) return RF_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool masked = mask && (mask->window != 0 || mask->parents);
+  if (many)
+    return from_cuda(launch_masked_rows(*cache, *mask, Q, O, Hq, Tq, scale, workspace, err, s));
   return from_cuda(masked ? launch_decode_paged_masked(*cache, *mask, Q, O, Hq, Tq, scale,
                                                        workspace, err, s)
                           : launch_decode_paged(*cache, Q, O, Hq, Tq, scale, workspace, err, s));
+}
+
+rf_status rf_attn_fwd_window(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V,
+                             int64_t ldv, void* O, int64_t ldo, const int32_t* cu_seqlens_q,
+                             const int32_t* cu_seqlens_k, int B, int Hq, int Hkv, int max_seqlen_q,
+                             int total_q, int total_k, int d, float scale, int window, int sinks,
+                             rf_stream_t stream) {
+  constexpr int kMost = 1 << 30;
+  if (B < 1 || Hq < 1 || Hkv < 1 || max_seqlen_q < 1 || total_q < 1 || total_k < 1 || d < 1 ||
+      Hq % Hkv != 0)
+    return RF_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return RF_ERR_UNSUPPORTED;
+  if (Hq / Hkv > 128) return RF_ERR_UNSUPPORTED;
+  if (B > kMost || total_q > kMost || total_k > kMost || max_seqlen_q > total_q ||
+      (int64_t)B * max_seqlen_q >= (1ll << 31) || Hq > (1 << 20) || !window_ok(window, sinks))
+    return RF_ERR_INVALID_ARG;
+  if (cu_seqlens_q ? !aligned4(cu_seqlens_q) : total_q % B != 0 || max_seqlen_q < total_q / B)
+    return RF_ERR_INVALID_ARG;
+  if (cu_seqlens_k ? !aligned4(cu_seqlens_k) : total_k % B != 0) return RF_ERR_INVALID_ARG;
+  if (!rows_ok(Q, ldq, total_q, Hq, d, 2) || !rows_ok(O, ldo, total_q, Hq, d, 2) ||
+      !rows_ok(K, ldk, total_k, Hkv, d, 2) || !rows_ok(V, ldv, total_k, Hkv, d, 2))
+    return RF_ERR_INVALID_ARG;
+  // a tensor map's strides are below 2^40 bytes
+  if (ldq >= (1ll << 39) || ldk >= (1ll << 39) || ldv >= (1ll << 39)) return RF_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale < INFINITY)) return RF_ERR_INVALID_ARG;
+  unsigned* err = device_error_word();
+  if (!err) return RF_ERR_CUDA;
+  return from_cuda(launch_attn_fwd_window(Q, ldq, K, ldk, V, ldv, O, ldo, cu_seqlens_q,
+                                          cu_seqlens_k, B, Hq, Hkv, max_seqlen_q, total_q, total_k,
+                                          d, scale, window, sinks, err,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int rf_selftest_masked_plan(const int32_t* seq_lens, const int32_t* cu_seqlens_q,
+                            const int32_t* cu_seqlens_k, int B, int Hkv, int G, int max_q,
+                            int total_q, int total_k, int window, int sinks, int tree, int sms) {
+  constexpr int kMost = 1 << 24;
+  if (B < 1 || Hkv < 1 || G < 1 || G > 128 || max_q < 1 || total_k < 1 || total_k > kMost ||
+      (int64_t)B * max_q > kMost || !window_ok(window, sinks) || sms < 1 || sms > (1 << 20) ||
+      Hkv > (1 << 20) || (tree != 0 && tree != 1) || (tree && !seq_lens))
+    return -1;
+  if (!seq_lens && (total_q < 1 || total_q > kMost || max_q > total_q ||
+                    (!cu_seqlens_q && (total_q % B != 0 || max_q < total_q / B)) ||
+                    (!cu_seqlens_k && total_k % B != 0)))
+    return -1;
+  try {
+    return masked_plan_selfcheck(seq_lens, cu_seqlens_q, cu_seqlens_k, B, Hkv, G, max_q, total_q,
+                                 total_k, window, sinks, tree, sms);
+  } catch (...) {                              // no memory for the walk
+    return -1;
+  }
 }
 
 int rf_selftest_append_plan(const int32_t* block_table, const int32_t* seq_lens,

@@ -1,0 +1,1050 @@
+// attn_masked_tc.cu -- attention whose rows read only some of the keys, on the tensor
+// cores: prompts with a sliding window and sinks (packed K and V), and many query rows
+// a kv head (drafted trees, chunks of a prompt) over a paged bf16 cache.
+//
+// For the row at position p, over the keys that it reads (p - j < W or j < S; of a
+// tree's nodes, its line of parents):
+//     m = max_j s_j,  l = sum_j exp(s_j - m),  o = sum_j exp(s_j - m) v_j / l,
+// the cascade of [E] §2.2 in its incremental form ([E] §2.3).  The plan (which rows
+// and keys an item has, how items are shared out) is in attn_masked_tc.cuh.
+//
+// A CTA takes items of two 128-row query tiles (a, b).  Per key tile j and tile x:
+//   1. MMA thread x: S_x = Q_x K_j^T (tcgen05 kind::f16, M = N = 128, fp32 in tensor
+//      memory);
+//   2. softmax warpgroup x, a thread a row: its 128 scores in registers, the keys it
+//      does not read at -inf (only in tiles that some row reads in part), running
+//      maximum moved lazily (by more than 2^8 only), P = 2^(S c - m) as bf16;
+//   3. MMA thread x: O_x += P_x V_j (P the tensor-memory A operand).
+// Tensor memory holds S_a, S_b, O_a, O_b, at d = 128 all of its 512 columns, so P_x
+// lies over S_x: the next S_x waits for P_x V_j.  While one tile's softmax runs, the
+// tensor core has the other tile's products.
+//
+// Rounding: P is rounded to bf16 (half a step, 2^-8 of a weight; l sums the unrounded
+// ones), since both operands of an MMA have one type and V is bf16.
+//
+// Masked places.  Scores are selected, not added to.  A value that is not finite
+// would reach rows that do not read it as 0 * inf, so a guard warp looks the values of
+// every partly read tile over; rows of such a tile that are not finite are zeroed in
+// shared memory, and the softmax threads of the rows that do read them add weight
+// times value themselves.
+#include <math.h>
+
+#include <vector>
+
+#include "attn_masked_tc.cuh"
+
+namespace rf {
+namespace masked {
+
+constexpr int kHalf = 128 * 128;                      // 128 rows of 64 values: 16 KB
+constexpr int kThreads = 384;                         // TMA, MMA a, MMA b, guard; softmax a; softmax b
+constexpr float kLazy = 8.f;
+// Registers: 384 threads start with 168 each (64512): the softmax warpgroups take 208
+// (53248) of them, the others keep 88 (11264).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+
+template <int D>
+struct Cfg {
+  static constexpr int kTile = D / 64 * kHalf;        // 128 rows of D values
+  static constexpr int kQSlots = D == 64 ? 4 : 3;
+  static constexpr int kStages = D == 64 ? 8 : 4;     // K and V tiles, in turn
+  static constexpr int kPairs = kStages / 2;
+  static constexpr int kRing = kQSlots * kTile;
+  static constexpr int kBarOff = kRing + kStages * kTile;
+  static constexpr int kSmem = kBarOff + 1024 + 1024; // barriers; alignment
+  static constexpr uint32_t kIdescS = make_idesc(BQ, BK, 1, 0, 0);
+  static constexpr uint32_t kIdescO = make_idesc(BQ, D, 1, 0, 1);
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+constexpr uint32_t kTmemCols = 512;
+__device__ __forceinline__ uint32_t col_s(int x) { return x * 128; }      // P_x over its first 64
+__device__ __forceinline__ uint32_t col_o(int x) { return 256 + x * 128; }
+
+struct Params {
+  Geo geo;
+  __nv_bfloat16* O;
+  const __nv_bfloat16* V;
+  int64_t ldo, ldv, n_v;                              // elements between tokens; of V
+  const int* parents;
+  const int* block_table;
+  int Hq, num_pages, page_size, page_shift, max_pages;
+  float c_log2;
+  float4* ws_o;                                       // [slots][2][D / 4][128]
+  float2* ws_ml;                                      // [slots][2][128]
+  int4* ws_cut;                                       // [grid]: tile, group, head where a CTA's range
+                                                      // begins; of the first: all tiles, active CTAs
+  unsigned* err;
+};
+
+struct Bars {
+  uint64_t q_full[4], q_empty[4];
+  uint64_t full[8], empty[8];
+  uint64_t v_ok[4];                                   // a V tile is looked over
+  uint64_t s_full[2], p_full[2], pv_done[2], drain[2];
+  unsigned pages[8];                                  // per key tile: bit per 16 keys that are there
+  // what the guard found, per V stage: values that are not finite, and `pages`
+  unsigned bad[4][4], there[4];
+  int64_t warp_sum[kThreads / 32];
+  int64_t x[2], total;                                // the CTA's range, all tiles
+  int g, h, j;                                        // where it begins
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 1024, "barriers");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Bits 0 .. n - 1 of a word.
+__device__ __forceinline__ unsigned below(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
+}
+
+// Whether some row of the piece may not read all of tile j's keys (the same for
+// every role).
+__device__ __forceinline__ bool partly(const Geo& p, const Piece& c, int key0) {
+  const int ctx = c.w.lk - c.w.lq;
+  const int first = p.tree ? ctx - 1 : ctx + c.w.t0;          // the first row's position
+  const int last = p.tree ? c.w.lk - 1 : ctx + c.w.t1 - 1;
+  return key0 + BK > first + 1 ||
+         (p.window > 0 && key0 < last - p.window + 1 && key0 + BK > p.sinks);
+}
+
+template <int D, bool kPaged>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_masked_kernel(const __grid_constant__ CUtensorMap tmQ,
+                       const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kBarOff);
+  volatile int* abort_flag = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = (int)blockIdx.x;
+  const Geo& geo = p.geo;
+  uint8_t* ring = smem + C::kRing;
+
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&bars->q_full[i]), 1);
+      mbar_init(smem_u32(&bars->q_empty[i]), 1);
+      mbar_init(smem_u32(&bars->v_ok[i]), 1);
+    }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(smem_u32(&bars->full[i]), 1);
+      mbar_init(smem_u32(&bars->empty[i]), 2);        // both MMA threads
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars->s_full[i]), 1);
+      mbar_init(smem_u32(&bars->p_full[i]), BQ);
+      mbar_init(smem_u32(&bars->pv_done[i]), 1);
+      mbar_init(smem_u32(&bars->drain[i]), 1);
+    }
+    bars->abort = 0;
+    bars->x[0] = bars->x[1] = 0;
+    bars->g = bars->h = bars->j = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&bars->tmem), kTmemCols);
+    tmem_relinquish();
+  }
+
+  // ---- plan: add up all tiles, find where this CTA's range begins
+  const int ng = geo.B * geo.npairs;
+  const int per = (ng + kThreads - 1) / kThreads;
+  const int g_lo = min((int)threadIdx.x * per, ng), g_hi = min(g_lo + per, ng);
+  int64_t mine = 0;
+  for (int g = g_lo; g < g_hi; ++g)
+    mine += (int64_t)group_of(geo, g, cta == 0, p.err).n * geo.Hkv;
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) bars->warp_sum[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int64_t pre = incl - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) pre += bars->warp_sum[w];
+    total += bars->warp_sum[w];
+  }
+  const int grid = total < (int64_t)gridDim.x ? (int)total : (int)gridDim.x;
+  if (cta < grid) {
+    const Split64 split(total, grid);
+    for (int i = 0; i < 2; ++i) {
+      const int64_t x = split.start(cta + i);
+      if (x >= total) {
+        if (threadIdx.x == 0) bars->x[i] = total;
+      } else if (x >= pre && x - pre < mine) {        // in this thread's groups: walk to it
+        int64_t at = pre;
+        for (int g = g_lo; g < g_hi; ++g) {
+          const int n = group_of(geo, g, false, p.err).n;
+          const int64_t all = (int64_t)n * geo.Hkv;
+          if (x - at < all) {
+            const int h = (int)((x - at) / n), off = (int)((x - at) % n);
+            const int j = kPaged ? off : snap(off, n);
+            bars->x[i] = x - off + j;
+            if (i == 0) {
+              bars->g = g;
+              bars->h = h;
+              bars->j = j;
+            }
+            break;
+          }
+          at += all;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem = bars->tmem;
+  const int64_t x0 = bars->x[0], x1 = bars->x[1];
+  if (kPaged && threadIdx.x == 0 && RF_IN(p.err, cta, gridDim.x))
+    p.ws_cut[cta] = cta == 0 ? make_int4(0, (int)(total & 0x7FFFFFFF), (int)(total >> 31), grid)
+                             : make_int4(x1 > x0 ? bars->j : 0, bars->g, bars->h, 0);
+  Walk walk(geo, bars->g, bars->h, bars->j, x1 - x0, p.err);
+  Piece c;
+  bool ok = true;
+
+  if (warp < 4) {
+    regs_dec<kOtherRegs>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- TMA
+      const uint64_t pol_kv = policy_evict_last(), pol_q = policy_evict_first();
+      int nq = 0, nt = 0;                             // Q tiles, key tiles issued
+      unsigned in_flight = 0;                         // stages filled so far (2 a key tile)
+      while (ok && walk.next(geo, c, p.err)) {
+        for (int x = 0; ok && x < 2; ++x) {
+          const Tile t = tile_of(geo, c, x);
+          if (!t.has()) continue;
+          const int slot = nq % C::kQSlots;
+          ok = __all_sync(0xffffffffu, nq < C::kQSlots ||
+                                           mbar_wait(smem_u32(&bars->q_empty[slot]),
+                                                     (uint32_t)((nq / C::kQSlots - 1) & 1)));
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&bars->q_full[slot]);
+            const uint32_t dst = smem_u32(smem + slot * C::kTile);
+            mbar_arrive_expect_tx(bar, (uint32_t)(D / 64 * geo.tpt * geo.G * 128));
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+              tma_load_3d_hint(dst + i * kHalf, &tmQ, bar, 64 * i, c.h * geo.G, c.w.q0 + t.t0, pol_q);
+          }
+          ++nq;
+        }
+        for (int j = c.j0; ok && j < c.j1; ++j, ++nt) {
+          const int key0 = key0_of(c.w, j);
+          const int st = 2 * (nt % C::kPairs);
+          const uint32_t ph = (uint32_t)((nt / C::kPairs - 1) & 1);
+          // over a cache: lane i has the tile's page i
+          int row = 0;
+          bool there = false;
+          if (kPaged) {
+            const int first = key0 + lane * p.page_size;
+            const bool read = lane < BK >> p.page_shift && first < c.w.lk;
+            if (read) {
+              const int page = ld_int(p.block_table,
+                                      (int64_t)c.w.b * p.max_pages + (first >> p.page_shift),
+                                      (int64_t)geo.B * p.max_pages, p.err);
+              // a page in which no row reads anything may be anything
+              const int ctx = c.w.lk - c.w.lq;
+              const int lo = geo.window > 0 ? (geo.tree ? ctx : ctx + c.w.t0) - geo.window + 1 : 0;
+              const bool wanted = first + p.page_size > lo || first < geo.sinks;
+              there = wanted && (unsigned)page < (unsigned)p.num_pages;
+              if (wanted && !there) raise_error(p.err, kDevErrInput);
+              row = (page * geo.Hkv + c.h) * p.page_size;
+            }
+          }
+          const unsigned pages = __ballot_sync(0xffffffffu, there);
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {               // K, then V
+            const uint32_t bar = smem_u32(&bars->full[st + v]);
+            ok = __all_sync(0xffffffffu,
+                            nt < C::kPairs || mbar_wait(smem_u32(&bars->empty[st + v]), ph));
+            if (!ok) break;
+            const uint32_t dst = smem_u32(ring + (st + v) * C::kTile);
+            const CUtensorMap* tm = v ? &tmV : &tmK;
+            if (kPaged) {
+              if (lane == 0) {
+                if (v == 0) {
+                  // K may be one round ahead of V, so the words' ring has two rounds
+                  const int per16 = p.page_size >> 4;           // bits of a page
+                  unsigned bits = 0;
+                  for (unsigned m = pages; m != 0; m &= m - 1)
+                    bits |= ((1u << per16) - 1u) << ((__ffs((int)m) - 1) * per16);
+                  bars->pages[nt % (2 * C::kPairs)] = bits;
+                }
+                mbar_arrive_expect_tx(bar, (uint32_t)(__popc(pages) * p.page_size * D * 2));
+              }
+              __syncwarp();
+              if (there)
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+                  tma_load_2d_hint(dst + i * kHalf + lane * p.page_size * 128, tm, bar, 64 * i, row,
+                                   pol_kv);
+            } else if (lane == 0) {
+              mbar_arrive_expect_tx(bar, C::kTile);
+#pragma unroll
+              for (int i = 0; i < D / 64; ++i)
+                tma_load_3d_hint(dst + i * kHalf, tm, bar, 64 * i, c.h, c.w.k0 + key0, pol_kv);
+            }
+            ++in_flight;
+          }
+        }
+        if (*abort_flag) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (!ok) {
+        raise_error(p.err, kDevErrTimeout);
+        *abort_flag = 1;
+        // copies in flight land before shared memory is released
+        for (int i = max(0, nq - C::kQSlots); i < nq; ++i)
+          (void)mbar_wait(smem_u32(&bars->q_full[i % C::kQSlots]), (uint32_t)((i / C::kQSlots) & 1),
+                          1000000ull);
+        for (unsigned i = in_flight > C::kStages ? in_flight - C::kStages : 0; i < in_flight; ++i)
+          (void)mbar_wait(smem_u32(&bars->full[i % C::kStages]), (i / C::kStages) & 1, 1000000ull);
+      }
+    } else if (warp < 3) {
+      // ---------------------------------------------------------- MMA of tile x
+      const int x = warp - 1;
+      if (lane == 0) {
+        int nq = 0, nt = 0, cnt = 0;                  // Q tiles, key tiles, own key tiles
+        while (ok && walk.next(geo, c, p.err)) {
+          const Tile t = tile_of(geo, c, x);
+          const int slot = (nq + x) % C::kQSlots;
+          if (t.has())
+            ok = mbar_wait(smem_u32(&bars->q_full[slot]), (uint32_t)(((nq + x) / C::kQSlots) & 1));
+          bool fresh = true;
+          for (int j = c.j0; ok && j < c.j1; ++j, ++nt) {
+            const int pr = nt % C::kPairs, st = 2 * pr;
+            const uint32_t ph = (uint32_t)((nt / C::kPairs) & 1);
+            const bool mine = takes(geo, c, t, j);
+            if (!mbar_wait(smem_u32(&bars->full[st]), ph)) {
+              ok = false;
+              break;
+            }
+            if (mine) {
+              // S_x's columns hold the last P_x until its product with V is done
+              if (cnt > 0 && !mbar_wait(smem_u32(&bars->pv_done[x]), (uint32_t)((cnt - 1) & 1))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t qa = smem_u32(smem + slot * C::kTile);
+              const uint32_t ka = smem_u32(ring + st * C::kTile);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                mma_bf16_ss(tmem + col_s(x), sw128_desc(qa + (k >> 2) * kHalf + (k & 3) * 32, 1024, 16),
+                            sw128_desc(ka + (k >> 2) * kHalf + (k & 3) * 32, 1024, 16), C::kIdescS,
+                            k != 0);
+              mma_commit(smem_u32(&bars->s_full[x]));
+              if (j == t.last) mma_commit(smem_u32(&bars->q_empty[slot]));
+            }
+            mma_commit(smem_u32(&bars->empty[st]));
+            if (!mbar_wait(smem_u32(&bars->v_ok[pr]), ph)) {
+              ok = false;
+              break;
+            }
+            if (mine) {
+              if (!mbar_wait(smem_u32(&bars->p_full[x]), (uint32_t)(cnt & 1))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const unsigned* b = bars->bad[pr];
+              const bool onto = !fresh || (b[0] | b[1] | b[2] | b[3]) != 0u;
+              const uint32_t va = smem_u32(ring + (st + 1) * C::kTile);
+#pragma unroll
+              for (int k = 0; k < BK / 16; ++k)
+                mma_bf16_ts(tmem + col_o(x), tmem + col_s(x) + k * 8,
+                            sw128_desc(va + k * 16 * 128, 1024, kHalf), C::kIdescO, onto || k != 0);
+              mma_commit(smem_u32(&bars->pv_done[x]));
+              fresh = false;
+              ++cnt;
+            }
+            mma_commit(smem_u32(&bars->empty[st + 1]));
+          }
+          nq += tile_of(geo, c, 1).has() ? 2 : 1;
+          if (*abort_flag) ok = false;
+        }
+        if (!ok) {
+          raise_error(p.err, kDevErrTimeout);
+          *abort_flag = 1;
+        }
+        // nothing may still run on the tensor core when memory is released
+        mma_commit(smem_u32(&bars->drain[x]));
+        (void)mbar_wait(smem_u32(&bars->drain[x]), 0, 1000000000ull);
+      }
+    } else {
+      // ---------------------------------------------------------- guard
+      int nt = 0;
+      while (ok && walk.next(geo, c, p.err)) {
+        for (int j = c.j0; ok && j < c.j1; ++j, ++nt) {
+          const int pr = nt % C::kPairs, st = 2 * pr;
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->full[st + 1]),
+                                                 (uint32_t)((nt / C::kPairs) & 1)));
+          if (!ok) break;
+          const int key0 = key0_of(c.w, j);
+          const unsigned pages = kPaged ? bars->pages[nt % (2 * C::kPairs)] : 0xFFu;
+          unsigned bad[4] = {0u, 0u, 0u, 0u};
+          if (partly(geo, c, key0) || pages != 0xFFu) {
+            uint4* v = reinterpret_cast<uint4*>(ring + (st + 1) * C::kTile);
+            unsigned seen = 0;
+#pragma unroll 8
+            for (int i = lane; i < C::kTile / 16; i += 32) {
+              const uint4 w = v[i];
+              // an exponent of ones carries into the sign's place
+              seen |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                      ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+            }
+            if (__any_sync(0xffffffffu, (seen & 0x80008000u) != 0u)) {
+#pragma unroll 1
+              for (int r = 0; r < BK; ++r) {          // which rows; they become zeros
+                bool hit = false;
+                if (lane < D / 8) {
+                  const uint4 w = v[(lane >> 3) * (kHalf / 16) + r * 8 + (lane & 7)];
+                  const unsigned y = ((w.x & 0x7F807F80u) + 0x00800080u) |
+                                     ((w.y & 0x7F807F80u) + 0x00800080u) |
+                                     ((w.z & 0x7F807F80u) + 0x00800080u) |
+                                     ((w.w & 0x7F807F80u) + 0x00800080u);
+                  hit = (y & 0x80008000u) != 0u;
+                }
+                if (!__any_sync(0xffffffffu, hit)) continue;
+                bad[0] |= r < 32 ? 1u << r : 0u;
+                bad[1] |= r >= 32 && r < 64 ? 1u << (r & 31) : 0u;
+                bad[2] |= r >= 64 && r < 96 ? 1u << (r & 31) : 0u;
+                bad[3] |= r >= 96 ? 1u << (r & 31) : 0u;
+                if (lane < D / 8)
+                  v[(lane >> 3) * (kHalf / 16) + r * 8 + (lane & 7)] = make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+            }
+          }
+          __syncwarp();
+          if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bars->bad[pr][i] = bad[i];
+            bars->there[pr] = pages;
+            mbar_arrive(smem_u32(&bars->v_ok[pr]));
+          }
+        }
+        if (*abort_flag) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (!ok) {
+        raise_error(p.err, kDevErrTimeout);
+        *abort_flag = 1;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax of tile x
+    regs_inc<kSoftmaxRegs>();
+    const int x = warp >= 8 ? 1 : 0;
+    const int r = (warp & 3) * 32 + lane;             // row of the tile
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lane_off + col_s(x), o_addr = tmem + lane_off + col_o(x);
+    const uint64_t c2 = f2(p.c_log2, p.c_log2);
+    const int my_t = r / geo.G, my_g = r - my_t * geo.G;
+    int nt = 0, cnt = 0;
+    int64_t s0 = x0 - (x1 > x0 ? bars->j : 0);        // first tile of the piece's item
+    while (ok && walk.next(geo, c, p.err)) {
+      const Tile t = tile_of(geo, c, x);
+      const int64_t item0 = s0;
+      s0 += c.w.n;
+      const int j_base = nt - c.j0;                   // key tile j is the CTA's j_base + j th
+      nt += c.j1 - c.j0;
+      if (!t.has()) continue;
+      const int tok = t.t0 + my_t;
+      const bool real = my_t < geo.tpt && tok < t.t1;
+      const int ctx = c.w.lk - c.w.lq;
+      int pos = ctx + tok;                            // the row's position; < 0: it reads nothing
+      if (geo.tree) {
+        bool line = real && ctx >= 0;
+        int u = tok, depth = 0;
+        while (line) {
+          const int up = ld_int(p.parents, (int64_t)c.w.b * geo.max_q + u,
+                                (int64_t)geo.B * geo.max_q, p.err);
+          if (up == -1) break;
+          line = up >= 0 && up < u;
+          u = up;
+          ++depth;
+        }
+        if (real && !line && c.w.lk > 0) raise_error(p.err, kDevErrInput);
+        pos = line ? ctx + depth : -1;
+      }
+      float m_ref = -INFINITY, l_run = 0.f;
+      bool fresh = true;
+      for (int j = c.j0; j < c.j1; ++j) {
+        if (!takes(geo, c, t, j)) continue;
+        const int key0 = key0_of(c.w, j), pr = (j_base + j) % C::kPairs;
+        bool part = partly(geo, c, key0);
+        unsigned w[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};   // keys it reads
+        unsigned bad[4] = {0u, 0u, 0u, 0u};
+        bool any_bad = false;
+        if (kPaged || part) {
+          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->v_ok[pr]),
+                                                 (uint32_t)(((j_base + j) / C::kPairs) & 1)))) {
+            ok = false;
+            break;
+          }
+          const unsigned pages = kPaged ? bars->there[pr] : 0xFFu;
+          part = part || pages != 0xFFu;
+          if (part) {
+            const int hi = geo.tree ? min(ctx, pos + 1) : pos + 1;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int k = key0 + 32 * q;
+              w[q] = below(hi - k);
+              if (geo.window > 0) w[q] &= ~below(pos - geo.window + 1 - k) | below(geo.sinks - k);
+              if (pos < 0 || !real) w[q] = 0u;
+              bad[q] = bars->bad[pr][q];
+              any_bad |= bad[q] != 0u;
+            }
+            if (geo.tree && key0 + BK > ctx && pos >= 0 && real) {
+              int u = tok;
+              for (int at = pos; u >= 0; --at) {      // node u at position `at`
+                const int bit = ctx + u - key0;
+                if (bit >= 0 && bit < BK &&
+                    (geo.window == 0 || at > pos - geo.window || at < geo.sinks)) {
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    if ((bit >> 5) == q) w[q] |= 1u << (bit & 31);
+                }
+                const int up = ld_int(p.parents, (int64_t)c.w.b * geo.max_q + u,
+                                      (int64_t)geo.B * geo.max_q, p.err);
+                u = up < u ? up : -1;
+              }
+            }
+            if (kPaged) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                w[q] &= ((pages >> (2 * q)) & 1u ? 0xFFFFu : 0u) |
+                        ((pages >> (2 * q + 1)) & 1u ? 0xFFFF0000u : 0u);
+            }
+          }
+        }
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(smem_u32(&bars->s_full[x]), (uint32_t)(cnt & 1)) && !*abort_flag)) {
+          ok = false;
+          break;
+        }
+        ++cnt;
+        tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + q * 32, v[q]);
+        tmem_ld_wait();
+        if (part && __any_sync(0xffffffffu, (w[0] & w[1] & w[2] & w[3]) != 0xFFFFFFFFu)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[q][i] = (w[q] >> i) & 1u ? v[q][i] : 0xff800000u;
+        }
+        // row maximum (four chains)
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            mx4[(i >> 1) & 3] =
+                fmax3(mx4[(i >> 1) & 3], __uint_as_float(v[q][i]), __uint_as_float(v[q][i + 1]));
+        const float mt = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * p.c_log2;
+        float alpha = 1.f;
+        if (fresh) {
+          m_ref = mt;                                 // P.V of the first tile overwrites O
+        } else if (mt > m_ref + kLazy) {
+          alpha = ex2(m_ref - mt);
+          l_run *= alpha;
+          m_ref = mt;
+        }
+        // O_x is complete through the last tile: its P.V was done before this S began
+        if (!fresh && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + q * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(o_addr + q * 32, o);
+          }
+        }
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        if (any_bad) {
+          // values that are not finite, for the rows that read them
+          tmem_st_wait();
+          if (fresh) {
+            uint32_t z[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = 0u;
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) tmem_st32(o_addr + q * 32, z);
+            tmem_st_wait();
+          }
+#pragma unroll 1
+          for (int k = 0; k < BK; ++k) {
+            const unsigned bw = k < 32 ? bad[0] : (k < 64 ? bad[1] : (k < 96 ? bad[2] : bad[3]));
+            if (!((bw >> (k & 31)) & 1u)) continue;
+            float sc = 0.f;
+            bool reads = false;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (q * 32 + i == k) {
+                  sc = __uint_as_float(v[q][i]);
+                  reads = (w[q] >> i) & 1u;
+                }
+            const float pk = ex2(fmaf(sc, p.c_log2, -m_use));
+            int64_t at;                               // the value's first element
+            bool inside;
+            if (kPaged) {
+              const int page = ld_int(p.block_table,
+                                      (int64_t)c.w.b * p.max_pages + ((key0 + k) >> p.page_shift),
+                                      (int64_t)geo.B * p.max_pages, p.err);
+              at = (((int64_t)page * geo.Hkv + c.h) * p.page_size + ((key0 + k) & (p.page_size - 1))) * D;
+              inside = key0 + k < c.w.lk && (unsigned)page < (unsigned)p.num_pages;
+            } else {
+              at = (int64_t)(c.w.k0 + key0 + k) * p.ldv + (int64_t)c.h * D;
+              inside = key0 + k < c.w.lk;
+            }
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32(o_addr + q * 32, o);
+              tmem_ld_wait();
+              if (reads && inside && RF_IN(p.err, at + D - 1, p.n_v))
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  o[i] = __float_as_uint(fmaf(pk, __bfloat162float(p.V[at + q * 32 + i]),
+                                              __uint_as_float(o[i])));
+              __syncwarp();
+              tmem_st32(o_addr + q * 32, o);
+              tmem_st_wait();
+            }
+          }
+        }
+        fresh = false;
+        // P = 2^(S c - m) as bf16 pairs, and its row sum (four chains)
+        const uint64_t negm2 = f2(-m_use, -m_use);
+        uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int q = 2 * hh + h;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float t0, t1;
+              f2_split(ffma2(f2(__uint_as_float(v[q][2 * i]), __uint_as_float(v[q][2 * i + 1])), c2,
+                             negm2),
+                       t0, t1);
+              const float p0 = ex2(t0), p1 = ex2(t1);
+              sum4[i & 3] = fadd2(sum4[i & 3], f2(p0, p1));
+              pk[h * 16 + i] = pack_bf16x2(p0, p1);
+            }
+          }
+          tmem_st32(s_addr + hh * 32, pk);
+        }
+        float s_lo, s_hi;
+        f2_split(fadd2(fadd2(sum4[0], sum4[1]), fadd2(sum4[2], sum4[3])), s_lo, s_hi);
+        l_run += s_lo + s_hi;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&bars->p_full[x]));
+      }
+      if (!ok) break;
+      // the piece's last product
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->pv_done[x]), (uint32_t)((cnt - 1) & 1)) &&
+                                       !*abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (pos < 0) l_run = 0.f;                       // it reads nothing: zeros
+      const bool whole = !kPaged || c.whole();
+      const int64_t slot = slot_of(cta, item0, x0) * 2 + x;
+      const int64_t row = ((int64_t)c.w.q0 + tok) * p.ldo + (int64_t)(c.h * geo.G + my_g) * D;
+      const bool out = real && RF_IN(p.err, row + D - 1,
+                                     ((int64_t)(kPaged ? geo.B * geo.max_q : geo.total_q) - 1) * p.ldo +
+                                         (int64_t)p.Hq * D);
+      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        tmem_ld32(o_addr + q * 32, o);
+        tmem_ld_wait();
+        if (whole) {
+          if (out) {
+            // a row that read no key: zeros, whatever O holds
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t u[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                u[k] = l_run == 0.f ? 0u
+                                    : pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv,
+                                                  __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+              reinterpret_cast<uint4*>(p.O + row)[q * 4 + i] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int64_t at = (slot * (D / 4) + q * 8 + i) * BQ + r;
+            if (RF_IN(p.err, at, (int64_t)4 * gridDim.x * (D / 4) * BQ))
+              p.ws_o[at] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+          }
+        }
+      }
+      if (!whole && RF_IN(p.err, slot * BQ + r, (int64_t)4 * gridDim.x * BQ))
+        p.ws_ml[slot * BQ + r] = make_float2(m_ref, l_run);
+      tc_fence_before();                              // O is read before the next product writes it
+    }
+    if (!ok) {
+      raise_error(p.err, kDevErrTimeout);
+      *abort_flag = 1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the states of the items that are cut between CTAs.  Block (c - 1, x, part) has
+// the item in which CTA c's range begins, if that is the item's first cut: tile x, 8 of
+// its dims, a thread a row; pieces in key order.
+template <int D>
+__global__ void __launch_bounds__(BQ)
+    merge_kernel(const __grid_constant__ Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Geo& geo = p.geo;
+  const int c1 = (int)blockIdx.x + 1, x = blockIdx.y, part = blockIdx.z, r = threadIdx.x;
+  const int slots = (int)gridDim.x + 1;               // CTAs of the attention kernel
+  if (!RF_IN(p.err, c1, slots)) return;
+  const int4 cut = __ldcg(&p.ws_cut[c1]);
+  if (cut.x <= 0) return;
+  // the same plan as there: the item, and all tiles' number from the CTA borders
+  const Group w = group_of(geo, cut.y, false, p.err);
+  if (w.n <= cut.x) return;
+  const int4 head = __ldcg(&p.ws_cut[0]);
+  const int64_t total = (int64_t)head.y | ((int64_t)head.z << 31);
+  const Split64 split(total, head.w);
+  const int64_t s0 = split.start(c1) - cut.x, s1 = s0 + w.n;
+  if (split.owner(s0) != c1 - 1) return;
+  const int pieces = split.owner(s1 - 1) - (c1 - 1) + 1;
+  Piece pc = {w, cut.z, 0, w.n};
+  const Tile t = tile_of(geo, pc, x);
+  const int my_t = r / geo.G, tok = t.t0 + my_t;
+  if (my_t >= geo.tpt || tok >= t.t1) return;
+  auto slot = [&](int i) { return slot_of(c1 - 1 + i, s0, split.start(c1 - 1 + i)) * 2 + x; };
+  float m = -INFINITY, l = 0.f, v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) {
+    const int64_t s = slot(i), at = (s * (D / 4) + part * 2) * BQ + r;
+    if (!RF_IN(p.err, s * BQ + r, (int64_t)4 * slots * BQ) ||
+        !RF_IN(p.err, at + BQ, (int64_t)4 * slots * (D / 4) * BQ))
+      continue;
+    const float2 ml = __ldcg(&p.ws_ml[s * BQ + r]);
+    const float4 a = __ldcg(&p.ws_o[at]), b = __ldcg(&p.ws_o[at + BQ]);
+    if (ml.y == 0.f) continue;                        // read no key: its O may be anything
+    const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+    const float keep = ex2(m - mu), f = ex2(ml.x - mu);
+    m = mn;
+    l = fmaf(l, keep, ml.y * f);
+    const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = fmaf(v[k], keep, u[k] * f);
+  }
+  const int64_t row = ((int64_t)w.q0 + tok) * p.ldo +
+                      (int64_t)(cut.z * geo.G + (r - my_t * geo.G)) * D + part * 8;
+  if (!RF_IN(p.err, row + 7, ((int64_t)geo.B * geo.max_q - 1) * p.ldo + (int64_t)p.Hq * D)) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t u[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    u[k] = l == 0.f ? 0u : pack_bf16x2(v[2 * k] * inv, v[2 * k + 1] * inv);
+  *reinterpret_cast<uint4*>(p.O + row) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+template <int D, bool kPaged>
+cudaError_t launch(const CUtensorMap (&tm)[3], Params& p, int grid, cudaStream_t s) {
+  using C = Cfg<D>;
+  auto kern = attn_masked_kernel<D, kPaged>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, C::kSmem, s>>>(tm[0], tm[1], tm[2], p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !kPaged || grid < 2) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid - 1, 2, D / 8);
+  cfg.blockDim = dim3(BQ, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p);
+}
+
+size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace masked
+
+using masked::Geo;
+
+namespace {
+
+Geo packed_geo(const int* cu_q, const int* cu_k, int B, int Hkv, int G, int max_q, int total_q,
+               int total_k, int window, int sinks) {
+  Geo g = {};
+  g.cu_q = cu_q;
+  g.cu_k = cu_k;
+  g.B = B;
+  g.Hkv = Hkv;
+  g.G = G;
+  g.tpt = masked::BQ / G;
+  g.npairs = (int)(((int64_t)max_q + 2 * g.tpt - 1) / (2 * g.tpt));
+  g.max_q = max_q;
+  g.total_q = total_q;
+  g.total_k = total_k;
+  g.window = window;
+  g.sinks = sinks;
+  return g;
+}
+
+Geo paged_geo(const int* seq_lens, int B, int Hkv, int G, int Tq, int max_len, int window, int sinks,
+              bool tree) {
+  Geo g = packed_geo(nullptr, nullptr, B, Hkv, G, Tq, 0, 0, window, sinks);
+  g.seq_lens = seq_lens;
+  g.max_len = max_len;
+  g.tree = tree;
+  return g;
+}
+
+}  // namespace
+
+cudaError_t launch_attn_fwd_window(const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                                   const void* V, int64_t ldv, void* O, int64_t ldo,
+                                   const int* cu_q, const int* cu_k, int B, int Hq, int Hkv,
+                                   int max_q, int total_q, int total_k, int d, float scale,
+                                   int window, int sinks, unsigned* err, cudaStream_t s) {
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidValue;
+  masked::Params p = {};
+  p.geo = packed_geo(cu_q, cu_k, B, Hkv, Hq / Hkv, max_q, total_q, total_k, window, sinks);
+  p.O = static_cast<__nv_bfloat16*>(O);
+  p.V = static_cast<const __nv_bfloat16*>(V);
+  p.ldo = ldo;
+  p.ldv = ldv;
+  p.n_v = (int64_t)(total_k - 1) * ldv + (int64_t)Hkv * d;
+  p.Hq = Hq;
+  p.c_log2 = scale * 1.4426950408889634f;
+  p.err = err;
+  CUtensorMap tm[3];
+  const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (!encode_tmap_3d(&tm[0], t, Q, d, Hq, total_q, d * 2, ldq * 2, 64, p.geo.G, p.geo.tpt, true) ||
+      !encode_tmap_3d(&tm[1], t, K, d, Hkv, total_k, d * 2, ldk * 2, 64, 1, masked::BK, true) ||
+      !encode_tmap_3d(&tm[2], t, V, d, Hkv, total_k, d * 2, ldv * 2, 64, 1, masked::BK, true))
+    return cudaErrorInvalidValue;
+  return d == 64 ? masked::launch<64, false>(tm, p, sms, s)
+                 : masked::launch<128, false>(tm, p, sms, s);
+}
+
+// Workspace: partial states [2 SMs][2][d / 4][128] float4, (m, l) [2 SMs][2][128],
+// the cuts [SMs].
+size_t masked_rows_workspace_bytes(int d) {
+  const int sms = sm_count();
+  if (sms <= 0) return 0;
+  const size_t rows = (size_t)sms * 4 * masked::BQ;
+  return rows * d * sizeof(float) + rows * sizeof(float2) + masked::pad256(sms * sizeof(int4));
+}
+
+cudaError_t launch_masked_rows(const PagedKV& c, const Mask& mask, const void* Q, void* O, int Hq,
+                               int Tq, float scale, void* workspace, unsigned* err,
+                               cudaStream_t s) {
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidValue;
+  masked::Params p = {};
+  p.geo = paged_geo(c.seq_lens, c.B, c.Hkv, Hq / c.Hkv, Tq, c.max_pages * c.page_size, mask.window,
+                    mask.sinks, mask.parents != nullptr);
+  p.O = static_cast<__nv_bfloat16*>(O);
+  p.V = static_cast<const __nv_bfloat16*>(c.v);
+  p.ldo = (int64_t)Hq * c.d;
+  const uint64_t keys = (uint64_t)c.num_pages * c.Hkv * c.page_size;
+  p.n_v = (int64_t)keys * c.d;
+  p.parents = mask.parents;
+  p.block_table = c.block_table;
+  p.Hq = Hq;
+  p.num_pages = c.num_pages;
+  p.page_size = c.page_size;
+  p.page_shift = c.page_size == 16 ? 4 : (c.page_size == 32 ? 5 : (c.page_size == 64 ? 6 : 7));
+  p.max_pages = c.max_pages;
+  p.c_log2 = scale * 1.4426950408889634f;
+  p.err = err;
+  const size_t rows = (size_t)sms * 4 * masked::BQ;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.ws_o = reinterpret_cast<float4*>(ws);
+  ws += rows * c.d * sizeof(float);
+  p.ws_ml = reinterpret_cast<float2*>(ws);
+  ws += rows * sizeof(float2);
+  p.ws_cut = reinterpret_cast<int4*>(ws);
+  CUtensorMap tm[3];
+  const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int d = c.d;
+  if (!encode_tmap_3d(&tm[0], t, Q, d, Hq, (uint64_t)c.B * Tq, d * 2, (uint64_t)Hq * d * 2, 64,
+                      p.geo.G, p.geo.tpt, true) ||
+      !encode_tmap_2d(&tm[1], t, c.k, d, keys, d * 2, 64, c.page_size, true) ||
+      !encode_tmap_2d(&tm[2], t, c.v, d, keys, d * 2, 64, c.page_size, true))
+    return cudaErrorInvalidValue;
+  return d == 64 ? masked::launch<64, true>(tm, p, sms, s) : masked::launch<128, true>(tm, p, sms, s);
+}
+
+// Host-side walk of the plan (the functions of the header, shared by host and device)
+// for `sms` CTAs.  Returns 0 when every invariant holds, else the number of the first
+// that fails:
+//   1 no index leaves its array;
+//   2 the CTAs' pieces, end to end, are all items' tiles, in order, once;
+//   3 a prompt's items are whole; over a cache a CTA cuts at most its first and its
+//     last item, into slots of their own;
+//   4 the merge counts a cut item's pieces and finds their slots, in key order;
+//   5 every row with tokens lies in one tile of one item;
+//   6 every key that a row reads lies in exactly one tile that its tile takes, and
+//     every tile has one to take.
+int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k, int B, int Hkv,
+                          int G, int max_q, int total_q, int total_k, int window, int sinks,
+                          int tree, int sms) {
+  using namespace masked;
+  const Geo p = seq_lens ? paged_geo(seq_lens, B, Hkv, G, max_q, total_k, window, sinks, tree != 0)
+                         : packed_geo(cu_q, cu_k, B, Hkv, G, max_q, total_q, total_k, window, sinks);
+  unsigned err = 0;
+  const int ng = p.B * p.npairs;
+  std::vector<int64_t> pre((size_t)ng + 1, 0);
+  for (int g = 0; g < ng; ++g)
+    pre[(size_t)g + 1] = pre[(size_t)g] + (int64_t)group_of(p, g, true, &err).n * Hkv;
+  const int64_t total = pre[(size_t)ng];
+  if (err & kDevErrBounds) return 1;
+  const int grid = total < sms ? (int)total : sms;
+  std::vector<int> want_rows((size_t)B, 0), rows((size_t)B, 0);
+  for (int g = 0; g < ng; ++g) {
+    const Group w = group_of(p, g, false, &err);
+    want_rows[(size_t)w.b] = w.lq;
+    if (w.n > 0) rows[(size_t)w.b] += w.t1 - w.t0;
+    Piece c = {w, 0, 0, w.n};
+    for (int x = 0; w.n > 0 && x < 2; ++x) {
+      const Tile t = tile_of(p, c, x);
+      if (!t.has()) continue;
+      if (t.t1 - t.t0 > p.tpt) return 5;
+      int some = 0;
+      for (int j = 0; j < w.n; ++j) some += takes(p, c, t, j);
+      if (!some || !takes(p, c, t, t.last)) return 6;
+      for (int i = t.t0; i < t.t1; ++i) {
+        // a tree's node may be at any position from its first on, and reads no other key
+        const int at[2] = {p.tree ? w.lk - w.lq : w.lk - w.lq + i, p.tree ? w.lk - 1 : w.lk - w.lq + i};
+        for (int key = 0; key < w.lk; ++key) {
+          const bool reads = key <= at[1] && (window == 0 || at[0] - key < window || key < sinks);
+          int hits = 0;
+          for (int j = 0; j < w.n; ++j)
+            hits += takes(p, c, t, j) && key >= key0_of(w, j) && key < key0_of(w, j) + BK;
+          if (reads ? hits != 1 : hits > 1) return 6;
+        }
+      }
+    }
+  }
+  for (int b = 0; b < B; ++b)
+    if (rows[(size_t)b] != want_rows[(size_t)b]) return 5;
+  if (total == 0) return 0;
+  const Split64 split(total, grid);
+  int64_t x = 0;
+  int wg = -1, wh = Hkv - 1, wj = 0, wn = 0;          // the next tile in the order of all
+  std::vector<unsigned char> used((size_t)2 * sms, 0);
+  std::vector<int64_t> parts;                         // of the item being cut
+  for (int c = 0; c < grid; ++c) {
+    int64_t r[2];
+    int start[3] = {0, 0, 0};
+    for (int i = 0; i < 2; ++i) {
+      r[i] = split.start(c + i);
+      if (r[i] >= total) continue;
+      int g = 0;
+      while (pre[(size_t)g + 1] <= r[i]) ++g;
+      const int n = group_of(p, g, false, &err).n;
+      const int h = (int)((r[i] - pre[(size_t)g]) / n), off = (int)((r[i] - pre[(size_t)g]) % n);
+      const int j = seq_lens ? off : snap(off, n);
+      r[i] += j - off;
+      if (i == 0) {
+        start[0] = g;
+        start[1] = h;
+        start[2] = j;
+      }
+    }
+    if (r[0] != x || r[1] < r[0]) return 2;
+    Walk walk(p, start[0], start[1], start[2], r[1] - r[0], &err);
+    Piece pc;
+    int cuts = 0;
+    int64_t s0 = x - (r[1] > r[0] ? start[2] : 0);
+    while (walk.next(p, pc, &err)) {
+      if (err & kDevErrBounds) return 1;
+      const int64_t item0 = s0;
+      s0 += pc.w.n;
+      for (int j = pc.j0; j < pc.j1; ++j, ++x) {
+        if (wj == wn) {                               // on to the next item
+          wj = 0;
+          if (++wh == Hkv) {
+            wh = 0;
+            do {
+              ++wg;
+            } while (wg < ng && pre[(size_t)wg + 1] == pre[(size_t)wg]);
+          }
+          if (wg >= ng) return 2;
+          wn = group_of(p, wg, false, &err).n;
+        }
+        const Group w = group_of(p, wg, false, &err);
+        if (pc.w.b != w.b || pc.w.t0 != w.t0 || pc.h != wh || j != wj) return 2;
+        ++wj;
+      }
+      if (pc.whole()) continue;
+      if (!seq_lens || ++cuts > 2) return 3;
+      const int64_t slot = slot_of(c, item0, r[0]);
+      if (slot < 0 || slot >= 2 * (int64_t)sms || used[(size_t)slot]++) return 3;
+      if (pc.j0 == 0) parts.clear();
+      parts.push_back(slot);
+      if (pc.j1 == pc.w.n) {                          // the last piece: as the merge finds them
+        const int64_t s1 = item0 + pc.w.n;
+        const int c0 = split.owner(item0), pieces = split.owner(s1 - 1) - c0 + 1;
+        if ((int)parts.size() != pieces || split.start(c0 + 1) <= item0) return 4;
+        for (int i = 0; i < pieces; ++i)
+          if (slot_of(c0 + i, item0, split.start(c0 + i)) != parts[(size_t)i]) return 4;
+      }
+    }
+  }
+  return x == total && wj == wn ? 0 : 2;
+}
+
+}  // namespace rf

@@ -1,0 +1,218 @@
+// attn_masked_tc.cuh -- the plan of the tensor-core attention whose rows read only
+// some of the keys (attn_masked_tc.cu): which rows and keys a work item has, and how
+// the items are shared out.  The same code on the device and, for the self-check, on
+// the host.
+//
+// Rows.  The G = Hq / Hkv query heads of a kv head read the same keys, so a tile of
+// 128 rows holds tpt = floor(128 / G) consecutive tokens of all G heads (row t G + g),
+// and a window costs the W + tpt keys of that tile rather than the W + 128 of a tile
+// of one head.  An item is a pair of tiles (a, b) of one sequence and kv head; both
+// read the key tiles that are loaded for it.
+//
+// Keys.  An item's key tiles (128 keys each) are `lead` tiles from key 0 on, with the
+// sinks, then tiles from `start` on, the beginning of its first row's window, up to
+// its last row's position.
+//
+// Partition.  The key tiles of all items, end to end in the order (sequence, pair,
+// head), are cut into one equal range per CTA.  Prompts take whole items (the border
+// next to the cut); over a cache, where few items may have many tiles, an item is
+// cut, the states of its pieces go to the workspace and a second kernel merges them.
+#pragma once
+
+#include "rf_device.cuh"
+#include "rf_internal.h"
+
+namespace rf {
+namespace masked {
+
+constexpr int BQ = 128, BK = 128;
+
+struct Geo {
+  const int* seq_lens;      // paged: [B] tokens of each sequence; else null
+  const int* cu_q;          // packed: [B + 1] cumulative lengths, or null: equal ones
+  const int* cu_k;
+  int B, Hkv, G, tpt;       // tpt: tokens of a tile
+  int npairs;               // pairs of a sequence, at most
+  int max_q;                // paged: query tokens of each sequence (Tq)
+  int total_q, total_k;     // packed
+  int max_len;              // paged
+  int window, sinks, tree;
+};
+
+__host__ __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
+__host__ __device__ __forceinline__ int imax(int a, int b) { return a > b ? a : b; }
+
+// Pair p of sequence b: its rows and its key tiles (of each kv head).
+struct Group {
+  int b, q0, k0;            // first query token, first key of the sequence (rows of Q, K)
+  int lq, lk;               // the sequence's query tokens and keys
+  int t0, t1;               // the pair's tokens t0 .. t1 - 1
+  int start, lead, n;       // key tiles; n = 0: there are no rows
+};
+
+__host__ __device__ __forceinline__ Group group_of(const Geo& p, int g, bool report,
+                                                   unsigned* err) {
+  Group w;
+  w.b = g / p.npairs;
+  const int pair = g - w.b * p.npairs;
+  if (p.seq_lens) {
+    w.lk = ld_int(p.seq_lens, w.b, p.B, err);
+    if (w.lk < 0 || w.lk > p.max_len) {
+      if (report && pair == 0) note_error(err, kDevErrInput);
+      w.lk = 0;
+    }
+    w.lq = p.max_q;
+    w.q0 = w.b * p.max_q;
+    w.k0 = 0;
+  } else {
+    int a0, a1, c0, c1;
+    if (p.cu_q) {
+      a0 = ld_int(p.cu_q, w.b, p.B + 1, err);
+      a1 = ld_int(p.cu_q, w.b + 1, p.B + 1, err);
+    } else {
+      a0 = w.b * (p.total_q / p.B);
+      a1 = a0 + p.total_q / p.B;
+    }
+    if (p.cu_k) {
+      c0 = ld_int(p.cu_k, w.b, p.B + 1, err);
+      c1 = ld_int(p.cu_k, w.b + 1, p.B + 1, err);
+    } else {
+      c0 = w.b * (p.total_k / p.B);
+      c1 = c0 + p.total_k / p.B;
+    }
+    const bool ok = 0 <= a0 && a0 <= a1 && a1 <= p.total_q && a1 - a0 <= p.max_q && 0 <= c0 &&
+                    c0 <= c1 && c1 <= p.total_k;
+    if (!ok && report && pair == 0) note_error(err, kDevErrInput);
+    w.q0 = ok ? a0 : 0;
+    w.k0 = ok ? c0 : 0;
+    w.lq = ok ? a1 - a0 : 0;
+    w.lk = ok ? c1 - c0 : 0;
+  }
+  w.t0 = 2 * pair * p.tpt;
+  w.t1 = imin(w.lq, w.t0 + 2 * p.tpt);
+  w.start = w.lead = w.n = 0;
+  if (w.t0 >= w.t1) return w;
+  const int ctx = w.lk - w.lq;                        // position of token 0
+  const int end = imax(0, imin(w.lk, p.tree ? w.lk : ctx + w.t1));      // behind the last key
+  if (p.window > 0) {
+    int lo = (p.tree ? ctx : ctx + w.t0) - p.window + 1;
+    if (p.seq_lens) lo = lo > 0 ? lo & ~(BK - 1) : lo;       // whole pages lie in one tile
+    if (lo > 0) {
+      const int lead = (imin(p.sinks, end) + BK - 1) / BK;
+      if (lead * BK < lo) {
+        w.start = lo;
+        w.lead = lead;
+      }
+    }
+  }
+  // rows that read nothing still take one (fully masked) tile, which writes their zeros
+  w.n = imax(1, w.lead + (end - w.start + BK - 1) / BK);
+  return w;
+}
+
+// The next group with rows from g on (B * npairs if there is none), left in w.
+__host__ __device__ __forceinline__ int next_group(const Geo& p, int g, Group& w, unsigned* err) {
+  const int ng = p.B * p.npairs;
+  while (g < ng) {
+    w = group_of(p, g, false, err);
+    if (w.n > 0) return g;
+    g = (w.b + 1) * p.npairs;                         // its later pairs have no rows either
+  }
+  return ng;
+}
+
+__host__ __device__ __forceinline__ int key0_of(const Group& w, int j) {
+  return j < w.lead ? j * BK : w.start + (j - w.lead) * BK;
+}
+
+// T tiles over n ranges, the first T % n of them one longer.
+struct Split64 {
+  int64_t q, rem;
+  __host__ __device__ __forceinline__ Split64(int64_t T, int n) : q(T / n), rem(T % n) {}
+  __host__ __device__ __forceinline__ int64_t start(int c) const {
+    return c * q + (c < rem ? c : rem);
+  }
+  __host__ __device__ __forceinline__ int owner(int64_t x) const {
+    const int64_t big = rem * (q + 1);
+    return (int)(x < big ? x / (q + 1) : rem + (x - big) / q);
+  }
+};
+
+// Where whole items are taken: the border next to tile `off` of an item of n.
+__host__ __device__ __forceinline__ int snap(int off, int n) { return 2 * off < n ? 0 : n; }
+
+// A CTA's range of tiles, piece by piece.
+struct Piece {
+  Group w;
+  int h, j0, j1;            // tiles j0 .. j1 - 1 of the item
+  __host__ __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == w.n; }
+};
+struct Walk {
+  int64_t left;             // tiles still to take
+  int g, h, j;
+  Group w;
+  // From tile j (which may be n: the item behind is meant) of head h of group g.
+  __host__ __device__ __forceinline__ Walk(const Geo& p, int g_, int h_, int j_, int64_t count,
+                                           unsigned* err)
+      : left(count), g(g_), h(h_), j(j_) {
+    if (left > 0) {
+      w = group_of(p, g, false, err);
+      settle(p, err);
+    }
+  }
+  __host__ __device__ __forceinline__ void settle(const Geo& p, unsigned* err) {
+    if (j < w.n) return;
+    j = 0;
+    if (++h < p.Hkv) return;
+    h = 0;
+    g = next_group(p, g + 1, w, err);
+    if (g >= p.B * p.npairs) left = 0;                // (on the device: the lengths changed)
+  }
+  __host__ __device__ __forceinline__ bool next(const Geo& p, Piece& out, unsigned* err) {
+    if (left <= 0) return false;
+    out.w = w;
+    out.h = h;
+    out.j0 = j;
+    out.j1 = (int64_t)(w.n - j) < left ? w.n : j + (int)left;
+    left -= out.j1 - out.j0;
+    j = out.j1;
+    if (left > 0) settle(p, err);
+    return true;
+  }
+};
+
+// Tile x (0, 1) of a piece: its tokens, and which of the piece's key tiles it takes.
+struct Tile {
+  int t0, t1;               // its tokens; t0 >= t1: it has no rows
+  int first, last;          // of the item's window tiles (whole items), see takes()
+  __host__ __device__ __forceinline__ bool has() const { return t0 < t1; }
+};
+__host__ __device__ __forceinline__ Tile tile_of(const Geo& p, const Piece& c, int x) {
+  Tile t;
+  t.t0 = c.w.t0 + x * p.tpt;
+  t.t1 = imin(c.w.t1, t.t0 + p.tpt);
+  t.first = c.j0;
+  t.last = c.j1 - 1;
+  if (p.seq_lens || !t.has()) return t;
+  const int ctx = c.w.lk - c.w.lq;
+  const int hi = imin(c.w.lk - 1, ctx + t.t1 - 1);    // its last row's position
+  const int lo = p.window > 0 ? ctx + t.t0 - p.window + 1 : 0;
+  t.first = lo > c.w.start ? c.w.lead + (lo - c.w.start) / BK : c.w.lead;
+  t.last = hi < 0 ? 0 : c.w.lead + (hi - c.w.start) / BK;
+  if (t.last < t.first) t.first = t.last;
+  return t;
+}
+__host__ __device__ __forceinline__ bool takes(const Geo& p, const Piece& c, const Tile& t, int j) {
+  if (!t.has() || j > t.last) return false;
+  return j >= t.first || key0_of(c.w, j) < p.sinks;
+}
+
+// The workspace slot of CTA c's piece of an item that begins at tile s0 (in the
+// order of all tiles), of which the CTA's range begins at x0: only its first and
+// its last item can be cut.
+__host__ __device__ __forceinline__ int64_t slot_of(int c, int64_t s0, int64_t x0) {
+  return 2 * (int64_t)c + (s0 < x0 ? 0 : 1);
+}
+
+}  // namespace masked
+}  // namespace rf

@@ -444,14 +444,21 @@ struct KFrag {
 // O += V^T P^T for the 16 keys of half mt.  Which dims an m-tile holds is
 // free too.  E4M3: lane (g, c) reads dims [g D/8, (g+1) D/8) of keys 2c, 2c+1,
 // 2c+8, 2c+9; m-tile i's rows g and g + 8 are dims g D/8 + 2i and + 1.
-// bf16: natural order.  Modes: kAll; kMasked, keys whose bit (counted within the
-// chunk) is not set in `keep` are replaced by zero; kSome, the same, and only the
-// rows whose bit is set in `rows` (bit 2 nt + e for this lane's row 2c + e) take
-// the result.
+// bf16: natural order.  Modes: kAll; kMasked, keys (counted within the chunk) that
+// are not `in` are replaced by zero; kSome, the same, and only the rows whose bit
+// is set in `rows` (bit 2 nt + e for this lane's row 2c + e) take the result.
 enum { kAll, kMasked, kSome };
-template <bool kF8, int D, int NT, int kMode>
+struct Below {             // the first n keys
+  int n;
+  __device__ __forceinline__ bool operator()(int key) const { return key < n; }
+};
+struct Among {             // the keys whose bit is set
+  unsigned bits;
+  __device__ __forceinline__ bool operator()(int key) const { return (bits >> key) & 1u; }
+};
+template <bool kF8, int D, int NT, int kMode, typename In>
 __device__ __forceinline__ void pv16(float (&o)[D / 16][NT][4], uint32_t base, int mt, int lane,
-                                     unsigned keep, unsigned rows,
+                                     In in, unsigned rows,
                                      const uint32_t (&p)[NT][kF8 ? 1 : 2][2]) {
   constexpr bool kMask = kMode != kAll;
   auto accumulate = [&](float(&acc)[4], const uint32_t(&a)[4], int nt) {
@@ -472,7 +479,7 @@ __device__ __forceinline__ void pv16(float (&o)[D / 16][NT][4], uint32_t base, i
       const int key = mt * 16 + 2 * c + (i & 1) + (i >> 1) * 8;
       if (D == 128) lds128(base + f8_off<D>(key, g * (D / 8)), v[i]);
       else lds64(base + f8_off<D>(key, g * (D / 8)), v[i]);
-      if (kMask && !((keep >> key) & 1u))
+      if (kMask && !in(key))
 #pragma unroll
         for (int j = 0; j < NW; ++j) v[i][j] = 0u;
     }
@@ -496,9 +503,9 @@ __device__ __forceinline__ void pv16(float (&o)[D / 16][NT][4], uint32_t base, i
     // which of this lane's keys 2c, 2c+1 (low, high halves), 2c+8, 2c+9 stay
     uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;
     if (kMask) {
-      const unsigned k0 = keep >> (mt * 16 + 2 * c);
-      keep0 = ((k0 & 1u) ? 0xFFFFu : 0u) | ((k0 & 2u) ? 0xFFFF0000u : 0u);
-      keep1 = ((k0 & 256u) ? 0xFFFFu : 0u) | ((k0 & 512u) ? 0xFFFF0000u : 0u);
+      const int k0 = mt * 16 + 2 * c;
+      keep0 = (in(k0) ? 0xFFFFu : 0u) | (in(k0 + 1) ? 0xFFFF0000u : 0u);
+      keep1 = (in(k0 + 8) ? 0xFFFFu : 0u) | (in(k0 + 9) ? 0xFFFF0000u : 0u);
     }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
@@ -521,12 +528,12 @@ __device__ __forceinline__ unsigned bits_below(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
 }
 
-// Whether any value of the chunk's keys in `keys` is an infinity or NaN.
-template <bool kF8, int D>
-__device__ __forceinline__ bool any_nonfinite(uint32_t base, int lane, unsigned keys) {
+// Whether any value of keys [lo, hi) of the chunk that are `in` is an infinity or NaN.
+template <bool kF8, int D, typename In>
+__device__ __forceinline__ bool any_nonfinite(uint32_t base, int lane, int lo, int hi, In in) {
   bool bad = false;
-  for (; keys != 0; keys &= keys - 1) {
-    const int key = __ffs((int)keys) - 1;
+  for (int key = lo; key < hi; ++key) {
+    if (!in(key)) continue;
     if (kF8) {
       if (lane < D / 16) {
         uint32_t w[4];
@@ -1082,14 +1089,14 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     uint32_t pb[2][NT][kF8 ? 1 : 2][2];
     const bool two = kF8 && lv[0] != lv[1];
     float cm[NT][2], cM[NT][2], mu[NT][2], Mu[NT][2], a_o[NT][2];
-    const unsigned pages_in = ((valid & 1) ? 0xFFFFu : 0u) | ((valid & 2) ? 0xFFFF0000u : 0u);
     unsigned seen[NT][2];
     if (kExt && tail) {
+      const unsigned there = ((valid & 1) ? 0xFFFFu : 0u) | ((valid & 2) ? 0xFFFF0000u : 0u);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          seen[nt][e] = seen_by(key0, nt, e) & pages_in;
+          seen[nt][e] = seen_by(key0, nt, e) & there;
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
@@ -1201,8 +1208,8 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
 
     // ---- O^T += V^T P^T
     if (!tail) {
-      pv16<kF8, D, NT, kAll>(o, vb, 0, lane, 0u, 0u, pb[0]);
-      pv16<kF8, D, NT, kAll>(o, vb, 1, lane, 0u, 0u, pb[1]);
+      pv16<kF8, D, NT, kAll>(o, vb, 0, lane, Below{0}, 0u, pb[0]);
+      pv16<kF8, D, NT, kAll>(o, vb, 1, lane, Below{0}, 0u, pb[1]);
     } else if (kExt) {
       unsigned any = 0u, all = 0xFFFFFFFFu;    // keys that some row, that every row reads
 #pragma unroll
@@ -1214,7 +1221,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
         }
       any = __reduce_or_sync(0xffffffffu, any);
       all = __reduce_and_sync(0xffffffffu, all);
-      if (any_nonfinite<kF8, D>(vb, lane, any & ~all)) {
+      if (any_nonfinite<kF8, D>(vb, lane, 0, kChunk, Among{any & ~all})) {
 #pragma unroll 1
         for (int r = 0; r < 8; ++r)            // a row at a time
 #pragma unroll
@@ -1222,17 +1229,19 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
             const unsigned a = __shfl_sync(0xffffffffu, seen[nt][0], r >> 1),
                            b = __shfl_sync(0xffffffffu, seen[nt][1], r >> 1);
             const unsigned rows = c == (r >> 1) ? 1u << (2 * nt + (r & 1)) : 0u;
-            pv16<kF8, D, NT, kSome>(o, vb, 0, lane, (r & 1) ? b : a, rows, pb[0]);
-            pv16<kF8, D, NT, kSome>(o, vb, 1, lane, (r & 1) ? b : a, rows, pb[1]);
+            pv16<kF8, D, NT, kSome>(o, vb, 0, lane, Among{(r & 1) ? b : a}, rows, pb[0]);
+            pv16<kF8, D, NT, kSome>(o, vb, 1, lane, Among{(r & 1) ? b : a}, rows, pb[1]);
           }
       } else {
-        pv16<kF8, D, NT, kMasked>(o, vb, 0, lane, any, 0u, pb[0]);
-        pv16<kF8, D, NT, kMasked>(o, vb, 1, lane, any, 0u, pb[1]);
+        pv16<kF8, D, NT, kMasked>(o, vb, 0, lane, Among{any}, 0u, pb[0]);
+        pv16<kF8, D, NT, kMasked>(o, vb, 1, lane, Among{any}, 0u, pb[1]);
       }
     } else {
-      const unsigned exist = bits_below(cur_len - key0);
-      const unsigned some = exist & ~bits_below(cur_len - p.Tq + 1 - key0);   // not for all rows
-      if (p.Tq > 1 && any_nonfinite<kF8, D>(vb, lane, some)) {
+      int end[2];                              // keys of each half that exist
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) end[h2] = ((valid >> h2) & 1) ? cur_len - key0 : 0;
+      const int lo = max(cur_len - p.Tq + 1 - key0, 0), hi = min(cur_len - key0, kChunk);
+      if (p.Tq > 1 && any_nonfinite<kF8, D>(vb, lane, lo, hi, Below{kChunk})) {
 #pragma unroll 1
         for (int t = 0; t < p.Tq; ++t) {       // the rows of one query token at a time
           unsigned rows = 0;
@@ -1243,13 +1252,13 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
               if (((cur_hr % p.tiles) * kTileRows + nt * 8 + 2 * c + e) / p.G == t)
                 rows |= 1u << (2 * nt + e);
           if (!__any_sync(0xffffffffu, rows != 0)) continue;
-          const unsigned seen = exist & pages_in & bits_below(cur_len - p.Tq + t + 1 - key0);
-          pv16<kF8, D, NT, kSome>(o, vb, 0, lane, seen, rows, pb[0]);
-          pv16<kF8, D, NT, kSome>(o, vb, 1, lane, seen, rows, pb[1]);
+          const int seen = cur_len - p.Tq + t + 1 - key0;
+          pv16<kF8, D, NT, kSome>(o, vb, 0, lane, Below{min(end[0], seen)}, rows, pb[0]);
+          pv16<kF8, D, NT, kSome>(o, vb, 1, lane, Below{min(end[1], seen)}, rows, pb[1]);
         }
       } else {
-        pv16<kF8, D, NT, kMasked>(o, vb, 0, lane, exist & pages_in, 0u, pb[0]);
-        pv16<kF8, D, NT, kMasked>(o, vb, 1, lane, exist & pages_in, 0u, pb[1]);
+        pv16<kF8, D, NT, kMasked>(o, vb, 0, lane, Below{end[0]}, 0u, pb[0]);
+        pv16<kF8, D, NT, kMasked>(o, vb, 1, lane, Below{end[1]}, 0u, pb[1]);
       }
     }
 

@@ -145,6 +145,22 @@ cudaError_t launch_decode_paged_masked(const PagedKV& c, const Mask& mask, const
                                        int Hq, int Tq, float scale, void* workspace, unsigned* err,
                                        cudaStream_t s);
 
+// Prompts with a window and sinks, bf16; cu_q, cu_k null: equal lengths.
+cudaError_t launch_attn_fwd_window(const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                                   const void* V, int64_t ldv, void* O, int64_t ldo,
+                                   const int* cu_q, const int* cu_k, int B, int Hq, int Hkv,
+                                   int max_q, int total_q, int total_k, int d, float scale,
+                                   int window, int sinks, unsigned* err, cudaStream_t s);
+// Many query rows a kv head over a bf16 cache.
+size_t masked_rows_workspace_bytes(int d);
+cudaError_t launch_masked_rows(const PagedKV& c, const Mask& mask, const void* Q, void* O, int Hq,
+                               int Tq, float scale, void* workspace, unsigned* err,
+                               cudaStream_t s);
+// host only (host arrays): 0 when the plan of the two above is consistent
+int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k, int B, int Hkv,
+                          int G, int max_q, int total_q, int total_k, int window, int sinks,
+                          int tree, int sms);
+
 cudaError_t launch_selftest_wait_timeout(int timeout_us, unsigned* err, cudaStream_t s);
 
 }  // namespace rf

@@ -167,6 +167,38 @@ rf_status rf_attn_fwd_varlen(int dtype, const void* Q, const void* K, const void
                              float scale, int causal, rf_stream_t stream);
 
 /*
+ * Attention of prompts with a sliding window and sinks: rf_attn_fwd_varlen's cascade
+ * and alignment (causal, the rows are the last of their sequence's keys), where the
+ * row at position p reads the keys p - window + 1 .. p and the first `sinks` keys
+ * (the pages define no mask; this is the usual reading).
+ *   Q, O   [total_q][Hq][d] bf16, tokens ldq (ldo) elements apart; K, V
+ *          [total_k][Hkv][d] bf16, ldk (ldv).  Rows of a fused projection's output
+ *          can be given as they are.  Query head hq reads kv head hq / (Hq / Hkv).
+ *          O may be Q (with equal strides); other overlaps are not allowed.
+ *   cu_seqlens_q, cu_seqlens_k   as in rf_attn_fwd_varlen (4-byte aligned), or NULL:
+ *          total_q / B (total_k / B) tokens for each sequence.
+ *   window   0: every key up to p; else >= 1.      sinks   >= 0 (looked at with a
+ *          window).
+ *   Sizes  B, total_q, total_k >= 1; B, total_q, total_k, window, sinks <= 2^30;
+ *          max_seqlen_q >= every query length, <= total_q, B * max_seqlen_q < 2^31;
+ *          Hq a multiple of Hkv, Hq / Hkv <= 128; d = 64 or 128; strides >=
+ *          heads * d, a multiple of 8, below 2^39 / tokens; scale finite, > 0.
+ * fp32 sums and softmax state; the weights are rounded to bf16 for the product with V
+ * (half a step is 2^-8 of a weight).  A row that reads no key, or whose scores are
+ * all -infinity, is written as zeros.  A key or value that a row does not read has
+ * no effect on it, whatever it is.  Rows behind the last sequence are not written.
+ * Device arrays that are inconsistent with the sizes are handled and reported as in
+ * rf_attn_fwd_varlen.  No workspace; the bits do not depend on timing.
+ * Errors: RF_ERR_INVALID_ARG, RF_ERR_UNSUPPORTED (d, or more than 128 query heads a
+ * kv head), RF_ERR_CUDA.
+ */
+rf_status rf_attn_fwd_window(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V,
+                             int64_t ldv, void* O, int64_t ldo, const int32_t* cu_seqlens_q,
+                             const int32_t* cu_seqlens_k, int B, int Hq, int Hkv, int max_seqlen_q,
+                             int total_q, int total_k, int d, float scale, int window, int sinks,
+                             rf_stream_t stream);
+
+/*
  * Number of key segments rf_attn_decode_splitkv cuts a (b, kv head) sequence
  * into for this shape when its num_splits argument is `num_splits`: that
  * number itself when it is > 0; for 0 (the automatic partition, sized to the
@@ -698,6 +730,23 @@ int rf_selftest_decode_paged_plan(const int32_t* seq_lens, int B, int tiles, int
  */
 int rf_selftest_decode_paged_ex_plan(const int32_t* seq_lens, int B, int tiles, int max_len, int Tq,
                                      int window, int sinks, int warps, int sms);
+
+/*
+ * Host-side check of the plan of rf_attn_fwd_window and, with seq_lens, of
+ * rf_attn_decode_paged_ex with many query rows (no counterpart in the paper; no GPU
+ * needed, no CUDA call made).  All arrays are HOST arrays.  Prompts (seq_lens NULL):
+ * as in rf_attn_fwd_window, with G = Hq / Hkv.  Cache: max_q is Tq, total_k the
+ * longest sequence it can hold (total_q and the cumulative lengths are ignored),
+ * tree 1 for a tree of drafted tokens.  For a device of `sms` SMs it checks that all
+ * tiles of all items are taken once, in order, that only a cache's items are cut, into
+ * workspace slots that the merge finds again, that every row lies in one tile and that
+ * its keys lie in the tiles loaded for it, once.  Returns 0 when all of that holds, -1
+ * for refused sizes (also: more than 2^24 rows or keys, or no memory for the walk),
+ * else the number (1..6) of the first check that fails.
+ */
+int rf_selftest_masked_plan(const int32_t* seq_lens, const int32_t* cu_seqlens_q,
+                            const int32_t* cu_seqlens_k, int B, int Hkv, int G, int max_q,
+                            int total_q, int total_k, int window, int sinks, int tree, int sms);
 
 #ifdef __cplusplus
 }
