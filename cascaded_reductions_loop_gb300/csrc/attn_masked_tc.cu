@@ -8,16 +8,19 @@
 // the cascade of [E] §2.2 in its incremental form ([E] §2.3).  The plan (which rows
 // and keys an item has, how items are shared out) is in attn_masked_tc.cuh.
 //
-// A CTA takes items of two 128-row query tiles (a, b).  Per key tile j and tile x:
-//   1. MMA thread x: S_x = Q_x K_j^T (tcgen05 kind::f16, M = N = 128, fp32 in tensor
-//      memory);
-//   2. softmax warpgroup x, a thread a row: its 128 scores in registers, the keys it
-//      does not read at -inf (only in tiles that some row reads in part), running
-//      maximum moved lazily (by more than 2^8 only), P = 2^(S c - m) as bf16;
-//   3. MMA thread x: O_x += P_x V_j (P the tensor-memory A operand).
-// Tensor memory holds S_a, S_b, O_a, O_b, at d = 128 all of its 512 columns, so P_x
-// lies over S_x: the next S_x waits for P_x V_j.  While one tile's softmax runs, the
-// tensor core has the other tile's products.
+// A CTA takes items of two 128-row query tiles (a, b); a unit of work is 64 keys (half
+// a key tile) for one of them.  Per unit u of tile x:
+//   1. MMA thread x: S_x = Q_x K_u^T (tcgen05 kind::f16, M = 128, N = 64, fp32 in tensor
+//      memory), into one of two buffers in turn;
+//   2. softmax warpgroup x, a thread a row: its 64 scores in registers, the keys it does
+//      not read at -inf (only where some row reads a part), running maximum moved lazily
+//      (by more than 2^8 only), P = 2^(S c - m) as bf16 over S_x's columns;
+//   3. MMA thread x: O_x += P_x V_u (P the tensor-memory A operand).
+// Tensor memory: S_a, S_b (two buffers of 64 columns each), O_a, O_b: at d = 128 all of
+// its 512 columns.  S_x(u + 1) is computed while unit u's softmax runs, so a softmax
+// warpgroup finds its next scores ready.  With 128 keys a unit and P over the only S, S
+// waited for P.V, softmax and tensor core took turns: 4900 clocks for 128 keys of both
+// tiles (clock stamps), 1536 us for the 16k prompt below.
 //
 // Rounding: P is rounded to bf16 (half a step, 2^-8 of a weight; l sums the unrounded
 // ones), since both operands of an MMA have one type and V is bf16.
@@ -52,12 +55,13 @@ struct Cfg {
   static constexpr int kRing = kQSlots * kTile;
   static constexpr int kBarOff = kRing + kStages * kTile;
   static constexpr int kSmem = kBarOff + 1024 + 1024; // barriers; alignment
-  static constexpr uint32_t kIdescS = make_idesc(BQ, BK, 1, 0, 0);
+  static constexpr uint32_t kIdescS = make_idesc(BQ, kHalfKeys, 1, 0, 0);
   static constexpr uint32_t kIdescO = make_idesc(BQ, D, 1, 0, 1);
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 constexpr uint32_t kTmemCols = 512;
-__device__ __forceinline__ uint32_t col_s(int x) { return x * 128; }      // P_x over its first 64
+// S_x of unit u (64 columns); P_x over its first 32
+__device__ __forceinline__ uint32_t col_s(int x, int u) { return x * 128 + (u & 1) * kHalfKeys; }
 __device__ __forceinline__ uint32_t col_o(int x) { return 256 + x * 128; }
 
 struct Params {
@@ -80,7 +84,9 @@ struct Bars {
   uint64_t q_full[4], q_empty[4];
   uint64_t full[8], empty[8];
   uint64_t v_ok[4];                                   // a V tile is looked over
-  uint64_t s_full[2], p_full[2], pv_done[2], drain[2];
+  // per tile, for the units of either buffer: either side may be a unit behind
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];
+  uint64_t drain[2];
   unsigned pages[8];                                  // per key tile: bit per 16 keys that are there
   // what the guard found, per V stage: values that are not finite, and `pages`
   unsigned bad[4][4], there[4];
@@ -104,6 +110,20 @@ __device__ __forceinline__ void regs_inc() {
 template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Waits for unit u's phase of a pair of barriers.
+__device__ __forceinline__ bool unit_wait(uint64_t (&bar)[2], int u) {
+  return mbar_wait(smem_u32(&bar[u & 1]), (uint32_t)((u >> 1) & 1));
+}
+// One column of this thread's lane (waits for it).
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r)
+      : "r"(taddr)
+      : "memory");
+  return r;
 }
 // Bits 0 .. n - 1 of a word.
 __device__ __forceinline__ unsigned below(int n) {
@@ -150,9 +170,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars->empty[i]), 2);        // both MMA threads
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars->s_full[i]), 1);
-      mbar_init(smem_u32(&bars->p_full[i]), BQ);
-      mbar_init(smem_u32(&bars->pv_done[i]), 1);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(smem_u32(&bars->s_full[i][k]), 1);
+        mbar_init(smem_u32(&bars->p_full[i][k]), BQ);
+        mbar_init(smem_u32(&bars->pv_done[i][k]), 1);
+      }
       mbar_init(smem_u32(&bars->drain[i]), 1);
     }
     bars->abort = 0;
@@ -221,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (kPaged && threadIdx.x == 0 && RF_IN(p.err, cta, gridDim.x))
     p.ws_cut[cta] = cta == 0 ? make_int4(0, (int)(total & 0x7FFFFFFF), (int)(total >> 31), grid)
                              : make_int4(x1 > x0 ? bars->j : 0, bars->g, bars->h, 0);
-  Walk walk(geo, bars->g, bars->h, bars->j, x1 - x0, p.err);
+  Walk walk(bars->g, bars->h, bars->j, x1 - x0);
   Piece c;
   bool ok = true;
 
@@ -234,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned in_flight = 0;                         // stages filled so far (2 a key tile)
       while (ok && walk.next(geo, c, p.err)) {
         for (int x = 0; ok && x < 2; ++x) {
-          const Tile t = tile_of(geo, c, x);
+          const Tile t = tile_of(geo, c.w, x);
           if (!t.has()) continue;
           const int slot = nq % C::kQSlots;
           ok = __all_sync(0xffffffffu, nq < C::kQSlots ||
@@ -327,63 +349,94 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- MMA of tile x
       const int x = warp - 1;
       if (lane == 0) {
-        int nq = 0, nt = 0, cnt = 0;                  // Q tiles, key tiles, own key tiles
-        while (ok && walk.next(geo, c, p.err)) {
-          const Tile t = tile_of(geo, c, x);
-          const int slot = (nq + x) % C::kQSlots;
-          if (t.has())
-            ok = mbar_wait(smem_u32(&bars->q_full[slot]), (uint32_t)(((nq + x) / C::kQSlots) & 1));
-          bool fresh = true;
-          for (int j = c.j0; ok && j < c.j1; ++j, ++nt) {
-            const int pr = nt % C::kPairs, st = 2 * pr;
-            const uint32_t ph = (uint32_t)((nt / C::kPairs) & 1);
-            const bool mine = takes(geo, c, t, j);
-            if (!mbar_wait(smem_u32(&bars->full[st]), ph)) {
-              ok = false;
-              break;
+        // Key tiles in order, the S side one tile ahead of the P.V side: K of the next
+        // tile arrives without anything that this thread has yet to release.
+        struct At {
+          Walk walk;
+          Piece c;
+          Tile t;
+          int j, nt, nq;                              // tile of the piece; tiles and Q tiles before
+          bool any;
+          __device__ __forceinline__ void next(const Geo& geo, int x, unsigned* err) {
+            if (any && ++j < c.j1) {
+              ++nt;
+              return;
             }
-            if (mine) {
-              // S_x's columns hold the last P_x until its product with V is done
-              if (cnt > 0 && !mbar_wait(smem_u32(&bars->pv_done[x]), (uint32_t)((cnt - 1) & 1))) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t qa = smem_u32(smem + slot * C::kTile);
-              const uint32_t ka = smem_u32(ring + st * C::kTile);
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                mma_bf16_ss(tmem + col_s(x), sw128_desc(qa + (k >> 2) * kHalf + (k & 3) * 32, 1024, 16),
-                            sw128_desc(ka + (k >> 2) * kHalf + (k & 3) * 32, 1024, 16), C::kIdescS,
-                            k != 0);
-              mma_commit(smem_u32(&bars->s_full[x]));
-              if (j == t.last) mma_commit(smem_u32(&bars->q_empty[slot]));
+            if (any) {
+              ++nt;
+              nq += tile_of(geo, c.w, 1).has() ? 2 : 1;
             }
-            mma_commit(smem_u32(&bars->empty[st]));
-            if (!mbar_wait(smem_u32(&bars->v_ok[pr]), ph)) {
-              ok = false;
-              break;
-            }
-            if (mine) {
-              if (!mbar_wait(smem_u32(&bars->p_full[x]), (uint32_t)(cnt & 1))) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const unsigned* b = bars->bad[pr];
-              const bool onto = !fresh || (b[0] | b[1] | b[2] | b[3]) != 0u;
-              const uint32_t va = smem_u32(ring + (st + 1) * C::kTile);
-#pragma unroll
-              for (int k = 0; k < BK / 16; ++k)
-                mma_bf16_ts(tmem + col_o(x), tmem + col_s(x) + k * 8,
-                            sw128_desc(va + k * 16 * 128, 1024, kHalf), C::kIdescO, onto || k != 0);
-              mma_commit(smem_u32(&bars->pv_done[x]));
-              fresh = false;
-              ++cnt;
-            }
-            mma_commit(smem_u32(&bars->empty[st + 1]));
+            any = walk.next(geo, c, err);
+            if (!any) return;
+            j = c.j0;
+            t = tile_of(geo, c.w, x);
           }
-          nq += tile_of(geo, c, 1).has() ? 2 : 1;
+        };
+        At s_at = {walk, c, {}, 0, 0, 0, false}, v_at = s_at;
+        int us = 0, up = 0;                           // units whose S, whose P.V is issued
+        // S of half h of the tile at s_at, after the product that reads its buffer's P
+        auto issue_s = [&](int h) -> bool {
+          const int pr = s_at.nt % C::kPairs;
+          if (h == 0) {
+            if (s_at.j == s_at.c.j0 && s_at.t.has() &&
+                !mbar_wait(smem_u32(&bars->q_full[(s_at.nq + x) % C::kQSlots]),
+                           (uint32_t)(((s_at.nq + x) / C::kQSlots) & 1)))
+              return false;
+            if (!mbar_wait(smem_u32(&bars->full[2 * pr]), (uint32_t)((s_at.nt / C::kPairs) & 1)))
+              return false;
+          }
+          if (takes(geo, s_at.c.w, s_at.t, s_at.j, h)) {
+            if (us >= 2 && !unit_wait(bars->pv_done[x], us - 2)) return false;
+            tc_fence_after();
+            const uint32_t qa = smem_u32(smem + ((s_at.nq + x) % C::kQSlots) * C::kTile);
+            const uint32_t ka = smem_u32(ring + 2 * pr * C::kTile) + h * kHalfKeys * 128;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_bf16_ss(tmem + col_s(x, us), sw128_desc(qa + (k >> 2) * kHalf + (k & 3) * 32, 1024, 16),
+                          sw128_desc(ka + (k >> 2) * kHalf + (k & 3) * 32, 1024, 16), C::kIdescS,
+                          k != 0);
+            mma_commit(smem_u32(&bars->s_full[x][us & 1]));
+            ++us;
+          }
+          if (h == 1) {
+            mma_commit(smem_u32(&bars->empty[2 * pr]));
+            if (s_at.j == s_at.c.j1 - 1 && s_at.t.has())
+              mma_commit(smem_u32(&bars->q_empty[(s_at.nq + x) % C::kQSlots]));
+          }
+          return true;
+        };
+        bool fresh = true;
+        auto issue_pv = [&](int h) -> bool {
+          const int pr = v_at.nt % C::kPairs;
+          if (h == 0) {
+            if (v_at.j == v_at.c.j0) fresh = true;
+            if (!mbar_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((v_at.nt / C::kPairs) & 1)))
+              return false;
+          }
+          if (takes(geo, v_at.c.w, v_at.t, v_at.j, h)) {
+            if (!unit_wait(bars->p_full[x], up)) return false;
+            tc_fence_after();
+            const unsigned* b = &bars->bad[pr][2 * h];
+            const bool onto = !fresh || (b[0] | b[1]) != 0u;
+            const uint32_t va = smem_u32(ring + (2 * pr + 1) * C::kTile) + h * kHalfKeys * 128;
+#pragma unroll
+            for (int k = 0; k < kHalfKeys / 16; ++k)
+              mma_bf16_ts(tmem + col_o(x), tmem + col_s(x, up) + k * 8,
+                          sw128_desc(va + k * 16 * 128, 1024, kHalf), C::kIdescO, onto || k != 0);
+            mma_commit(smem_u32(&bars->pv_done[x][up & 1]));
+            fresh = false;
+            ++up;
+          }
+          if (h == 1) mma_commit(smem_u32(&bars->empty[2 * pr + 1]));
+          return true;
+        };
+        s_at.next(geo, x, p.err);
+        if (s_at.any) ok = issue_s(0) && issue_s(1);
+        v_at.next(geo, x, p.err);
+        while (ok && v_at.any) {
+          s_at.next(geo, x, p.err);
+          ok = issue_pv(0) && (!s_at.any || issue_s(0)) && issue_pv(1) && (!s_at.any || issue_s(1));
+          v_at.next(geo, x, p.err);
           if (*abort_flag) ok = false;
         }
         if (!ok) {
@@ -461,13 +514,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = warp >= 8 ? 1 : 0;
     const int r = (warp & 3) * 32 + lane;             // row of the tile
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + lane_off + col_s(x), o_addr = tmem + lane_off + col_o(x);
+    const uint32_t o_addr = tmem + lane_off + col_o(x);
     const uint64_t c2 = f2(p.c_log2, p.c_log2);
     const int my_t = r / geo.G, my_g = r - my_t * geo.G;
-    int nt = 0, cnt = 0;
+    int nt = 0, cnt = 0;                              // key tiles; units of this warpgroup
     int64_t s0 = x0 - (x1 > x0 ? bars->j : 0);        // first tile of the piece's item
     while (ok && walk.next(geo, c, p.err)) {
-      const Tile t = tile_of(geo, c, x);
+      const Tile t = tile_of(geo, c.w, x);
       const int64_t item0 = s0;
       s0 += c.w.n;
       const int j_base = nt - c.j0;                   // key tile j is the CTA's j_base + j th
@@ -491,93 +544,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (real && !line && c.w.lk > 0) raise_error(p.err, kDevErrInput);
         pos = line ? ctx + depth : -1;
       }
+      if (!real) pos = -1;
       float m_ref = -INFINITY, l_run = 0.f;
-      bool fresh = true;
-      for (int j = c.j0; j < c.j1; ++j) {
-        if (!takes(geo, c, t, j)) continue;
-        const int key0 = key0_of(c.w, j), pr = (j_base + j) % C::kPairs;
-        bool part = partly(geo, c, key0);
-        unsigned w[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};   // keys it reads
-        unsigned bad[4] = {0u, 0u, 0u, 0u};
+      const int cnt0 = cnt;
+      // one unit: half h of key tile j (at key0); part: some row reads a part of the tile
+      auto unit = [&](int key0, int pr, int h, bool part, unsigned pages) -> bool {
+        const int k0 = key0 + h * kHalfKeys;
+        const uint32_t s_addr = tmem + lane_off + col_s(x, cnt);
+        unsigned w[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};   // keys it reads
         bool any_bad = false;
-        if (kPaged || part) {
-          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->v_ok[pr]),
-                                                 (uint32_t)(((j_base + j) / C::kPairs) & 1)))) {
-            ok = false;
-            break;
+        if (part) {
+          const int hi = geo.tree ? min(ctx, pos + 1) : pos + 1;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int k = k0 + 32 * q;
+            w[q] = below(hi - k);
+            if (geo.window > 0) w[q] &= ~below(pos - geo.window + 1 - k) | below(geo.sinks - k);
+            if (pos < 0) w[q] = 0u;
+            any_bad |= bars->bad[pr][2 * h + q] != 0u;
           }
-          const unsigned pages = kPaged ? bars->there[pr] : 0xFFu;
-          part = part || pages != 0xFFu;
-          if (part) {
-            const int hi = geo.tree ? min(ctx, pos + 1) : pos + 1;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int k = key0 + 32 * q;
-              w[q] = below(hi - k);
-              if (geo.window > 0) w[q] &= ~below(pos - geo.window + 1 - k) | below(geo.sinks - k);
-              if (pos < 0 || !real) w[q] = 0u;
-              bad[q] = bars->bad[pr][q];
-              any_bad |= bad[q] != 0u;
-            }
-            if (geo.tree && key0 + BK > ctx && pos >= 0 && real) {
-              int u = tok;
-              for (int at = pos; u >= 0; --at) {      // node u at position `at`
-                const int bit = ctx + u - key0;
-                if (bit >= 0 && bit < BK &&
-                    (geo.window == 0 || at > pos - geo.window || at < geo.sinks)) {
-#pragma unroll
-                  for (int q = 0; q < 4; ++q)
-                    if ((bit >> 5) == q) w[q] |= 1u << (bit & 31);
-                }
-                const int up = ld_int(p.parents, (int64_t)c.w.b * geo.max_q + u,
-                                      (int64_t)geo.B * geo.max_q, p.err);
-                u = up < u ? up : -1;
+          if (geo.tree && k0 + kHalfKeys > ctx && pos >= 0) {
+            int u = tok;
+            for (int at = pos; u >= 0; --at) {        // node u at position `at`
+              const int bit = ctx + u - k0;
+              if (bit >= 0 && bit < kHalfKeys &&
+                  (geo.window == 0 || at > pos - geo.window || at < geo.sinks)) {
+                w[0] |= bit < 32 ? 1u << bit : 0u;
+                w[1] |= bit >= 32 ? 1u << (bit & 31) : 0u;
               }
-            }
-            if (kPaged) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                w[q] &= ((pages >> (2 * q)) & 1u ? 0xFFFFu : 0u) |
-                        ((pages >> (2 * q + 1)) & 1u ? 0xFFFF0000u : 0u);
+              const int up = ld_int(p.parents, (int64_t)c.w.b * geo.max_q + u,
+                                    (int64_t)geo.B * geo.max_q, p.err);
+              u = up < u ? up : -1;
             }
           }
+          if (kPaged) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              w[q] &= ((pages >> (4 * h + 2 * q)) & 1u ? 0xFFFFu : 0u) |
+                      ((pages >> (4 * h + 2 * q + 1)) & 1u ? 0xFFFF0000u : 0u);
+          }
         }
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(smem_u32(&bars->s_full[x]), (uint32_t)(cnt & 1)) && !*abort_flag)) {
-          ok = false;
-          break;
-        }
-        ++cnt;
+        if (!__all_sync(0xffffffffu, unit_wait(bars->s_full[x], cnt) && !*abort_flag)) return false;
         tc_fence_after();
-        uint32_t v[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + q * 32, v[q]);
+        uint32_t v[2][32];
+        tmem_ld32(s_addr, v[0]);
+        tmem_ld32(s_addr + 32, v[1]);
         tmem_ld_wait();
-        if (part && __any_sync(0xffffffffu, (w[0] & w[1] & w[2] & w[3]) != 0xFFFFFFFFu)) {
+        if (part && __any_sync(0xffffffffu, (w[0] & w[1]) != 0xFFFFFFFFu)) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[q][i] = (w[q] >> i) & 1u ? v[q][i] : 0xff800000u;
         }
         // row maximum (four chains)
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
             mx4[(i >> 1) & 3] =
                 fmax3(mx4[(i >> 1) & 3], __uint_as_float(v[q][i]), __uint_as_float(v[q][i + 1]));
         const float mt = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * p.c_log2;
+        const bool fresh = cnt == cnt0;
         float alpha = 1.f;
         if (fresh) {
-          m_ref = mt;                                 // P.V of the first tile overwrites O
+          m_ref = mt;                                 // P.V of the first unit overwrites O
         } else if (mt > m_ref + kLazy) {
           alpha = ex2(m_ref - mt);
           l_run *= alpha;
           m_ref = mt;
         }
-        // O_x is complete through the last tile: its P.V was done before this S began
-        if (!fresh && __any_sync(0xffffffffu, alpha != 1.f)) {
+        const bool move = !fresh && __any_sync(0xffffffffu, alpha != 1.f);
+        if ((move || any_bad) && cnt > 0) {
+          // O_x is complete through the last unit
+          if (!__all_sync(0xffffffffu, unit_wait(bars->pv_done[x], cnt - 1))) return false;
+          tc_fence_after();
+        }
+        if (move) {
 #pragma unroll
           for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
@@ -601,31 +644,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
           }
 #pragma unroll 1
-          for (int k = 0; k < BK; ++k) {
-            const unsigned bw = k < 32 ? bad[0] : (k < 64 ? bad[1] : (k < 96 ? bad[2] : bad[3]));
-            if (!((bw >> (k & 31)) & 1u)) continue;
-            float sc = 0.f;
-            bool reads = false;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (q * 32 + i == k) {
-                  sc = __uint_as_float(v[q][i]);
-                  reads = (w[q] >> i) & 1u;
-                }
-            const float pk = ex2(fmaf(sc, p.c_log2, -m_use));
+          for (int k = 0; k < kHalfKeys; ++k) {
+            if (!((bars->bad[pr][2 * h + (k >> 5)] >> (k & 31)) & 1u)) continue;
+            const bool reads = ((k < 32 ? w[0] : w[1]) >> (k & 31)) & 1u;
+            const float pk = ex2(fmaf(__uint_as_float(tmem_ld1(s_addr + k)), p.c_log2, -m_use));
             int64_t at;                               // the value's first element
             bool inside;
             if (kPaged) {
-              const int page = ld_int(p.block_table,
-                                      (int64_t)c.w.b * p.max_pages + ((key0 + k) >> p.page_shift),
-                                      (int64_t)geo.B * p.max_pages, p.err);
-              at = (((int64_t)page * geo.Hkv + c.h) * p.page_size + ((key0 + k) & (p.page_size - 1))) * D;
-              inside = key0 + k < c.w.lk && (unsigned)page < (unsigned)p.num_pages;
+              const int page = k0 + k < c.w.lk
+                                   ? ld_int(p.block_table,
+                                            (int64_t)c.w.b * p.max_pages + ((k0 + k) >> p.page_shift),
+                                            (int64_t)geo.B * p.max_pages, p.err)
+                                   : -1;
+              at = (((int64_t)page * geo.Hkv + c.h) * p.page_size + ((k0 + k) & (p.page_size - 1))) * D;
+              inside = (unsigned)page < (unsigned)p.num_pages;
             } else {
-              at = (int64_t)(c.w.k0 + key0 + k) * p.ldv + (int64_t)c.h * D;
-              inside = key0 + k < c.w.lk;
+              at = (int64_t)(c.w.k0 + k0 + k) * p.ldv + (int64_t)c.h * D;
+              inside = k0 + k < c.w.lk;
             }
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
@@ -643,40 +678,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        fresh = false;
         // P = 2^(S c - m) as bf16 pairs, and its row sum (four chains)
         const uint64_t negm2 = f2(-m_use, -m_use);
         uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t pk[32];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t pk[32];
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int q = 2 * hh + h;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float t0, t1;
-              f2_split(ffma2(f2(__uint_as_float(v[q][2 * i]), __uint_as_float(v[q][2 * i + 1])), c2,
-                             negm2),
-                       t0, t1);
-              const float p0 = ex2(t0), p1 = ex2(t1);
-              sum4[i & 3] = fadd2(sum4[i & 3], f2(p0, p1));
-              pk[h * 16 + i] = pack_bf16x2(p0, p1);
-            }
+          for (int i = 0; i < 16; ++i) {
+            float t0, t1;
+            f2_split(ffma2(f2(__uint_as_float(v[q][2 * i]), __uint_as_float(v[q][2 * i + 1])), c2,
+                           negm2),
+                     t0, t1);
+            const float p0 = ex2(t0), p1 = ex2(t1);
+            sum4[i & 3] = fadd2(sum4[i & 3], f2(p0, p1));
+            pk[q * 16 + i] = pack_bf16x2(p0, p1);
           }
-          tmem_st32(s_addr + hh * 32, pk);
-        }
+        tmem_st32(s_addr, pk);
         float s_lo, s_hi;
         f2_split(fadd2(fadd2(sum4[0], sum4[1]), fadd2(sum4[2], sum4[3])), s_lo, s_hi);
         l_run += s_lo + s_hi;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(&bars->p_full[x]));
+        mbar_arrive(smem_u32(&bars->p_full[x][cnt & 1]));
+        ++cnt;
+        return true;
+      };
+      for (int j = c.j0; ok && j < c.j1; ++j) {
+        const bool u0 = takes(geo, c.w, t, j, 0), u1 = takes(geo, c.w, t, j, 1);
+        if (!u0 && !u1) continue;
+        const int key0 = key0_of(c.w, j), pr = (j_base + j) % C::kPairs;
+        bool part = partly(geo, c, key0);
+        unsigned pages = 0xFFu;
+        if (kPaged || part) {
+          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->v_ok[pr]),
+                                                 (uint32_t)(((j_base + j) / C::kPairs) & 1)))) {
+            ok = false;
+            break;
+          }
+          if (kPaged) pages = bars->there[pr];
+          part = part || pages != 0xFFu;
+        }
+#pragma unroll 1
+        for (int h = u0 ? 0 : 1; ok && h < (u1 ? 2 : 1); ++h) ok = unit(key0, pr, h, part, pages);
       }
       if (!ok) break;
-      // the piece's last product
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->pv_done[x]), (uint32_t)((cnt - 1) & 1)) &&
-                                       !*abort_flag)) {
+      // the piece's last product (a tile may have no unit in it)
+      if (cnt > cnt0 &&
+          !__all_sync(0xffffffffu, unit_wait(bars->pv_done[x], cnt - 1) && !*abort_flag)) {
         ok = false;
         break;
       }
@@ -757,8 +806,7 @@ __global__ void __launch_bounds__(BQ)
   const int64_t s0 = split.start(c1) - cut.x, s1 = s0 + w.n;
   if (split.owner(s0) != c1 - 1) return;
   const int pieces = split.owner(s1 - 1) - (c1 - 1) + 1;
-  Piece pc = {w, cut.z, 0, w.n};
-  const Tile t = tile_of(geo, pc, x);
+  const Tile t = tile_of(geo, w, x);
   const int my_t = r / geo.G, tok = t.t0 + my_t;
   if (my_t >= geo.tpt || tok >= t.t1) return;
   auto slot = [&](int i) { return slot_of(c1 - 1 + i, s0, split.start(c1 - 1 + i)) * 2 + x; };
@@ -936,8 +984,8 @@ cudaError_t launch_masked_rows(const PagedKV& c, const Mask& mask, const void* Q
 //     last item, into slots of their own;
 //   4 the merge counts a cut item's pieces and finds their slots, in key order;
 //   5 every row with tokens lies in one tile of one item;
-//   6 every key that a row reads lies in exactly one tile that its tile takes, and
-//     every tile has one to take.
+//   6 every key that a row reads lies in exactly one half of a key tile that its tile
+//     takes.
 int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k, int B, int Hkv,
                           int G, int max_q, int total_q, int total_k, int window, int sinks,
                           int tree, int sms) {
@@ -957,22 +1005,20 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
     const Group w = group_of(p, g, false, &err);
     want_rows[(size_t)w.b] = w.lq;
     if (w.n > 0) rows[(size_t)w.b] += w.t1 - w.t0;
-    Piece c = {w, 0, 0, w.n};
     for (int x = 0; w.n > 0 && x < 2; ++x) {
-      const Tile t = tile_of(p, c, x);
+      const Tile t = tile_of(p, w, x);
       if (!t.has()) continue;
       if (t.t1 - t.t0 > p.tpt) return 5;
-      int some = 0;
-      for (int j = 0; j < w.n; ++j) some += takes(p, c, t, j);
-      if (!some || !takes(p, c, t, t.last)) return 6;
       for (int i = t.t0; i < t.t1; ++i) {
         // a tree's node may be at any position from its first on, and reads no other key
         const int at[2] = {p.tree ? w.lk - w.lq : w.lk - w.lq + i, p.tree ? w.lk - 1 : w.lk - w.lq + i};
         for (int key = 0; key < w.lk; ++key) {
           const bool reads = key <= at[1] && (window == 0 || at[0] - key < window || key < sinks);
           int hits = 0;
-          for (int j = 0; j < w.n; ++j)
-            hits += takes(p, c, t, j) && key >= key0_of(w, j) && key < key0_of(w, j) + BK;
+          for (int u = 0; u < 2 * w.n; ++u) {
+            const int k0 = key0_of(w, u >> 1) + (u & 1) * kHalfKeys;
+            hits += takes(p, w, t, u >> 1, u & 1) && key >= k0 && key < k0 + kHalfKeys;
+          }
           if (reads ? hits != 1 : hits > 1) return 6;
         }
       }
@@ -1005,7 +1051,7 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
       }
     }
     if (r[0] != x || r[1] < r[0]) return 2;
-    Walk walk(p, start[0], start[1], start[2], r[1] - r[0], &err);
+    Walk walk(start[0], start[1], start[2], r[1] - r[0]);
     Piece pc;
     int cuts = 0;
     int64_t s0 = x - (r[1] > r[0] ? start[2] : 0);

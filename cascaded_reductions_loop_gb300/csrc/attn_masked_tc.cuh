@@ -149,62 +149,59 @@ struct Piece {
 };
 struct Walk {
   int64_t left;             // tiles still to take
-  int g, h, j;
-  Group w;
-  // From tile j (which may be n: the item behind is meant) of head h of group g.
-  __host__ __device__ __forceinline__ Walk(const Geo& p, int g_, int h_, int j_, int64_t count,
-                                           unsigned* err)
-      : left(count), g(g_), h(h_), j(j_) {
-    if (left > 0) {
-      w = group_of(p, g, false, err);
-      settle(p, err);
-    }
-  }
-  __host__ __device__ __forceinline__ void settle(const Geo& p, unsigned* err) {
-    if (j < w.n) return;
-    j = 0;
-    if (++h < p.Hkv) return;
-    h = 0;
-    g = next_group(p, g + 1, w, err);
-    if (g >= p.B * p.npairs) left = 0;                // (on the device: the lengths changed)
-  }
+  int g, h, j;              // the next one; j may be behind the item's last: the next item's
+  __host__ __device__ __forceinline__ Walk(int g_, int h_, int j_, int64_t count)
+      : left(count), g(g_), h(h_), j(j_) {}
   __host__ __device__ __forceinline__ bool next(const Geo& p, Piece& out, unsigned* err) {
     if (left <= 0) return false;
-    out.w = w;
+    out.w = group_of(p, g, false, err);
+    if (j >= out.w.n) {
+      j = 0;
+      if (++h >= p.Hkv) {
+        h = 0;
+        g = next_group(p, g + 1, out.w, err);
+        if (g >= p.B * p.npairs) {                    // (on the device: the lengths changed)
+          left = 0;
+          return false;
+        }
+      }
+    }
     out.h = h;
     out.j0 = j;
-    out.j1 = (int64_t)(w.n - j) < left ? w.n : j + (int)left;
+    out.j1 = (int64_t)(out.w.n - j) < left ? out.w.n : j + (int)left;
     left -= out.j1 - out.j0;
     j = out.j1;
-    if (left > 0) settle(p, err);
     return true;
   }
 };
 
-// Tile x (0, 1) of a piece: its tokens, and which of the piece's key tiles it takes.
+// Tile x (0, 1) of a piece: its tokens, and which halves (kHalfKeys keys) of the
+// item's key tiles it takes: those in which some row may read a key.
+constexpr int kHalfKeys = BK / 2;
 struct Tile {
   int t0, t1;               // its tokens; t0 >= t1: it has no rows
-  int first, last;          // of the item's window tiles (whole items), see takes()
+  int first, last;          // halves of the item's window tiles; last < 0: none
   __host__ __device__ __forceinline__ bool has() const { return t0 < t1; }
 };
-__host__ __device__ __forceinline__ Tile tile_of(const Geo& p, const Piece& c, int x) {
+__host__ __device__ __forceinline__ Tile tile_of(const Geo& p, const Group& w, int x) {
   Tile t;
-  t.t0 = c.w.t0 + x * p.tpt;
-  t.t1 = imin(c.w.t1, t.t0 + p.tpt);
-  t.first = c.j0;
-  t.last = c.j1 - 1;
-  if (p.seq_lens || !t.has()) return t;
-  const int ctx = c.w.lk - c.w.lq;
-  const int hi = imin(c.w.lk - 1, ctx + t.t1 - 1);    // its last row's position
-  const int lo = p.window > 0 ? ctx + t.t0 - p.window + 1 : 0;
-  t.first = lo > c.w.start ? c.w.lead + (lo - c.w.start) / BK : c.w.lead;
-  t.last = hi < 0 ? 0 : c.w.lead + (hi - c.w.start) / BK;
-  if (t.last < t.first) t.first = t.last;
+  t.t0 = w.t0 + x * p.tpt;
+  t.t1 = imin(w.t1, t.t0 + p.tpt);
+  const int ctx = w.lk - w.lq;
+  const int hi = p.tree ? w.lk - 1 : imin(w.lk - 1, ctx + t.t1 - 1);     // its last row's position
+  const int lo = p.window > 0 ? (p.tree ? ctx : ctx + t.t0) - p.window + 1 : 0;
+  t.first = lo > w.start ? (lo - w.start) / kHalfKeys : 0;
+  t.last = hi < 0 || !t.has() ? -1 : (hi - w.start) / kHalfKeys;
   return t;
 }
-__host__ __device__ __forceinline__ bool takes(const Geo& p, const Piece& c, const Tile& t, int j) {
-  if (!t.has() || j > t.last) return false;
-  return j >= t.first || key0_of(c.w, j) < p.sinks;
+// Half h of key tile j.
+__host__ __device__ __forceinline__ bool takes(const Geo& p, const Group& w, const Tile& t, int j,
+                                               int h) {
+  if (t.last < 0) return false;
+  const bool sink = p.window > 0 && key0_of(w, j) + h * kHalfKeys < p.sinks;
+  if (j < w.lead) return sink;
+  const int u = 2 * (j - w.lead) + h;
+  return u <= t.last && (u >= t.first || sink);
 }
 
 // The workspace slot of CTA c's piece of an item that begins at tile s0 (in the
