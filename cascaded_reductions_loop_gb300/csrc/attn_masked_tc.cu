@@ -55,13 +55,13 @@ struct Cfg {
   static constexpr int kRing = kQSlots * kTile;
   static constexpr int kBarOff = kRing + kStages * kTile;
   static constexpr int kSmem = kBarOff + 1024 + 1024; // barriers; alignment
-  static constexpr uint32_t kIdescS = make_idesc(BQ, kHalfKeys, 1, 0, 0);
+  static constexpr uint32_t kIdescS = make_idesc(BQ, kUnit, 1, 0, 0);
   static constexpr uint32_t kIdescO = make_idesc(BQ, D, 1, 0, 1);
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 constexpr uint32_t kTmemCols = 512;
 // S_x of unit u (64 columns); P_x over its first 32
-__device__ __forceinline__ uint32_t col_s(int x, int u) { return x * 128 + (u & 1) * kHalfKeys; }
+__device__ __forceinline__ uint32_t col_s(int x, int u) { return x * 128 + (u & 1) * kUnit; }
 __device__ __forceinline__ uint32_t col_o(int x) { return 256 + x * 128; }
 
 struct Params {
@@ -87,8 +87,8 @@ struct Bars {
   // per tile, for the units of either buffer: either side may be a unit behind
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];
   uint64_t drain[2];
-  unsigned pages[8];                                  // per key tile: bit per 16 keys that are there
-  // what the guard found, per V stage: values that are not finite, and `pages`
+  unsigned rec[8];                                    // per key tile; K may be a round ahead of V
+  // what the guard found, per V stage: values that are not finite; rec's pages
   unsigned bad[4][4], there[4];
   int64_t warp_sum[kThreads / 32];
   int64_t x[2], total;                                // the CTA's range, all tiles
@@ -130,15 +130,15 @@ __device__ __forceinline__ unsigned below(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
 }
 
-// Whether some row of the piece may not read all of tile j's keys (the same for
-// every role).
-__device__ __forceinline__ bool partly(const Geo& p, const Piece& c, int key0) {
-  const int ctx = c.w.lk - c.w.lq;
-  const int first = p.tree ? ctx - 1 : ctx + c.w.t0;          // the first row's position
-  const int last = p.tree ? c.w.lk - 1 : ctx + c.w.t1 - 1;
-  return key0 + BK > first + 1 ||
-         (p.window > 0 && key0 < last - p.window + 1 && key0 + BK > p.sinks);
-}
+// What the TMA warp tells the MMA threads and the guard about a key tile.
+enum : unsigned {
+  kTakes = 1u,              // << (2 x + h): tile x takes half h
+  kFirst = 16u,             // of its piece
+  kLast = 32u,
+  kHasB = 64u,              // the piece has a tile b
+  kPartly = 128u,           // << h: some row may not read all keys of half h
+  kPages = 16,              // over a cache, from this bit on: bit per 16 keys that are there
+};
 
 template <int D, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -273,8 +273,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ++nq;
         }
+        const Tile ta = tile_of(geo, c.w, 0), tb = tile_of(geo, c.w, 1);
+        const Whole whole = whole_of(geo, c.w);
         for (int j = c.j0; ok && j < c.j1; ++j, ++nt) {
           const int key0 = key0_of(c.w, j);
+          unsigned rec = (ta.takes(2 * j) ? 1u : 0u) | (ta.takes(2 * j + 1) ? 2u : 0u) |
+                         (tb.takes(2 * j) ? 4u : 0u) | (tb.takes(2 * j + 1) ? 8u : 0u) |
+                         (j == c.j0 ? kFirst : 0u) | (j == c.j1 - 1 ? kLast : 0u) |
+                         (tb.has() ? kHasB : 0u) | (whole.partly(geo, key0, kUnit) ? kPartly : 0u) |
+                         (whole.partly(geo, key0 + kUnit, kUnit) ? kPartly << 1 : 0u);
           const int st = 2 * (nt % C::kPairs);
           const uint32_t ph = (uint32_t)((nt / C::kPairs - 1) & 1);
           // over a cache: lane i has the tile's page i
@@ -297,6 +304,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const unsigned pages = __ballot_sync(0xffffffffu, there);
+          if (kPaged) {
+            const int per16 = p.page_size >> 4;       // bits of a page
+            unsigned bits = 0;
+            for (unsigned m = pages; m != 0; m &= m - 1)
+              bits |= ((1u << per16) - 1u) << ((__ffs((int)m) - 1) * per16);
+            rec |= bits << kPages;
+          }
 #pragma unroll
           for (int v = 0; v < 2; ++v) {               // K, then V
             const uint32_t bar = smem_u32(&bars->full[st + v]);
@@ -307,14 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const CUtensorMap* tm = v ? &tmV : &tmK;
             if (kPaged) {
               if (lane == 0) {
-                if (v == 0) {
-                  // K may be one round ahead of V, so the words' ring has two rounds
-                  const int per16 = p.page_size >> 4;           // bits of a page
-                  unsigned bits = 0;
-                  for (unsigned m = pages; m != 0; m &= m - 1)
-                    bits |= ((1u << per16) - 1u) << ((__ffs((int)m) - 1) * per16);
-                  bars->pages[nt % (2 * C::kPairs)] = bits;
-                }
+                if (v == 0) bars->rec[nt % 8] = rec;
                 mbar_arrive_expect_tx(bar, (uint32_t)(__popc(pages) * p.page_size * D * 2));
               }
               __syncwarp();
@@ -324,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tma_load_2d_hint(dst + i * kHalf + lane * p.page_size * 128, tm, bar, 64 * i, row,
                                    pol_kv);
             } else if (lane == 0) {
+              if (v == 0) bars->rec[nt % 8] = rec;
               mbar_arrive_expect_tx(bar, C::kTile);
 #pragma unroll
               for (int i = 0; i < D / 64; ++i)
@@ -351,78 +359,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         // Key tiles in order, the S side one tile ahead of the P.V side: K of the next
         // tile arrives without anything that this thread has yet to release.
-        struct At {
-          Walk walk;
-          Piece c;
-          Tile t;
-          int j, nt, nq;                              // tile of the piece; tiles and Q tiles before
-          bool any;
-          __device__ __forceinline__ void next(const Geo& geo, int x, unsigned* err) {
-            if (any && ++j < c.j1) {
-              ++nt;
-              return;
-            }
-            if (any) {
-              ++nt;
-              nq += tile_of(geo, c.w, 1).has() ? 2 : 1;
-            }
-            any = walk.next(geo, c, err);
-            if (!any) return;
-            j = c.j0;
-            t = tile_of(geo, c.w, x);
-          }
-        };
-        At s_at = {walk, c, {}, 0, 0, 0, false}, v_at = s_at;
+        const int count = (int)(x1 - x0);
+        const uint64_t kd = sw128_desc(smem_u32(ring), 1024, 16);
+        const uint64_t vd = sw128_desc(smem_u32(ring + C::kTile), 1024, kHalf);
+        uint64_t qd = 0;
+        int nq = x, slot = 0;                         // this thread's Q tile (a, b in turn) and place
         int us = 0, up = 0;                           // units whose S, whose P.V is issued
-        // S of half h of the tile at s_at, after the product that reads its buffer's P
-        auto issue_s = [&](int h) -> bool {
-          const int pr = s_at.nt % C::kPairs;
-          if (h == 0) {
-            if (s_at.j == s_at.c.j0 && s_at.t.has() &&
-                !mbar_wait(smem_u32(&bars->q_full[(s_at.nq + x) % C::kQSlots]),
-                           (uint32_t)(((s_at.nq + x) / C::kQSlots) & 1)))
+        auto open = [&](int nt, unsigned& rec) -> bool {
+          if (!mbar_wait(smem_u32(&bars->full[2 * (nt % C::kPairs)]), (uint32_t)((nt / C::kPairs) & 1)))
+            return false;
+          rec = bars->rec[nt % 8];
+          if (rec & kFirst) {
+            slot = nq % C::kQSlots;
+            if ((x == 0 || (rec & kHasB)) &&
+                !mbar_wait(smem_u32(&bars->q_full[slot]), (uint32_t)((nq / C::kQSlots) & 1)))
               return false;
-            if (!mbar_wait(smem_u32(&bars->full[2 * pr]), (uint32_t)((s_at.nt / C::kPairs) & 1)))
-              return false;
+            qd = sw128_desc(smem_u32(smem + slot * C::kTile), 1024, 16);
+            nq += (rec & kHasB) ? 2 : 1;
           }
-          if (takes(geo, s_at.c.w, s_at.t, s_at.j, h)) {
+          return true;
+        };
+        // S of half h, after the product that reads its buffer's P
+        auto issue_s = [&](int nt, unsigned rec, int h) -> bool {
+          if ((rec >> (2 * x + h)) & 1u) {
             if (us >= 2 && !unit_wait(bars->pv_done[x], us - 2)) return false;
             tc_fence_after();
-            const uint32_t qa = smem_u32(smem + ((s_at.nq + x) % C::kQSlots) * C::kTile);
-            const uint32_t ka = smem_u32(ring + 2 * pr * C::kTile) + h * kHalfKeys * 128;
+            const uint64_t b = kd + (uint64_t)((2 * (nt % C::kPairs) * C::kTile + h * kUnit * 128) >> 4);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_bf16_ss(tmem + col_s(x, us), sw128_desc(qa + (k >> 2) * kHalf + (k & 3) * 32, 1024, 16),
-                          sw128_desc(ka + (k >> 2) * kHalf + (k & 3) * 32, 1024, 16), C::kIdescS,
-                          k != 0);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+              mma_bf16_ss(tmem + col_s(x, us), qd + off, b + off, C::kIdescS, k != 0);
+            }
             mma_commit(smem_u32(&bars->s_full[x][us & 1]));
             ++us;
           }
           if (h == 1) {
-            mma_commit(smem_u32(&bars->empty[2 * pr]));
-            if (s_at.j == s_at.c.j1 - 1 && s_at.t.has())
-              mma_commit(smem_u32(&bars->q_empty[(s_at.nq + x) % C::kQSlots]));
+            mma_commit(smem_u32(&bars->empty[2 * (nt % C::kPairs)]));
+            if ((rec & kLast) && (x == 0 || (rec & kHasB))) mma_commit(smem_u32(&bars->q_empty[slot]));
           }
           return true;
         };
         bool fresh = true;
-        auto issue_pv = [&](int h) -> bool {
-          const int pr = v_at.nt % C::kPairs;
+        auto issue_pv = [&](int nt, unsigned rec, int h) -> bool {
+          const int pr = nt % C::kPairs;
           if (h == 0) {
-            if (v_at.j == v_at.c.j0) fresh = true;
-            if (!mbar_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((v_at.nt / C::kPairs) & 1)))
-              return false;
+            if (rec & kFirst) fresh = true;
+            if (!mbar_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((nt / C::kPairs) & 1))) return false;
           }
-          if (takes(geo, v_at.c.w, v_at.t, v_at.j, h)) {
+          if ((rec >> (2 * x + h)) & 1u) {
             if (!unit_wait(bars->p_full[x], up)) return false;
             tc_fence_after();
-            const unsigned* b = &bars->bad[pr][2 * h];
-            const bool onto = !fresh || (b[0] | b[1]) != 0u;
-            const uint32_t va = smem_u32(ring + (2 * pr + 1) * C::kTile) + h * kHalfKeys * 128;
+            // values that are not finite are in O before the first product
+            bool onto = !fresh;
+            if (kPaged || ((rec >> h) & kPartly))
+              onto = onto || (bars->bad[pr][2 * h] | bars->bad[pr][2 * h + 1]) != 0u;
+            const uint64_t b = vd + (uint64_t)((2 * pr * C::kTile + h * kUnit * 128) >> 4);
 #pragma unroll
-            for (int k = 0; k < kHalfKeys / 16; ++k)
+            for (int k = 0; k < kUnit / 16; ++k)
               mma_bf16_ts(tmem + col_o(x), tmem + col_s(x, up) + k * 8,
-                          sw128_desc(va + k * 16 * 128, 1024, kHalf), C::kIdescO, onto || k != 0);
+                          b + (uint64_t)((k * 16 * 128) >> 4), C::kIdescO, onto || k != 0);
             mma_commit(smem_u32(&bars->pv_done[x][up & 1]));
             fresh = false;
             ++up;
@@ -430,13 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (h == 1) mma_commit(smem_u32(&bars->empty[2 * pr + 1]));
           return true;
         };
-        s_at.next(geo, x, p.err);
-        if (s_at.any) ok = issue_s(0) && issue_s(1);
-        v_at.next(geo, x, p.err);
-        while (ok && v_at.any) {
-          s_at.next(geo, x, p.err);
-          ok = issue_pv(0) && (!s_at.any || issue_s(0)) && issue_pv(1) && (!s_at.any || issue_s(1));
-          v_at.next(geo, x, p.err);
+        unsigned rec = 0, next = 0;
+        if (count > 0) ok = open(0, rec) && issue_s(0, rec, 0) && issue_s(0, rec, 1);
+        for (int nt = 0; ok && nt < count; ++nt, rec = next) {
+          const bool more = nt + 1 < count;
+          ok = issue_pv(nt, rec, 0);
+          if (more) ok = ok && open(nt + 1, next) && issue_s(nt + 1, next, 0);
+          ok = ok && issue_pv(nt, rec, 1);
+          if (more) ok = ok && issue_s(nt + 1, next, 1);
           if (*abort_flag) ok = false;
         }
         if (!ok) {
@@ -449,48 +445,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ---------------------------------------------------------- guard
-      int nt = 0;
-      while (ok && walk.next(geo, c, p.err)) {
-        for (int j = c.j0; ok && j < c.j1; ++j, ++nt) {
+      const int count = (int)(x1 - x0);
+      for (int nt = 0; ok && nt < count; ++nt) {
+        {
           const int pr = nt % C::kPairs, st = 2 * pr;
           ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->full[st + 1]),
                                                  (uint32_t)((nt / C::kPairs) & 1)));
           if (!ok) break;
-          const int key0 = key0_of(c.w, j);
-          const unsigned pages = kPaged ? bars->pages[nt % (2 * C::kPairs)] : 0xFFu;
+          const unsigned rec = bars->rec[nt % 8];
+          const unsigned pages = kPaged ? (rec >> kPages) & 0xFFu : 0xFFu;
           unsigned bad[4] = {0u, 0u, 0u, 0u};
-          if (partly(geo, c, key0) || pages != 0xFFu) {
-            uint4* v = reinterpret_cast<uint4*>(ring + (st + 1) * C::kTile);
-            unsigned seen = 0;
-#pragma unroll 8
-            for (int i = lane; i < C::kTile / 16; i += 32) {
-              const uint4 w = v[i];
-              // an exponent of ones carries into the sign's place
-              seen |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
-                      ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
-            }
-            if (__any_sync(0xffffffffu, (seen & 0x80008000u) != 0u)) {
+          uint4* v = reinterpret_cast<uint4*>(ring + (st + 1) * C::kTile);
+          // an exponent of ones carries into the sign's place
+          auto ones = [](const uint4& w) {
+            return ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                   ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+          };
 #pragma unroll 1
-              for (int r = 0; r < BK; ++r) {          // which rows; they become zeros
-                bool hit = false;
-                if (lane < D / 8) {
-                  const uint4 w = v[(lane >> 3) * (kHalf / 16) + r * 8 + (lane & 7)];
-                  const unsigned y = ((w.x & 0x7F807F80u) + 0x00800080u) |
-                                     ((w.y & 0x7F807F80u) + 0x00800080u) |
-                                     ((w.z & 0x7F807F80u) + 0x00800080u) |
-                                     ((w.w & 0x7F807F80u) + 0x00800080u);
-                  hit = (y & 0x80008000u) != 0u;
-                }
-                if (!__any_sync(0xffffffffu, hit)) continue;
-                bad[0] |= r < 32 ? 1u << r : 0u;
-                bad[1] |= r >= 32 && r < 64 ? 1u << (r & 31) : 0u;
-                bad[2] |= r >= 64 && r < 96 ? 1u << (r & 31) : 0u;
-                bad[3] |= r >= 96 ? 1u << (r & 31) : 0u;
-                if (lane < D / 8)
-                  v[(lane >> 3) * (kHalf / 16) + r * 8 + (lane & 7)] = make_uint4(0u, 0u, 0u, 0u);
-              }
-              fence_proxy_async_smem();
+          for (int h = 0; h < 2; ++h) {
+            if (!((rec >> h) & kPartly) && pages == 0xFFu) continue;
+            unsigned seen = 0;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {        // 64 rows of 128 bytes
+              const uint4* at = v + i * (kHalf / 16) + h * (kUnit * 8);
+#pragma unroll 8
+              for (int k = lane; k < kUnit * 8; k += 32) seen |= ones(at[k]);
             }
+            if (!__any_sync(0xffffffffu, (seen & 0x80008000u) != 0u)) continue;
+#pragma unroll 1
+            for (int r = h * kUnit; r < (h + 1) * kUnit; ++r) {       // which rows; they become zeros
+              uint4* at = v + (lane >> 3) * (kHalf / 16) + r * 8 + (lane & 7);
+              const bool hit = lane < D / 8 && (ones(*at) & 0x80008000u) != 0u;
+              if (!__any_sync(0xffffffffu, hit)) continue;
+              bad[0] |= r < 32 ? 1u << r : 0u;
+              bad[1] |= r >= 32 && r < 64 ? 1u << (r & 31) : 0u;
+              bad[2] |= r >= 64 && r < 96 ? 1u << (r & 31) : 0u;
+              bad[3] |= r >= 96 ? 1u << (r & 31) : 0u;
+              if (lane < D / 8) *at = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
           }
           __syncwarp();
           if (lane == 0) {
@@ -547,9 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!real) pos = -1;
       float m_ref = -INFINITY, l_run = 0.f;
       const int cnt0 = cnt;
-      // one unit: half h of key tile j (at key0); part: some row reads a part of the tile
-      auto unit = [&](int key0, int pr, int h, bool part, unsigned pages) -> bool {
-        const int k0 = key0 + h * kHalfKeys;
+      // one unit: the keys from k0 on, in half h of V stage pr; part: some row may not read all
+      auto unit = [&](int k0, int pr, int h, bool part, unsigned pages) -> bool {
         const uint32_t s_addr = tmem + lane_off + col_s(x, cnt);
         unsigned w[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};   // keys it reads
         bool any_bad = false;
@@ -563,11 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (pos < 0) w[q] = 0u;
             any_bad |= bars->bad[pr][2 * h + q] != 0u;
           }
-          if (geo.tree && k0 + kHalfKeys > ctx && pos >= 0) {
+          if (geo.tree && k0 + kUnit > ctx && pos >= 0) {
             int u = tok;
             for (int at = pos; u >= 0; --at) {        // node u at position `at`
               const int bit = ctx + u - k0;
-              if (bit >= 0 && bit < kHalfKeys &&
+              if (bit >= 0 && bit < kUnit &&
                   (geo.window == 0 || at > pos - geo.window || at < geo.sinks)) {
                 w[0] |= bit < 32 ? 1u << bit : 0u;
                 w[1] |= bit >= 32 ? 1u << (bit & 31) : 0u;
@@ -644,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
           }
 #pragma unroll 1
-          for (int k = 0; k < kHalfKeys; ++k) {
+          for (int k = 0; k < kUnit; ++k) {
             if (!((bars->bad[pr][2 * h + (k >> 5)] >> (k & 31)) & 1u)) continue;
             const bool reads = ((k < 32 ? w[0] : w[1]) >> (k & 31)) & 1u;
             const float pk = ex2(fmaf(__uint_as_float(tmem_ld1(s_addr + k)), p.c_log2, -m_use));
@@ -704,23 +696,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++cnt;
         return true;
       };
-      for (int j = c.j0; ok && j < c.j1; ++j) {
-        const bool u0 = takes(geo, c.w, t, j, 0), u1 = takes(geo, c.w, t, j, 1);
-        if (!u0 && !u1) continue;
-        const int key0 = key0_of(c.w, j), pr = (j_base + j) % C::kPairs;
-        bool part = partly(geo, c, key0);
+      const Whole whole = whole_of(geo, c.w);
+#pragma unroll 1
+      for (int u = 2 * c.j0; u < 2 * c.j1; ++u) {
+        if (!t.takes(u)) continue;
+        const int tile = j_base + (u >> 1), pr = tile % C::kPairs;
+        const int k0 = (u < 2 * c.w.lead ? 0 : c.w.start - c.w.lead * BK) + u * kUnit;
+        bool part = whole.partly(geo, k0, kUnit);
         unsigned pages = 0xFFu;
         if (kPaged || part) {
           if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->v_ok[pr]),
-                                                 (uint32_t)(((j_base + j) / C::kPairs) & 1)))) {
+                                                 (uint32_t)((tile / C::kPairs) & 1)))) {
             ok = false;
             break;
           }
           if (kPaged) pages = bars->there[pr];
           part = part || pages != 0xFFu;
         }
-#pragma unroll 1
-        for (int h = u0 ? 0 : 1; ok && h < (u1 ? 2 : 1); ++h) ok = unit(key0, pr, h, part, pages);
+        if (!unit(k0, pr, u & 1, part, pages)) {
+          ok = false;
+          break;
+        }
       }
       if (!ok) break;
       // the piece's last product (a tile may have no unit in it)
@@ -731,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       if (pos < 0) l_run = 0.f;                       // it reads nothing: zeros
-      const bool whole = !kPaged || c.whole();
+      const bool all = !kPaged || c.whole();
       const int64_t slot = slot_of(cta, item0, x0) * 2 + x;
       const int64_t row = ((int64_t)c.w.q0 + tok) * p.ldo + (int64_t)(c.h * geo.G + my_g) * D;
       const bool out = real && RF_IN(p.err, row + D - 1,
@@ -743,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t o[32];
         tmem_ld32(o_addr + q * 32, o);
         tmem_ld_wait();
-        if (whole) {
+        if (all) {
           if (out) {
             // a row that read no key: zeros, whatever O holds
 #pragma unroll
@@ -767,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!whole && RF_IN(p.err, slot * BQ + r, (int64_t)4 * gridDim.x * BQ))
+      if (!all && RF_IN(p.err, slot * BQ + r, (int64_t)4 * gridDim.x * BQ))
         p.ws_ml[slot * BQ + r] = make_float2(m_ref, l_run);
       tc_fence_before();                              // O is read before the next product writes it
     }
@@ -1016,8 +1012,8 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
           const bool reads = key <= at[1] && (window == 0 || at[0] - key < window || key < sinks);
           int hits = 0;
           for (int u = 0; u < 2 * w.n; ++u) {
-            const int k0 = key0_of(w, u >> 1) + (u & 1) * kHalfKeys;
-            hits += takes(p, w, t, u >> 1, u & 1) && key >= k0 && key < k0 + kHalfKeys;
+            const int k0 = key0_of(w, u >> 1) + (u & 1) * kUnit;
+            hits += t.takes(u) && key >= k0 && key < k0 + kUnit;
           }
           if (reads ? hits != 1 : hits > 1) return 6;
         }

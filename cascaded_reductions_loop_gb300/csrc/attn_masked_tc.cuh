@@ -175,13 +175,16 @@ struct Walk {
   }
 };
 
-// Tile x (0, 1) of a piece: its tokens, and which halves (kHalfKeys keys) of the
-// item's key tiles it takes: those in which some row may read a key.
-constexpr int kHalfKeys = BK / 2;
+// Tile x (0, 1) of a piece: its tokens, and which units it takes (unit u: the keys of
+// half u & 1 of the item's key tile u / 2): those in which some row may read a key.
+constexpr int kUnit = BK / 2;
 struct Tile {
   int t0, t1;               // its tokens; t0 >= t1: it has no rows
-  int first, last;          // halves of the item's window tiles; last < 0: none
+  int sink, first, last;    // units 0 .. sink - 1 and first .. last
   __host__ __device__ __forceinline__ bool has() const { return t0 < t1; }
+  __host__ __device__ __forceinline__ bool takes(int u) const {
+    return u < sink || (u >= first && u <= last);
+  }
 };
 __host__ __device__ __forceinline__ Tile tile_of(const Geo& p, const Group& w, int x) {
   Tile t;
@@ -190,18 +193,30 @@ __host__ __device__ __forceinline__ Tile tile_of(const Geo& p, const Group& w, i
   const int ctx = w.lk - w.lq;
   const int hi = p.tree ? w.lk - 1 : imin(w.lk - 1, ctx + t.t1 - 1);     // its last row's position
   const int lo = p.window > 0 ? (p.tree ? ctx : ctx + t.t0) - p.window + 1 : 0;
-  t.first = lo > w.start ? (lo - w.start) / kHalfKeys : 0;
-  t.last = hi < 0 || !t.has() ? -1 : (hi - w.start) / kHalfKeys;
+  t.sink = t.first = 0;
+  t.last = -1;
+  if (hi < 0 || !t.has()) return t;
+  t.first = 2 * w.lead + (lo > w.start ? (lo - w.start) / kUnit : 0);
+  t.last = 2 * w.lead + (hi - w.start) / kUnit;
+  if (p.window > 0)
+    t.sink = imin((imin(p.sinks, w.lk) + kUnit - 1) / kUnit, w.lead > 0 ? 2 * w.lead : t.last + 1);
   return t;
 }
-// Half h of key tile j.
-__host__ __device__ __forceinline__ bool takes(const Geo& p, const Group& w, const Tile& t, int j,
-                                               int h) {
-  if (t.last < 0) return false;
-  const bool sink = p.window > 0 && key0_of(w, j) + h * kHalfKeys < p.sinks;
-  if (j < w.lead) return sink;
-  const int u = 2 * (j - w.lead) + h;
-  return u <= t.last && (u >= t.first || sink);
+
+// Whether some row of a pair may not read all of the n keys from key0 on: they are all
+// read if they end at or before `end` and begin at or behind `begin` (or are sinks).
+struct Whole {
+  int end, begin;
+  __host__ __device__ __forceinline__ bool partly(const Geo& p, int key0, int n) const {
+    return key0 + n > end || (key0 < begin && key0 + n > p.sinks);
+  }
+};
+__host__ __device__ __forceinline__ Whole whole_of(const Geo& p, const Group& w) {
+  const int ctx = w.lk - w.lq;
+  Whole a;
+  a.end = p.tree ? ctx : ctx + w.t0 + 1;
+  a.begin = p.window > 0 ? (p.tree ? w.lk : ctx + w.t1) - p.window : -2147483647;
+  return a;
 }
 
 // The workspace slot of CTA c's piece of an item that begins at tile s0 (in the
