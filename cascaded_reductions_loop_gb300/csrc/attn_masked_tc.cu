@@ -8,19 +8,24 @@
 // the cascade of [E] §2.2 in its incremental form ([E] §2.3).  The plan (which rows
 // and keys an item has, how items are shared out) is in attn_masked_tc.cuh.
 //
-// A CTA takes items of two 128-row query tiles (a, b); a unit of work is 64 keys (half
-// a key tile) for one of them.  Per unit u of tile x:
-//   1. MMA thread x: S_x = Q_x K_u^T (tcgen05 kind::f16, M = 128, N = 64, fp32 in tensor
-//      memory), into one of two buffers in turn;
-//   2. softmax warpgroup x, a thread a row: its 64 scores in registers, the keys it does
-//      not read at -inf (only where some row reads a part), running maximum moved lazily
-//      (by more than 2^8 only), P = 2^(S c - m) as bf16 over S_x's columns;
-//   3. MMA thread x: O_x += P_x V_u (P the tensor-memory A operand).
-// Tensor memory: S_a, S_b (two buffers of 64 columns each), O_a, O_b: at d = 128 all of
-// its 512 columns.  S_x(u + 1) is computed while unit u's softmax runs, so a softmax
-// warpgroup finds its next scores ready.  With 128 keys a unit and P over the only S, S
-// waited for P.V, softmax and tensor core took turns: 4900 clocks for 128 keys of both
-// tiles (clock stamps), 1536 us for the 16k prompt below.
+// A CTA takes items of two 128-row query tiles (a, b).  An event is a key tile for one
+// of them; events go in the order (key tile, a before b).  Per event of tile x:
+//   1. S = Q_x K_j^T (tcgen05 kind::f16, M = N = 128, fp32 in tensor memory), into the
+//      one S that both tiles use in turn;
+//   2. softmax warpgroup x, a thread a row: reads its 128 scores into registers, which
+//      frees S for the next event; keys the row does not read at -inf (only where some
+//      row reads a part); running maximum moved lazily (by more than 2^8 only);
+//      P_x = 2^(S c - m) as bf16;
+//   3. O_x += P_x V_j (P the tensor-memory A operand).
+// Half key tiles that a query tile does not read are left out of its event.
+// Tensor memory: S, P_a, P_b, O_a, O_b, at d = 128 all of its 512 columns.  One thread
+// issues all products, S three events ahead of P.V, so that a warpgroup that ends an
+// event finds its next scores, the two run half an event out of phase, and the tensor
+// core has the one's products during the other's softmax.
+// Measured for 128 keys of both tiles (clock stamps; the products alone take 1900):
+// 4900 clocks with S_a, S_b and P over S (the next S waits for P.V), 3835 in units of 64
+// keys with two S buffers a tile (S in N = 64 takes 56 clocks a step for half the keys,
+// N = 128 takes 64).
 //
 // Rounding: P is rounded to bf16 (half a step, 2^-8 of a weight; l sums the unrounded
 // ones), since both operands of an MMA have one type and V is bf16.
@@ -40,11 +45,11 @@ namespace rf {
 namespace masked {
 
 constexpr int kHalf = 128 * 128;                      // 128 rows of 64 values: 16 KB
-constexpr int kThreads = 384;                         // TMA, MMA a, MMA b, guard; softmax a; softmax b
+constexpr int kThreads = 384;                         // TMA, MMA, two guards; softmax a; softmax b
 constexpr float kLazy = 8.f;
-// Registers: 384 threads start with 168 each (64512): the softmax warpgroups take 208
-// (53248) of them, the others keep 88 (11264).
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+// Registers: 384 threads start with 168 each (64512): the softmax warpgroups take 216
+// (55296) of them, the others keep 72 (9216).
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 
 template <int D>
 struct Cfg {
@@ -55,13 +60,14 @@ struct Cfg {
   static constexpr int kRing = kQSlots * kTile;
   static constexpr int kBarOff = kRing + kStages * kTile;
   static constexpr int kSmem = kBarOff + 1024 + 1024; // barriers; alignment
-  static constexpr uint32_t kIdescS = make_idesc(BQ, kUnit, 1, 0, 0);
+  static constexpr uint32_t kIdescS = make_idesc(BQ, BK, 1, 0, 0);
+  static constexpr uint32_t kIdescHalf = make_idesc(BQ, kUnit, 1, 0, 0);
   static constexpr uint32_t kIdescO = make_idesc(BQ, D, 1, 0, 1);
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 constexpr uint32_t kTmemCols = 512;
-// S_x of unit u (64 columns); P_x over its first 32
-__device__ __forceinline__ uint32_t col_s(int x, int u) { return x * 128 + (u & 1) * kUnit; }
+constexpr uint32_t kColS = 0;                         // 128 columns
+__device__ __forceinline__ uint32_t col_p(int x) { return 128 + x * 64; }
 __device__ __forceinline__ uint32_t col_o(int x) { return 256 + x * 128; }
 
 struct Params {
@@ -84,9 +90,8 @@ struct Bars {
   uint64_t q_full[4], q_empty[4];
   uint64_t full[8], empty[8];
   uint64_t v_ok[4];                                   // a V tile is looked over
-  // per tile, for the units of either buffer: either side may be a unit behind
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];
-  uint64_t drain[2];
+  uint64_t s_full[2], p_full[2], pv_done[2];          // of a query tile's events
+  uint64_t s_read, drain;                             // of all events: S is in registers
   unsigned rec[8];                                    // per key tile; K may be a round ahead of V
   // what the guard found, per V stage: values that are not finite; rec's pages
   unsigned bad[4][4], there[4];
@@ -111,9 +116,20 @@ template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// Waits for unit u's phase of a pair of barriers.
-__device__ __forceinline__ bool unit_wait(uint64_t (&bar)[2], int u) {
-  return mbar_wait(smem_u32(&bar[u & 1]), (uint32_t)((u >> 1) & 1));
+// The same value in every lane, which the compiler then knows (uniform registers, which
+// the tensor core's instructions take their operands from).
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// mbar_wait of a whole warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 // One column of this thread's lane (waits for it).
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
@@ -151,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kBarOff);
   volatile int* abort_flag = &bars->abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int cta = (int)blockIdx.x;
   const Geo& geo = p.geo;
   uint8_t* ring = smem + C::kRing;
@@ -163,20 +179,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 1);
       mbar_init(smem_u32(&bars->q_empty[i]), 1);
-      mbar_init(smem_u32(&bars->v_ok[i]), 1);
+      mbar_init(smem_u32(&bars->v_ok[i]), 2);         // both guards
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&bars->full[i]), 1);
-      mbar_init(smem_u32(&bars->empty[i]), 2);        // both MMA threads
+      mbar_init(smem_u32(&bars->empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      for (int k = 0; k < 2; ++k) {
-        mbar_init(smem_u32(&bars->s_full[i][k]), 1);
-        mbar_init(smem_u32(&bars->p_full[i][k]), BQ);
-        mbar_init(smem_u32(&bars->pv_done[i][k]), 1);
-      }
-      mbar_init(smem_u32(&bars->drain[i]), 1);
+      mbar_init(smem_u32(&bars->s_full[i]), 1);
+      mbar_init(smem_u32(&bars->p_full[i]), BQ);
+      mbar_init(smem_u32(&bars->pv_done[i]), 1);
     }
+    mbar_init(smem_u32(&bars->s_read), 4);            // a warpgroup's warps
+    mbar_init(smem_u32(&bars->drain), 1);
     bars->abort = 0;
     bars->x[0] = bars->x[1] = 0;
     bars->g = bars->h = bars->j = 0;
@@ -238,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  const uint32_t tmem = bars->tmem;
+  const uint32_t tmem = (uint32_t)uniform((int)bars->tmem);
   const int64_t x0 = bars->x[0], x1 = bars->x[1];
   if (kPaged && threadIdx.x == 0 && RF_IN(p.err, cta, gridDim.x))
     p.ws_cut[cta] = cta == 0 ? make_int4(0, (int)(total & 0x7FFFFFFF), (int)(total >> 31), grid)
@@ -353,145 +368,168 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (unsigned i = in_flight > C::kStages ? in_flight - C::kStages : 0; i < in_flight; ++i)
           (void)mbar_wait(smem_u32(&bars->full[i % C::kStages]), (i / C::kStages) & 1, 1000000ull);
       }
-    } else if (warp < 3) {
-      // ---------------------------------------------------------- MMA of tile x
-      const int x = warp - 1;
-      if (lane == 0) {
-        // Key tiles in order, the S side one tile ahead of the P.V side: K of the next
-        // tile arrives without anything that this thread has yet to release.
-        const int count = (int)(x1 - x0);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA
+      // The whole warp runs the schedule, one lane issues: with the schedule in one lane
+      // an MMA took 100 clocks to issue (its operands went through vector registers).
+      {
+        const int count = uniform((int)(x1 - x0));
+        const bool leader = elect_one();
         const uint64_t kd = sw128_desc(smem_u32(ring), 1024, 16);
         const uint64_t vd = sw128_desc(smem_u32(ring + C::kTile), 1024, kHalf);
-        uint64_t qd = 0;
-        int nq = x, slot = 0;                         // this thread's Q tile (a, b in turn) and place
-        int us = 0, up = 0;                           // units whose S, whose P.V is issued
-        auto open = [&](int nt, unsigned& rec) -> bool {
-          if (!mbar_wait(smem_u32(&bars->full[2 * (nt % C::kPairs)]), (uint32_t)((nt / C::kPairs) & 1)))
-            return false;
-          rec = bars->rec[nt % 8];
-          if (rec & kFirst) {
-            slot = nq % C::kQSlots;
-            if ((x == 0 || (rec & kHasB)) &&
-                !mbar_wait(smem_u32(&bars->q_full[slot]), (uint32_t)((nq / C::kQSlots) & 1)))
-              return false;
-            qd = sw128_desc(smem_u32(smem + slot * C::kTile), 1024, 16);
-            nq += (rec & kHasB) ? 2 : 1;
-          }
-          return true;
-        };
-        // S of half h, after the product that reads its buffer's P
-        auto issue_s = [&](int nt, unsigned rec, int h) -> bool {
-          if ((rec >> (2 * x + h)) & 1u) {
-            if (us >= 2 && !unit_wait(bars->pv_done[x], us - 2)) return false;
-            tc_fence_after();
-            const uint64_t b = kd + (uint64_t)((2 * (nt % C::kPairs) * C::kTile + h * kUnit * 128) >> 4);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint64_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-              mma_bf16_ss(tmem + col_s(x, us), qd + off, b + off, C::kIdescS, k != 0);
+        int ns = 0, xs = 0, np = 0, xp = 0;           // next event: S side, P.V side
+        int nq = 0, q_at = 0;                         // Q tiles before the next piece's, this one's
+        int reads = 0, ahead = 0;                     // S events issued; of them before P.V
+        int js = -1, piece = 0, js_piece = -1;        // the last S event's tile; where pieces begin
+        unsigned rs = 0, rp = 0;                      // the tiles' records
+        unsigned phase = 0, fresh = 3;                // bit x: of p_full[x]; O_x is to be overwritten
+        // One step of the S side: an event, or a query tile that does not take the key tile
+        auto step_s = [&]() -> bool {
+          const int pr = ns % C::kPairs;
+          if (xs == 0) {
+            if (!warp_wait(smem_u32(&bars->full[2 * pr]), (uint32_t)((ns / C::kPairs) & 1))) return false;
+            rs = (unsigned)uniform((int)bars->rec[ns % 8]);
+            if (rs & kFirst) {
+              piece = ns;
+              q_at = nq;
+              nq += (rs & kHasB) ? 2 : 1;
             }
-            mma_commit(smem_u32(&bars->s_full[x][us & 1]));
-            ++us;
           }
-          if (h == 1) {
-            mma_commit(smem_u32(&bars->empty[2 * (nt % C::kPairs)]));
-            if ((rec & kLast) && (x == 0 || (rec & kHasB))) mma_commit(smem_u32(&bars->q_empty[slot]));
+          const int slot = (q_at + xs) % C::kQSlots;
+          if ((rs & kFirst) && (xs == 0 || (rs & kHasB)) &&
+              !warp_wait(smem_u32(&bars->q_full[slot]), (uint32_t)(((q_at + xs) / C::kQSlots) & 1)))
+            return false;
+          const unsigned halves = (rs >> (2 * xs)) & 3u;
+          if (halves) {
+            if (reads > 0 && !warp_wait(smem_u32(&bars->s_read), (uint32_t)((reads - 1) & 1)))
+              return false;
+            tc_fence_after();
+            const int h = halves == 2u ? 1 : 0;       // the first half it takes
+            const uint64_t a = sw128_desc(smem_u32(smem + slot * C::kTile), 1024, 16);
+            const uint64_t b = kd + (uint64_t)((2 * pr * C::kTile + h * kUnit * 128) >> 4);
+            const uint32_t idesc = halves == 3u ? C::kIdescS : C::kIdescHalf;
+            if (leader) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint64_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+                mma_bf16_ss(tmem + kColS + h * kUnit, a + off, b + off, idesc, k != 0);
+              }
+              mma_commit(smem_u32(&bars->s_full[xs]));
+            }
+            ++reads;
+            ++ahead;
+            js = ns;
+            js_piece = piece;
           }
+          if ((rs & kLast) && (xs == 0 || (rs & kHasB)) && leader) mma_commit(smem_u32(&bars->q_empty[slot]));
+          if (xs == 1) {
+            if (leader) mma_commit(smem_u32(&bars->empty[2 * pr]));
+            ++ns;
+          }
+          xs ^= 1;
           return true;
         };
-        bool fresh = true;
-        auto issue_pv = [&](int nt, unsigned rec, int h) -> bool {
-          const int pr = nt % C::kPairs;
-          if (h == 0) {
-            if (rec & kFirst) fresh = true;
-            if (!mbar_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((nt / C::kPairs) & 1))) return false;
+        auto step_pv = [&]() -> bool {
+          const int pr = np % C::kPairs, x = xp;
+          if (x == 0) {
+            if (!warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((np / C::kPairs) & 1))) return false;
+            rp = (unsigned)uniform((int)bars->rec[np % 8]);
+            if (rp & kFirst) fresh = 3u;
           }
-          if ((rec >> (2 * x + h)) & 1u) {
-            if (!unit_wait(bars->p_full[x], up)) return false;
+          const unsigned halves = (rp >> (2 * x)) & 3u;
+          if (halves) {
+            if (!warp_wait(smem_u32(&bars->p_full[x]), (phase >> x) & 1u)) return false;
             tc_fence_after();
             // values that are not finite are in O before the first product
-            bool onto = !fresh;
-            if (kPaged || ((rec >> h) & kPartly))
-              onto = onto || (bars->bad[pr][2 * h] | bars->bad[pr][2 * h + 1]) != 0u;
-            const uint64_t b = vd + (uint64_t)((2 * pr * C::kTile + h * kUnit * 128) >> 4);
+            bool onto = !((fresh >> x) & 1u);
+            if (kPaged || (rp & (3u * kPartly))) {
+              const unsigned* b = bars->bad[pr];
+              onto = onto || uniform(((halves & 1u) && (b[0] | b[1])) || ((halves & 2u) && (b[2] | b[3])));
+            }
+            const uint64_t b = vd + (uint64_t)((2 * pr * C::kTile) >> 4);
+            if (leader) {
 #pragma unroll
-            for (int k = 0; k < kUnit / 16; ++k)
-              mma_bf16_ts(tmem + col_o(x), tmem + col_s(x, up) + k * 8,
-                          b + (uint64_t)((k * 16 * 128) >> 4), C::kIdescO, onto || k != 0);
-            mma_commit(smem_u32(&bars->pv_done[x][up & 1]));
-            fresh = false;
-            ++up;
+              for (int k = 0; k < BK / 16; ++k) {
+                if (!((halves >> (k / 4)) & 1u)) continue;
+                mma_bf16_ts(tmem + col_o(x), tmem + col_p(x) + k * 8,
+                            b + (uint64_t)((k * 16 * 128) >> 4), C::kIdescO, onto);
+                onto = true;
+              }
+              mma_commit(smem_u32(&bars->pv_done[x]));
+            }
+            fresh &= ~(1u << x);
+            phase ^= 1u << x;
+            --ahead;
           }
-          if (h == 1) mma_commit(smem_u32(&bars->empty[2 * pr + 1]));
+          if (x == 1) {
+            if (leader) mma_commit(smem_u32(&bars->empty[2 * pr + 1]));
+            ++np;
+          }
+          xp ^= 1;
           return true;
         };
-        unsigned rec = 0, next = 0;
-        if (count > 0) ok = open(0, rec) && issue_s(0, rec, 0) && issue_s(0, rec, 1);
-        for (int nt = 0; ok && nt < count; ++nt, rec = next) {
-          const bool more = nt + 1 < count;
-          ok = issue_pv(nt, rec, 0);
-          if (more) ok = ok && open(nt + 1, next) && issue_s(nt + 1, next, 0);
-          ok = ok && issue_pv(nt, rec, 1);
-          if (more) ok = ok && issue_s(nt + 1, next, 1);
+        while (ok && np < count) {
+          // What the S side waits for comes without anything that the P.V side has yet to
+          // do: K of its tile (no further than two tiles ahead), and that the last event's
+          // scores are read, which waits for that tile's V to be looked over (so V has its
+          // stage) and, at the beginning of a piece, for the last piece's O.
+          while (ok && ahead < 3 && ns < count && ns <= np + 2 && js <= np + 1 && js_piece <= np)
+            ok = step_s();
+          ok = ok && step_pv();
           if (*abort_flag) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
         }
         if (!ok) {
           raise_error(p.err, kDevErrTimeout);
           *abort_flag = 1;
         }
         // nothing may still run on the tensor core when memory is released
-        mma_commit(smem_u32(&bars->drain[x]));
-        (void)mbar_wait(smem_u32(&bars->drain[x]), 0, 1000000000ull);
+        if (leader) mma_commit(smem_u32(&bars->drain));
+        (void)mbar_wait(smem_u32(&bars->drain), 0, 1000000000ull);
       }
     } else {
-      // ---------------------------------------------------------- guard
+      // ---------------------------------------------------------- guard of half h
+      const int h = warp - 2;
       const int count = (int)(x1 - x0);
+      // an exponent of ones carries into the sign's place
+      auto ones = [](const uint4& w) {
+        return ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+               ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+      };
       for (int nt = 0; ok && nt < count; ++nt) {
-        {
-          const int pr = nt % C::kPairs, st = 2 * pr;
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->full[st + 1]),
-                                                 (uint32_t)((nt / C::kPairs) & 1)));
-          if (!ok) break;
-          const unsigned rec = bars->rec[nt % 8];
-          const unsigned pages = kPaged ? (rec >> kPages) & 0xFFu : 0xFFu;
-          unsigned bad[4] = {0u, 0u, 0u, 0u};
-          uint4* v = reinterpret_cast<uint4*>(ring + (st + 1) * C::kTile);
-          // an exponent of ones carries into the sign's place
-          auto ones = [](const uint4& w) {
-            return ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
-                   ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
-          };
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            if (!((rec >> h) & kPartly) && pages == 0xFFu) continue;
-            unsigned seen = 0;
+        const int pr = nt % C::kPairs;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->full[2 * pr + 1]),
+                                               (uint32_t)((nt / C::kPairs) & 1)));
+        if (!ok) break;
+        const unsigned rec = bars->rec[nt % 8];
+        const unsigned pages = kPaged ? (rec >> kPages) & 0xFFu : 0xFFu;
+        unsigned bad[2] = {0u, 0u};
+        if (((rec >> h) & kPartly) || pages != 0xFFu) {
+          uint4* v = reinterpret_cast<uint4*>(ring + (2 * pr + 1) * C::kTile) + h * (kUnit * 8);
+          unsigned seen = 0;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {        // 64 rows of 128 bytes
-              const uint4* at = v + i * (kHalf / 16) + h * (kUnit * 8);
+          for (int i = 0; i < D / 64; ++i)            // 64 rows of 128 bytes
 #pragma unroll 8
-              for (int k = lane; k < kUnit * 8; k += 32) seen |= ones(at[k]);
-            }
-            if (!__any_sync(0xffffffffu, (seen & 0x80008000u) != 0u)) continue;
+            for (int k = lane; k < kUnit * 8; k += 32) seen |= ones(v[i * (kHalf / 16) + k]);
+          if (__any_sync(0xffffffffu, (seen & 0x80008000u) != 0u)) {
 #pragma unroll 1
-            for (int r = h * kUnit; r < (h + 1) * kUnit; ++r) {       // which rows; they become zeros
+            for (int r = 0; r < kUnit; ++r) {         // which rows; they become zeros
               uint4* at = v + (lane >> 3) * (kHalf / 16) + r * 8 + (lane & 7);
               const bool hit = lane < D / 8 && (ones(*at) & 0x80008000u) != 0u;
               if (!__any_sync(0xffffffffu, hit)) continue;
               bad[0] |= r < 32 ? 1u << r : 0u;
-              bad[1] |= r >= 32 && r < 64 ? 1u << (r & 31) : 0u;
-              bad[2] |= r >= 64 && r < 96 ? 1u << (r & 31) : 0u;
-              bad[3] |= r >= 96 ? 1u << (r & 31) : 0u;
+              bad[1] |= r >= 32 ? 1u << (r & 31) : 0u;
               if (lane < D / 8) *at = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
           }
-          __syncwarp();
-          if (lane == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) bars->bad[pr][i] = bad[i];
-            bars->there[pr] = pages;
-            mbar_arrive(smem_u32(&bars->v_ok[pr]));
-          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          bars->bad[pr][2 * h] = bad[0];
+          bars->bad[pr][2 * h + 1] = bad[1];
+          if (h == 0) bars->there[pr] = pages;
+          mbar_arrive(smem_u32(&bars->v_ok[pr]));
         }
         if (*abort_flag) ok = false;
         ok = __all_sync(0xffffffffu, ok);
@@ -507,10 +545,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = warp >= 8 ? 1 : 0;
     const int r = (warp & 3) * 32 + lane;             // row of the tile
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lane_off + kColS, p_addr = tmem + lane_off + col_p(x);
     const uint32_t o_addr = tmem + lane_off + col_o(x);
     const uint64_t c2 = f2(p.c_log2, p.c_log2);
     const int my_t = r / geo.G, my_g = r - my_t * geo.G;
-    int nt = 0, cnt = 0;                              // key tiles; units of this warpgroup
+    int nt = 0, cnt = 0;                              // key tiles; events of this warpgroup
     int64_t s0 = x0 - (x1 > x0 ? bars->j : 0);        // first tile of the piece's item
     while (ok && walk.next(geo, c, p.err)) {
       const Tile t = tile_of(geo, c.w, x);
@@ -540,29 +579,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!real) pos = -1;
       float m_ref = -INFINITY, l_run = 0.f;
       const int cnt0 = cnt;
-      // one unit: the keys from k0 on, in half h of V stage pr; part: some row may not read all
-      auto unit = [&](int k0, int pr, int h, bool part, unsigned pages) -> bool {
-        const uint32_t s_addr = tmem + lane_off + col_s(x, cnt);
-        unsigned w[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};   // keys it reads
+      // one event: halves (bits) of the key tile at key0, in V stage pr; part: of which
+      // halves some row may not read all keys
+      auto event = [&](int key0, int pr, unsigned halves, unsigned part, unsigned pages) -> bool {
+        unsigned w[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};   // keys it reads
         bool any_bad = false;
         if (part) {
           const int hi = geo.tree ? min(ctx, pos + 1) : pos + 1;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int k = k0 + 32 * q;
+          for (int q = 0; q < 4; ++q) {
+            const int k = key0 + 32 * q;
             w[q] = below(hi - k);
             if (geo.window > 0) w[q] &= ~below(pos - geo.window + 1 - k) | below(geo.sinks - k);
             if (pos < 0) w[q] = 0u;
-            any_bad |= bars->bad[pr][2 * h + q] != 0u;
+            if ((halves >> (q / 2)) & 1u) any_bad |= bars->bad[pr][q] != 0u;
           }
-          if (geo.tree && k0 + kUnit > ctx && pos >= 0) {
+          if (geo.tree && key0 + BK > ctx && pos >= 0) {
             int u = tok;
             for (int at = pos; u >= 0; --at) {        // node u at position `at`
-              const int bit = ctx + u - k0;
-              if (bit >= 0 && bit < kUnit &&
+              const int bit = ctx + u - key0;
+              if (bit >= 0 && bit < BK &&
                   (geo.window == 0 || at > pos - geo.window || at < geo.sinks)) {
-                w[0] |= bit < 32 ? 1u << bit : 0u;
-                w[1] |= bit >= 32 ? 1u << (bit & 31) : 0u;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] |= (bit >> 5) == q ? 1u << (bit & 31) : 0u;
               }
               const int up = ld_int(p.parents, (int64_t)c.w.b * geo.max_q + u,
                                     (int64_t)geo.B * geo.max_q, p.err);
@@ -571,49 +610,65 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (kPaged) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-              w[q] &= ((pages >> (4 * h + 2 * q)) & 1u ? 0xFFFFu : 0u) |
-                      ((pages >> (4 * h + 2 * q + 1)) & 1u ? 0xFFFF0000u : 0u);
+            for (int q = 0; q < 4; ++q)
+              w[q] &= ((pages >> (2 * q)) & 1u ? 0xFFFFu : 0u) |
+                      ((pages >> (2 * q + 1)) & 1u ? 0xFFFF0000u : 0u);
           }
         }
-        if (!__all_sync(0xffffffffu, unit_wait(bars->s_full[x], cnt) && !*abort_flag)) return false;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(smem_u32(&bars->s_full[x]), (uint32_t)(cnt & 1)) && !*abort_flag))
+          return false;
         tc_fence_after();
-        uint32_t v[2][32];
-        tmem_ld32(s_addr, v[0]);
-        tmem_ld32(s_addr + 32, v[1]);
+        uint32_t v[4][32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if ((halves >> h) & 1u) {
+            tmem_ld32(s_addr + 64 * h, v[2 * h]);
+            tmem_ld32(s_addr + 64 * h + 32, v[2 * h + 1]);
+          }
         tmem_ld_wait();
-        if (part && __any_sync(0xffffffffu, (w[0] & w[1]) != 0xFFFFFFFFu)) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[q][i] = (w[q] >> i) & 1u ? v[q][i] : 0xff800000u;
+        if (!any_bad) {                               // S may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->s_read));
         }
-        // row maximum (four chains)
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // row maximum (chains of their own)
+        float mh[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int h = 0; h < 2; ++h)
+          if ((halves >> h) & 1u) {
+            if (part && __any_sync(0xffffffffu, (w[2 * h] & w[2 * h + 1]) != 0xFFFFFFFFu)) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            mx4[(i >> 1) & 3] =
-                fmax3(mx4[(i >> 1) & 3], __uint_as_float(v[q][i]), __uint_as_float(v[q][i + 1]));
-        const float mt = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * p.c_log2;
+              for (int q = 2 * h; q < 2 * h + 2; ++q)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[q][i] = (w[q] >> i) & 1u ? v[q][i] : 0xff800000u;
+            }
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int q = 2 * h; q < 2 * h + 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                mx4[(i >> 1) & 3] =
+                    fmax3(mx4[(i >> 1) & 3], __uint_as_float(v[q][i]), __uint_as_float(v[q][i + 1]));
+            mh[h] = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]);
+          }
+        const float mt = fmaxf(mh[0], mh[1]) * p.c_log2;
         const bool fresh = cnt == cnt0;
         float alpha = 1.f;
         if (fresh) {
-          m_ref = mt;                                 // P.V of the first unit overwrites O
+          m_ref = mt;                                 // P.V of the first event overwrites O
         } else if (mt > m_ref + kLazy) {
           alpha = ex2(m_ref - mt);
           l_run *= alpha;
           m_ref = mt;
         }
-        const bool move = !fresh && __any_sync(0xffffffffu, alpha != 1.f);
-        if ((move || any_bad) && cnt > 0) {
-          // O_x is complete through the last unit
-          if (!__all_sync(0xffffffffu, unit_wait(bars->pv_done[x], cnt - 1))) return false;
-          tc_fence_after();
-        }
-        if (move) {
-#pragma unroll
+        // P_x may be overwritten and O_x is complete once the last event's P.V is done
+        if (cnt > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->pv_done[x]),
+                                                          (uint32_t)((cnt - 1) & 1))))
+          return false;
+        tc_fence_after();
+        if (!fresh && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
           for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
             tmem_ld32(o_addr + q * 32, o);
@@ -636,23 +691,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
           }
 #pragma unroll 1
-          for (int k = 0; k < kUnit; ++k) {
-            if (!((bars->bad[pr][2 * h + (k >> 5)] >> (k & 31)) & 1u)) continue;
-            const bool reads = ((k < 32 ? w[0] : w[1]) >> (k & 31)) & 1u;
+          for (int k = 0; k < BK; ++k) {
+            if (!((halves >> (k >> 6)) & 1u) || !((bars->bad[pr][k >> 5] >> (k & 31)) & 1u)) continue;
+            const unsigned rw = k < 32 ? w[0] : (k < 64 ? w[1] : (k < 96 ? w[2] : w[3]));
+            const bool reads = (rw >> (k & 31)) & 1u;
             const float pk = ex2(fmaf(__uint_as_float(tmem_ld1(s_addr + k)), p.c_log2, -m_use));
             int64_t at;                               // the value's first element
             bool inside;
             if (kPaged) {
-              const int page = k0 + k < c.w.lk
+              const int page = key0 + k < c.w.lk
                                    ? ld_int(p.block_table,
-                                            (int64_t)c.w.b * p.max_pages + ((k0 + k) >> p.page_shift),
+                                            (int64_t)c.w.b * p.max_pages + ((key0 + k) >> p.page_shift),
                                             (int64_t)geo.B * p.max_pages, p.err)
                                    : -1;
-              at = (((int64_t)page * geo.Hkv + c.h) * p.page_size + ((k0 + k) & (p.page_size - 1))) * D;
+              at = (((int64_t)page * geo.Hkv + c.h) * p.page_size + ((key0 + k) & (p.page_size - 1))) * D;
               inside = (unsigned)page < (unsigned)p.num_pages;
             } else {
-              at = (int64_t)(c.w.k0 + k0 + k) * p.ldv + (int64_t)c.h * D;
-              inside = k0 + k < c.w.lk;
+              at = (int64_t)(c.w.k0 + key0 + k) * p.ldv + (int64_t)c.h * D;
+              inside = key0 + k < c.w.lk;
             }
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
@@ -669,51 +725,60 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_wait();
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->s_read));
         }
         // P = 2^(S c - m) as bf16 pairs, and its row sum (four chains)
         const uint64_t negm2 = f2(-m_use, -m_use);
         uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
-        uint32_t pk[32];
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int h = 0; h < 2; ++h)
+          if ((halves >> h) & 1u) {
+            uint32_t pk[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float t0, t1;
-            f2_split(ffma2(f2(__uint_as_float(v[q][2 * i]), __uint_as_float(v[q][2 * i + 1])), c2,
-                           negm2),
-                     t0, t1);
-            const float p0 = ex2(t0), p1 = ex2(t1);
-            sum4[i & 3] = fadd2(sum4[i & 3], f2(p0, p1));
-            pk[q * 16 + i] = pack_bf16x2(p0, p1);
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float t0, t1;
+                f2_split(ffma2(f2(__uint_as_float(v[2 * h + q][2 * i]),
+                                  __uint_as_float(v[2 * h + q][2 * i + 1])),
+                               c2, negm2),
+                         t0, t1);
+                const float p0 = ex2(t0), p1 = ex2(t1);
+                sum4[i & 3] = fadd2(sum4[i & 3], f2(p0, p1));
+                pk[q * 16 + i] = pack_bf16x2(p0, p1);
+              }
+            tmem_st32(p_addr + 32 * h, pk);
           }
-        tmem_st32(s_addr, pk);
         float s_lo, s_hi;
         f2_split(fadd2(fadd2(sum4[0], sum4[1]), fadd2(sum4[2], sum4[3])), s_lo, s_hi);
         l_run += s_lo + s_hi;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(&bars->p_full[x][cnt & 1]));
+        mbar_arrive(smem_u32(&bars->p_full[x]));
         ++cnt;
         return true;
       };
       const Whole whole = whole_of(geo, c.w);
 #pragma unroll 1
-      for (int u = 2 * c.j0; u < 2 * c.j1; ++u) {
-        if (!t.takes(u)) continue;
-        const int tile = j_base + (u >> 1), pr = tile % C::kPairs;
-        const int k0 = (u < 2 * c.w.lead ? 0 : c.w.start - c.w.lead * BK) + u * kUnit;
-        bool part = whole.partly(geo, k0, kUnit);
+      for (int j = c.j0; j < c.j1; ++j) {
+        const unsigned halves = (t.takes(2 * j) ? 1u : 0u) | (t.takes(2 * j + 1) ? 2u : 0u);
+        if (!halves) continue;
+        const int key0 = key0_of(c.w, j), pr = (j_base + j) % C::kPairs;
+        unsigned part = (whole.partly(geo, key0, kUnit) ? 1u : 0u) |
+                        (whole.partly(geo, key0 + kUnit, kUnit) ? 2u : 0u);
         unsigned pages = 0xFFu;
         if (kPaged || part) {
           if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->v_ok[pr]),
-                                                 (uint32_t)((tile / C::kPairs) & 1)))) {
+                                                 (uint32_t)(((j_base + j) / C::kPairs) & 1)))) {
             ok = false;
             break;
           }
           if (kPaged) pages = bars->there[pr];
-          part = part || pages != 0xFFu;
+          if (pages != 0xFFu) part = 3u;
         }
-        if (!unit(k0, pr, u & 1, part, pages)) {
+        if (!event(key0, pr, halves, part, pages)) {
           ok = false;
           break;
         }
@@ -721,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // the piece's last product (a tile may have no unit in it)
       if (cnt > cnt0 &&
-          !__all_sync(0xffffffffu, unit_wait(bars->pv_done[x], cnt - 1) && !*abort_flag)) {
+          !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->pv_done[x]), (uint32_t)((cnt - 1) & 1)) && !*abort_flag)) {
         ok = false;
         break;
       }
