@@ -18,14 +18,15 @@
 //      P_x = 2^(S c - m) as bf16;
 //   3. O_x += P_x V_j (P the tensor-memory A operand).
 // Half key tiles that a query tile does not read are left out of its event.
-// Tensor memory: S, P_a, P_b, O_a, O_b, at d = 128 all of its 512 columns.  One thread
-// issues all products, S three events ahead of P.V, so that a warpgroup that ends an
-// event finds its next scores, the two run half an event out of phase, and the tensor
-// core has the one's products during the other's softmax.
-// Measured for 128 keys of both tiles (clock stamps; the products alone take 1900):
-// 4900 clocks with S_a, S_b and P over S (the next S waits for P.V), 3835 in units of 64
-// keys with two S buffers a tile (S in N = 64 takes 56 clocks a step for half the keys,
-// N = 128 takes 64).
+// Tensor memory: S, P_a, P_b, O_a, O_b, at d = 128 all of its 512 columns.  One warp
+// issues the S products, another P.V: S may be as far ahead as its tiles are there, a
+// warpgroup that ends an event finds its next scores, the two run half an event out of
+// phase, and the tensor core has the one's products during the other's softmax.
+// What it took for 128 keys of both tiles (clock stamps; the products alone take 2048
+// clocks): 4900 clocks with S_a, S_b and P over S (the next S waits for P.V); 3835 in
+// units of 64 keys with two S buffers a tile (48 clocks a step for half the keys); 5000
+// with one S and one warp for all products, whose waits and commits (70 to 200 clocks
+// each) then follow one another.
 //
 // Rounding: P is rounded to bf16 (half a step, 2^-8 of a weight; l sums the unrounded
 // ones), since both operands of an MMA have one type and V is bf16.
@@ -45,7 +46,7 @@ namespace rf {
 namespace masked {
 
 constexpr int kHalf = 128 * 128;                      // 128 rows of 64 values: 16 KB
-constexpr int kThreads = 384;                         // TMA, MMA, two guards; softmax a; softmax b
+constexpr int kThreads = 384;                         // TMA, S, P.V, guard; softmax a; softmax b
 constexpr float kLazy = 8.f;
 // Registers: 384 threads start with 168 each (64512): the softmax warpgroups take 216
 // (55296) of them, the others keep 72 (9216).
@@ -91,7 +92,8 @@ struct Bars {
   uint64_t full[8], empty[8];
   uint64_t v_ok[4];                                   // a V tile is looked over
   uint64_t s_full[2], p_full[2], pv_done[2];          // of a query tile's events
-  uint64_t s_read, drain;                             // of all events: S is in registers
+  uint64_t s_read;                                    // of all events: S is in registers
+  uint64_t drain[2];
   unsigned rec[8];                                    // per key tile; K may be a round ahead of V
   // what the guard found, per V stage: values that are not finite; rec's pages
   unsigned bad[4][4], there[4];
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 1);
       mbar_init(smem_u32(&bars->q_empty[i]), 1);
-      mbar_init(smem_u32(&bars->v_ok[i]), 2);         // both guards
+      mbar_init(smem_u32(&bars->v_ok[i]), 1);
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&bars->full[i]), 1);
@@ -191,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars->pv_done[i]), 1);
     }
     mbar_init(smem_u32(&bars->s_read), 4);            // a warpgroup's warps
-    mbar_init(smem_u32(&bars->drain), 1);
+    mbar_init(smem_u32(&bars->drain[0]), 1);
+    mbar_init(smem_u32(&bars->drain[1]), 1);
     bars->abort = 0;
     bars->x[0] = bars->x[1] = 0;
     bars->g = bars->h = bars->j = 0;
@@ -368,85 +371,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (unsigned i = in_flight > C::kStages ? in_flight - C::kStages : 0; i < in_flight; ++i)
           (void)mbar_wait(smem_u32(&bars->full[i % C::kStages]), (i / C::kStages) & 1, 1000000ull);
       }
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- MMA
-      // The whole warp runs the schedule, one lane issues: with the schedule in one lane
-      // an MMA took 100 clocks to issue (its operands went through vector registers).
-      {
-        const int count = uniform((int)(x1 - x0));
-        const bool leader = elect_one();
+    } else if (warp < 3) {
+      // ---------------------------------------------------------- MMA: S (warp 1), P.V (warp 2)
+      // The whole warp runs the schedule, one lane issues: with the schedule in one lane an
+      // MMA took 100 clocks to issue (its operands went through vector registers).
+      const int count = uniform((int)(x1 - x0));
+      const bool leader = elect_one();
+      if (warp == 1) {
+        const uint64_t qd = sw128_desc(smem_u32(smem), 1024, 16);
         const uint64_t kd = sw128_desc(smem_u32(ring), 1024, 16);
-        const uint64_t vd = sw128_desc(smem_u32(ring + C::kTile), 1024, kHalf);
-        int ns = 0, xs = 0, np = 0, xp = 0;           // next event: S side, P.V side
         int nq = 0, q_at = 0;                         // Q tiles before the next piece's, this one's
-        int reads = 0, ahead = 0;                     // S events issued; of them before P.V
-        int js = -1, piece = 0, js_piece = -1;        // the last S event's tile; where pieces begin
-        unsigned rs = 0, rp = 0;                      // the tiles' records
-        unsigned phase = 0, fresh = 3;                // bit x: of p_full[x]; O_x is to be overwritten
-        // One step of the S side: an event, or a query tile that does not take the key tile
-        auto step_s = [&]() -> bool {
-          const int pr = ns % C::kPairs;
-          if (xs == 0) {
-            if (!warp_wait(smem_u32(&bars->full[2 * pr]), (uint32_t)((ns / C::kPairs) & 1))) return false;
-            rs = (unsigned)uniform((int)bars->rec[ns % 8]);
-            if (rs & kFirst) {
-              piece = ns;
-              q_at = nq;
-              nq += (rs & kHasB) ? 2 : 1;
-            }
+        int events = 0;
+        for (int nt = 0; ok && nt < count; ++nt) {
+          const int pr = nt % C::kPairs;
+          ok = warp_wait(smem_u32(&bars->full[2 * pr]), (uint32_t)((nt / C::kPairs) & 1));
+          if (!ok) break;
+          const unsigned rec = (unsigned)uniform((int)bars->rec[nt % 8]);
+          const int tiles = (rec & kHasB) ? 2 : 1;
+          if (rec & kFirst) {
+            q_at = nq;
+            nq += tiles;
           }
-          const int slot = (q_at + xs) % C::kQSlots;
-          if ((rs & kFirst) && (xs == 0 || (rs & kHasB)) &&
-              !warp_wait(smem_u32(&bars->q_full[slot]), (uint32_t)(((q_at + xs) / C::kQSlots) & 1)))
-            return false;
-          const unsigned halves = (rs >> (2 * xs)) & 3u;
-          if (halves) {
-            if (reads > 0 && !warp_wait(smem_u32(&bars->s_read), (uint32_t)((reads - 1) & 1)))
-              return false;
-            tc_fence_after();
-            const int h = halves == 2u ? 1 : 0;       // the first half it takes
-            const uint64_t a = sw128_desc(smem_u32(smem + slot * C::kTile), 1024, 16);
-            const uint64_t b = kd + (uint64_t)((2 * pr * C::kTile + h * kUnit * 128) >> 4);
-            const uint32_t idesc = halves == 3u ? C::kIdescS : C::kIdescHalf;
-            if (leader) {
+#pragma unroll 1
+          for (int x = 0; ok && x < tiles; ++x) {
+            const int slot = (q_at + x) % C::kQSlots;
+            if (rec & kFirst)
+              ok = warp_wait(smem_u32(&bars->q_full[slot]), (uint32_t)(((q_at + x) / C::kQSlots) & 1));
+            const unsigned halves = (rec >> (2 * x)) & 3u;
+            if (ok && halves) {
+              if (events > 0) ok = warp_wait(smem_u32(&bars->s_read), (uint32_t)((events - 1) & 1));
+              if (!ok) break;
+              ++events;
+              tc_fence_after();
+              const int h = halves == 2u ? 1 : 0;     // the first half it takes
+              const uint64_t a = qd + (uint64_t)((slot * C::kTile) >> 4);
+              const uint64_t b = kd + (uint64_t)((2 * pr * C::kTile + h * kUnit * 128) >> 4);
+              const uint32_t idesc = halves == 3u ? C::kIdescS : C::kIdescHalf;
+              if (leader) {
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint64_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-                mma_bf16_ss(tmem + kColS + h * kUnit, a + off, b + off, idesc, k != 0);
+                for (int k = 0; k < D / 16; ++k) {
+                  const uint64_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+                  mma_bf16_ss(tmem + kColS + h * kUnit, a + off, b + off, idesc, k != 0);
+                }
+                mma_commit(smem_u32(&bars->s_full[x]));
               }
-              mma_commit(smem_u32(&bars->s_full[xs]));
             }
-            ++reads;
-            ++ahead;
-            js = ns;
-            js_piece = piece;
+            if (ok && (rec & kLast) && leader) mma_commit(smem_u32(&bars->q_empty[slot]));
           }
-          if ((rs & kLast) && (xs == 0 || (rs & kHasB)) && leader) mma_commit(smem_u32(&bars->q_empty[slot]));
-          if (xs == 1) {
-            if (leader) mma_commit(smem_u32(&bars->empty[2 * pr]));
-            ++ns;
+          if (ok && leader) mma_commit(smem_u32(&bars->empty[2 * pr]));
+          if (*abort_flag) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
+        }
+      } else {
+        const uint64_t vd = sw128_desc(smem_u32(ring + C::kTile), 1024, kHalf);
+        unsigned phase = 0, fresh = 3;                // bit x: of p_full[x]; O_x is to be overwritten
+        for (int nt = 0; ok && nt < count; ++nt) {
+          const int pr = nt % C::kPairs;
+          ok = warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((nt / C::kPairs) & 1));
+          if (!ok) break;
+          const unsigned rec = (unsigned)uniform((int)bars->rec[nt % 8]);
+          if (rec & kFirst) fresh = 3u;
+          // values that are not finite are in O before the first product
+          unsigned bad = 0;
+          if (kPaged || (rec & (3u * kPartly))) {
+            const unsigned* b = bars->bad[pr];
+            bad = (unsigned)uniform(((b[0] | b[1]) ? 1 : 0) | ((b[2] | b[3]) ? 2 : 0));
           }
-          xs ^= 1;
-          return true;
-        };
-        auto step_pv = [&]() -> bool {
-          const int pr = np % C::kPairs, x = xp;
-          if (x == 0) {
-            if (!warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((np / C::kPairs) & 1))) return false;
-            rp = (unsigned)uniform((int)bars->rec[np % 8]);
-            if (rp & kFirst) fresh = 3u;
-          }
-          const unsigned halves = (rp >> (2 * x)) & 3u;
-          if (halves) {
-            if (!warp_wait(smem_u32(&bars->p_full[x]), (phase >> x) & 1u)) return false;
+          const uint64_t b = vd + (uint64_t)((2 * pr * C::kTile) >> 4);
+#pragma unroll 1
+          for (int x = 0; ok && x < 2; ++x) {
+            const unsigned halves = (rec >> (2 * x)) & 3u;
+            if (!halves) continue;
+            ok = warp_wait(smem_u32(&bars->p_full[x]), (phase >> x) & 1u);
+            if (!ok) break;
             tc_fence_after();
-            // values that are not finite are in O before the first product
-            bool onto = !((fresh >> x) & 1u);
-            if (kPaged || (rp & (3u * kPartly))) {
-              const unsigned* b = bars->bad[pr];
-              onto = onto || uniform(((halves & 1u) && (b[0] | b[1])) || ((halves & 2u) && (b[2] | b[3])));
-            }
-            const uint64_t b = vd + (uint64_t)((2 * pr * C::kTile) >> 4);
+            bool onto = !((fresh >> x) & 1u) || (halves & bad) != 0u;
             if (leader) {
 #pragma unroll
               for (int k = 0; k < BK / 16; ++k) {
@@ -459,37 +458,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fresh &= ~(1u << x);
             phase ^= 1u << x;
-            --ahead;
           }
-          if (x == 1) {
-            if (leader) mma_commit(smem_u32(&bars->empty[2 * pr + 1]));
-            ++np;
-          }
-          xp ^= 1;
-          return true;
-        };
-        while (ok && np < count) {
-          // What the S side waits for comes without anything that the P.V side has yet to
-          // do: K of its tile (no further than two tiles ahead), and that the last event's
-          // scores are read, which waits for that tile's V to be looked over (so V has its
-          // stage) and, at the beginning of a piece, for the last piece's O.
-          while (ok && ahead < 3 && ns < count && ns <= np + 2 && js <= np + 1 && js_piece <= np)
-            ok = step_s();
-          ok = ok && step_pv();
+          if (ok && leader) mma_commit(smem_u32(&bars->empty[2 * pr + 1]));
           if (*abort_flag) ok = false;
           ok = __all_sync(0xffffffffu, ok);
         }
-        if (!ok) {
-          raise_error(p.err, kDevErrTimeout);
-          *abort_flag = 1;
-        }
-        // nothing may still run on the tensor core when memory is released
-        if (leader) mma_commit(smem_u32(&bars->drain));
-        (void)mbar_wait(smem_u32(&bars->drain), 0, 1000000000ull);
       }
+      if (!ok) {
+        raise_error(p.err, kDevErrTimeout);
+        *abort_flag = 1;
+      }
+      // nothing may still run on the tensor core when memory is released
+      if (leader) mma_commit(smem_u32(&bars->drain[warp - 1]));
+      (void)mbar_wait(smem_u32(&bars->drain[warp - 1]), 0, 1000000000ull);
     } else {
-      // ---------------------------------------------------------- guard of half h
-      const int h = warp - 2;
+      // ---------------------------------------------------------- guard
       const int count = (int)(x1 - x0);
       // an exponent of ones carries into the sign's place
       auto ones = [](const uint4& w) {
@@ -503,32 +486,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const unsigned rec = bars->rec[nt % 8];
         const unsigned pages = kPaged ? (rec >> kPages) & 0xFFu : 0xFFu;
-        unsigned bad[2] = {0u, 0u};
-        if (((rec >> h) & kPartly) || pages != 0xFFu) {
-          uint4* v = reinterpret_cast<uint4*>(ring + (2 * pr + 1) * C::kTile) + h * (kUnit * 8);
-          unsigned seen = 0;
-#pragma unroll
-          for (int i = 0; i < D / 64; ++i)            // 64 rows of 128 bytes
-#pragma unroll 8
-            for (int k = lane; k < kUnit * 8; k += 32) seen |= ones(v[i * (kHalf / 16) + k]);
-          if (__any_sync(0xffffffffu, (seen & 0x80008000u) != 0u)) {
 #pragma unroll 1
-            for (int r = 0; r < kUnit; ++r) {         // which rows; they become zeros
-              uint4* at = v + (lane >> 3) * (kHalf / 16) + r * 8 + (lane & 7);
-              const bool hit = lane < D / 8 && (ones(*at) & 0x80008000u) != 0u;
-              if (!__any_sync(0xffffffffu, hit)) continue;
-              bad[0] |= r < 32 ? 1u << r : 0u;
-              bad[1] |= r >= 32 ? 1u << (r & 31) : 0u;
-              if (lane < D / 8) *at = make_uint4(0u, 0u, 0u, 0u);
+        for (int h = 0; h < 2; ++h) {
+          unsigned bad[2] = {0u, 0u};
+          if (((rec >> h) & kPartly) || pages != 0xFFu) {
+            uint4* v = reinterpret_cast<uint4*>(ring + (2 * pr + 1) * C::kTile) + h * (kUnit * 8);
+            unsigned seen = 0;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)          // 64 rows of 128 bytes
+#pragma unroll 8
+              for (int k = lane; k < kUnit * 8; k += 32) seen |= ones(v[i * (kHalf / 16) + k]);
+            if (__any_sync(0xffffffffu, (seen & 0x80008000u) != 0u)) {
+#pragma unroll 1
+              for (int r = 0; r < kUnit; ++r) {       // which rows; they become zeros
+                uint4* at = v + (lane >> 3) * (kHalf / 16) + r * 8 + (lane & 7);
+                const bool hit = lane < D / 8 && (ones(*at) & 0x80008000u) != 0u;
+                if (!__any_sync(0xffffffffu, hit)) continue;
+                bad[0] |= r < 32 ? 1u << r : 0u;
+                bad[1] |= r >= 32 ? 1u << (r & 31) : 0u;
+                if (lane < D / 8) *at = make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
             }
-            fence_proxy_async_smem();
+          }
+          if (lane == 0) {
+            bars->bad[pr][2 * h] = bad[0];
+            bars->bad[pr][2 * h + 1] = bad[1];
           }
         }
         __syncwarp();
         if (lane == 0) {
-          bars->bad[pr][2 * h] = bad[0];
-          bars->bad[pr][2 * h + 1] = bad[1];
-          if (h == 0) bars->there[pr] = pages;
+          bars->there[pr] = pages;
           mbar_arrive(smem_u32(&bars->v_ok[pr]));
         }
         if (*abort_flag) ok = false;
