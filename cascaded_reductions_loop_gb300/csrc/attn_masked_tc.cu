@@ -155,6 +155,7 @@ enum : unsigned {
   kLast = 32u,
   kHasB = 64u,              // the piece has a tile b
   kPartly = 128u,           // << h: some row may not read all keys of half h
+  kEnd = 512u,              // of the CTA's range
   kPages = 16,              // over a cache, from this bit on: bit per 16 keys that are there
 };
 
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g_lo = min((int)threadIdx.x * per, ng), g_hi = min(g_lo + per, ng);
   int64_t mine = 0;
   for (int g = g_lo; g < g_hi; ++g)
-    mine += (int64_t)group_of(geo, g, cta == 0, p.err).n * geo.Hkv;
+    mine += (int64_t)places(geo, group_of(geo, g, cta == 0, p.err)) * geo.Hkv;
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -237,16 +238,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (x >= pre && x - pre < mine) {        // in this thread's groups: walk to it
         int64_t at = pre;
         for (int g = g_lo; g < g_hi; ++g) {
-          const int n = group_of(geo, g, false, p.err).n;
+          const Group w = group_of(geo, g, false, p.err);
+          const int n = places(geo, w);
           const int64_t all = (int64_t)n * geo.Hkv;
           if (x - at < all) {
             const int h = (int)((x - at) / n), off = (int)((x - at) % n);
-            const int j = kPaged ? off : snap(off, n);
-            bars->x[i] = x - off + j;
+            const bool up = !kPaged && snaps_up(off, n);
+            bars->x[i] = kPaged ? x : x - off + (up ? n : 0);
             if (i == 0) {
               bars->g = g;
               bars->h = h;
-              bars->j = j;
+              bars->j = kPaged ? off : (up ? w.n : 0);
             }
             break;
           }
@@ -298,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           unsigned rec = (ta.takes(2 * j) ? 1u : 0u) | (ta.takes(2 * j + 1) ? 2u : 0u) |
                          (tb.takes(2 * j) ? 4u : 0u) | (tb.takes(2 * j + 1) ? 8u : 0u) |
                          (j == c.j0 ? kFirst : 0u) | (j == c.j1 - 1 ? kLast : 0u) |
+                         (j == c.j1 - 1 && walk.left <= 0 ? kEnd : 0u) |
                          (tb.has() ? kHasB : 0u) | (whole.partly(geo, key0, kUnit) ? kPartly : 0u) |
                          (whole.partly(geo, key0 + kUnit, kUnit) ? kPartly << 1 : 0u);
           const int st = 2 * (nt % C::kPairs);
@@ -375,18 +378,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- MMA: S (warp 1), P.V (warp 2)
       // The whole warp runs the schedule, one lane issues: with the schedule in one lane an
       // MMA took 100 clocks to issue (its operands went through vector registers).
-      const int count = uniform((int)(x1 - x0));
+      bool more = x1 > x0;
       const bool leader = elect_one();
       if (warp == 1) {
         const uint64_t qd = sw128_desc(smem_u32(smem), 1024, 16);
         const uint64_t kd = sw128_desc(smem_u32(ring), 1024, 16);
         int nq = 0, q_at = 0;                         // Q tiles before the next piece's, this one's
         int events = 0;
-        for (int nt = 0; ok && nt < count; ++nt) {
+        for (int nt = 0; ok && more; ++nt) {
           const int pr = nt % C::kPairs;
           ok = warp_wait(smem_u32(&bars->full[2 * pr]), (uint32_t)((nt / C::kPairs) & 1));
           if (!ok) break;
           const unsigned rec = (unsigned)uniform((int)bars->rec[nt % 8]);
+          more = !(rec & kEnd);
           const int tiles = (rec & kHasB) ? 2 : 1;
           if (rec & kFirst) {
             q_at = nq;
@@ -425,11 +429,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const uint64_t vd = sw128_desc(smem_u32(ring + C::kTile), 1024, kHalf);
         unsigned phase = 0, fresh = 3;                // bit x: of p_full[x]; O_x is to be overwritten
-        for (int nt = 0; ok && nt < count; ++nt) {
+        for (int nt = 0; ok && more; ++nt) {
           const int pr = nt % C::kPairs;
           ok = warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((nt / C::kPairs) & 1));
           if (!ok) break;
           const unsigned rec = (unsigned)uniform((int)bars->rec[nt % 8]);
+          more = !(rec & kEnd);
           if (rec & kFirst) fresh = 3u;
           // values that are not finite are in O before the first product
           unsigned bad = 0;
@@ -473,18 +478,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       (void)mbar_wait(smem_u32(&bars->drain[warp - 1]), 0, 1000000000ull);
     } else {
       // ---------------------------------------------------------- guard
-      const int count = (int)(x1 - x0);
+      bool more = x1 > x0;
       // an exponent of ones carries into the sign's place
       auto ones = [](const uint4& w) {
         return ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
                ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
       };
-      for (int nt = 0; ok && nt < count; ++nt) {
+      for (int nt = 0; ok && more; ++nt) {
         const int pr = nt % C::kPairs;
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->full[2 * pr + 1]),
                                                (uint32_t)((nt / C::kPairs) & 1)));
         if (!ok) break;
         const unsigned rec = bars->rec[nt % 8];
+        more = !(rec & kEnd);
         const unsigned pages = kPaged ? (rec >> kPages) & 0xFFu : 0xFFu;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -603,9 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       ((pages >> (2 * q + 1)) & 1u ? 0xFFFF0000u : 0u);
           }
         }
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(smem_u32(&bars->s_full[x]), (uint32_t)(cnt & 1)) && !*abort_flag))
-          return false;
+        if (!warp_wait(smem_u32(&bars->s_full[x]), (uint32_t)(cnt & 1))) return false;
         tc_fence_after();
         uint32_t v[4][32];
 #pragma unroll
@@ -650,25 +654,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_run *= alpha;
           m_ref = mt;
         }
+        const bool move = !fresh && __any_sync(0xffffffffu, alpha != 1.f);
         // P_x may be overwritten and O_x is complete once the last event's P.V is done
-        if (cnt > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->pv_done[x]),
-                                                          (uint32_t)((cnt - 1) & 1))))
-          return false;
-        tc_fence_after();
-        if (!fresh && __any_sync(0xffffffffu, alpha != 1.f)) {
+        auto settle = [&]() -> bool {
+          if (cnt > 0 && !warp_wait(smem_u32(&bars->pv_done[x]), (uint32_t)((cnt - 1) & 1))) return false;
+          tc_fence_after();
+          if (move) {
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32(o_addr + q * 32, o);
-            tmem_ld_wait();
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32(o_addr + q * 32, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(o_addr + q * 32, o);
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(o_addr + q * 32, o);
+            }
           }
-        }
+          return true;
+        };
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
         if (any_bad) {
           // values that are not finite, for the rows that read them
+          if (!settle()) return false;
           tmem_st_wait();
           if (fresh) {
             uint32_t z[32];
@@ -717,6 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars->s_read));
         }
+        if (!any_bad && !settle()) return false;
         // P = 2^(S c - m) as bf16 pairs, and its row sum (four chains)
         const uint64_t negm2 = f2(-m_use, -m_use);
         uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
@@ -749,28 +757,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       const Whole whole = whole_of(geo, c.w);
+      // tiles whose keys every row reads: window tiles from `begin` to `end`
+      const int over = c.w.start - c.w.lead * BK;     // key0 of window tile j is over + j * BK
+      const int full0 = max(c.w.lead, (max(whole.begin, c.w.start) - over + BK - 1) / BK);
+      const int full1 = (max(whole.end, over) - over) / BK;
 #pragma unroll 1
       for (int j = c.j0; j < c.j1; ++j) {
-        const unsigned halves = (t.takes(2 * j) ? 1u : 0u) | (t.takes(2 * j + 1) ? 2u : 0u);
-        if (!halves) continue;
-        const int key0 = key0_of(c.w, j), pr = (j_base + j) % C::kPairs;
-        unsigned part = (whole.partly(geo, key0, kUnit) ? 1u : 0u) |
-                        (whole.partly(geo, key0 + kUnit, kUnit) ? 2u : 0u);
+        const int pr = (j_base + j) % C::kPairs;
         unsigned pages = 0xFFu;
-        if (kPaged || part) {
-          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->v_ok[pr]),
-                                                 (uint32_t)(((j_base + j) / C::kPairs) & 1)))) {
+        bool fast = j >= full0 && j < full1;
+        if (kPaged) {
+          if (!warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)(((j_base + j) / C::kPairs) & 1))) {
             ok = false;
             break;
           }
-          if (kPaged) pages = bars->there[pr];
+          pages = bars->there[pr];
+          fast = fast && pages == 0xFFu;
+        }
+        int key0 = 0;
+        unsigned halves = 3u, part = 0u;
+        if (!fast) {
+          halves = (t.takes(2 * j) ? 1u : 0u) | (t.takes(2 * j + 1) ? 2u : 0u);
+          if (!halves) continue;
+          key0 = key0_of(c.w, j);
+          part = (whole.partly(geo, key0, kUnit) ? 1u : 0u) |
+                 (whole.partly(geo, key0 + kUnit, kUnit) ? 2u : 0u);
+          if (!kPaged && part &&
+              !warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)(((j_base + j) / C::kPairs) & 1))) {
+            ok = false;
+            break;
+          }
           if (pages != 0xFFu) part = 3u;
         }
-        if (!event(key0, pr, halves, part, pages)) {
-          ok = false;
-          break;
-        }
+        ok = event(key0, pr, halves, part, pages);
+        if (!ok) break;
       }
+      if (*abort_flag) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       // the piece's last product (a tile may have no unit in it)
       if (cnt > cnt0 &&
@@ -1045,7 +1068,7 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
   const int ng = p.B * p.npairs;
   std::vector<int64_t> pre((size_t)ng + 1, 0);
   for (int g = 0; g < ng; ++g)
-    pre[(size_t)g + 1] = pre[(size_t)g] + (int64_t)group_of(p, g, true, &err).n * Hkv;
+    pre[(size_t)g + 1] = pre[(size_t)g] + (int64_t)places(p, group_of(p, g, true, &err)) * Hkv;
   const int64_t total = pre[(size_t)ng];
   if (err & kDevErrBounds) return 1;
   const int grid = total < sms ? (int)total : sms;
@@ -1077,7 +1100,7 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
     if (rows[(size_t)b] != want_rows[(size_t)b]) return 5;
   if (total == 0) return 0;
   const Split64 split(total, grid);
-  int64_t x = 0;
+  int64_t at = 0;                                     // where the last range ended
   int wg = -1, wh = Hkv - 1, wj = 0, wn = 0;          // the next tile in the order of all
   std::vector<unsigned char> used((size_t)2 * sms, 0);
   std::vector<int64_t> parts;                         // of the item being cut
@@ -1089,26 +1112,28 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
       if (r[i] >= total) continue;
       int g = 0;
       while (pre[(size_t)g + 1] <= r[i]) ++g;
-      const int n = group_of(p, g, false, &err).n;
+      const Group w = group_of(p, g, false, &err);
+      const int n = places(p, w);
       const int h = (int)((r[i] - pre[(size_t)g]) / n), off = (int)((r[i] - pre[(size_t)g]) % n);
-      const int j = seq_lens ? off : snap(off, n);
-      r[i] += j - off;
+      const bool up = !seq_lens && snaps_up(off, n);
+      if (!seq_lens) r[i] += (up ? n : 0) - off;
       if (i == 0) {
         start[0] = g;
         start[1] = h;
-        start[2] = j;
+        start[2] = seq_lens ? off : (up ? w.n : 0);
       }
     }
-    if (r[0] != x || r[1] < r[0]) return 2;
+    if (r[0] != at || r[1] < r[0]) return 2;
+    at = r[1];
     Walk walk(start[0], start[1], start[2], r[1] - r[0]);
     Piece pc;
     int cuts = 0;
-    int64_t s0 = x - (r[1] > r[0] ? start[2] : 0);
+    int64_t s0 = r[0] - (r[1] > r[0] ? start[2] : 0);
     while (walk.next(p, pc, &err)) {
       if (err & kDevErrBounds) return 1;
       const int64_t item0 = s0;
       s0 += pc.w.n;
-      for (int j = pc.j0; j < pc.j1; ++j, ++x) {
+      for (int j = pc.j0; j < pc.j1; ++j) {
         if (wj == wn) {                               // on to the next item
           wj = 0;
           if (++wh == Hkv) {
@@ -1139,7 +1164,10 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
       }
     }
   }
-  return x == total && wj == wn ? 0 : 2;
+  if (at != total || wj != wn || wh != Hkv - 1) return 2;
+  for (++wg; wg < ng; ++wg)
+    if (pre[(size_t)wg + 1] != pre[(size_t)wg]) return 2;
+  return 0;
 }
 
 }  // namespace rf

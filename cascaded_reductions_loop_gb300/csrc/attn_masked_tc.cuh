@@ -15,8 +15,10 @@
 //
 // Partition.  The key tiles of all items, end to end in the order (sequence, pair,
 // head), are cut into one equal range per CTA.  Prompts take whole items (the border
-// next to the cut); over a cache, where few items may have many tiles, an item is
-// cut, the states of its pieces go to the workspace and a second kernel merges them.
+// next to the cut), and an item counts as its tiles and kItemCost more, since what
+// surrounds them (queries, first scores, output) takes that long; over a cache, where
+// few items may have many tiles, an item is cut, the states of its pieces go to the
+// workspace and a second kernel merges them.
 #pragma once
 
 #include "rf_device.cuh"
@@ -26,6 +28,7 @@ namespace rf {
 namespace masked {
 
 constexpr int BQ = 128, BK = 128;
+constexpr int kItemCost = 2;
 
 struct Geo {
   const int* seq_lens;      // paged: [B] tokens of each sequence; else null
@@ -37,6 +40,9 @@ struct Geo {
   int total_q, total_k;     // packed
   int max_len;              // paged
   int window, sinks, tree;
+  // What an item counts as beside its tiles (16k prompt 1235 -> 826 us: the first items
+  // have few tiles; 2, 3 and 4 within 1 %).
+  __host__ __device__ __forceinline__ int extra() const { return seq_lens ? 0 : kItemCost; }
 };
 
 __host__ __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
@@ -125,6 +131,11 @@ __host__ __device__ __forceinline__ int key0_of(const Group& w, int j) {
   return j < w.lead ? j * BK : w.start + (j - w.lead) * BK;
 }
 
+// What an item of the group counts as (0: it has no rows).
+__host__ __device__ __forceinline__ int places(const Geo& p, const Group& w) {
+  return w.n > 0 ? w.n + p.extra() : 0;
+}
+
 // T tiles over n ranges, the first T % n of them one longer.
 struct Split64 {
   int64_t q, rem;
@@ -138,18 +149,19 @@ struct Split64 {
   }
 };
 
-// Where whole items are taken: the border next to tile `off` of an item of n.
-__host__ __device__ __forceinline__ int snap(int off, int n) { return 2 * off < n ? 0 : n; }
+// Where whole items are taken: the border next to place `off` of an item that counts
+// as `all`; its tile there.
+__host__ __device__ __forceinline__ bool snaps_up(int off, int all) { return 2 * off >= all; }
 
-// A CTA's range of tiles, piece by piece.
+// A CTA's range, piece by piece.
 struct Piece {
   Group w;
   int h, j0, j1;            // tiles j0 .. j1 - 1 of the item
   __host__ __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == w.n; }
 };
 struct Walk {
-  int64_t left;             // tiles still to take
-  int g, h, j;              // the next one; j may be behind the item's last: the next item's
+  int64_t left;             // what is still to take, as items count
+  int g, h, j;              // the next tile; j may be behind the item's last: the next item's
   __host__ __device__ __forceinline__ Walk(int g_, int h_, int j_, int64_t count)
       : left(count), g(g_), h(h_), j(j_) {}
   __host__ __device__ __forceinline__ bool next(const Geo& p, Piece& out, unsigned* err) {
@@ -166,9 +178,10 @@ struct Walk {
         }
       }
     }
+    left -= p.extra();
     out.h = h;
     out.j0 = j;
-    out.j1 = (int64_t)(out.w.n - j) < left ? out.w.n : j + (int)left;
+    out.j1 = p.extra() || (int64_t)(out.w.n - j) < left ? out.w.n : j + (int)left;
     left -= out.j1 - out.j0;
     j = out.j1;
     return true;
