@@ -90,7 +90,7 @@ struct Params {
 struct Bars {
   uint64_t q_full[4], q_empty[4];
   uint64_t full[8], empty[8];
-  uint64_t v_ok[4];                                   // a V tile is looked over
+  uint64_t v_ok[4], pages_ok[4];                      // a V tile is looked over; `there` is set
   uint64_t s_full[2], p_full[2], pv_done[2];          // of a query tile's events
   uint64_t s_read;                                    // of all events: S is in registers
   uint64_t drain[2];
@@ -156,6 +156,7 @@ enum : unsigned {
   kHasB = 64u,              // the piece has a tile b
   kPartly = 128u,           // << h: some row may not read all keys of half h
   kEnd = 512u,              // of the CTA's range
+  kYield = 1024u,           // P.V lets S go first (see there)
   kPages = 16,              // over a cache, from this bit on: bit per 16 keys that are there
 };
 
@@ -183,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars->q_full[i]), 1);
       mbar_init(smem_u32(&bars->q_empty[i]), 1);
       mbar_init(smem_u32(&bars->v_ok[i]), 1);
+      mbar_init(smem_u32(&bars->pages_ok[i]), 1);
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&bars->full[i]), 1);
@@ -303,6 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                          (j == c.j1 - 1 && walk.left <= 0 ? kEnd : 0u) |
                          (tb.has() ? kHasB : 0u) | (whole.partly(geo, key0, kUnit) ? kPartly : 0u) |
                          (whole.partly(geo, key0 + kUnit, kUnit) ? kPartly << 1 : 0u);
+          auto both = [&](int i) {                    // query tiles take key tile i
+            return i < c.j1 && (ta.takes(2 * i) || ta.takes(2 * i + 1)) &&
+                   (tb.takes(2 * i) || tb.takes(2 * i + 1));
+          };
+          if (both(j) && both(j + 1)) rec |= kYield;
           const int st = 2 * (nt % C::kPairs);
           const uint32_t ph = (uint32_t)((nt / C::kPairs - 1) & 1);
           // over a cache: lane i has the tile's page i
@@ -429,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const uint64_t vd = sw128_desc(smem_u32(ring + C::kTile), 1024, kHalf);
         unsigned phase = 0, fresh = 3;                // bit x: of p_full[x]; O_x is to be overwritten
+        constexpr int kPolls = 24;
         for (int nt = 0; ok && more; ++nt) {
           const int pr = nt % C::kPairs;
           ok = warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((nt / C::kPairs) & 1));
@@ -449,6 +457,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!halves) continue;
             ok = warp_wait(smem_u32(&bars->p_full[x]), (phase >> x) & 1u);
             if (!ok) break;
+            // The S product that the same warpgroup will read next runs about now, and is
+            // waited for; P is not, before that warpgroup's next one.  So this product lets
+            // it end first (3670 -> 3000 clocks for a key tile of both): an order that
+            // nothing relies on, looked for kPolls times (some 800 clocks) and no longer.
+            if (rec & kYield) {
+              const uint32_t next = smem_u32(&bars->s_full[x]);
+              for (int i = 0; i < kPolls; ++i)
+                if (__any_sync(0xffffffffu, mbar_test_wait(next, ((phase >> x) & 1u) ^ 1u))) break;
+            }
             tc_fence_after();
             bool onto = !((fresh >> x) & 1u) || (halves & bad) != 0u;
             if (leader) {
@@ -492,6 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned rec = bars->rec[nt % 8];
         more = !(rec & kEnd);
         const unsigned pages = kPaged ? (rec >> kPages) & 0xFFu : 0xFFu;
+        if (kPaged && lane == 0) {
+          bars->there[pr] = pages;
+          mbar_arrive(smem_u32(&bars->pages_ok[pr]));
+        }
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           unsigned bad[2] = {0u, 0u};
@@ -522,7 +543,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) {
-          bars->there[pr] = pages;
           mbar_arrive(smem_u32(&bars->v_ok[pr]));
         }
         if (*abort_flag) ok = false;
@@ -575,9 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cnt0 = cnt;
       // one event: halves (bits) of the key tile at key0, in V stage pr; part: of which
       // halves some row may not read all keys
-      auto event = [&](int key0, int pr, unsigned halves, unsigned part, unsigned pages) -> bool {
+      auto event = [&](int key0, int tile, unsigned halves, unsigned part, unsigned pages) -> bool {
         unsigned w[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};   // keys it reads
-        bool any_bad = false;
         if (part) {
           const int hi = geo.tree ? min(ctx, pos + 1) : pos + 1;
 #pragma unroll
@@ -586,7 +605,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[q] = below(hi - k);
             if (geo.window > 0) w[q] &= ~below(pos - geo.window + 1 - k) | below(geo.sinks - k);
             if (pos < 0) w[q] = 0u;
-            if ((halves >> (q / 2)) & 1u) any_bad |= bars->bad[pr][q] != 0u;
           }
           if (geo.tree && key0 + BK > ctx && pos >= 0) {
             int u = tok;
@@ -619,11 +637,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(s_addr + 64 * h + 32, v[2 * h + 1]);
           }
         tmem_ld_wait();
-        if (!any_bad) {                               // S may be overwritten
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->s_read));
-        }
+        tc_fence_before();                            // S may be overwritten
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->s_read));
         // row maximum (chains of their own)
         float mh[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -673,58 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        if (any_bad) {
-          // values that are not finite, for the rows that read them
-          if (!settle()) return false;
-          tmem_st_wait();
-          if (fresh) {
-            uint32_t z[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = 0u;
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) tmem_st32(o_addr + q * 32, z);
-            tmem_st_wait();
-          }
-#pragma unroll 1
-          for (int k = 0; k < BK; ++k) {
-            if (!((halves >> (k >> 6)) & 1u) || !((bars->bad[pr][k >> 5] >> (k & 31)) & 1u)) continue;
-            const unsigned rw = k < 32 ? w[0] : (k < 64 ? w[1] : (k < 96 ? w[2] : w[3]));
-            const bool reads = (rw >> (k & 31)) & 1u;
-            const float pk = ex2(fmaf(__uint_as_float(tmem_ld1(s_addr + k)), p.c_log2, -m_use));
-            int64_t at;                               // the value's first element
-            bool inside;
-            if (kPaged) {
-              const int page = key0 + k < c.w.lk
-                                   ? ld_int(p.block_table,
-                                            (int64_t)c.w.b * p.max_pages + ((key0 + k) >> p.page_shift),
-                                            (int64_t)geo.B * p.max_pages, p.err)
-                                   : -1;
-              at = (((int64_t)page * geo.Hkv + c.h) * p.page_size + ((key0 + k) & (p.page_size - 1))) * D;
-              inside = (unsigned)page < (unsigned)p.num_pages;
-            } else {
-              at = (int64_t)(c.w.k0 + key0 + k) * p.ldv + (int64_t)c.h * D;
-              inside = key0 + k < c.w.lk;
-            }
-#pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld32(o_addr + q * 32, o);
-              tmem_ld_wait();
-              if (reads && inside && RF_IN(p.err, at + D - 1, p.n_v))
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  o[i] = __float_as_uint(fmaf(pk, __bfloat162float(p.V[at + q * 32 + i]),
-                                              __uint_as_float(o[i])));
-              __syncwarp();
-              tmem_st32(o_addr + q * 32, o);
-              tmem_st_wait();
-            }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->s_read));
-        }
-        if (!any_bad && !settle()) return false;
+        if (!settle()) return false;
         // P = 2^(S c - m) as bf16 pairs, and its row sum (four chains)
         const uint64_t negm2 = f2(-m_use, -m_use);
         uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
@@ -751,6 +716,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         f2_split(fadd2(fadd2(sum4[0], sum4[1]), fadd2(sum4[2], sum4[3])), s_lo, s_hi);
         l_run += s_lo + s_hi;
         tmem_st_wait();
+        if (part) {
+          const int pr = tile % C::kPairs;
+          if (!warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((tile / C::kPairs) & 1))) return false;
+          const unsigned* bad = bars->bad[pr];
+          if (((halves & 1u) && (bad[0] | bad[1])) || ((halves & 2u) && (bad[2] | bad[3]))) {
+            // values that are not finite, for the rows that read them: P times value
+            if (fresh) {
+              uint32_t z[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) z[i] = 0u;
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) tmem_st32(o_addr + q * 32, z);
+              tmem_st_wait();
+            }
+#pragma unroll 1
+            for (int k = 0; k < BK; ++k) {
+              if (!((halves >> (k >> 6)) & 1u) || !((bad[k >> 5] >> (k & 31)) & 1u)) continue;
+              const unsigned rw = k < 32 ? w[0] : (k < 64 ? w[1] : (k < 96 ? w[2] : w[3]));
+              const bool reads = (rw >> (k & 31)) & 1u;
+              const uint32_t two = tmem_ld1(p_addr + k / 2);
+              const float pk = (k & 1) ? bf16hi(two) : bf16lo(two);
+              int64_t at;                             // the value's first element
+              bool inside;
+              if (kPaged) {
+                const int page = key0 + k < c.w.lk
+                                     ? ld_int(p.block_table,
+                                              (int64_t)c.w.b * p.max_pages + ((key0 + k) >> p.page_shift),
+                                              (int64_t)geo.B * p.max_pages, p.err)
+                                     : -1;
+                at = (((int64_t)page * geo.Hkv + c.h) * p.page_size + ((key0 + k) & (p.page_size - 1))) * D;
+                inside = (unsigned)page < (unsigned)p.num_pages;
+              } else {
+                at = (int64_t)(c.w.k0 + key0 + k) * p.ldv + (int64_t)c.h * D;
+                inside = key0 + k < c.w.lk;
+              }
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                tmem_ld32(o_addr + q * 32, o);
+                tmem_ld_wait();
+                if (reads && inside && RF_IN(p.err, at + D - 1, p.n_v))
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    o[i] = __float_as_uint(fmaf(pk, __bfloat162float(p.V[at + q * 32 + i]),
+                                                __uint_as_float(o[i])));
+                __syncwarp();
+                tmem_st32(o_addr + q * 32, o);
+                tmem_st_wait();
+              }
+            }
+          }
+        }
         tc_fence_before();
         mbar_arrive(smem_u32(&bars->p_full[x]));
         ++cnt;
@@ -763,11 +780,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int full1 = (max(whole.end, over) - over) / BK;
 #pragma unroll 1
       for (int j = c.j0; j < c.j1; ++j) {
-        const int pr = (j_base + j) % C::kPairs;
         unsigned pages = 0xFFu;
         bool fast = j >= full0 && j < full1;
         if (kPaged) {
-          if (!warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)(((j_base + j) / C::kPairs) & 1))) {
+          const int pr = (j_base + j) % C::kPairs;
+          if (!warp_wait(smem_u32(&bars->pages_ok[pr]), (uint32_t)(((j_base + j) / C::kPairs) & 1))) {
             ok = false;
             break;
           }
@@ -782,14 +799,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           key0 = key0_of(c.w, j);
           part = (whole.partly(geo, key0, kUnit) ? 1u : 0u) |
                  (whole.partly(geo, key0 + kUnit, kUnit) ? 2u : 0u);
-          if (!kPaged && part &&
-              !warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)(((j_base + j) / C::kPairs) & 1))) {
-            ok = false;
-            break;
-          }
           if (pages != 0xFFu) part = 3u;
         }
-        ok = event(key0, pr, halves, part, pages);
+        ok = event(key0, j_base + j, halves, part, pages);
         if (!ok) break;
       }
       if (*abort_flag) ok = false;

@@ -28,7 +28,7 @@ namespace rf {
 namespace masked {
 
 constexpr int BQ = 128, BK = 128;
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 5;
 
 struct Geo {
   const int* seq_lens;      // paged: [B] tokens of each sequence; else null
@@ -40,8 +40,8 @@ struct Geo {
   int total_q, total_k;     // packed
   int max_len;              // paged
   int window, sinks, tree;
-  // What an item counts as beside its tiles (16k prompt 1235 -> 826 us: the first items
-  // have few tiles; 2, 3 and 4 within 1 %).
+  // What an item counts as beside its tiles (the first items of a long prompt have few;
+  // 16k prompt 910 us at 2, 785 at 4, 775 at 6).
   __host__ __device__ __forceinline__ int extra() const { return seq_lens ? 0 : kItemCost; }
 };
 
