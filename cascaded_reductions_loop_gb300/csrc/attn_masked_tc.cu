@@ -82,21 +82,22 @@ struct Params {
   float c_log2;
   float4* ws_o;                                       // [slots][2][D / 4][128]
   float2* ws_ml;                                      // [slots][2][128]
-  int4* ws_cut;                                       // [grid]: tile, group, head where a CTA's range
-                                                      // begins; of the first: all tiles, active CTAs
+  int4* ws_cut;                                       // [grid]: see the kernel
   unsigned* err;
 };
 
 struct Bars {
   uint64_t q_full[4], q_empty[4];
   uint64_t full[8], empty[8];
-  uint64_t v_ok[4], pages_ok[4];                      // a V tile is looked over; `there` is set
+  uint64_t v_ok[4];                                   // a V tile is looked over
+  uint64_t rec_ok[8];                                 // over a cache: rec is set, for the softmax
   uint64_t s_full[2], p_full[2], pv_done[2];          // of a query tile's events
   uint64_t s_read;                                    // of all events: S is in registers
   uint64_t drain[2];
-  unsigned rec[8];                                    // per key tile; K may be a round ahead of V
-  // what the guard found, per V stage: values that are not finite; rec's pages
-  unsigned bad[4][4], there[4];
+  // Per key tile.  That of tile m is written once V of tile m - 1 has a stage, so the P.V
+  // of tile m - 1 - kPairs is done and what was 8 tiles ago is not looked at any more.
+  unsigned rec[8];
+  unsigned bad[4][4];                                 // per V stage: values that are not finite
   int64_t warp_sum[kThreads / 32];
   int64_t x[2], total;                                // the CTA's range, all tiles
   int g, h, j;                                        // where it begins
@@ -184,10 +185,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars->q_full[i]), 1);
       mbar_init(smem_u32(&bars->q_empty[i]), 1);
       mbar_init(smem_u32(&bars->v_ok[i]), 1);
-      mbar_init(smem_u32(&bars->pages_ok[i]), 1);
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&bars->full[i]), 1);
+      mbar_init(smem_u32(&bars->rec_ok[i]), 1);
       mbar_init(smem_u32(&bars->empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -262,9 +263,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const uint32_t tmem = (uint32_t)uniform((int)bars->tmem);
   const int64_t x0 = bars->x[0], x1 = bars->x[1];
-  if (kPaged && threadIdx.x == 0 && RF_IN(p.err, cta, gridDim.x))
-    p.ws_cut[cta] = cta == 0 ? make_int4(0, (int)(total & 0x7FFFFFFF), (int)(total >> 31), grid)
-                             : make_int4(x1 > x0 ? bars->j : 0, bars->g, bars->h, 0);
+  if (kPaged && threadIdx.x == 0 && RF_IN(p.err, cta, gridDim.x)) {
+    // For the merge: the item in which this CTA's range begins, if that is its first cut:
+    // its pieces (0: it is not), group and head.
+    int pieces = 0;
+    if (x1 > x0 && bars->j > 0) {
+      const Split64 split(total, grid);
+      const int64_t first = x0 - bars->j;
+      if (split.start(cta - 1) <= first)
+        pieces = split.owner(first + group_of(geo, bars->g, false, p.err).n - 1) - (cta - 1) + 1;
+    }
+    p.ws_cut[cta] = make_int4(pieces, bars->g, bars->h, 0);
+  }
   Walk walk(bars->g, bars->h, bars->j, x1 - x0);
   Piece c;
   bool ok = true;
@@ -349,7 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const CUtensorMap* tm = v ? &tmV : &tmK;
             if (kPaged) {
               if (lane == 0) {
-                if (v == 0) bars->rec[nt % 8] = rec;
+                if (v == 0) {
+                  bars->rec[nt % 8] = rec;
+                  mbar_arrive(smem_u32(&bars->rec_ok[nt % 8]));
+                }
                 mbar_arrive_expect_tx(bar, (uint32_t)(__popc(pages) * p.page_size * D * 2));
               }
               __syncwarp();
@@ -509,10 +522,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned rec = bars->rec[nt % 8];
         more = !(rec & kEnd);
         const unsigned pages = kPaged ? (rec >> kPages) & 0xFFu : 0xFFu;
-        if (kPaged && lane == 0) {
-          bars->there[pr] = pages;
-          mbar_arrive(smem_u32(&bars->pages_ok[pr]));
-        }
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           unsigned bad[2] = {0u, 0u};
@@ -783,12 +792,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned pages = 0xFFu;
         bool fast = j >= full0 && j < full1;
         if (kPaged) {
-          const int pr = (j_base + j) % C::kPairs;
-          if (!warp_wait(smem_u32(&bars->pages_ok[pr]), (uint32_t)(((j_base + j) / C::kPairs) & 1))) {
+          const int tile = j_base + j;
+          if (!warp_wait(smem_u32(&bars->rec_ok[tile % 8]), (uint32_t)((tile / 8) & 1))) {
             ok = false;
             break;
           }
-          pages = bars->there[pr];
+          pages = (bars->rec[tile % 8] >> kPages) & 0xFFu;
           fast = fast && pages == 0xFFu;
         }
         int key0 = 0;
@@ -869,60 +878,65 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the states of the items that are cut between CTAs.  Block (c - 1, x, part) has
-// the item in which CTA c's range begins, if that is the item's first cut: tile x, 8 of
-// its dims, a thread a row; pieces in key order.
+// the item in which CTA c's range begins, if that is the item's first cut: tile x, kDims
+// of its dims, a thread a row; pieces in key order.  The first is CTA c - 1's last, the
+// others are the first of the CTAs from c on.
+constexpr int kDims = 16;
 template <int D>
-__global__ void __launch_bounds__(BQ)
-    merge_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(BQ) merge_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Geo& geo = p.geo;
-  const int c1 = (int)blockIdx.x + 1, x = blockIdx.y, part = blockIdx.z, r = threadIdx.x;
-  const int slots = (int)gridDim.x + 1;               // CTAs of the attention kernel
-  if (!RF_IN(p.err, c1, slots)) return;
-  const int4 cut = __ldcg(&p.ws_cut[c1]);
-  if (cut.x <= 0) return;
-  // the same plan as there: the item, and all tiles' number from the CTA borders
-  const Group w = group_of(geo, cut.y, false, p.err);
-  if (w.n <= cut.x) return;
-  const int4 head = __ldcg(&p.ws_cut[0]);
-  const int64_t total = (int64_t)head.y | ((int64_t)head.z << 31);
-  const Split64 split(total, head.w);
-  const int64_t s0 = split.start(c1) - cut.x, s1 = s0 + w.n;
-  if (split.owner(s0) != c1 - 1) return;
-  const int pieces = split.owner(s1 - 1) - (c1 - 1) + 1;
-  const Tile t = tile_of(geo, w, x);
-  const int my_t = r / geo.G, tok = t.t0 + my_t;
-  if (my_t >= geo.tpt || tok >= t.t1) return;
-  auto slot = [&](int i) { return slot_of(c1 - 1 + i, s0, split.start(c1 - 1 + i)) * 2 + x; };
-  float m = -INFINITY, l = 0.f, v[8];
+  const int c = (int)blockIdx.x + 1, x = blockIdx.y, part = blockIdx.z, r = threadIdx.x;
+  const int ctas = (int)gridDim.x + 1;                // of the attention kernel
+  if (!RF_IN(p.err, c, ctas)) return;
+  const int4 cut = __ldcg(&p.ws_cut[c]);
+  const int pieces = cut.x;
+  if (pieces == 0) return;
+  constexpr int kQuads = kDims / 4;
+  float m = -INFINITY, l = 0.f, v[kDims];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = 0.f;
-#pragma unroll 4
+  for (int k = 0; k < kDims; ++k) v[k] = 0.f;
+#pragma unroll 2
   for (int i = 0; i < pieces; ++i) {
-    const int64_t s = slot(i), at = (s * (D / 4) + part * 2) * BQ + r;
-    if (!RF_IN(p.err, s * BQ + r, (int64_t)4 * slots * BQ) ||
-        !RF_IN(p.err, at + BQ, (int64_t)4 * slots * (D / 4) * BQ))
+    const int64_t s = (i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c - 1 + i)) * 2 + x;
+    const int64_t at = (s * (D / 4) + part * kQuads) * BQ + r;
+    if (!RF_IN(p.err, s * BQ + r, (int64_t)4 * ctas * BQ) ||
+        !RF_IN(p.err, at + (kQuads - 1) * BQ, (int64_t)4 * ctas * (D / 4) * BQ))
       continue;
     const float2 ml = __ldcg(&p.ws_ml[s * BQ + r]);
-    const float4 a = __ldcg(&p.ws_o[at]), b = __ldcg(&p.ws_o[at + BQ]);
+    float4 u[kQuads];
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) u[k] = __ldcg(&p.ws_o[at + k * BQ]);
     if (ml.y == 0.f) continue;                        // read no key: its O may be anything
     const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
     const float keep = ex2(m - mu), f = ex2(ml.x - mu);
     m = mn;
     l = fmaf(l, keep, ml.y * f);
-    const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = fmaf(v[k], keep, u[k] * f);
+    for (int k = 0; k < kQuads; ++k) {
+      v[4 * k] = fmaf(v[4 * k], keep, u[k].x * f);
+      v[4 * k + 1] = fmaf(v[4 * k + 1], keep, u[k].y * f);
+      v[4 * k + 2] = fmaf(v[4 * k + 2], keep, u[k].z * f);
+      v[4 * k + 3] = fmaf(v[4 * k + 3], keep, u[k].w * f);
+    }
   }
+  const Group w = group_of(geo, cut.y, false, p.err);
+  const Tile t = tile_of(geo, w, x);
+  const int my_t = r / geo.G, tok = t.t0 + my_t;
+  if (my_t >= geo.tpt || tok >= t.t1) return;
   const int64_t row = ((int64_t)w.q0 + tok) * p.ldo +
-                      (int64_t)(cut.z * geo.G + (r - my_t * geo.G)) * D + part * 8;
-  if (!RF_IN(p.err, row + 7, ((int64_t)geo.B * geo.max_q - 1) * p.ldo + (int64_t)p.Hq * D)) return;
+                      (int64_t)(cut.z * geo.G + (r - my_t * geo.G)) * D + part * kDims;
+  if (!RF_IN(p.err, row + kDims - 1, ((int64_t)geo.B * geo.max_q - 1) * p.ldo + (int64_t)p.Hq * D))
+    return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t u[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    u[k] = l == 0.f ? 0u : pack_bf16x2(v[2 * k] * inv, v[2 * k + 1] * inv);
-  *reinterpret_cast<uint4*>(p.O + row) = make_uint4(u[0], u[1], u[2], u[3]);
+  for (int i = 0; i < kDims / 8; ++i) {
+    uint32_t u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      u[k] = l == 0.f ? 0u : pack_bf16x2(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
+    reinterpret_cast<uint4*>(p.O + row)[i] = make_uint4(u[0], u[1], u[2], u[3]);
+  }
 }
 
 template <int D, bool kPaged>
@@ -935,7 +949,7 @@ cudaError_t launch(const CUtensorMap (&tm)[3], Params& p, int grid, cudaStream_t
   e = cudaGetLastError();
   if (e != cudaSuccess || !kPaged || grid < 2) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid - 1, 2, D / 8);
+  cfg.gridDim = dim3((unsigned)grid - 1, 2, D / kDims);
   cfg.blockDim = dim3(BQ, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -1170,9 +1184,10 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
       if (pc.j1 == pc.w.n) {                          // the last piece: as the merge finds them
         const int64_t s1 = item0 + pc.w.n;
         const int c0 = split.owner(item0), pieces = split.owner(s1 - 1) - c0 + 1;
-        if ((int)parts.size() != pieces || split.start(c0 + 1) <= item0) return 4;
+        if ((int)parts.size() != pieces || split.start(c0 + 1) <= item0 || split.start(c0) > item0)
+          return 4;
         for (int i = 0; i < pieces; ++i)
-          if (slot_of(c0 + i, item0, split.start(c0 + i)) != parts[(size_t)i]) return 4;
+          if (parts[(size_t)i] != (i == 0 ? 2 * (int64_t)c0 + 1 : 2 * (int64_t)(c0 + i))) return 4;
       }
     }
   }
