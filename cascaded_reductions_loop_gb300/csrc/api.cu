@@ -540,16 +540,14 @@ size_t rf_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Tq, int d
   return decode_paged_workspace_bytes(B, Hkv, Hq / Hkv * Tq, d);
 }
 
-// With a mask, a bf16 cache and more query rows a kv head than this, the tensor-core
-// kernel with tiles of 128 rows takes the call.
+// With a mask and more query rows a kv head than this, the tensor-core kernel with tiles
+// of 128 rows takes the call.
 static constexpr int kFewRows = 16;
-static bool many_rows(int dtype, int R, int G) {
-  return dtype == RF_BF16 && R > kFewRows && G <= 128;
-}
+static bool many_rows(int R, int G) { return R > kFewRows && G <= 128; }
 
 size_t rf_attn_decode_paged_ex_workspace_size(int B, int Hq, int Hkv, int Tq, int d) {
   const size_t few = rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq, d);
-  if (few == 0 || !many_rows(RF_BF16, Hq / Hkv * Tq, Hq / Hkv)) return few;
+  if (few == 0 || !many_rows(Hq / Hkv * Tq, Hq / Hkv)) return few;
   const size_t many = masked_rows_workspace_bytes(d);
   return many > few ? many : few;
 }
@@ -580,7 +578,7 @@ rf_status rf_attn_decode_paged_ex(const rf_paged_kv* cache, const void* Q, void*
   const bool masked = mask && (mask->window != 0 || mask->parents);
   if (masked && Tq > (1 << 30)) return RF_ERR_INVALID_ARG;
   const int R = Hq / cache->Hkv * Tq;
-  const bool many = masked && many_rows(cache->dtype, R, Hq / cache->Hkv);
+  const bool many = masked && many_rows(R, Hq / cache->Hkv);
   if (decode_paged_max_chunks(cache->B, cache->Hkv, R, cache->max_pages, cache->page_size) >=
       (1ll << 31))
     return RF_ERR_INVALID_ARG;

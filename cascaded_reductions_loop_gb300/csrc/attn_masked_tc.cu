@@ -46,24 +46,29 @@ namespace rf {
 namespace masked {
 
 constexpr int kHalf = 128 * 128;                      // 128 rows of 64 values: 16 KB
-constexpr int kThreads = 384;                         // TMA, S, P.V, guard; softmax a; softmax b
 constexpr float kLazy = 8.f;
-// Registers: 384 threads start with 168 each (64512): the softmax warpgroups take 216
-// (55296) of them, the others keep 72 (9216).
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr float kTop = 7.f;                           // E4M3: log2 of P's first largest
 
-template <int D>
+template <int D, bool kF8>
 struct Cfg {
-  static constexpr int kTile = D / 64 * kHalf;        // 128 rows of D values
-  static constexpr int kQSlots = D == 64 ? 4 : 3;
+  // TMA, S, P.V, guard; softmax a; softmax b; E4M3: four warps that widen the codes
+  static constexpr int kThreads = kF8 ? 512 : 384;
+  // Registers: 384 threads start with 168 each (64512): the softmax warpgroups take 216
+  // (55296) of them, the others keep 72 (9216).  512 start with 128 each (65536): 200
+  // (51200) and 56 (14336).
+  static constexpr int kSoftmaxRegs = kF8 ? 200 : 216, kOtherRegs = kF8 ? 56 : 72;
+  static constexpr int kTile = D / 64 * kHalf;        // 128 rows of D 16-bit values
+  static constexpr int kQSlots = D == 64 ? 4 : (kF8 ? 2 : 3);
   static constexpr int kStages = D == 64 ? 8 : 4;     // K and V tiles, in turn
   static constexpr int kPairs = kStages / 2;
   static constexpr int kRing = kQSlots * kTile;
-  static constexpr int kBarOff = kRing + kStages * kTile;
-  static constexpr int kSmem = kBarOff + 1024 + 1024; // barriers; alignment
-  static constexpr uint32_t kIdescS = make_idesc(BQ, BK, 1, 0, 0);
-  static constexpr uint32_t kIdescHalf = make_idesc(BQ, kUnit, 1, 0, 0);
-  static constexpr uint32_t kIdescO = make_idesc(BQ, D, 1, 0, 1);
+  static constexpr int kRawOff = kRing + kStages * kTile;
+  static constexpr int kRaw = kF8 ? BK * D : 0;       // a tile's codes: K, then V
+  static constexpr int kBarOff = kRawOff + 2 * kRaw;
+  static constexpr int kSmem = kBarOff + 2048 + 1024; // barriers; alignment
+  static constexpr uint32_t kIdescS = make_idesc(BQ, BK, kF8 ? 0 : 1, 0, 0);
+  static constexpr uint32_t kIdescHalf = make_idesc(BQ, kUnit, kF8 ? 0 : 1, 0, 0);
+  static constexpr uint32_t kIdescO = make_idesc(BQ, D, kF8 ? 0 : 1, 0, 1);
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 constexpr uint32_t kTmemCols = 512;
@@ -74,14 +79,16 @@ __device__ __forceinline__ uint32_t col_o(int x) { return 256 + x * 128; }
 struct Params {
   Geo geo;
   __nv_bfloat16* O;
-  const __nv_bfloat16* V;
+  const void* V;                                      // bf16, or codes
   int64_t ldo, ldv, n_v;                              // elements between tokens; of V
+  const float* k_scale;
+  const float* v_scale;
   const int* parents;
   const int* block_table;
   int Hq, num_pages, page_size, page_shift, max_pages;
   float c_log2;
   float4* ws_o;                                       // [slots][2][D / 4][128]
-  float2* ws_ml;                                      // [slots][2][128]
+  float4* ws_st;                                      // [slots][2][128]: M, m, l
   int4* ws_cut;                                       // [grid]: see the kernel
   unsigned* err;
 };
@@ -98,13 +105,18 @@ struct Bars {
   // of tile m - 1 - kPairs is done and what was 8 tiles ago is not looked at any more.
   unsigned rec[8];
   unsigned bad[4][4];                                 // per V stage: values that are not finite
-  int64_t warp_sum[kThreads / 32];
+  // E4M3: codes have come, are widened; queries are; per key tile, the pages' scales as
+  // they come, and per 16 keys the key scale and log2 of the value scale
+  uint64_t raw_full[2], raw_empty[2], q_ok[4];
+  float sc_k[8][8], sc_v[8][8];
+  float2 scale[8][8];
+  int64_t warp_sum[16];
   int64_t x[2], total;                                // the CTA's range, all tiles
   int g, h, j;                                        // where it begins
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Bars) <= 1024, "barriers");
+static_assert(sizeof(Bars) <= 2048, "barriers");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -144,6 +156,32 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
       : "memory");
   return r;
 }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives on `bar` when this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Two E4M3 codes (the low or high half of a word) -> two f16, exact.
+__device__ __forceinline__ uint32_t widen(uint32_t w, bool high) {
+  uint32_t r;
+  if (high)
+    asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;}" : "=r"(r) : "r"(w));
+  else
+    asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float f16_to_f32(uint32_t w, bool high) {
+  float r;
+  asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;}" : "=f"(r) : "r"(high ? w >> 16 : w));
+  return r;
+}
 // Bits 0 .. n - 1 of a word.
 __device__ __forceinline__ unsigned below(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
@@ -161,12 +199,14 @@ enum : unsigned {
   kPages = 16,              // over a cache, from this bit on: bit per 16 keys that are there
 };
 
-template <int D, bool kPaged>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool kPaged, bool kF8>
+__global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
     attn_masked_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, kF8>;
+  constexpr int kThreads = C::kThreads;
+  static_assert(kPaged || !kF8, "codes are a cache's");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -184,10 +224,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 1);
       mbar_init(smem_u32(&bars->q_empty[i]), 1);
-      mbar_init(smem_u32(&bars->v_ok[i]), 1);
+      mbar_init(smem_u32(&bars->v_ok[i]), kF8 ? 4 : 1);
+      mbar_init(smem_u32(&bars->q_ok[i]), BQ);
     }
     for (int i = 0; i < 8; ++i) {
-      mbar_init(smem_u32(&bars->full[i]), 1);
+      mbar_init(smem_u32(&bars->full[i]), kF8 ? 4 : 1);       // a copy, or the widening warps
       mbar_init(smem_u32(&bars->rec_ok[i]), 1);
       mbar_init(smem_u32(&bars->empty[i]), 1);
     }
@@ -199,6 +240,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&bars->s_read), 4);            // a warpgroup's warps
     mbar_init(smem_u32(&bars->drain[0]), 1);
     mbar_init(smem_u32(&bars->drain[1]), 1);
+    if (kF8) {
+      mbar_init(smem_u32(&bars->raw_full[0]), 1 + 32);          // the copies' bytes; scales
+      mbar_init(smem_u32(&bars->raw_full[1]), 1);
+      mbar_init(smem_u32(&bars->raw_empty[0]), 4);
+      mbar_init(smem_u32(&bars->raw_empty[1]), 4);
+    }
     bars->abort = 0;
     bars->x[0] = bars->x[1] = 0;
     bars->g = bars->h = bars->j = 0;
@@ -280,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   if (warp < 4) {
-    regs_dec<kOtherRegs>();
+    regs_dec<C::kOtherRegs>();
     if (warp == 0) {
       // ---------------------------------------------------------- TMA
       const uint64_t pol_kv = policy_evict_last(), pol_q = policy_evict_first();
@@ -324,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ph = (uint32_t)((nt / C::kPairs - 1) & 1);
           // over a cache: lane i has the tile's page i
           int row = 0;
+          int64_t scale_at = 0;
           bool there = false;
           if (kPaged) {
             const int first = key0 + lane * p.page_size;
@@ -339,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               there = wanted && (unsigned)page < (unsigned)p.num_pages;
               if (wanted && !there) raise_error(p.err, kDevErrInput);
               row = (page * geo.Hkv + c.h) * p.page_size;
+              scale_at = (int64_t)page * geo.Hkv + c.h;
             }
           }
           const unsigned pages = __ballot_sync(0xffffffffu, there);
@@ -351,26 +400,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int v = 0; v < 2; ++v) {               // K, then V
-            const uint32_t bar = smem_u32(&bars->full[st + v]);
-            ok = __all_sync(0xffffffffu,
-                            nt < C::kPairs || mbar_wait(smem_u32(&bars->empty[st + v]), ph));
+            const uint32_t bar = smem_u32(kF8 ? &bars->raw_full[v] : &bars->full[st + v]);
+            if (kF8)
+              ok = nt < 1 || warp_wait(smem_u32(&bars->raw_empty[v]), (uint32_t)((nt - 1) & 1));
+            else
+              ok = nt < C::kPairs || warp_wait(smem_u32(&bars->empty[st + v]), ph);
             if (!ok) break;
-            const uint32_t dst = smem_u32(ring + (st + v) * C::kTile);
+            const uint32_t dst = smem_u32(kF8 ? smem + C::kRawOff + v * C::kRaw
+                                              : ring + (st + v) * C::kTile);
             const CUtensorMap* tm = v ? &tmV : &tmK;
             if (kPaged) {
               if (lane == 0) {
                 if (v == 0) {
                   bars->rec[nt % 8] = rec;
-                  mbar_arrive(smem_u32(&bars->rec_ok[nt % 8]));
+                  if (!kF8) mbar_arrive(smem_u32(&bars->rec_ok[nt % 8]));
                 }
-                mbar_arrive_expect_tx(bar, (uint32_t)(__popc(pages) * p.page_size * D * 2));
+                mbar_arrive_expect_tx(bar, (uint32_t)(__popc(pages) * p.page_size * D * (kF8 ? 1 : 2)));
               }
               __syncwarp();
-              if (there)
+              if (kF8) {                              // 128-byte rows: a key, or two of 64 dims
+                if (there) {
+                  tma_load_2d_hint(dst + lane * p.page_size * D, tm, bar, 0, row * D / 128, pol_kv);
+                  if (v == 0 && RF_IN(p.err, scale_at, (int64_t)p.num_pages * geo.Hkv)) {
+                    cp_async4(smem_u32(&bars->sc_k[nt % 8][lane]), p.k_scale + scale_at);
+                    cp_async4(smem_u32(&bars->sc_v[nt % 8][lane]), p.v_scale + scale_at);
+                  }
+                }
+                if (v == 0) cp_async_arrive(bar);
+              } else if (there) {
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i)
                   tma_load_2d_hint(dst + i * kHalf + lane * p.page_size * 128, tm, bar, 64 * i, row,
                                    pol_kv);
+              }
             } else if (lane == 0) {
               if (v == 0) bars->rec[nt % 8] = rec;
               mbar_arrive_expect_tx(bar, C::kTile);
@@ -391,8 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = max(0, nq - C::kQSlots); i < nq; ++i)
           (void)mbar_wait(smem_u32(&bars->q_full[i % C::kQSlots]), (uint32_t)((i / C::kQSlots) & 1),
                           1000000ull);
-        for (unsigned i = in_flight > C::kStages ? in_flight - C::kStages : 0; i < in_flight; ++i)
-          (void)mbar_wait(smem_u32(&bars->full[i % C::kStages]), (i / C::kStages) & 1, 1000000ull);
+        constexpr unsigned kPlaces = kF8 ? 2 : C::kStages;
+        for (unsigned i = in_flight > kPlaces ? in_flight - kPlaces : 0; i < in_flight; ++i)
+          (void)mbar_wait(smem_u32(kF8 ? &bars->raw_full[i % 2] : &bars->full[i % kPlaces]),
+                          (i / kPlaces) & 1, 1000000ull);
       }
     } else if (warp < 3) {
       // ---------------------------------------------------------- MMA: S (warp 1), P.V (warp 2)
@@ -420,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; ok && x < tiles; ++x) {
             const int slot = (q_at + x) % C::kQSlots;
             if (rec & kFirst)
-              ok = warp_wait(smem_u32(&bars->q_full[slot]), (uint32_t)(((q_at + x) / C::kQSlots) & 1));
+              ok = warp_wait(smem_u32(kF8 ? &bars->q_ok[slot] : &bars->q_full[slot]),
+                             (uint32_t)(((q_at + x) / C::kQSlots) & 1));
             const unsigned halves = (rec >> (2 * x)) & 3u;
             if (ok && halves) {
               if (events > 0) ok = warp_wait(smem_u32(&bars->s_read), (uint32_t)((events - 1) & 1));
@@ -506,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // nothing may still run on the tensor core when memory is released
       if (leader) mma_commit(smem_u32(&bars->drain[warp - 1]));
       (void)mbar_wait(smem_u32(&bars->drain[warp - 1]), 0, 1000000000ull);
-    } else {
+    } else if (!kF8) {
       // ---------------------------------------------------------- guard
       bool more = x1 > x0;
       // an exponent of ones carries into the sign's place
@@ -562,9 +627,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 1;
       }
     }
+  } else if (kF8 && warp >= 12) {
+    // ------------------------------------------------------------ E4M3: codes to f16
+    // A thread a key.  A code of NaN is dealt with as the guard does with bf16.
+    regs_dec<C::kOtherRegs>();
+    const int key = threadIdx.x - 384, word = warp - 12;
+    bool more = x1 > x0;
+    for (int nt = 0; ok && more; ++nt) {
+      const int pr = nt % C::kPairs;
+      unsigned rec = 0;
+#pragma unroll 1
+      for (int v = 0; ok && v < 2; ++v) {
+        ok = warp_wait(smem_u32(&bars->raw_full[v]), (uint32_t)(nt & 1));
+        if (!ok) break;
+        if (v == 0) rec = bars->rec[nt % 8];
+        if (v == 0 && word == 0) {                    // the scales of 16 keys each
+          if (lane < 8) {
+            const bool in = (rec >> (kPages + lane)) & 1u;
+            const int page = lane >> (p.page_shift - 4);
+            bars->scale[nt % 8][lane] = make_float2(in ? bars->sc_k[nt % 8][page] : 1.f,
+                                                    in ? __log2f(bars->sc_v[nt % 8][page]) : 0.f);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->rec_ok[nt % 8]));
+        }
+        ok = nt < C::kPairs ||
+             warp_wait(smem_u32(&bars->empty[2 * pr + v]), (uint32_t)((nt / C::kPairs - 1) & 1));
+        if (!ok) break;
+        const uint8_t* raw = smem + C::kRawOff + v * C::kRaw + (D == 128 ? key : key >> 1) * 128;
+        const int row = D == 128 ? key : key >> 1, base = D == 128 ? 0 : (key & 1) * 4;
+        uint8_t* out = ring + (2 * pr + v) * C::kTile + key * 128;
+        uint4 w[D / 16];
+        unsigned nan = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          w[i] = *reinterpret_cast<const uint4*>(raw + (((base + i) ^ (row & 7)) << 4));
+          nan |= ((w[i].x & 0x7F7F7F7Fu) + 0x01010101u) | ((w[i].y & 0x7F7F7F7Fu) + 0x01010101u) |
+                 ((w[i].z & 0x7F7F7F7Fu) + 0x01010101u) | ((w[i].w & 0x7F7F7F7Fu) + 0x01010101u);
+        }
+        const bool alone = v == 1 && (((rec >> (word >> 1)) & kPartly) ||
+                                      ((rec >> kPages) & 0xFFu) != 0xFFu);
+        const bool zero = alone && (nan & 0x80808080u) != 0u;
+        const unsigned bad = __ballot_sync(0xffffffffu, zero);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint4 a = make_uint4(widen(w[i].x, false), widen(w[i].x, true), widen(w[i].y, false),
+                               widen(w[i].y, true));
+          uint4 b = make_uint4(widen(w[i].z, false), widen(w[i].z, true), widen(w[i].w, false),
+                               widen(w[i].w, true));
+          if (zero) a = b = make_uint4(0u, 0u, 0u, 0u);
+          uint8_t* at = out + (i >> 2) * kHalf;
+          const int ch = (2 * i) & 7;
+          *reinterpret_cast<uint4*>(at + ((ch ^ (key & 7)) << 4)) = a;
+          *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (key & 7)) << 4)) = b;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars->raw_empty[v]));
+          if (v == 0) {
+            mbar_arrive(smem_u32(&bars->full[2 * pr]));
+          } else {
+            bars->bad[pr][word] = bad;
+            mbar_arrive(smem_u32(&bars->v_ok[pr]));
+          }
+        }
+      }
+      more = !(rec & kEnd);
+      if (*abort_flag) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (!ok) {
+      raise_error(p.err, kDevErrTimeout);
+      *abort_flag = 1;
+    }
   } else {
     // ------------------------------------------------------------ softmax of tile x
-    regs_inc<kSoftmaxRegs>();
+    regs_inc<C::kSoftmaxRegs>();
     const int x = warp >= 8 ? 1 : 0;
     const int r = (warp & 3) * 32 + lane;             // row of the tile
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -573,6 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t c2 = f2(p.c_log2, p.c_log2);
     const int my_t = r / geo.G, my_g = r - my_t * geo.G;
     int nt = 0, cnt = 0;                              // key tiles; events of this warpgroup
+    int nq = 0;                                       // Q tiles
     int64_t s0 = x0 - (x1 > x0 ? bars->j : 0);        // first tile of the piece's item
     while (ok && walk.next(geo, c, p.err)) {
       const Tile t = tile_of(geo, c.w, x);
@@ -580,6 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       s0 += c.w.n;
       const int j_base = nt - c.j0;                   // key tile j is the CTA's j_base + j th
       nt += c.j1 - c.j0;
+      const int q_at = nq + x;
+      nq += tile_of(geo, c.w, 1).has() ? 2 : 1;
       if (!t.has()) continue;
       const int tok = t.t0 + my_t;
       const bool real = my_t < geo.tpt && tok < t.t1;
@@ -601,6 +743,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!real) pos = -1;
       float m_ref = -INFINITY, l_run = 0.f;
+      float M_ref = -INFINITY, f_row = 0.f;           // E4M3: P's reference; the row's factor
+      if (kF8) {
+        // The row's queries as f16, scaled by a power of two to a largest element in
+        // [2^14, 2^15): exact down to 2^-28 of it.
+        const int slot = q_at % C::kQSlots;
+        if (!warp_wait(smem_u32(&bars->q_full[slot]), (uint32_t)((q_at / C::kQSlots) & 1))) {
+          ok = false;
+          break;
+        }
+        uint8_t* q = smem + slot * C::kTile + r * 128;
+        uint32_t qw[D / 2];
+        unsigned mx = 0;                              // largest finite magnitude, as bits
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 u = *reinterpret_cast<const uint4*>(q + (i >> 3) * kHalf + (((i & 7) ^ (r & 7)) << 4));
+          qw[4 * i] = u.x;
+          qw[4 * i + 1] = u.y;
+          qw[4 * i + 2] = u.z;
+          qw[4 * i + 3] = u.w;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i) {
+          const unsigned lo = qw[i] & 0x7FFFu, hi = (qw[i] >> 16) & 0x7FFFu;
+          if (lo < 0x7F80u) mx = max(mx, lo);
+          if (hi < 0x7F80u) mx = max(mx, hi);
+        }
+        const int e = max((int)(mx >> 7), 15);        // biased exponent
+        const float up = __uint_as_float((unsigned)(268 - e) << 23);
+        f_row = p.c_log2 * __uint_as_float((unsigned)(e - 14) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint32_t u[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+                : "=r"(u[k])
+                : "f"(bf16hi(qw[4 * i + k]) * up), "f"(bf16lo(qw[4 * i + k]) * up));
+          *reinterpret_cast<uint4*>(q + (i >> 3) * kHalf + (((i & 7) ^ (r & 7)) << 4)) =
+              make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(smem_u32(&bars->q_ok[slot]));
+      }
       const int cnt0 = cnt;
       // one event: halves (bits) of the key tile at key0, in V stage pr; part: of which
       // halves some row may not read all keys
@@ -649,35 +834,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();                            // S may be overwritten
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->s_read));
-        // row maximum (chains of their own)
-        float mh[2] = {-INFINITY, -INFINITY};
+        if (part)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if ((halves >> h) & 1u) {
-            if (part && __any_sync(0xffffffffu, (w[2 * h] & w[2 * h + 1]) != 0xFFFFFFFFu)) {
+          for (int h = 0; h < 2; ++h)
+            if (((halves >> h) & 1u) &&
+                __any_sync(0xffffffffu, (w[2 * h] & w[2 * h + 1]) != 0xFFFFFFFFu)) {
 #pragma unroll
               for (int q = 2 * h; q < 2 * h + 2; ++q)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[q][i] = (w[q] >> i) & 1u ? v[q][i] : 0xff800000u;
             }
-            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int q = 2 * h; q < 2 * h + 2; ++q)
-#pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                mx4[(i >> 1) & 3] =
-                    fmax3(mx4[(i >> 1) & 3], __uint_as_float(v[q][i]), __uint_as_float(v[q][i + 1]));
-            mh[h] = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]);
-          }
-        const float mt = fmaxf(mh[0], mh[1]) * p.c_log2;
+        // row maximum (chains of their own)
         const bool fresh = cnt == cnt0;
-        float alpha = 1.f;
-        if (fresh) {
-          m_ref = mt;                                 // P.V of the first event overwrites O
-        } else if (mt > m_ref + kLazy) {
-          alpha = ex2(m_ref - mt);
-          l_run *= alpha;
-          m_ref = mt;
+        float alpha = 1.f;                            // of O_x
+        const float2* scale = bars->scale[tile % 8];
+        if (!kF8) {
+          float mh[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if ((halves >> h) & 1u) {
+              float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int q = 2 * h; q < 2 * h + 2; ++q)
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                  mx4[(i >> 1) & 3] = fmax3(mx4[(i >> 1) & 3], __uint_as_float(v[q][i]),
+                                            __uint_as_float(v[q][i + 1]));
+              mh[h] = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]);
+            }
+          const float mt = fmaxf(mh[0], mh[1]) * p.c_log2;
+          if (fresh) {
+            m_ref = mt;                               // P.V of the first event overwrites O
+          } else if (mt > m_ref + kLazy) {
+            alpha = ex2(m_ref - mt);
+            l_run *= alpha;
+            m_ref = mt;
+          }
+        } else {
+          // e = s f_row ks (log2 of a weight); m for the sum, M for P = 2^(e + log2 vs - M)
+          float mt = -INFINITY, Mt = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            if ((halves >> (g >> 2)) & 1u) {
+              float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const uint32_t* u = &v[g >> 1][(g & 1) * 16 + i];
+                a = fmax3(a, __uint_as_float(u[0]), __uint_as_float(u[1]));
+                b = fmax3(b, __uint_as_float(u[2]), __uint_as_float(u[3]));
+              }
+              const float2 sc = scale[g];
+              const float e = fmaxf(a, b) * fmaxf(f_row * sc.x, 1.17549435e-38f);
+              mt = fmaxf(mt, e);
+              Mt = fmaxf(Mt, e + sc.y);
+            }
+          Mt -= kTop;
+          if (fresh) {
+            m_ref = mt;
+            M_ref = Mt;
+          } else {
+            if (mt > m_ref + kLazy) {
+              l_run *= ex2(m_ref - mt);
+              m_ref = mt;
+            }
+            if (Mt > M_ref + kLazy) {
+              alpha = ex2(M_ref - Mt);
+              M_ref = Mt;
+            }
+          }
         }
         const bool move = !fresh && __any_sync(0xffffffffu, alpha != 1.f);
         // P_x may be overwritten and O_x is complete once the last event's P.V is done
@@ -699,7 +923,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
         if (!settle()) return false;
-        // P = 2^(S c - m) as bf16 pairs, and its row sum (four chains)
+        // P = 2^(S c - m) as bf16 pairs (E4M3: f16, with the value scale), and the row sum
+        // (four chains)
+        const float M_use = M_ref == -INFINITY ? 0.f : M_ref;
         const uint64_t negm2 = f2(-m_use, -m_use);
         uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -707,18 +933,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((halves >> h) & 1u) {
             uint32_t pk[32];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < 2; ++q) {
+              uint64_t fac = c2, top = 0ull;
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
+                if (kF8 && i % 8 == 0) {              // the next 16 keys
+                  const float2 sc = scale[4 * h + 2 * q + i / 8];
+                  const float fk = fmaxf(f_row * sc.x, 1.17549435e-38f);
+                  const float up = fminf(ex2(sc.y + (m_use - M_use)), 8.5e37f);
+                  fac = f2(fk, fk);
+                  top = f2(up, up);
+                }
                 float t0, t1;
                 f2_split(ffma2(f2(__uint_as_float(v[2 * h + q][2 * i]),
                                   __uint_as_float(v[2 * h + q][2 * i + 1])),
-                               c2, negm2),
+                               fac, negm2),
                          t0, t1);
                 const float p0 = ex2(t0), p1 = ex2(t1);
                 sum4[i & 3] = fadd2(sum4[i & 3], f2(p0, p1));
-                pk[q * 16 + i] = pack_bf16x2(p0, p1);
+                if (kF8) {
+                  float w0, w1;
+                  f2_split(fmul2(f2(p0, p1), top), w0, w1);
+                  pk[q * 16 + i] = pack_f16x2(w0, w1);
+                } else {
+                  pk[q * 16 + i] = pack_bf16x2(p0, p1);
+                }
               }
+            }
             tmem_st32(p_addr + 32 * h, pk);
           }
         float s_lo, s_hi;
@@ -745,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const unsigned rw = k < 32 ? w[0] : (k < 64 ? w[1] : (k < 96 ? w[2] : w[3]));
               const bool reads = (rw >> (k & 31)) & 1u;
               const uint32_t two = tmem_ld1(p_addr + k / 2);
-              const float pk = (k & 1) ? bf16hi(two) : bf16lo(two);
+              const float pk = kF8 ? f16_to_f32(two, k & 1) : ((k & 1) ? bf16hi(two) : bf16lo(two));
               int64_t at;                             // the value's first element
               bool inside;
               if (kPaged) {
@@ -767,9 +1008,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait();
                 if (reads && inside && RF_IN(p.err, at + D - 1, p.n_v))
 #pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    o[i] = __float_as_uint(fmaf(pk, __bfloat162float(p.V[at + q * 32 + i]),
-                                                __uint_as_float(o[i])));
+                  for (int i = 0; i < 32; ++i) {
+                    const int64_t e = at + q * 32 + i;
+                    const float val =
+                        kF8 ? f16_to_f32(widen(static_cast<const uint8_t*>(p.V)[e], false), false)
+                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p.V)[e]);
+                    o[i] = __float_as_uint(fmaf(pk, val, __uint_as_float(o[i])));
+                  }
                 __syncwarp();
                 tmem_st32(o_addr + q * 32, o);
                 tmem_st_wait();
@@ -830,7 +1075,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool out = real && RF_IN(p.err, row + D - 1,
                                      ((int64_t)(kPaged ? geo.B * geo.max_q : geo.total_q) - 1) * p.ldo +
                                          (int64_t)p.Hq * D);
-      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+      // E4M3: 2^(M - m) / l in two factors, since 2^(M - m) itself may underflow
+      const float half = kF8 ? ex2(0.5f * (M_ref - m_ref)) : 1.f;
+      const float inv = l_run == 0.f ? 0.f : half / l_run;
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
         uint32_t o[32];
@@ -845,8 +1092,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 u[k] = l_run == 0.f ? 0u
-                                    : pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv,
-                                                  __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                                    : pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv * half,
+                                                  __uint_as_float(o[8 * i + 2 * k + 1]) * inv * half);
               reinterpret_cast<uint4*>(p.O + row)[q * 4 + i] = make_uint4(u[0], u[1], u[2], u[3]);
             }
           }
@@ -861,7 +1108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!all && RF_IN(p.err, slot * BQ + r, (int64_t)4 * gridDim.x * BQ))
-        p.ws_ml[slot * BQ + r] = make_float2(m_ref, l_run);
+        p.ws_st[slot * BQ + r] = make_float4(kF8 ? M_ref : m_ref, m_ref, l_run, 0.f);
       tc_fence_before();                              // O is read before the next product writes it
     }
     if (!ok) {
@@ -893,7 +1140,7 @@ __global__ void __launch_bounds__(BQ) merge_kernel(const __grid_constant__ Param
   const int pieces = cut.x;
   if (pieces == 0) return;
   constexpr int kQuads = kDims / 4;
-  float m = -INFINITY, l = 0.f, v[kDims];
+  float M = -INFINITY, m = -INFINITY, l = 0.f, v[kDims];        // bf16: M = m
 #pragma unroll
   for (int k = 0; k < kDims; ++k) v[k] = 0.f;
 #pragma unroll 2
@@ -903,15 +1150,17 @@ __global__ void __launch_bounds__(BQ) merge_kernel(const __grid_constant__ Param
     if (!RF_IN(p.err, s * BQ + r, (int64_t)4 * ctas * BQ) ||
         !RF_IN(p.err, at + (kQuads - 1) * BQ, (int64_t)4 * ctas * (D / 4) * BQ))
       continue;
-    const float2 ml = __ldcg(&p.ws_ml[s * BQ + r]);
+    const float4 st = __ldcg(&p.ws_st[s * BQ + r]);
     float4 u[kQuads];
 #pragma unroll
     for (int k = 0; k < kQuads; ++k) u[k] = __ldcg(&p.ws_o[at + k * BQ]);
-    if (ml.y == 0.f) continue;                        // read no key: its O may be anything
-    const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
-    const float keep = ex2(m - mu), f = ex2(ml.x - mu);
+    if (st.z == 0.f) continue;                        // read no key: its O may be anything
+    const float Mn = fmaxf(M, st.x), Mu = Mn == -INFINITY ? 0.f : Mn;
+    const float mn = fmaxf(m, st.y), mu = mn == -INFINITY ? 0.f : mn;
+    const float keep = ex2(M - Mu), f = ex2(st.x - Mu);
+    l = fmaf(l, ex2(m - mu), st.z * ex2(st.y - mu));
+    M = Mn;
     m = mn;
-    l = fmaf(l, keep, ml.y * f);
 #pragma unroll
     for (int k = 0; k < kQuads; ++k) {
       v[4 * k] = fmaf(v[4 * k], keep, u[k].x * f);
@@ -928,24 +1177,25 @@ __global__ void __launch_bounds__(BQ) merge_kernel(const __grid_constant__ Param
                       (int64_t)(cut.z * geo.G + (r - my_t * geo.G)) * D + part * kDims;
   if (!RF_IN(p.err, row + kDims - 1, ((int64_t)geo.B * geo.max_q - 1) * p.ldo + (int64_t)p.Hq * D))
     return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float half = M == m ? 1.f : ex2(0.5f * (M - m));
+  const float inv = l == 0.f ? 0.f : half / l;
 #pragma unroll
   for (int i = 0; i < kDims / 8; ++i) {
     uint32_t u[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      u[k] = l == 0.f ? 0u : pack_bf16x2(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
+      u[k] = l == 0.f ? 0u : pack_bf16x2(v[8 * i + 2 * k] * inv * half, v[8 * i + 2 * k + 1] * inv * half);
     reinterpret_cast<uint4*>(p.O + row)[i] = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
-template <int D, bool kPaged>
+template <int D, bool kPaged, bool kF8>
 cudaError_t launch(const CUtensorMap (&tm)[3], Params& p, int grid, cudaStream_t s) {
-  using C = Cfg<D>;
-  auto kern = attn_masked_kernel<D, kPaged>;
+  using C = Cfg<D, kF8>;
+  auto kern = attn_masked_kernel<D, kPaged, kF8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, C::kSmem, s>>>(tm[0], tm[1], tm[2], p);
+  kern<<<grid, C::kThreads, C::kSmem, s>>>(tm[0], tm[1], tm[2], p);
   e = cudaGetLastError();
   if (e != cudaSuccess || !kPaged || grid < 2) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1007,7 +1257,7 @@ cudaError_t launch_attn_fwd_window(const void* Q, int64_t ldq, const void* K, in
   masked::Params p = {};
   p.geo = packed_geo(cu_q, cu_k, B, Hkv, Hq / Hkv, max_q, total_q, total_k, window, sinks);
   p.O = static_cast<__nv_bfloat16*>(O);
-  p.V = static_cast<const __nv_bfloat16*>(V);
+  p.V = V;
   p.ldo = ldo;
   p.ldv = ldv;
   p.n_v = (int64_t)(total_k - 1) * ldv + (int64_t)Hkv * d;
@@ -1020,17 +1270,17 @@ cudaError_t launch_attn_fwd_window(const void* Q, int64_t ldq, const void* K, in
       !encode_tmap_3d(&tm[1], t, K, d, Hkv, total_k, d * 2, ldk * 2, 64, 1, masked::BK, true) ||
       !encode_tmap_3d(&tm[2], t, V, d, Hkv, total_k, d * 2, ldv * 2, 64, 1, masked::BK, true))
     return cudaErrorInvalidValue;
-  return d == 64 ? masked::launch<64, false>(tm, p, sms, s)
-                 : masked::launch<128, false>(tm, p, sms, s);
+  return d == 64 ? masked::launch<64, false, false>(tm, p, sms, s)
+                 : masked::launch<128, false, false>(tm, p, sms, s);
 }
 
-// Workspace: partial states [2 SMs][2][d / 4][128] float4, (m, l) [2 SMs][2][128],
+// Workspace: partial states [2 SMs][2][d / 4][128] float4, (M, m, l) [2 SMs][2][128],
 // the cuts [SMs].
 size_t masked_rows_workspace_bytes(int d) {
   const int sms = sm_count();
   if (sms <= 0) return 0;
   const size_t rows = (size_t)sms * 4 * masked::BQ;
-  return rows * d * sizeof(float) + rows * sizeof(float2) + masked::pad256(sms * sizeof(int4));
+  return rows * d * sizeof(float) + rows * sizeof(float4) + masked::pad256(sms * sizeof(int4));
 }
 
 cudaError_t launch_masked_rows(const PagedKV& c, const Mask& mask, const void* Q, void* O, int Hq,
@@ -1042,7 +1292,9 @@ cudaError_t launch_masked_rows(const PagedKV& c, const Mask& mask, const void* Q
   p.geo = paged_geo(c.seq_lens, c.B, c.Hkv, Hq / c.Hkv, Tq, c.max_pages * c.page_size, mask.window,
                     mask.sinks, mask.parents != nullptr);
   p.O = static_cast<__nv_bfloat16*>(O);
-  p.V = static_cast<const __nv_bfloat16*>(c.v);
+  p.V = c.v;
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
   p.ldo = (int64_t)Hq * c.d;
   const uint64_t keys = (uint64_t)c.num_pages * c.Hkv * c.page_size;
   p.n_v = (int64_t)keys * c.d;
@@ -1059,18 +1311,28 @@ cudaError_t launch_masked_rows(const PagedKV& c, const Mask& mask, const void* Q
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.ws_o = reinterpret_cast<float4*>(ws);
   ws += rows * c.d * sizeof(float);
-  p.ws_ml = reinterpret_cast<float2*>(ws);
-  ws += rows * sizeof(float2);
+  p.ws_st = reinterpret_cast<float4*>(ws);
+  ws += rows * sizeof(float4);
   p.ws_cut = reinterpret_cast<int4*>(ws);
   CUtensorMap tm[3];
   const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int d = c.d;
   if (!encode_tmap_3d(&tm[0], t, Q, d, Hq, (uint64_t)c.B * Tq, d * 2, (uint64_t)Hq * d * 2, 64,
-                      p.geo.G, p.geo.tpt, true) ||
-      !encode_tmap_2d(&tm[1], t, c.k, d, keys, d * 2, 64, c.page_size, true) ||
-      !encode_tmap_2d(&tm[2], t, c.v, d, keys, d * 2, 64, c.page_size, true))
+                      p.geo.G, p.geo.tpt, true))
     return cudaErrorInvalidValue;
-  return d == 64 ? masked::launch<64, true>(tm, p, sms, s) : masked::launch<128, true>(tm, p, sms, s);
+  const bool f8 = c.dtype == RF_E4M3;
+  for (int i = 0; i < 2; ++i) {
+    const void* base = i ? c.v : c.k;
+    if (!(f8 ? encode_tmap_2d(&tm[1 + i], CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 128, keys * d / 128,
+                              128, 128, c.page_size * d / 128, true)
+             : encode_tmap_2d(&tm[1 + i], t, base, d, keys, d * 2, 64, c.page_size, true)))
+      return cudaErrorInvalidValue;
+  }
+  if (f8)
+    return d == 64 ? masked::launch<64, true, true>(tm, p, sms, s)
+                   : masked::launch<128, true, true>(tm, p, sms, s);
+  return d == 64 ? masked::launch<64, true, false>(tm, p, sms, s)
+                 : masked::launch<128, true, false>(tm, p, sms, s);
 }
 
 // Host-side walk of the plan (the functions of the header, shared by host and device)
