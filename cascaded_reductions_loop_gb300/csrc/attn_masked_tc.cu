@@ -59,12 +59,13 @@ struct Cfg {
   static constexpr int kSoftmaxRegs = kF8 ? 200 : 216, kOtherRegs = kF8 ? 56 : 72;
   static constexpr int kTile = D / 64 * kHalf;        // 128 rows of D 16-bit values
   static constexpr int kQSlots = D == 64 ? 4 : (kF8 ? 2 : 3);
-  static constexpr int kStages = D == 64 ? 8 : 4;     // K and V tiles, in turn
+  static constexpr int kStages = kF8 ? (D == 64 ? 4 : 2) : (D == 64 ? 8 : 4);  // K, V tiles in turn
   static constexpr int kPairs = kStages / 2;
   static constexpr int kRing = kQSlots * kTile;
   static constexpr int kRawOff = kRing + kStages * kTile;
-  static constexpr int kRaw = kF8 ? BK * D : 0;       // a tile's codes: K, then V
-  static constexpr int kBarOff = kRawOff + 2 * kRaw;
+  static constexpr int kRaw = kF8 ? BK * D : 0;       // a tile's codes, K and V in turn
+  static constexpr int kRawPairs = kF8 ? (D == 64 ? 5 : 3) : 1;
+  static constexpr int kBarOff = kRawOff + 2 * kRawPairs * kRaw;
   static constexpr int kSmem = kBarOff + 2048 + 1024; // barriers; alignment
   static constexpr uint32_t kIdescS = make_idesc(BQ, BK, kF8 ? 0 : 1, 0, 0);
   static constexpr uint32_t kIdescHalf = make_idesc(BQ, kUnit, kF8 ? 0 : 1, 0, 0);
@@ -107,7 +108,7 @@ struct Bars {
   unsigned bad[4][4];                                 // per V stage: values that are not finite
   // E4M3: codes have come, are widened; queries are; per key tile, the pages' scales as
   // they come, and per 16 keys the key scale and log2 of the value scale
-  uint64_t raw_full[2], raw_empty[2], q_ok[4];
+  uint64_t raw_full[2][5], raw_empty[2][5], q_ok[4];
   float sc_k[8][8], sc_v[8][8];
   float2 scale[8][8];
   int64_t warp_sum[16];
@@ -224,11 +225,11 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 1);
       mbar_init(smem_u32(&bars->q_empty[i]), 1);
-      mbar_init(smem_u32(&bars->v_ok[i]), kF8 ? 4 : 1);
+      mbar_init(smem_u32(&bars->v_ok[i]), kF8 ? 2 : 1);
       mbar_init(smem_u32(&bars->q_ok[i]), BQ);
     }
     for (int i = 0; i < 8; ++i) {
-      mbar_init(smem_u32(&bars->full[i]), kF8 ? 4 : 1);       // a copy, or the widening warps
+      mbar_init(smem_u32(&bars->full[i]), kF8 ? 2 : 1);       // a copy, or the widening warps
       mbar_init(smem_u32(&bars->rec_ok[i]), 1);
       mbar_init(smem_u32(&bars->empty[i]), 1);
     }
@@ -241,10 +242,12 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
     mbar_init(smem_u32(&bars->drain[0]), 1);
     mbar_init(smem_u32(&bars->drain[1]), 1);
     if (kF8) {
-      mbar_init(smem_u32(&bars->raw_full[0]), 1 + 32);          // the copies' bytes; scales
-      mbar_init(smem_u32(&bars->raw_full[1]), 1);
-      mbar_init(smem_u32(&bars->raw_empty[0]), 4);
-      mbar_init(smem_u32(&bars->raw_empty[1]), 4);
+      for (int i = 0; i < C::kRawPairs; ++i) {
+        mbar_init(smem_u32(&bars->raw_full[0][i]), 1 + 32);     // the copies' bytes; scales
+        mbar_init(smem_u32(&bars->raw_full[1][i]), 1);
+        mbar_init(smem_u32(&bars->raw_empty[0][i]), 2);
+        mbar_init(smem_u32(&bars->raw_empty[1][i]), 2);
+      }
     }
     bars->abort = 0;
     bars->x[0] = bars->x[1] = 0;
@@ -400,13 +403,15 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
           }
 #pragma unroll
           for (int v = 0; v < 2; ++v) {               // K, then V
-            const uint32_t bar = smem_u32(kF8 ? &bars->raw_full[v] : &bars->full[st + v]);
+            const int rp = nt % C::kRawPairs;
+            const uint32_t bar = smem_u32(kF8 ? &bars->raw_full[v][rp] : &bars->full[st + v]);
             if (kF8)
-              ok = nt < 1 || warp_wait(smem_u32(&bars->raw_empty[v]), (uint32_t)((nt - 1) & 1));
+              ok = nt < C::kRawPairs || warp_wait(smem_u32(&bars->raw_empty[v][rp]),
+                                                  (uint32_t)((nt / C::kRawPairs - 1) & 1));
             else
               ok = nt < C::kPairs || warp_wait(smem_u32(&bars->empty[st + v]), ph);
             if (!ok) break;
-            const uint32_t dst = smem_u32(kF8 ? smem + C::kRawOff + v * C::kRaw
+            const uint32_t dst = smem_u32(kF8 ? smem + C::kRawOff + (2 * rp + v) * C::kRaw
                                               : ring + (st + v) * C::kTile);
             const CUtensorMap* tm = v ? &tmV : &tmK;
             if (kPaged) {
@@ -453,9 +458,10 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
         for (int i = max(0, nq - C::kQSlots); i < nq; ++i)
           (void)mbar_wait(smem_u32(&bars->q_full[i % C::kQSlots]), (uint32_t)((i / C::kQSlots) & 1),
                           1000000ull);
-        constexpr unsigned kPlaces = kF8 ? 2 : C::kStages;
+        constexpr unsigned kPlaces = kF8 ? 2 * C::kRawPairs : C::kStages;
         for (unsigned i = in_flight > kPlaces ? in_flight - kPlaces : 0; i < in_flight; ++i)
-          (void)mbar_wait(smem_u32(kF8 ? &bars->raw_full[i % 2] : &bars->full[i % kPlaces]),
+          (void)mbar_wait(smem_u32(kF8 ? &bars->raw_full[i % 2][i / 2 % C::kRawPairs]
+                                       : &bars->full[i % kPlaces]),
                           (i / kPlaces) & 1, 1000000ull);
       }
     } else if (warp < 3) {
@@ -629,71 +635,68 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
     }
   } else if (kF8 && warp >= 12) {
     // ------------------------------------------------------------ E4M3: codes to f16
-    // A thread a key.  A code of NaN is dealt with as the guard does with bf16.
+    // Two warps for K and two for V, a lane a key.  A code of NaN is dealt with as the guard
+    // does with bf16.
     regs_dec<C::kOtherRegs>();
-    const int key = threadIdx.x - 384, word = warp - 12;
+    const int v = (warp - 12) >> 1, h = warp & 1;     // K or V; the half of the key tile
     bool more = x1 > x0;
     for (int nt = 0; ok && more; ++nt) {
-      const int pr = nt % C::kPairs;
-      unsigned rec = 0;
+      const int pr = nt % C::kPairs, rp = nt % C::kRawPairs;
+      ok = warp_wait(smem_u32(&bars->raw_full[v][rp]), (uint32_t)((nt / C::kRawPairs) & 1));
+      if (!ok) break;
+      const unsigned rec = bars->rec[nt % 8];
+      more = !(rec & kEnd);
+      if (v == 0 && h == 0) {                         // the scales of 16 keys each
+        if (lane < 8) {
+          const bool in = (rec >> (kPages + lane)) & 1u;
+          const int page = lane >> (p.page_shift - 4);
+          bars->scale[nt % 8][lane] = make_float2(in ? bars->sc_k[nt % 8][page] : 1.f,
+                                                  in ? __log2f(bars->sc_v[nt % 8][page]) : 0.f);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->rec_ok[nt % 8]));
+      }
+      ok = nt < C::kPairs ||
+           warp_wait(smem_u32(&bars->empty[2 * pr + v]), (uint32_t)((nt / C::kPairs - 1) & 1));
+      if (!ok) break;
+      const bool alone = v == 1 && (((rec >> h) & kPartly) || ((rec >> kPages) & 0xFFu) != 0xFFu);
 #pragma unroll 1
-      for (int v = 0; ok && v < 2; ++v) {
-        ok = warp_wait(smem_u32(&bars->raw_full[v]), (uint32_t)(nt & 1));
-        if (!ok) break;
-        if (v == 0) rec = bars->rec[nt % 8];
-        if (v == 0 && word == 0) {                    // the scales of 16 keys each
-          if (lane < 8) {
-            const bool in = (rec >> (kPages + lane)) & 1u;
-            const int page = lane >> (p.page_shift - 4);
-            bars->scale[nt % 8][lane] = make_float2(in ? bars->sc_k[nt % 8][page] : 1.f,
-                                                    in ? __log2f(bars->sc_v[nt % 8][page]) : 0.f);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->rec_ok[nt % 8]));
-        }
-        ok = nt < C::kPairs ||
-             warp_wait(smem_u32(&bars->empty[2 * pr + v]), (uint32_t)((nt / C::kPairs - 1) & 1));
-        if (!ok) break;
-        const uint8_t* raw = smem + C::kRawOff + v * C::kRaw + (D == 128 ? key : key >> 1) * 128;
+      for (int i32 = 0; i32 < 2; ++i32) {
+        const int key = h * kUnit + i32 * 32 + lane;
         const int row = D == 128 ? key : key >> 1, base = D == 128 ? 0 : (key & 1) * 4;
+        const uint8_t* raw = smem + C::kRawOff + (2 * rp + v) * C::kRaw + row * 128;
         uint8_t* out = ring + (2 * pr + v) * C::kTile + key * 128;
-        uint4 w[D / 16];
-        unsigned nan = 0;
+        bool zero = false;
+        if (alone) {
+          unsigned nan = 0;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          w[i] = *reinterpret_cast<const uint4*>(raw + (((base + i) ^ (row & 7)) << 4));
-          nan |= ((w[i].x & 0x7F7F7F7Fu) + 0x01010101u) | ((w[i].y & 0x7F7F7F7Fu) + 0x01010101u) |
-                 ((w[i].z & 0x7F7F7F7Fu) + 0x01010101u) | ((w[i].w & 0x7F7F7F7Fu) + 0x01010101u);
+          for (int i = 0; i < D / 16; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4*>(raw + (((base + i) ^ (row & 7)) << 4));
+            nan |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                   ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+          }
+          zero = (nan & 0x80808080u) != 0u;
         }
-        const bool alone = v == 1 && (((rec >> (word >> 1)) & kPartly) ||
-                                      ((rec >> kPages) & 0xFFu) != 0xFFu);
-        const bool zero = alone && (nan & 0x80808080u) != 0u;
         const unsigned bad = __ballot_sync(0xffffffffu, zero);
+        if (v == 1 && lane == 0) bars->bad[pr][2 * h + i32] = bad;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          uint4 a = make_uint4(widen(w[i].x, false), widen(w[i].x, true), widen(w[i].y, false),
-                               widen(w[i].y, true));
-          uint4 b = make_uint4(widen(w[i].z, false), widen(w[i].z, true), widen(w[i].w, false),
-                               widen(w[i].w, true));
-          if (zero) a = b = make_uint4(0u, 0u, 0u, 0u);
+          uint4 w = *reinterpret_cast<const uint4*>(raw + (((base + i) ^ (row & 7)) << 4));
+          if (zero) w = make_uint4(0u, 0u, 0u, 0u);
           uint8_t* at = out + (i >> 2) * kHalf;
           const int ch = (2 * i) & 7;
-          *reinterpret_cast<uint4*>(at + ((ch ^ (key & 7)) << 4)) = a;
-          *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (key & 7)) << 4)) = b;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&bars->raw_empty[v]));
-          if (v == 0) {
-            mbar_arrive(smem_u32(&bars->full[2 * pr]));
-          } else {
-            bars->bad[pr][word] = bad;
-            mbar_arrive(smem_u32(&bars->v_ok[pr]));
-          }
+          *reinterpret_cast<uint4*>(at + ((ch ^ (key & 7)) << 4)) =
+              make_uint4(widen(w.x, false), widen(w.x, true), widen(w.y, false), widen(w.y, true));
+          *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (key & 7)) << 4)) =
+              make_uint4(widen(w.z, false), widen(w.z, true), widen(w.w, false), widen(w.w, true));
         }
       }
-      more = !(rec & kEnd);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&bars->raw_empty[v][rp]));
+        mbar_arrive(smem_u32(v ? &bars->v_ok[pr] : &bars->full[2 * pr]));
+      }
       if (*abort_flag) ok = false;
       ok = __all_sync(0xffffffffu, ok);
     }
