@@ -157,6 +157,9 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
       : "memory");
   return r;
 }
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -218,6 +221,8 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
   const Geo& geo = p.geo;
   uint8_t* ring = smem + C::kRing;
 
+  // The merge may take its place as soon as CTAs leave; it waits for the end of this grid.
+  if (kPaged) asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 0) {
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
@@ -976,11 +981,8 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
           if (((halves & 1u) && (bad[0] | bad[1])) || ((halves & 2u) && (bad[2] | bad[3]))) {
             // values that are not finite, for the rows that read them: P times value
             if (fresh) {
-              uint32_t z[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) z[i] = 0u;
-#pragma unroll
-              for (int q = 0; q < D / 32; ++q) tmem_st32(o_addr + q * 32, z);
+#pragma unroll 1
+              for (int i = 0; i < D; ++i) tmem_st1(o_addr + i, 0u);
               tmem_st_wait();
             }
 #pragma unroll 1
@@ -1005,21 +1007,16 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
                 inside = key0 + k < c.w.lk;
               }
 #pragma unroll 1
-              for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[32];
-                tmem_ld32(o_addr + q * 32, o);
-                tmem_ld_wait();
-                if (reads && inside && RF_IN(p.err, at + D - 1, p.n_v))
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) {
-                    const int64_t e = at + q * 32 + i;
-                    const float val =
-                        kF8 ? f16_to_f32(widen(static_cast<const uint8_t*>(p.V)[e], false), false)
-                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p.V)[e]);
-                    o[i] = __float_as_uint(fmaf(pk, val, __uint_as_float(o[i])));
-                  }
+              for (int i = 0; i < D; ++i) {
+                float o = __uint_as_float(tmem_ld1(o_addr + i));
+                if (reads && inside && RF_IN(p.err, at + i, p.n_v)) {
+                  const float val =
+                      kF8 ? f16_to_f32(widen(static_cast<const uint8_t*>(p.V)[at + i], false), false)
+                          : __bfloat162float(static_cast<const __nv_bfloat16*>(p.V)[at + i]);
+                  o = fmaf(pk, val, o);
+                }
                 __syncwarp();
-                tmem_st32(o_addr + q * 32, o);
+                tmem_st1(o_addr + i, __float_as_uint(o));
                 tmem_st_wait();
               }
             }
@@ -1146,7 +1143,7 @@ __global__ void __launch_bounds__(BQ) merge_kernel(const __grid_constant__ Param
   float M = -INFINITY, m = -INFINITY, l = 0.f, v[kDims];        // bf16: M = m
 #pragma unroll
   for (int k = 0; k < kDims; ++k) v[k] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
   for (int i = 0; i < pieces; ++i) {
     const int64_t s = (i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c - 1 + i)) * 2 + x;
     const int64_t at = (s * (D / 4) + part * kQuads) * BQ + r;
