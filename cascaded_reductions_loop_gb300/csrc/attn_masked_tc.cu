@@ -1,6 +1,6 @@
 // attn_masked_tc.cu -- attention whose rows read only some of the keys, on the tensor
 // cores: prompts with a sliding window and sinks (packed K and V), and many query rows
-// a kv head (drafted trees, chunks of a prompt) over a paged bf16 cache.
+// a kv head (drafted trees, chunks of a prompt) over a paged bf16 or E4M3 cache.
 //
 // For the row at position p, over the keys that it reads (p - j < W or j < S; of a
 // tree's nodes, its line of parents):
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
         bool zero = false;
         if (alone) {
           unsigned nan = 0;
-#pragma unroll
+#pragma unroll 2
           for (int i = 0; i < D / 16; ++i) {
             const uint4 w = *reinterpret_cast<const uint4*>(raw + (((base + i) ^ (row & 7)) << 4));
             nan |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
         }
         const unsigned bad = __ballot_sync(0xffffffffu, zero);
         if (v == 1 && lane == 0) bars->bad[pr][2 * h + i32] = bad;
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < D / 16; ++i) {
           uint4 w = *reinterpret_cast<const uint4*>(raw + (((base + i) ^ (row & 7)) << 4));
           if (zero) w = make_uint4(0u, 0u, 0u, 0u);
@@ -1097,7 +1097,7 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
               reinterpret_cast<uint4*>(p.O + row)[q * 4 + i] = make_uint4(u[0], u[1], u[2], u[3]);
             }
           }
-        } else {
+        } else if (real) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int64_t at = (slot * (D / 4) + q * 8 + i) * BQ + r;
@@ -1107,7 +1107,7 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
           }
         }
       }
-      if (!all && RF_IN(p.err, slot * BQ + r, (int64_t)4 * gridDim.x * BQ))
+      if (!all && real && RF_IN(p.err, slot * BQ + r, (int64_t)4 * gridDim.x * BQ))
         p.ws_st[slot * BQ + r] = make_float4(kF8 ? M_ref : m_ref, m_ref, l_run, 0.f);
       tc_fence_before();                              // O is read before the next product writes it
     }
@@ -1139,6 +1139,10 @@ __global__ void __launch_bounds__(BQ) merge_kernel(const __grid_constant__ Param
   const int4 cut = __ldcg(&p.ws_cut[c]);
   const int pieces = cut.x;
   if (pieces == 0) return;
+  const Group w = group_of(geo, cut.y, false, p.err);
+  const Tile t = tile_of(geo, w, x);
+  const int my_t = r / geo.G, tok = t.t0 + my_t;
+  if (my_t >= geo.tpt || tok >= t.t1) return;
   constexpr int kQuads = kDims / 4;
   float M = -INFINITY, m = -INFINITY, l = 0.f, v[kDims];        // bf16: M = m
 #pragma unroll
@@ -1169,10 +1173,6 @@ __global__ void __launch_bounds__(BQ) merge_kernel(const __grid_constant__ Param
       v[4 * k + 3] = fmaf(v[4 * k + 3], keep, u[k].w * f);
     }
   }
-  const Group w = group_of(geo, cut.y, false, p.err);
-  const Tile t = tile_of(geo, w, x);
-  const int my_t = r / geo.G, tok = t.t0 + my_t;
-  if (my_t >= geo.tpt || tok >= t.t1) return;
   const int64_t row = ((int64_t)w.q0 + tok) * p.ldo +
                       (int64_t)(cut.z * geo.G + (r - my_t * geo.G)) * D + part * kDims;
   if (!RF_IN(p.err, row + kDims - 1, ((int64_t)geo.B * geo.max_q - 1) * p.ldo + (int64_t)p.Hq * D))

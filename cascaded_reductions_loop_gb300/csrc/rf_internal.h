@@ -151,7 +151,7 @@ cudaError_t launch_attn_fwd_window(const void* Q, int64_t ldq, const void* K, in
                                    const int* cu_q, const int* cu_k, int B, int Hq, int Hkv,
                                    int max_q, int total_q, int total_k, int d, float scale,
                                    int window, int sinks, unsigned* err, cudaStream_t s);
-// Many query rows a kv head over a bf16 cache.
+// Many query rows a kv head.
 size_t masked_rows_workspace_bytes(int d);
 cudaError_t launch_masked_rows(const PagedKV& c, const Mask& mask, const void* Q, void* O, int Hq,
                                int Tq, float scale, void* workspace, unsigned* err,

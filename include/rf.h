@@ -623,6 +623,13 @@ size_t rf_attn_decode_paged_ex_workspace_size(int B, int Hq, int Hkv, int Tq, in
  * Tq - 1 tokens, and a node whose line of parents meets an entry that is neither
  * -1 nor that of an earlier node, are reported as RF_ERR_DEVICE_INPUT and their
  * rows written as zeros.
+ * With a mask (a window, or parents) and many query rows a kv head (Tq * Hq / Hkv
+ * more than 16 for RF_BF16, 40 for RF_E4M3; at most 128 heads a kv head) a weight is
+ * rounded once for the product with the values: RF_BF16 to bf16 (off by at most 2^-8
+ * of itself), RF_E4M3, times its v_scale, to f16 (2^-11 of itself, or 2^-32 of the
+ * row's largest where that is more; softmax weights below 2^-126 of the row's largest
+ * count as zero).
+ *   Sizes   as there; with a mask Tq <= 2^30.
  *   workspace   as there, of rf_attn_decode_paged_ex_workspace_size bytes.
  * Errors: those of rf_attn_decode_paged, and RF_ERR_INVALID_ARG for window or
  * sinks outside 0 .. 2^30 and a misaligned `parents`.

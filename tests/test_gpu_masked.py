@@ -35,8 +35,11 @@ def half_of_a_weight(kind, rows):
     return 2.0 ** -11 if kind == "e4m3" else (2.0 ** -16 if rows <= FEW_ROWS else 2.0 ** -8)
 
 
-def masked_reference(q, bt, scale, window=0, sinks=0, parents=None, lens=None):
-    """(o, tolerance) in fp64; the sum of the error bounds that the file's head names."""
+def masked_reference(q, bt, scale, window=0, sinks=0, parents=None, lens=None, floor=2.0 ** -25,
+                     below=2.0 ** -14, more=0.0):
+    """(o, tolerance) in fp64; the sum of the error bounds that the file's head names.
+    E4M3: weights below `below` of the row's largest are off by `floor` of it; `more` is
+    a further relative error of a weight."""
     q = to64(q)
     B, Tq, Hq, d = q.shape
     K, V = (G.values(*bt.host(i)) for i in (0, 1))
@@ -65,14 +68,14 @@ def masked_reference(q, bt, scale, window=0, sinks=0, parents=None, lens=None):
                 p /= p.sum(1, keepdims=True)
                 va = np.abs(vb)
                 e = (d + 8) * u * size.max(1) + 4 * u * np.abs(s).max(1) + 8 * u
-                per = 2 * e + half_of_a_weight(bt.kind, Tq * G_) + (len(j) / 8 + 64) * u
+                per = 2 * e + half_of_a_weight(bt.kind, Tq * G_) + (len(j) / 8 + 64) * u + more
                 o[b, t, rows] = p @ vb
                 tol[b, t, rows] = per[:, None] * (p @ va)
                 if e4m3:
                     w = p * vs
                     top = w.max(1, keepdims=True)
-                    small = w < 2.0 ** -14 * top
-                    tol[b, t, rows] += 2.0 ** -25 * top * (small @ (va / vs[:, None]))
+                    small = w < below * top
+                    tol[b, t, rows] += floor * top * (small @ (va / vs[:, None]))
     return o, tol + 2.0 ** -8 * (np.abs(o) + tol) + 1e-37
 
 
