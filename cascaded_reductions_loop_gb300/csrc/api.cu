@@ -569,6 +569,8 @@ rf_status rf_attn_decode_paged(const rf_paged_kv* cache, const void* Q, void* O,
                                  stream);
 }
 
+static constexpr int kMostNodes = 4096;
+
 static bool window_ok(int window, int sinks) {
   return window >= 0 && window <= (1 << 30) && sinks >= 0 && sinks <= (1 << 30);
 }
@@ -586,7 +588,8 @@ rf_status rf_attn_decode_paged_ex(const rf_paged_kv* cache, const void* Q, void*
                (reinterpret_cast<uintptr_t>(mask->parents) & 3u)))
     return RF_ERR_INVALID_ARG;
   const bool masked = mask && (mask->window != 0 || mask->parents);
-  if (masked && Tq > (1 << 30)) return RF_ERR_INVALID_ARG;
+  // a row walks up its line of parents, one load after the other, for every tile of nodes
+  if (masked && Tq > (mask->parents ? kMostNodes : 1 << 30)) return RF_ERR_INVALID_ARG;
   const int R = Hq / cache->Hkv * Tq;
   const bool many = masked && many_rows(R, Hq / cache->Hkv, cache->dtype == RF_E4M3);
   if (decode_paged_max_chunks(cache->B, cache->Hkv, R, cache->max_pages, cache->page_size) >=

@@ -810,7 +810,7 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
           }
           if (geo.tree && key0 + BK > ctx && pos >= 0) {
             int u = tok;
-            for (int at = pos; u >= 0; --at) {        // node u at position `at`
+            for (int at = pos; u >= 0 && ctx + u >= key0; --at) {      // node u at position `at`
               const int bit = ctx + u - key0;
               if (bit >= 0 && bit < BK &&
                   (geo.window == 0 || at > pos - geo.window || at < geo.sinks)) {

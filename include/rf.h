@@ -629,10 +629,10 @@ size_t rf_attn_decode_paged_ex_workspace_size(int B, int Hq, int Hkv, int Tq, in
  * of itself), RF_E4M3, times its v_scale, to f16 (2^-11 of itself, or 2^-32 of the
  * row's largest where that is more; softmax weights below 2^-126 of the row's largest
  * count as zero).
- *   Sizes   as there; with a mask Tq <= 2^30.
+ *   Sizes   as there; with a window Tq <= 2^30, with parents Tq <= 4096.
  *   workspace   as there, of rf_attn_decode_paged_ex_workspace_size bytes.
  * Errors: those of rf_attn_decode_paged, and RF_ERR_INVALID_ARG for window or
- * sinks outside 0 .. 2^30 and a misaligned `parents`.
+ * sinks outside 0 .. 2^30, a misaligned `parents` and too many query tokens.
  */
 rf_status rf_attn_decode_paged_ex(const rf_paged_kv* cache, const void* Q, void* O, int Hq, int Tq,
                                   float scale, const rf_attn_mask* mask, void* workspace,

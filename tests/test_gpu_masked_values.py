@@ -111,6 +111,15 @@ def test_queries_of_any_size(rf, exp):  # noqa: F811
 
 
 @pytest.mark.parametrize("kind", ["e4m3", "bf16"])
+@pytest.mark.parametrize("window", [0, 90])
+def test_trees_of_many_nodes(rf, kind, window):  # noqa: F811
+    """Lines of hundreds of parents, over several key tiles."""
+    bt = Batch(kind, [900, 650], 1, 64, 32, seed=968).garbage()
+    q = torch.randn(2, 650, 2, 64, generator=_gen(969)).to(BF16)
+    compare(rf, bt, q, 0.125, "many nodes", window, 3, [chain(650), tree_of(_gen(967), 650)])
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "bf16"])
 @pytest.mark.parametrize("Tq,Hq", [(24, 4), (45, 1)])
 def test_bad_trees(rf, kind, Tq, Hq):  # noqa: F811
     M.test_bad_trees_are_reported_and_their_rows_are_zeros(rf, kind, Tq, Hq)

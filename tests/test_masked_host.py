@@ -38,6 +38,9 @@ def test_attn_decode_paged_ex_refusals(rf):
         assert f(None, P, P, 8, 1, 0.1, m, P, big, None) == rf.RF_ERR_INVALID_ARG
         assert f(c, P, P, 8, 1, 0.1, m, None, big, None) == rf.RF_ERR_WORKSPACE
         assert f(c, P, P, 8, 1, 0.1, m, P + 4, big, None) == rf.RF_ERR_WORKSPACE
+    tree = _mask(rf, 0, 0, P)
+    assert f(c, P, P, 8, 4097, 0.1, tree, P, big, None) == rf.RF_ERR_INVALID_ARG
+    assert f(c, P, P, 8, 4096, 0.1, tree, None, big, None) == rf.RF_ERR_WORKSPACE
     for a in [(0, 8, 2, 1, 128), (1, 8, 3, 1, 128), (1, 8, 2, 0, 128), (1, 8, 2, 1, 96)]:
         assert rf.rf_attn_decode_paged_ex_workspace_size(*a) == 0
 
