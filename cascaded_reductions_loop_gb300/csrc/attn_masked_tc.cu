@@ -49,7 +49,7 @@ constexpr int kHalf = 128 * 128;                      // 128 rows of 64 values: 
 constexpr float kLazy = 8.f;
 constexpr float kTop = 7.f;                           // E4M3: log2 of P's first largest
 
-template <int D, bool kF8>
+template <int D, bool kPaged, bool kF8>
 struct Cfg {
   // TMA, S, P.V, guard; softmax a; softmax b; E4M3: four warps that widen the codes
   static constexpr int kThreads = kF8 ? 512 : 384;
@@ -67,6 +67,8 @@ struct Cfg {
   static constexpr int kRawPairs = kF8 ? (D == 64 ? 5 : 3) : 1;
   static constexpr int kBarOff = kRawOff + 2 * kRawPairs * kRaw;
   static constexpr int kSmem = kBarOff + 2048 + 1024; // barriers; alignment
+  // Prompts: the output goes through the item's own Q tile to whole 128-byte lines.
+  static constexpr bool kStaged = !kPaged;
   static constexpr uint32_t kIdescS = make_idesc(BQ, BK, kF8 ? 0 : 1, 0, 0);
   static constexpr uint32_t kIdescHalf = make_idesc(BQ, kUnit, kF8 ? 0 : 1, 0, 0);
   static constexpr uint32_t kIdescO = make_idesc(BQ, D, kF8 ? 0 : 1, 0, 1);
@@ -94,6 +96,8 @@ struct Params {
   unsigned* err;
 };
 
+constexpr int kPieces = 3;
+
 struct Bars {
   uint64_t q_full[4], q_empty[4];
   uint64_t full[8], empty[8];
@@ -111,7 +115,12 @@ struct Bars {
   uint64_t raw_full[2][5], raw_empty[2][5], q_ok[4];
   float sc_k[8][8], sc_v[8][8];
   float2 scale[8][8];
-  int64_t warp_sum[16];
+  // The TMA warp's pieces, for the softmax: walked once, ahead of time.
+  uint64_t piece_full[kPieces], piece_empty[kPieces];
+  union {
+    int64_t warp_sum[16];                             // of the plan, before there are pieces
+    Piece piece[kPieces];                             // j0 < 0: there are no more
+  };
   int64_t x[2], total;                                // the CTA's range, all tiles
   int g, h, j;                                        // where it begins
   uint32_t tmem;
@@ -204,11 +213,11 @@ enum : unsigned {
 };
 
 template <int D, bool kPaged, bool kF8>
-__global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
+__global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
     attn_masked_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
-  using C = Cfg<D, kF8>;
+  using C = Cfg<D, kPaged, kF8>;
   constexpr int kThreads = C::kThreads;
   static_assert(kPaged || !kF8, "codes are a cache's");
   extern __shared__ uint8_t smem_raw[];
@@ -229,7 +238,7 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
     prefetch_tmap(&tmV);
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 1);
-      mbar_init(smem_u32(&bars->q_empty[i]), 1);
+      mbar_init(smem_u32(&bars->q_empty[i]), C::kStaged ? 1 + 4 : 1);
       mbar_init(smem_u32(&bars->v_ok[i]), kF8 ? 2 : 1);
       mbar_init(smem_u32(&bars->q_ok[i]), BQ);
     }
@@ -244,6 +253,10 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
       mbar_init(smem_u32(&bars->pv_done[i]), 1);
     }
     mbar_init(smem_u32(&bars->s_read), 4);            // a warpgroup's warps
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(smem_u32(&bars->piece_full[i]), 1);
+      mbar_init(smem_u32(&bars->piece_empty[i]), 8);  // both warpgroups' warps
+    }
     mbar_init(smem_u32(&bars->drain[0]), 1);
     mbar_init(smem_u32(&bars->drain[1]), 1);
     if (kF8) {
@@ -341,15 +354,24 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
       const uint64_t pol_kv = policy_evict_last(), pol_q = policy_evict_first();
       int nq = 0, nt = 0;                             // Q tiles, key tiles issued
       unsigned in_flight = 0;                         // stages filled so far (2 a key tile)
-      while (ok && walk.next(geo, c, p.err)) {
-        for (int x = 0; ok && x < 2; ++x) {
-          const Tile t = tile_of(geo, c.w, x);
-          if (!t.has()) continue;
+      for (int np = 0; ok; ++np) {
+        const int pc = np % kPieces;
+        const bool last = !walk.next(geo, c, p.err);
+        if (last) c.j0 = -1;
+        ok = np < kPieces ||
+             warp_wait(smem_u32(&bars->piece_empty[pc]), (uint32_t)((np / kPieces - 1) & 1));
+        if (!ok) break;
+        if (lane == 0) {
+          bars->piece[pc] = c;
+          mbar_arrive(smem_u32(&bars->piece_full[pc]));
+        }
+        if (last) break;
+        const Tile ta = tile_of(geo, c.w, 0), tb = tile_of(geo, c.w, 1);
+        auto load_q = [&](const Tile& t) {
           const int slot = nq % C::kQSlots;
-          ok = __all_sync(0xffffffffu, nq < C::kQSlots ||
-                                           mbar_wait(smem_u32(&bars->q_empty[slot]),
-                                                     (uint32_t)((nq / C::kQSlots - 1) & 1)));
-          if (!ok) break;
+          ok = nq < C::kQSlots || warp_wait(smem_u32(&bars->q_empty[slot]),
+                                            (uint32_t)((nq / C::kQSlots - 1) & 1));
+          if (!ok) return;
           if (lane == 0) {
             const uint32_t bar = smem_u32(&bars->q_full[slot]);
             const uint32_t dst = smem_u32(smem + slot * C::kTile);
@@ -359,8 +381,10 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
               tma_load_3d_hint(dst + i * kHalf, &tmQ, bar, 64 * i, c.h * geo.G, c.w.q0 + t.t0, pol_q);
           }
           ++nq;
-        }
-        const Tile ta = tile_of(geo, c.w, 0), tb = tile_of(geo, c.w, 1);
+        };
+        load_q(ta);
+        // Q_b behind the first keys: its place may still have an output in it
+        if (!C::kStaged && ok && tb.has()) load_q(tb);
         const Whole whole = whole_of(geo, c.w);
         for (int j = c.j0; ok && j < c.j1; ++j, ++nt) {
           const int key0 = key0_of(c.w, j);
@@ -452,6 +476,7 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
             }
             ++in_flight;
           }
+          if (C::kStaged && ok && j == c.j0 && tb.has()) load_q(tb);
         }
         if (*abort_flag) ok = false;
         ok = __all_sync(0xffffffffu, ok);
@@ -722,7 +747,14 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
     int nt = 0, cnt = 0;                              // key tiles; events of this warpgroup
     int nq = 0;                                       // Q tiles
     int64_t s0 = x0 - (x1 > x0 ? bars->j : 0);        // first tile of the piece's item
-    while (ok && walk.next(geo, c, p.err)) {
+    for (int np = 0; ok; ++np) {
+      const int pc = np % kPieces;
+      ok = warp_wait(smem_u32(&bars->piece_full[pc]), (uint32_t)((np / kPieces) & 1));
+      if (!ok) break;
+      c = bars->piece[pc];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->piece_empty[pc]));
+      if (c.j0 < 0) break;
       const Tile t = tile_of(geo, c.w, x);
       const int64_t item0 = s0;
       s0 += c.w.n;
@@ -1078,13 +1110,18 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
       // E4M3: 2^(M - m) / l in two factors, since 2^(M - m) itself may underflow
       const float half = kF8 ? ex2(0.5f * (M_ref - m_ref)) : 1.f;
       const float inv = l_run == 0.f ? 0.f : half / l_run;
+      uint8_t* stage = smem + q_at % C::kQSlots * C::kTile;
+      if (C::kStaged) {                               // (a tile may have had no event)
+        ok = warp_wait(smem_u32(&bars->q_full[q_at % C::kQSlots]), (uint32_t)((q_at / C::kQSlots) & 1));
+        if (!ok) break;
+      }
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
         uint32_t o[32];
         tmem_ld32(o_addr + q * 32, o);
         tmem_ld_wait();
         if (all) {
-          if (out) {
+          if (out || C::kStaged) {
             // a row that read no key: zeros, whatever O holds
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -1094,7 +1131,14 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
                 u[k] = l_run == 0.f ? 0u
                                     : pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv * half,
                                                   __uint_as_float(o[8 * i + 2 * k + 1]) * inv * half);
-              reinterpret_cast<uint4*>(p.O + row)[q * 4 + i] = make_uint4(u[0], u[1], u[2], u[3]);
+              const uint4 o8 = make_uint4(u[0], u[1], u[2], u[3]);
+              if (C::kStaged) {
+                const int ch = q * 4 + i;
+                *reinterpret_cast<uint4*>(stage + (ch >> 3) * kHalf + r * 128 +
+                                          (((ch & 7) ^ (r & 7)) << 4)) = o8;
+              } else {
+                reinterpret_cast<uint4*>(p.O + row)[q * 4 + i] = o8;
+              }
             }
           }
         } else if (real) {
@@ -1106,6 +1150,26 @@ __global__ void __launch_bounds__((Cfg<D, kF8>::kThreads), 1)
                                        __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
           }
         }
+      }
+      if (C::kStaged) {
+        // A row of its own for each lane cost 32 lines a store and 1.6 us a tile; 8 lanes
+        // write a line of a row now.
+        __syncwarp();
+        const unsigned outs = __ballot_sync(0xffffffffu, out);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int from = i * 4 + (lane >> 3);       // the row's lane
+          const int64_t at = __shfl_sync(0xffffffffu, row, from);
+          const uint8_t* line = stage + (r - lane + from) * 128 + (((lane & 7) ^ (from & 7)) << 4);
+          if ((outs >> from) & 1u)
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              reinterpret_cast<uint4*>(p.O + at)[h * 8 + (lane & 7)] =
+                  *reinterpret_cast<const uint4*>(line + h * kHalf);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->q_empty[q_at % C::kQSlots]));
       }
       if (!all && real && RF_IN(p.err, slot * BQ + r, (int64_t)4 * gridDim.x * BQ))
         p.ws_st[slot * BQ + r] = make_float4(kF8 ? M_ref : m_ref, m_ref, l_run, 0.f);
@@ -1191,7 +1255,7 @@ __global__ void __launch_bounds__(BQ) merge_kernel(const __grid_constant__ Param
 
 template <int D, bool kPaged, bool kF8>
 cudaError_t launch(const CUtensorMap (&tm)[3], Params& p, int grid, cudaStream_t s) {
-  using C = Cfg<D, kF8>;
+  using C = Cfg<D, kPaged, kF8>;
   auto kern = attn_masked_kernel<D, kPaged, kF8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
