@@ -466,7 +466,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
               __syncwarp();
               if (kF8) {                              // 128-byte rows: a key, or two of 64 dims
                 if (there) {
-                  tma_load_2d_hint(dst + lane * p.page_size * D, tm, bar, 0, row * D / 128, pol_kv);
+                  tma_load_2d_hint(dst + lane * p.page_size * D, tm, bar, 0, D == 128 ? row : row >> 1, pol_kv);
                   if (v == 0 && RF_IN(p.err, scale_at, (int64_t)p.num_pages * geo.Hkv)) {
                     cp_async4(smem_u32(&bars->sc_k[nt % 8][lane]), p.k_scale + scale_at);
                     cp_async4(smem_u32(&bars->sc_v[nt % 8][lane]), p.v_scale + scale_at);

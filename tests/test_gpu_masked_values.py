@@ -177,3 +177,39 @@ def test_repeatable_in_place_on_two_streams(rf):  # noqa: F811
             rf.rf_attn_decode_paged_ex(cache, q, a, 0.0884, mask, ws[:1024])
         assert e.value.status == rf.RF_ERR_WORKSPACE
     assert rf.rf_get_device_status() == rf.RF_OK
+
+
+@pytest.mark.parametrize("kind,d,Tq", [(k, d, t) for k in ("e4m3", "bf16") for d in (64, 128)
+                                       for t in (1, 3, 16)])
+def test_pages_beyond_32_bits(rf, kind, d, Tq):  # noqa: F811
+    """A pool of more than 2^31 elements a tensor; the sequences live in its last pages,
+    a value that is not finite in front of the window."""
+    num_pages, ps, e = 140000, 128, kind == "e4m3"
+    bt = Batch(kind, [700, 310], 2, d, ps, seed=990)
+    base = num_pages - bt.num_pages
+    pages = [torch.zeros(num_pages, 2, ps, d, dtype=torch.uint8 if e else BF16, device="cuda")
+             for _ in range(2)]
+    scales = [torch.ones(num_pages, 2, device="cuda") if e else None for _ in range(2)]
+    q = torch.randn(2, Tq, 8, d, generator=_gen(991)).to(BF16)
+    ref, tol = masked_reference(q, bt, d ** -0.5, 150, 4)
+    bt.pages[1][int(bt.table[0, 4]), 1, 20] = 0x7F if e else float("nan")       # key 532
+    for t in range(2):
+        pages[t][base:] = (torch.from_numpy(bt.pages[t]) if e else bt.pages[t]).cuda()
+        if e:
+            scales[t][base:] = torch.from_numpy(bt.scale[t]).cuda()
+    cache = rf.rf_paged_kv(pages[0], pages[1], (bt.table + base).cuda(),
+                           torch.tensor(bt.lens, dtype=torch.int32, device="cuda"), *scales)
+    got, status = run(rf, bt, q, d ** -0.5, 150, 4, cache=cache)
+    assert status == rf.RF_OK
+    assert (np.abs(to64(got) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "bf16"])
+@pytest.mark.parametrize("G_", [128, 130])
+def test_groups_of_a_whole_tile_and_more(rf, kind, G_):  # noqa: F811
+    """More heads than a tile's 128 rows take the kernel with tiles of 16."""
+    bt = Batch(kind, [200, 0, 33], 1, 64, 16, seed=995).garbage()
+    for Tq, window, sinks, tree in ((1, 20, 3, False), (3, 0, 0, True)):
+        q = torch.randn(3, Tq, G_, 64, generator=_gen(996)).to(BF16)
+        M.check(rf, bt, q, 0.125, window, sinks, [tree_of(_gen(997), Tq)] * 3 if tree else None,
+                f"{G_} heads")
