@@ -569,6 +569,9 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
   constexpr int W = C::kWarps, S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared<W, S> sh;
+  // kExt: a tile's rows: position + 1; which keys of a chunk they read
+  __shared__ int end_sh[kExt ? W : 1][C::kRows];
+  __shared__ unsigned seen_sh[kExt ? W : 1][C::kRows];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -873,11 +876,22 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
         }
         f[nt][0] = f[nt][1] = p.scale_log2;
       }
+      if (!kExt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int t = p.Tq == 1 ? 0 : min((r0_ + nt * 8 + 2 * c + e) / p.G, p.Tq - 1);
-        lim[nt][e] = cur_len - p.Tq + t + 1;             // keys this row reads
-        if (kExt && p.parents) {
+        for (int e = 0; e < 2; ++e) {
+          const int t = p.Tq == 1 ? 0 : min((r0_ + nt * 8 + 2 * c + e) / p.G, p.Tq - 1);
+          lim[nt][e] = cur_len - p.Tq + t + 1;           // keys this row reads
+        }
+    }
+    if (kExt) {
+      // A lane a row, through shared memory: the registers are the softmax's (at 16 rows
+      // in E4M3 350 bytes were spilled with a row's limits in each lane that has it, and
+      // 8000 keys took 82 us instead of the unmasked kernel's 62).
+      int end = 1;                                       // the row's position + 1
+      if (lane < C::kRows) {
+        const int t = p.Tq == 1 ? 0 : min((r0_ + lane) / p.G, p.Tq - 1);
+        end = cur_len - p.Tq + t + 1;
+        if (p.parents) {
           // a node's position is that of its depth; parents come before children,
           // so the walk ends
           int u = t, depth = 0;
@@ -889,22 +903,18 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
             u = up;
             ++depth;
           }
-          if (!line && g == 0) raise_error(p.err, kDevErrInput);
-          lim[nt][e] = line ? cur_len - p.Tq + depth + 1 : 0;
+          if (!line) raise_error(p.err, kDevErrInput);
+          end = line ? cur_len - p.Tq + depth + 1 : 0;
         }
+        end_sh[warp][lane] = end;
       }
-    }
-    if (kExt) {
-      cut_off = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) cut_off |= lim[nt][0] <= 0 || lim[nt][1] <= 0;
-      cut_off = __any_sync(0xffffffffu, cut_off);
+      cut_off = __any_sync(0xffffffffu, end <= 0);
     }
   };
 
-  // kExt: which of the chunk's keys row (nt, e) of this lane reads.
-  auto seen_by = [&](int key0, int nt, int e) -> unsigned {
-    const int end = lim[nt][e];                          // its position + 1
+  // kExt: which of the chunk's keys the tile's row r reads.
+  auto seen_by = [&](int key0, int r) -> unsigned {
+    const int end = end_sh[warp][r];                     // its position + 1 (this lane's own)
     if (end <= 0) return 0u;
     const unsigned win = lens.window == 0 ? 0xFFFFFFFFu
                                           : ~bits_below(end - lens.window - key0) |
@@ -914,8 +924,8 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     unsigned w = win & bits_below(ctx - key0);
     if (key0 + kChunk > ctx) {
       const int h = p.tiles == 1 ? cur_hr : cur_hr / p.tiles;
-      int u = min(((cur_hr - h * p.tiles) * kTileRows + nt * 8 + 2 * c + e) / p.G, p.Tq - 1);
-      for (int at = end - 1; u >= 0; --at) {             // node u at position `at`
+      int u = min(((cur_hr - h * p.tiles) * kTileRows + r) / p.G, p.Tq - 1);
+      for (int at = end - 1; u >= 0 && ctx + u >= key0; --at) {          // node u at position `at`
         const int bit = ctx + u - key0;
         if (bit >= 0 && bit < kChunk &&
             (lens.window == 0 || at >= end - lens.window || at < lens.sinks))
@@ -1093,19 +1103,20 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     uint32_t pb[2][NT][kF8 ? 1 : 2][2];
     const bool two = kF8 && lv[0] != lv[1];
     float cm[NT][2], cM[NT][2], mu[NT][2], Mu[NT][2], a_o[NT][2];
-    unsigned seen[NT][2];
     if (kExt && tail) {
       const unsigned there = ((valid & 1) ? 0xFFFFu : 0u) | ((valid & 2) ? 0xFFFF0000u : 0u);
+      if (lane < C::kRows) seen_sh[warp][lane] = seen_by(key0, lane) & there;
+      __syncwarp();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          seen[nt][e] = seen_by(key0, nt, e) & there;
+          const unsigned seen = seen_sh[warp][nt * 8 + 2 * c + e];
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-              if (!((seen[nt][e] >> (16 * h2 + g + 8 * k)) & 1u)) s[h2][nt][2 * k + e] = -INFINITY;
+              if (!((seen >> (16 * h2 + g + 8 * k)) & 1u)) s[h2][nt][2 * k + e] = -INFINITY;
         }
     }
     if (!kExt && tail) {
@@ -1215,27 +1226,18 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
       pv16<kF8, D, NT, kAll>(o, vb, 0, lane, Below{0}, 0u, pb[0]);
       pv16<kF8, D, NT, kAll>(o, vb, 1, lane, Below{0}, 0u, pb[1]);
     } else if (kExt) {
-      unsigned any = 0u, all = 0xFFFFFFFFu;    // keys that some row, that every row reads
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          any |= seen[nt][e];
-          all &= seen[nt][e];
-        }
-      any = __reduce_or_sync(0xffffffffu, any);
-      all = __reduce_and_sync(0xffffffffu, all);
+      // keys that some row, that every row reads
+      const unsigned mine = seen_sh[warp][lane % C::kRows];
+      const unsigned any = __reduce_or_sync(0xffffffffu, mine);
+      const unsigned all = __reduce_and_sync(0xffffffffu, mine);
       if (any_nonfinite<kF8, D>(vb, lane, 0, kChunk, Among{any & ~all})) {
 #pragma unroll 1
-        for (int r = 0; r < 8; ++r)            // a row at a time
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const unsigned a = __shfl_sync(0xffffffffu, seen[nt][0], r >> 1),
-                           b = __shfl_sync(0xffffffffu, seen[nt][1], r >> 1);
-            const unsigned rows = c == (r >> 1) ? 1u << (2 * nt + (r & 1)) : 0u;
-            pv16<kF8, D, NT, kSome>(o, vb, 0, lane, Among{(r & 1) ? b : a}, rows, pb[0]);
-            pv16<kF8, D, NT, kSome>(o, vb, 1, lane, Among{(r & 1) ? b : a}, rows, pb[1]);
-          }
+        for (int r = 0; r < C::kRows; ++r) {   // a row at a time
+          const unsigned seen = seen_sh[warp][r];
+          const unsigned rows = c == ((r & 7) >> 1) ? 1u << (2 * (r >> 3) + (r & 1)) : 0u;
+          pv16<kF8, D, NT, kSome>(o, vb, 0, lane, Among{seen}, rows, pb[0]);
+          pv16<kF8, D, NT, kSome>(o, vb, 1, lane, Among{seen}, rows, pb[1]);
+        }
       } else {
         pv16<kF8, D, NT, kMasked>(o, vb, 0, lane, Among{any}, 0u, pb[0]);
         pv16<kF8, D, NT, kMasked>(o, vb, 1, lane, Among{any}, 0u, pb[1]);
