@@ -558,6 +558,26 @@ __device__ __forceinline__ bool any_nonfinite(uint32_t base, int lane, int lo, i
   return __any_sync(0xffffffffu, bad);
 }
 
+// The same for the keys whose bit is set, all 32 side by side (a key after the other took
+// 1.1 us a chunk, as long as three chunks' products).
+template <bool kF8, int D>
+__device__ __forceinline__ bool any_nonfinite_among(uint32_t base, int lane, unsigned bits) {
+  if (bits == 0u) return false;
+  constexpr int L = kF8 ? D / 16 : D / 8;              // lanes of a key
+  constexpr unsigned kExp = kF8 ? 0x7F7F7F7Fu : 0x7F807F80u, kOne = kF8 ? 0x01010101u : 0x00800080u;
+  unsigned bad = 0u;                                   // an exponent of ones carries into the sign
+#pragma unroll 4
+  for (int i = 0; i < L; ++i) {
+    const int key = i * (32 / L) + lane / L;
+    uint32_t w[4];
+    lds128(base + (kF8 ? f8_off<D>(key, (lane % L) * 16) : bf_off(key, lane % L)), w);
+    const unsigned x = ((w[0] & kExp) + kOne) | ((w[1] & kExp) + kOne) | ((w[2] & kExp) + kOne) |
+                       ((w[3] & kExp) + kOne);
+    bad |= (bits >> key) & 1u ? x : 0u;
+  }
+  return __any_sync(0xffffffffu, (bad & (kF8 ? 0x80808080u : 0x80008000u)) != 0u);
+}
+
 // ------------------------------------------------------------- the kernel
 
 template <bool kF8, int D, int NT, bool kExt>
@@ -1230,7 +1250,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
       const unsigned mine = seen_sh[warp][lane % C::kRows];
       const unsigned any = __reduce_or_sync(0xffffffffu, mine);
       const unsigned all = __reduce_and_sync(0xffffffffu, mine);
-      if (any_nonfinite<kF8, D>(vb, lane, 0, kChunk, Among{any & ~all})) {
+      if (any_nonfinite_among<kF8, D>(vb, lane, any & ~all)) {
 #pragma unroll 1
         for (int r = 0; r < C::kRows; ++r) {   // a row at a time
           const unsigned seen = seen_sh[warp][r];
