@@ -541,23 +541,23 @@ size_t rf_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Tq, int d
 }
 
 // With a mask and more query rows a kv head than this, the tensor-core kernel with tiles
-// of 128 rows takes the call; the kernel with tiles of 16 rows reads the cache once for up
-// to 16 of them, then its time grows with the rows.  128-row tiles against 16-row tiles,
-// heads 32/8, d = 128, trees over caches of 500 to 8000 tokens:
-//   bf16, 16 sequences: 16 rows 81 us against 75, 20 rows 81 against 116, 64 rows 84
-//     against 203, 256 rows 122 against 1001; one sequence of 16000 tokens: 20 rows 59
-//     against 50, 40 rows 61 against 61, 128 rows 59 against 106.
-//   E4M3 (the 128-row tiles' codes are widened to f16 first), 16 sequences: 16 rows 124 us
-//     against 71, 32 rows 136 against 110, 40 rows 124 against 138, 64 rows 126 against
-//     181, 256 rows 188 against 952; 64 sequences: 32 rows 445 against 347, 64 rows 448
-//     against 722; one sequence of 16000 tokens: 48 rows 71 against 59, 64 rows 71 against
-//     65, 128 rows 71 against 100.
-static constexpr int kFewRows = 16, kFewRowsF8 = 40;
-static bool many_rows(int R, int G, bool f8) { return R > (f8 ? kFewRowsF8 : kFewRows) && G <= 128; }
+// of 128 rows takes the call; the kernel with tiles of 16 rows reads (and, in E4M3, widens)
+// the keys again for every 16 of them.  128-row tiles against 16-row tiles, us, trees over
+// caches of 500 to 8000 tokens (16 sequences where nothing else is said), cold L2:
+//   d = 128, 8 kv heads, bf16: 16 rows 74 against 67, 20 rows 77 against 104, 64 rows 75
+//     against 176; one sequence of 16000 tokens: 20 rows 52 against 44, 64 rows 46 against 61
+//   d = 128, 8 kv heads, E4M3: 32 rows 120 against 85, 48 rows 124 against 110, 52 rows 118
+//     against 136; 64 sequences: 48 rows 437 against 401, 64 rows 421 against 528; one
+//     sequence of 16000 tokens: 64 rows 62 against 52, 80 rows 61 against 61
+//   d = 64, 8 kv heads, bf16: 32 rows 69 against 67, 48 rows 70 against 85
+//   d = 64, 8 kv heads, E4M3: 64 rows 108 against 102, 80 rows 118 against 116, 96 rows 114
+//     against 137
+static int few_rows(int d, bool f8) { return d == 64 ? (f8 ? 80 : 32) : (f8 ? 48 : 16); }
+static bool many_rows(int R, int G, int d, bool f8) { return R > few_rows(d, f8) && G <= 128; }
 
 size_t rf_attn_decode_paged_ex_workspace_size(int B, int Hq, int Hkv, int Tq, int d) {
   const size_t few = rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq, d);
-  if (few == 0 || !many_rows(Hq / Hkv * Tq, Hq / Hkv, false)) return few;
+  if (few == 0 || !many_rows(Hq / Hkv * Tq, Hq / Hkv, d, false)) return few;
   const size_t many = masked_rows_workspace_bytes(d);
   return many > few ? many : few;
 }
@@ -591,7 +591,7 @@ rf_status rf_attn_decode_paged_ex(const rf_paged_kv* cache, const void* Q, void*
   // a row walks up its line of parents, one load after the other, for every tile of nodes
   if (masked && Tq > (mask->parents ? kMostNodes : 1 << 30)) return RF_ERR_INVALID_ARG;
   const int R = Hq / cache->Hkv * Tq;
-  const bool many = masked && many_rows(R, Hq / cache->Hkv, cache->dtype == RF_E4M3);
+  const bool many = masked && many_rows(R, Hq / cache->Hkv, cache->d, cache->dtype == RF_E4M3);
   if (decode_paged_max_chunks(cache->B, cache->Hkv, R, cache->max_pages, cache->page_size) >=
       (1ll << 31))
     return RF_ERR_INVALID_ARG;

@@ -301,12 +301,13 @@ def test_in_place_and_repeatable(rf):
     assert rf.rf_get_device_status() == rf.RF_OK
 
 
-def test_draft_verify_accept_in_a_graph(rf):
+@pytest.mark.parametrize("Tq", [6, 12])
+def test_draft_verify_accept_in_a_graph(rf, Tq):
     """A drafting loop: norm and rotation of the nodes at their depths, append, attention
     over the tree; the accepted line is appended again behind the context and the next tree
     follows.  Captured once, replayed with trees, lengths and positions that change; each
     step equals the oracle's for the cache it left."""
-    B, Tq, Hq, Hkv, d, ps, window = 2, 6, 4, 1, 64, 16, 50
+    B, Hq, Hkv, d, ps, window = 2, 4, 1, 64, 16, 50
     bt = Batch("bf16", [300, 300], Hkv, d, ps, seed=500)
     cache = bt.device(rf, [40, 61])
     a = torch.arange(400, dtype=torch.float64)[:, None] * \
