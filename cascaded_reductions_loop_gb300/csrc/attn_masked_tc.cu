@@ -1204,7 +1204,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
 // the item in which CTA c's range begins, if that is the item's first cut: tile x, kDims
 // of its dims, a thread a row; pieces in key order.  The first is CTA c - 1's last, the
 // others are the first of the CTAs from c on.
-constexpr int kDims = 16;
+constexpr int kDims = 8;
 template <int D>
 __global__ void __launch_bounds__(BQ) merge_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1219,34 +1219,42 @@ __global__ void __launch_bounds__(BQ) merge_kernel(const __grid_constant__ Param
   const Tile t = tile_of(geo, w, x);
   const int my_t = r / geo.G, tok = t.t0 + my_t;
   if (my_t >= geo.tpt || tok >= t.t1) return;
+  // All pieces' references first, then their sums, each loop with many loads in flight
+  // and no branch (one running loop took 0.5 us a piece).  A piece that read no key has
+  // l = 0, and its O may be anything.
   constexpr int kQuads = kDims / 4;
+  const int64_t slots = (int64_t)4 * ctas;
+  auto slot = [&](int i) -> int64_t {
+    return (i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c - 1 + i)) * 2 + x;
+  };
+  auto state = [&](int64_t s) -> float4 {
+    return RF_IN(p.err, s, slots) ? __ldcg(&p.ws_st[s * BQ + r]) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
   float M = -INFINITY, m = -INFINITY, l = 0.f, v[kDims];        // bf16: M = m
+#pragma unroll 8
+  for (int i = 0; i < pieces; ++i) {
+    const float4 st = state(slot(i));
+    M = fmaxf(M, st.z == 0.f ? -INFINITY : st.x);
+    m = fmaxf(m, st.z == 0.f ? -INFINITY : st.y);
+  }
+  const float Mu = M == -INFINITY ? 0.f : M, mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
   for (int k = 0; k < kDims; ++k) v[k] = 0.f;
 #pragma unroll 4
   for (int i = 0; i < pieces; ++i) {
-    const int64_t s = (i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c - 1 + i)) * 2 + x;
-    const int64_t at = (s * (D / 4) + part * kQuads) * BQ + r;
-    if (!RF_IN(p.err, s * BQ + r, (int64_t)4 * ctas * BQ) ||
-        !RF_IN(p.err, at + (kQuads - 1) * BQ, (int64_t)4 * ctas * (D / 4) * BQ))
-      continue;
-    const float4 st = __ldcg(&p.ws_st[s * BQ + r]);
-    float4 u[kQuads];
-#pragma unroll
-    for (int k = 0; k < kQuads; ++k) u[k] = __ldcg(&p.ws_o[at + k * BQ]);
-    if (st.z == 0.f) continue;                        // read no key: its O may be anything
-    const float Mn = fmaxf(M, st.x), Mu = Mn == -INFINITY ? 0.f : Mn;
-    const float mn = fmaxf(m, st.y), mu = mn == -INFINITY ? 0.f : mn;
-    const float keep = ex2(M - Mu), f = ex2(st.x - Mu);
-    l = fmaf(l, ex2(m - mu), st.z * ex2(st.y - mu));
-    M = Mn;
-    m = mn;
+    const int64_t s = slot(i), at = (s * (D / 4) + part * kQuads) * BQ + r;
+    const float4 st = state(s);
+    const bool some = st.z != 0.f;
+    const float f = some ? ex2(st.x - Mu) : 0.f;
+    l = fmaf(st.z, some ? ex2(st.y - mu) : 0.f, l);
 #pragma unroll
     for (int k = 0; k < kQuads; ++k) {
-      v[4 * k] = fmaf(v[4 * k], keep, u[k].x * f);
-      v[4 * k + 1] = fmaf(v[4 * k + 1], keep, u[k].y * f);
-      v[4 * k + 2] = fmaf(v[4 * k + 2], keep, u[k].z * f);
-      v[4 * k + 3] = fmaf(v[4 * k + 3], keep, u[k].w * f);
+      const float4 u = RF_IN(p.err, at + k * BQ, slots * (D / 4) * BQ) ? __ldcg(&p.ws_o[at + k * BQ])
+                                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[4 * k] = fmaf(some ? u.x : 0.f, f, v[4 * k]);
+      v[4 * k + 1] = fmaf(some ? u.y : 0.f, f, v[4 * k + 1]);
+      v[4 * k + 2] = fmaf(some ? u.z : 0.f, f, v[4 * k + 2]);
+      v[4 * k + 3] = fmaf(some ? u.w : 0.f, f, v[4 * k + 3]);
     }
   }
   const int64_t row = ((int64_t)w.q0 + tok) * p.ldo +
@@ -1275,7 +1283,7 @@ cudaError_t launch(const CUtensorMap (&tm)[3], Params& p, int grid, cudaStream_t
   e = cudaGetLastError();
   if (e != cudaSuccess || !kPaged || grid < 2) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid - 1, 2, D / kDims);
+  cfg.gridDim = dim3((unsigned)grid - 1, p.geo.max_q > p.geo.tpt ? 2 : 1, D / kDims);
   cfg.blockDim = dim3(BQ, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
