@@ -130,7 +130,10 @@ struct Bars {
   // The TMA warp's pieces, for the softmax: walked once, ahead of time.
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   union {
-    int64_t warp_sum[16];                             // of the plan, before there are pieces
+    struct {                                          // of the plan, before there are pieces
+      int64_t warp_sum[16];
+      int warp_items[16], warp_most[16];
+    };
     Piece piece[kPieces];                             // j0 < 0: there are no more
   };
   int64_t x[2], total;                                // the CTA's range, all tiles
@@ -294,25 +297,69 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
   const int per = (ng + kThreads - 1) / kThreads;
   const int g_lo = min((int)threadIdx.x * per, ng), g_hi = min(g_lo + per, ng);
   int64_t mine = 0;
-  for (int g = g_lo; g < g_hi; ++g)
-    mine += (int64_t)places(geo, group_of(geo, g, cta == 0, p.err)) * geo.Hkv;
+  int items = 0, most = 0;                            // (items: at most B Tq Hq, below 2^31)
+  for (int g = g_lo; g < g_hi; ++g) {
+    const int n = places(geo, group_of(geo, g, cta == 0, p.err));
+    mine += (int64_t)n * geo.Hkv;
+    items += kPaged && n > 0 ? geo.Hkv : 0;
+    most = max(most, n);
+  }
   int64_t incl = mine;
+  int incl_items = items;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
+    if (kPaged) {
+      const int u = __shfl_up_sync(0xffffffffu, incl_items, o);
+      if (lane >= o) incl_items += u;
+    }
   }
-  if (lane == 31) bars->warp_sum[warp] = incl;
+  if (kPaged) most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    bars->warp_sum[warp] = incl;
+    bars->warp_items[warp] = incl_items;
+    bars->warp_most[warp] = most;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   int64_t pre = incl - mine, total = 0;
+  int pre_items = incl_items - items, all_items = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) pre += bars->warp_sum[w];
+    if (w < warp) {
+      pre += bars->warp_sum[w];
+      pre_items += bars->warp_items[w];
+    }
     total += bars->warp_sum[w];
+    all_items += bars->warp_items[w];
+    most = max(most, bars->warp_most[w]);
   }
   const int grid = total < (int64_t)gridDim.x ? (int)total : (int)gridDim.x;
-  if (cta < grid) {
+  if (kPaged && cta < grid && keeps_items(all_items, most, total, grid)) {
+    for (int i = 0; i < 2; ++i) {                     // item cta + i begins a range
+      const int x = cta + i;
+      if (x >= all_items) {
+        if (threadIdx.x == 0) bars->x[i] = total;
+      } else if (x >= pre_items && x - pre_items < items) {
+        int64_t at = pre;
+        int left = x - pre_items;
+        for (int g = g_lo; g < g_hi; ++g) {
+          const int n = places(geo, group_of(geo, g, false, p.err));
+          if (n > 0 && left < geo.Hkv) {
+            bars->x[i] = at + (int64_t)left * n;
+            if (i == 0) {
+              bars->g = g;
+              bars->h = left;
+            }
+            break;
+          }
+          at += (int64_t)n * geo.Hkv;
+          left -= n > 0 ? geo.Hkv : 0;
+        }
+      }
+    }
+  } else if (cta < grid) {
     const Split64 split(total, grid);
     for (int i = 0; i < 2; ++i) {
       const int64_t x = split.start(cta + i);
@@ -1439,8 +1486,14 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
   unsigned err = 0;
   const int ng = p.B * p.npairs;
   std::vector<int64_t> pre((size_t)ng + 1, 0);
-  for (int g = 0; g < ng; ++g)
-    pre[(size_t)g + 1] = pre[(size_t)g] + (int64_t)places(p, group_of(p, g, true, &err)) * Hkv;
+  int64_t items = 0;
+  int most = 0;
+  for (int g = 0; g < ng; ++g) {
+    const int n = places(p, group_of(p, g, true, &err));
+    pre[(size_t)g + 1] = pre[(size_t)g] + (int64_t)n * Hkv;
+    most = imax(most, n);
+    items += n > 0 ? Hkv : 0;
+  }
   const int64_t total = pre[(size_t)ng];
   if (err & kDevErrBounds) return 1;
   const int grid = total < sms ? (int)total : sms;
@@ -1472,6 +1525,11 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
     if (rows[(size_t)b] != want_rows[(size_t)b]) return 5;
   if (total == 0) return 0;
   const Split64 split(total, grid);
+  const bool keep = seq_lens && keeps_items(items, most, total, grid);
+  std::vector<int64_t> begins;                        // of the items, if they are kept
+  for (int g = 0; keep && g < ng; ++g)
+    for (int h = 0; h < Hkv && pre[(size_t)g + 1] > pre[(size_t)g]; ++h)
+      begins.push_back(pre[(size_t)g] + (pre[(size_t)g + 1] - pre[(size_t)g]) / Hkv * h);
   int64_t at = 0;                                     // where the last range ended
   int wg = -1, wh = Hkv - 1, wj = 0, wn = 0;          // the next tile in the order of all
   std::vector<unsigned char> used((size_t)2 * sms, 0);
@@ -1480,7 +1538,8 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
     int64_t r[2];
     int start[3] = {0, 0, 0};
     for (int i = 0; i < 2; ++i) {
-      r[i] = split.start(c + i);
+      r[i] = !keep ? split.start(c + i)
+                   : ((size_t)(c + i) < begins.size() ? begins[(size_t)(c + i)] : total);
       if (r[i] >= total) continue;
       int g = 0;
       while (pre[(size_t)g + 1] <= r[i]) ++g;
@@ -1522,7 +1581,7 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
         ++wj;
       }
       if (pc.whole()) continue;
-      if (!seq_lens || ++cuts > 2) return 3;
+      if (!seq_lens || keep || ++cuts > 2) return 3;
       const int64_t slot = slot_of(c, item0, r[0]);
       if (slot < 0 || slot >= 2 * (int64_t)sms || used[(size_t)slot]++) return 3;
       if (pc.j0 == 0) parts.clear();

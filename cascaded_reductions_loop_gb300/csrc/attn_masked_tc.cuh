@@ -18,7 +18,8 @@
 // next to the cut), and an item counts as its tiles and kItemCost more, since what
 // surrounds them (queries, first scores, output) takes that long; over a cache, where
 // few items may have many tiles, an item is cut, the states of its pieces go to the
-// workspace and a second kernel merges them.
+// workspace and a second kernel merges them; but where there are no more items than CTAs
+// and none is much longer than an even range, each CTA takes one whole (keeps_items).
 #pragma once
 
 #include "rf_device.cuh"
@@ -148,6 +149,15 @@ struct Split64 {
     return (int)(x < big ? x / (q + 1) : rem + (x - big) / q);
   }
 };
+
+// Over a cache: items (most: the tiles of the longest) that are not cut.  A cut costs a
+// second piece's start and output and the merge.  Trees of 16 nodes, 8 kv heads of 128, cut
+// against whole, us: 16 sequences of 250 / 1000 / 2500 tokens 17 / 34 / 53 against 15 / 24 / 45,
+// of 100 to 2000 41 against 31; one sequence (8 items) of 500 / 1000 14 / 15 against 17 / 23.
+// 64 nodes, 8 sequences (64 items) of 1500 / 2000 tokens: 37 / 41 against 36 / 44.
+__host__ __device__ __forceinline__ bool keeps_items(int64_t items, int most, int64_t total, int grid) {
+  return items <= grid && most <= total / grid + (4 * items > grid ? 7 : 1);
+}
 
 // Where whole items are taken: the border next to place `off` of an item that counts
 // as `all`; its tile there.
