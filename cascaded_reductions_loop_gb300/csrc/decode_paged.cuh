@@ -80,10 +80,10 @@
 // before them and, of the nodes, those on its line of parents, each at the position
 // of its depth.  A chunk that every row reads whole takes no other step than
 // without masks; in the others a row's keys are a word of 32 bits.  A call among others:
-//   32 x 24-32k keys, window 4096, E4M3, 8 kv heads of 4      60 us   0.27 GB   4.5 TB/s
-//   48 x 1-4k keys, window 500, bf16, 16 heads of 64          33 us   0.10 GB   2.9 TB/s
-//   16 x 0.5-8k keys, four query tokens, window 2048, E4M3    45 us   (two tiles of 16)
-//   one tree of 8 nodes over 1000 tokens / one step, window 1024   22.5 / 14.4 us, latency
+//   32 x 24-32k keys, window 4096, E4M3, 8 kv heads of 4      57 us   0.27 GB   4.7 TB/s
+//   48 x 1-4k keys, window 500, bf16, 16 heads of 64          28 us   0.10 GB   3.4 TB/s
+//   16 x 0.5-8k keys, four query tokens, window 2048, E4M3    35 us   (two tiles of 16)
+//   one tree of 8 nodes over 1000 tokens / one step, window 1024   17.8 / 14.3 us, latency
 //
 // Masked places.  Keys behind a sequence's last may hold anything: scores are
 // selected, not added to, and values are replaced by zero.  Where the last Tq
@@ -906,7 +906,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
     if (kExt) {
       // A lane a row, through shared memory: the registers are the softmax's (at 16 rows
       // in E4M3 350 bytes were spilled with a row's limits in each lane that has it, and
-      // 8000 keys took 82 us instead of the unmasked kernel's 62).
+      // 8000 keys took 82 us, now 69; without masks 62).
       int end = 1;                                       // the row's position + 1
       if (lane < C::kRows) {
         const int t = p.Tq == 1 ? 0 : min((r0_ + lane) / p.G, p.Tq - 1);
