@@ -71,12 +71,14 @@ struct Cfg {
   static constexpr int kSoftmaxRegs = kF8 ? 200 : 216, kOtherRegs = kF8 ? 56 : 72;
   static constexpr int kTile = D / 64 * kHalf;        // 128 rows of D 16-bit values
   static constexpr int kQSlots = D == 64 ? 4 : (kF8 ? 2 : 3);
-  static constexpr int kStages = kF8 ? (D == 64 ? 4 : 2) : (D == 64 ? 8 : 4);  // K, V tiles in turn
-  static constexpr int kPairs = kStages / 2;
+  // Places of K and of V tiles (E4M3: widened; two of V, since the next waits for P.V; one
+  // and a third of codes is as fast)
+  static constexpr int kKs = kF8 ? (D == 64 ? 2 : 1) : (D == 64 ? 4 : 2);
+  static constexpr int kVs = kF8 ? 2 : kKs;
   static constexpr int kRing = kQSlots * kTile;
-  static constexpr int kRawOff = kRing + kStages * kTile;
+  static constexpr int kRawOff = kRing + (kKs + kVs) * kTile;
   static constexpr int kRaw = kF8 ? BK * D : 0;       // a tile's codes, K and V in turn
-  static constexpr int kRawPairs = kF8 ? (D == 64 ? 5 : 3) : 1;
+  static constexpr int kRawPairs = kF8 ? (D == 64 ? 5 : 2) : 1;
   static constexpr int kBarOff = kRawOff + 2 * kRawPairs * kRaw;
   static constexpr int kSmem = kBarOff + 2048 + 1024; // barriers; alignment
   // Prompts: the output goes through the item's own Q tile to whole 128-byte lines.
@@ -112,14 +114,14 @@ constexpr int kPieces = 3;
 
 struct Bars {
   uint64_t q_full[4], q_empty[4];
-  uint64_t full[8], empty[8];
+  uint64_t full[8], empty[8];                         // of K's places, from 4 on V's
   uint64_t v_ok[4];                                   // a V tile is looked over
   uint64_t rec_ok[8];                                 // over a cache: rec is set, for the softmax
   uint64_t s_full[2], p_full[2], pv_done[2];          // of a query tile's events
   uint64_t s_read;                                    // of all events: S is in registers
   uint64_t drain[2];
   // Per key tile.  That of tile m is written once V of tile m - 1 has a stage, so the P.V
-  // of tile m - 1 - kPairs is done and what was 8 tiles ago is not looked at any more.
+  // of tile m - 1 - kVs is done and what was 8 tiles ago is not looked at any more.
   unsigned rec[8];
   unsigned bad[4][4];                                 // per V stage: values that are not finite
   // E4M3: codes have come, are widened; queries are; per key tile, the pages' scales as
@@ -458,8 +460,6 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
                    (tb.takes(2 * i) || tb.takes(2 * i + 1));
           };
           if (both(j) && both(j + 1)) rec |= kYield;
-          const int st = 2 * (nt % C::kPairs);
-          const uint32_t ph = (uint32_t)((nt / C::kPairs - 1) & 1);
           // over a cache: lane i has the tile's page i
           int row = 0;
           int64_t scale_at = 0;
@@ -492,15 +492,16 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
 #pragma unroll
           for (int v = 0; v < 2; ++v) {               // K, then V
             const int rp = nt % C::kRawPairs;
-            const uint32_t bar = smem_u32(kF8 ? &bars->raw_full[v][rp] : &bars->full[st + v]);
+            const int ks = v ? C::kVs : C::kKs, st = nt % ks, sb = v ? 4 + st : st;
+            const uint32_t bar = smem_u32(kF8 ? &bars->raw_full[v][rp] : &bars->full[sb]);
             if (kF8)
               ok = nt < C::kRawPairs || warp_wait(smem_u32(&bars->raw_empty[v][rp]),
                                                   (uint32_t)((nt / C::kRawPairs - 1) & 1));
             else
-              ok = nt < C::kPairs || warp_wait(smem_u32(&bars->empty[st + v]), ph);
+              ok = nt < ks || warp_wait(smem_u32(&bars->empty[sb]), (uint32_t)((nt / ks - 1) & 1));
             if (!ok) break;
             const uint32_t dst = smem_u32(kF8 ? smem + C::kRawOff + (2 * rp + v) * C::kRaw
-                                              : ring + (st + v) * C::kTile);
+                                              : ring + ((v ? C::kKs : 0) + st) * C::kTile);
             const CUtensorMap* tm = v ? &tmV : &tmK;
             if (kPaged) {
               if (lane == 0) {
@@ -547,10 +548,10 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         for (int i = max(0, nq - C::kQSlots); i < nq; ++i)
           (void)mbar_wait(smem_u32(&bars->q_full[i % C::kQSlots]), (uint32_t)((i / C::kQSlots) & 1),
                           1000000ull);
-        constexpr unsigned kPlaces = kF8 ? 2 * C::kRawPairs : C::kStages;
+        constexpr unsigned kPlaces = 2 * (kF8 ? C::kRawPairs : C::kKs);
         for (unsigned i = in_flight > kPlaces ? in_flight - kPlaces : 0; i < in_flight; ++i)
           (void)mbar_wait(smem_u32(kF8 ? &bars->raw_full[i % 2][i / 2 % C::kRawPairs]
-                                       : &bars->full[i % kPlaces]),
+                                       : &bars->full[i % 2 * 4 + i / 2 % C::kKs]),
                           (i / kPlaces) & 1, 1000000ull);
       }
     } else if (warp < 3) {
@@ -565,8 +566,8 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         int nq = 0, q_at = 0;                         // Q tiles before the next piece's, this one's
         int events = 0;
         for (int nt = 0; ok && more; ++nt) {
-          const int pr = nt % C::kPairs;
-          ok = warp_wait(smem_u32(&bars->full[2 * pr]), (uint32_t)((nt / C::kPairs) & 1));
+          const int pr = nt % C::kKs;
+          ok = warp_wait(smem_u32(&bars->full[pr]), (uint32_t)((nt / C::kKs) & 1));
           if (!ok) break;
           const unsigned rec = (unsigned)uniform((int)bars->rec[nt % 8]);
           more = !(rec & kEnd);
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
               tc_fence_after();
               const int h = halves == 2u ? 1 : 0;     // the first half it takes
               const uint64_t a = qd + (uint64_t)((slot * C::kTile) >> 4);
-              const uint64_t b = kd + (uint64_t)((2 * pr * C::kTile + h * kUnit * 128) >> 4);
+              const uint64_t b = kd + (uint64_t)((pr * C::kTile + h * kUnit * 128) >> 4);
               const uint32_t idesc = halves == 3u ? C::kIdescS : C::kIdescHalf;
               if (leader) {
 #pragma unroll
@@ -602,17 +603,17 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
             }
             if (ok && (rec & kLast) && leader) mma_commit(smem_u32(&bars->q_empty[slot]));
           }
-          if (ok && leader) mma_commit(smem_u32(&bars->empty[2 * pr]));
+          if (ok && leader) mma_commit(smem_u32(&bars->empty[pr]));
           if (*abort_flag) ok = false;
           ok = __all_sync(0xffffffffu, ok);
         }
       } else {
-        const uint64_t vd = sw128_desc(smem_u32(ring + C::kTile), 1024, kHalf);
+        const uint64_t vd = sw128_desc(smem_u32(ring + C::kKs * C::kTile), 1024, kHalf);
         unsigned phase = 0, fresh = 3;                // bit x: of p_full[x]; O_x is to be overwritten
         constexpr int kPolls = 24;
         for (int nt = 0; ok && more; ++nt) {
-          const int pr = nt % C::kPairs;
-          ok = warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((nt / C::kPairs) & 1));
+          const int pr = nt % C::kVs;
+          ok = warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((nt / C::kVs) & 1));
           if (!ok) break;
           const unsigned rec = (unsigned)uniform((int)bars->rec[nt % 8]);
           more = !(rec & kEnd);
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
             const unsigned* b = bars->bad[pr];
             bad = (unsigned)uniform(((b[0] | b[1]) ? 1 : 0) | ((b[2] | b[3]) ? 2 : 0));
           }
-          const uint64_t b = vd + (uint64_t)((2 * pr * C::kTile) >> 4);
+          const uint64_t b = vd + (uint64_t)((pr * C::kTile) >> 4);
 #pragma unroll 1
           for (int x = 0; ok && x < 2; ++x) {
             const unsigned halves = (rec >> (2 * x)) & 3u;
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
             fresh &= ~(1u << x);
             phase ^= 1u << x;
           }
-          if (ok && leader) mma_commit(smem_u32(&bars->empty[2 * pr + 1]));
+          if (ok && leader) mma_commit(smem_u32(&bars->empty[4 + pr]));
           if (*abort_flag) ok = false;
           ok = __all_sync(0xffffffffu, ok);
         }
@@ -675,9 +676,9 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
                ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
       };
       for (int nt = 0; ok && more; ++nt) {
-        const int pr = nt % C::kPairs;
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->full[2 * pr + 1]),
-                                               (uint32_t)((nt / C::kPairs) & 1)));
+        const int pr = nt % C::kVs;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->full[4 + pr]),
+                                               (uint32_t)((nt / C::kVs) & 1)));
         if (!ok) break;
         const unsigned rec = bars->rec[nt % 8];
         more = !(rec & kEnd);
@@ -686,7 +687,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         for (int h = 0; h < 2; ++h) {
           unsigned bad[2] = {0u, 0u};
           if (((rec >> h) & kPartly) || pages != 0xFFu) {
-            uint4* v = reinterpret_cast<uint4*>(ring + (2 * pr + 1) * C::kTile) + h * (kUnit * 8);
+            uint4* v = reinterpret_cast<uint4*>(ring + (C::kKs + pr) * C::kTile) + h * (kUnit * 8);
             unsigned seen = 0;
 #pragma unroll
             for (int i = 0; i < D / 64; ++i)          // 64 rows of 128 bytes
@@ -730,7 +731,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
     const int v = (warp - 12) >> 1, h = warp & 1;     // K or V; the half of the key tile
     bool more = x1 > x0;
     for (int nt = 0; ok && more; ++nt) {
-      const int pr = nt % C::kPairs, rp = nt % C::kRawPairs;
+      const int ks = v ? C::kVs : C::kKs, pr = nt % ks, rp = nt % C::kRawPairs;
       ok = warp_wait(smem_u32(&bars->raw_full[v][rp]), (uint32_t)((nt / C::kRawPairs) & 1));
       if (!ok) break;
       const unsigned rec = bars->rec[nt % 8];
@@ -745,8 +746,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->rec_ok[nt % 8]));
       }
-      ok = nt < C::kPairs ||
-           warp_wait(smem_u32(&bars->empty[2 * pr + v]), (uint32_t)((nt / C::kPairs - 1) & 1));
+      ok = nt < ks || warp_wait(smem_u32(&bars->empty[4 * v + pr]), (uint32_t)((nt / ks - 1) & 1));
       if (!ok) break;
       const bool alone = v == 1 && (((rec >> h) & kPartly) || ((rec >> kPages) & 0xFFu) != 0xFFu);
 #pragma unroll 1
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         const int key = h * kUnit + i32 * 32 + lane;
         const int row = D == 128 ? key : key >> 1, base = D == 128 ? 0 : (key & 1) * 4;
         const uint8_t* raw = smem + C::kRawOff + (2 * rp + v) * C::kRaw + row * 128;
-        uint8_t* out = ring + (2 * pr + v) * C::kTile + key * 128;
+        uint8_t* out = ring + ((v ? C::kKs : 0) + pr) * C::kTile + key * 128;
         bool zero = false;
         if (alone) {
           unsigned nan = 0;
@@ -784,7 +784,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(smem_u32(&bars->raw_empty[v][rp]));
-        mbar_arrive(smem_u32(v ? &bars->v_ok[pr] : &bars->full[2 * pr]));
+        mbar_arrive(smem_u32(v ? &bars->v_ok[pr] : &bars->full[pr]));
       }
       if (*abort_flag) ok = false;
       ok = __all_sync(0xffffffffu, ok);
@@ -1065,8 +1065,8 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         l_run += s_lo + s_hi;
         tmem_st_wait();
         if (part) {
-          const int pr = tile % C::kPairs;
-          if (!warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((tile / C::kPairs) & 1))) return false;
+          const int pr = tile % C::kVs;
+          if (!warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((tile / C::kVs) & 1))) return false;
           const unsigned* bad = bars->bad[pr];
           if (((halves & 1u) && (bad[0] | bad[1])) || ((halves & 2u) && (bad[2] | bad[3]))) {
             // values that are not finite, for the rows that read them: P times value
