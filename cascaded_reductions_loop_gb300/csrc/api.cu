@@ -685,7 +685,8 @@ int rf_selftest_append_plan(const int32_t* block_table, const int32_t* seq_lens,
 
 static int decode_paged_plan(const int32_t* seq_lens, int B, int tiles, int max_len, int Tq,
                              int window, int sinks, int warps, int sms) {
-  if (!seq_lens || Tq < 1 || !window_ok(window, sinks) || B < 1 || tiles < 1 || max_len < 1 || max_len > (1 << 30) ||
+  if (!seq_lens || Tq < 1 || !window_ok(window, sinks) || B < 1 || tiles < 1 || max_len < 1 ||
+      max_len > (1 << 30) ||
       (warps != 4 && warps != 8) || sms < 1 || sms > (1 << 20) ||
       (int64_t)B * tiles > (1ll << 24) || (int64_t)B * tiles * (max_len / 32 + 1) >= (1ll << 31))
     return -1;

@@ -625,11 +625,10 @@ size_t rf_attn_decode_paged_ex_workspace_size(int B, int Hq, int Hkv, int Tq, in
  * rows written as zeros.
  * With a mask (a window, or parents) and many query rows a kv head (Tq * Hq / Hkv
  * more than 16 for RF_BF16, 48 for RF_E4M3, with d = 64 more than 32 and 80; at most
- * 128 query heads a kv head) a weight is
- * rounded once for the product with the values: RF_BF16 to bf16 (off by at most 2^-8
- * of itself), RF_E4M3, times its v_scale, to f16 (2^-11 of itself, or 2^-32 of the
- * row's largest where that is more; softmax weights below 2^-126 of the row's largest
- * count as zero).
+ * 128 query heads a kv head) a weight is rounded once for the product with the
+ * values: RF_BF16 to bf16 (off by at most 2^-8 of itself), RF_E4M3, times its
+ * v_scale, to f16 (2^-11 of itself, or 2^-32 of the row's largest where that is more;
+ * softmax weights below 2^-126 of the row's largest count as zero).
  *   Sizes   as there; with a window Tq <= 2^30, with parents Tq <= 4096.
  *   workspace   as there, of rf_attn_decode_paged_ex_workspace_size bytes.
  * Errors: those of rf_attn_decode_paged, and RF_ERR_INVALID_ARG for window or

@@ -27,7 +27,7 @@ Modules: ``attention`` (safe-softmax cascade, its incremental and
 multi-segment forms, the latent-KV decode), ``moe_gate`` (gate scores, top-k, softmax of the
 selected scores), ``fp8_quant_gemm`` (row absmax, E4M3 quantisation, GEMM,
 dequantisation), ``paged`` (norm and rotation, the paged cache's append and the
-decode attention over it, with windows, sinks and trees; prompts with a window).  Every function is pinned by tests under ``tests/`` against
-closed forms, library routines, brute force or worked examples; none is
+decode attention over it, with windows, sinks and trees; prompts with a window).
+Every function is pinned by tests under ``tests/`` against closed forms, library routines, brute force or worked examples; none is
 "parity unpinned".
 """
