@@ -71,6 +71,8 @@ struct Cfg {
   static constexpr int kSoftmaxRegs = kF8 ? 200 : 216, kOtherRegs = kF8 ? 56 : 72;
   static constexpr int kTile = D / 64 * kHalf;        // 128 rows of D 16-bit values
   static constexpr int kQSlots = D == 64 ? 4 : (kF8 ? 2 : 3);
+  // E4M3: a tile's softmax waits for that tile's queries, and converts them in place.
+  using Queries = QTurns<kQSlots, kF8>;
   // Places of K and of V tiles (E4M3: widened; two of V, since the next waits for P.V; one
   // and a third of codes is as fast)
   static constexpr int kKs = kF8 ? (D == 64 ? 2 : 1) : (D == 64 ? 4 : 2);
@@ -413,7 +415,8 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
     if (warp == 0) {
       // ---------------------------------------------------------- TMA
       const uint64_t pol_kv = policy_evict_last(), pol_q = policy_evict_first();
-      int nq = 0, nt = 0;                             // Q tiles, key tiles issued
+      typename C::Queries queries(geo);               // issued
+      int nt = 0;                                     // key tiles issued
       unsigned in_flight = 0;                         // stages filled so far (2 a key tile)
       for (int np = 0; ok; ++np) {
         const int pc = np % kPieces;
@@ -428,24 +431,23 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         }
         if (last) break;
         const Tile ta = tile_of(geo, c.w, 0), tb = tile_of(geo, c.w, 1);
-        auto load_q = [&](const Tile& t) {
-          const int slot = nq % C::kQSlots;
-          ok = nq < C::kQSlots || warp_wait(smem_u32(&bars->q_empty[slot]),
-                                            (uint32_t)((nq / C::kQSlots - 1) & 1));
+        auto load_q = [&](int x, const Tile& t) {
+          const QPlace at = queries.next(x);
+          ok = at.turn == 0 ||
+               warp_wait(smem_u32(&bars->q_empty[at.slot]), (uint32_t)((at.turn - 1) & 1));
           if (!ok) return;
           if (lane == 0) {
-            const uint32_t bar = smem_u32(&bars->q_full[slot]);
-            const uint32_t dst = smem_u32(smem + slot * C::kTile);
+            const uint32_t bar = smem_u32(&bars->q_full[at.slot]);
+            const uint32_t dst = smem_u32(smem + at.slot * C::kTile);
             mbar_arrive_expect_tx(bar, (uint32_t)(D / 64 * geo.tpt * geo.G * 128));
 #pragma unroll
             for (int i = 0; i < D / 64; ++i)
               tma_load_3d_hint(dst + i * kHalf, &tmQ, bar, 64 * i, c.h * geo.G, c.w.q0 + t.t0, pol_q);
           }
-          ++nq;
         };
-        load_q(ta);
+        load_q(0, ta);
         // Q_b behind the first keys: its place may still have an output in it
-        if (!C::kStaged && ok && tb.has()) load_q(tb);
+        if (!C::kStaged && ok && tb.has()) load_q(1, tb);
         const Whole whole = whole_of(geo, c.w);
         for (int j = c.j0; ok && j < c.j1; ++j, ++nt) {
           const int key0 = key0_of(c.w, j);
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
             }
             ++in_flight;
           }
-          if (C::kStaged && ok && j == c.j0 && tb.has()) load_q(tb);
+          if (C::kStaged && ok && j == c.j0 && tb.has()) load_q(1, tb);
         }
         if (*abort_flag) ok = false;
         ok = __all_sync(0xffffffffu, ok);
@@ -545,9 +547,13 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         raise_error(p.err, kDevErrTimeout);
         *abort_flag = 1;
         // copies in flight land before shared memory is released
-        for (int i = max(0, nq - C::kQSlots); i < nq; ++i)
-          (void)mbar_wait(smem_u32(&bars->q_full[i % C::kQSlots]), (uint32_t)((i / C::kQSlots) & 1),
-                          1000000ull);
+        for (int x = 0; x < 2; ++x) {
+          const int n = x ? queries.nb : queries.na;
+          for (int i = max(0, n - queries.places()); i < n; ++i) {
+            const QPlace at = queries.at(x, i);
+            (void)mbar_wait(smem_u32(&bars->q_full[at.slot]), (uint32_t)(at.turn & 1), 1000000ull);
+          }
+        }
         constexpr unsigned kPlaces = 2 * (kF8 ? C::kRawPairs : C::kKs);
         for (unsigned i = in_flight > kPlaces ? in_flight - kPlaces : 0; i < in_flight; ++i)
           (void)mbar_wait(smem_u32(kF8 ? &bars->raw_full[i % 2][i / 2 % C::kRawPairs]
@@ -563,7 +569,8 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       if (warp == 1) {
         const uint64_t qd = sw128_desc(smem_u32(smem), 1024, 16);
         const uint64_t kd = sw128_desc(smem_u32(ring), 1024, 16);
-        int nq = 0, q_at = 0;                         // Q tiles before the next piece's, this one's
+        typename C::Queries queries(geo);
+        QPlace qa = {0, 0}, qb = {0, 0};              // the piece's
         int events = 0;
         for (int nt = 0; ok && more; ++nt) {
           const int pr = nt % C::kKs;
@@ -573,15 +580,15 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
           more = !(rec & kEnd);
           const int tiles = (rec & kHasB) ? 2 : 1;
           if (rec & kFirst) {
-            q_at = nq;
-            nq += tiles;
+            qa = queries.next(0);
+            if (tiles == 2) qb = queries.next(1);
           }
 #pragma unroll 1
           for (int x = 0; ok && x < tiles; ++x) {
-            const int slot = (q_at + x) % C::kQSlots;
+            const int slot = x ? qb.slot : qa.slot;
             if (rec & kFirst)
               ok = warp_wait(smem_u32(kF8 ? &bars->q_ok[slot] : &bars->q_full[slot]),
-                             (uint32_t)(((q_at + x) / C::kQSlots) & 1));
+                             (uint32_t)((x ? qb.turn : qa.turn) & 1));
             const unsigned halves = (rec >> (2 * x)) & 3u;
             if (ok && halves) {
               if (events > 0) ok = warp_wait(smem_u32(&bars->s_read), (uint32_t)((events - 1) & 1));
@@ -804,7 +811,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
     const uint64_t c2 = f2(p.c_log2, p.c_log2);
     const int my_t = r / geo.G, my_g = r - my_t * geo.G;
     int nt = 0, cnt = 0;                              // key tiles; events of this warpgroup
-    int nq = 0;                                       // Q tiles
+    typename C::Queries queries(geo);
     int64_t s0 = x0 - (x1 > x0 ? bars->j : 0);        // first tile of the piece's item
     for (int np = 0; ok; ++np) {
       const int pc = np % kPieces;
@@ -819,9 +826,14 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       s0 += c.w.n;
       const int j_base = nt - c.j0;                   // key tile j is the CTA's j_base + j th
       nt += c.j1 - c.j0;
-      const int q_at = nq + x;
-      nq += tile_of(geo, c.w, 1).has() ? 2 : 1;
+      QPlace mine_q = queries.next(0);
+      if (tile_of(geo, c.w, 1).has()) {
+        const QPlace qb = queries.next(1);
+        if (x == 1) mine_q = qb;
+      }
       if (!t.has()) continue;
+      const int slot = mine_q.slot;
+      const uint32_t q_full = smem_u32(&bars->q_full[slot]);
       const int tok = t.t0 + my_t;
       const bool real = my_t < geo.tpt && tok < t.t1;
       const int ctx = c.w.lk - c.w.lq;
@@ -846,8 +858,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       if (kF8) {
         // The row's queries as f16, scaled by a power of two to a largest element in
         // [2^14, 2^15): exact down to 2^-28 of it.
-        const int slot = q_at % C::kQSlots;
-        if (!warp_wait(smem_u32(&bars->q_full[slot]), (uint32_t)((q_at / C::kQSlots) & 1))) {
+        if (!warp_wait(q_full, (uint32_t)(mine_q.turn & 1))) {
           ok = false;
           break;
         }
@@ -1160,7 +1171,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       tc_fence_after();
       if (pos < 0) l_run = 0.f;                       // it reads nothing: zeros
       const bool all = !kPaged || c.whole();
-      const int64_t slot = slot_of(cta, item0, x0) * 2 + x;
+      const int64_t state = slot_of(cta, item0, x0) * 2 + x;
       const int64_t row = ((int64_t)c.w.q0 + tok) * p.ldo + (int64_t)(c.h * geo.G + my_g) * D;
       const bool out = real && RF_IN(p.err, row + D - 1,
                                      ((int64_t)(kPaged ? geo.B * geo.max_q : geo.total_q) - 1) * p.ldo +
@@ -1168,9 +1179,9 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       // E4M3: 2^(M - m) / l in two factors, since 2^(M - m) itself may underflow
       const float half = kF8 ? ex2(0.5f * (M_ref - m_ref)) : 1.f;
       const float inv = l_run == 0.f ? 0.f : half / l_run;
-      uint8_t* stage = smem + q_at % C::kQSlots * C::kTile;
+      uint8_t* stage = smem + slot * C::kTile;
       if (C::kStaged) {                               // (a tile may have had no event)
-        ok = warp_wait(smem_u32(&bars->q_full[q_at % C::kQSlots]), (uint32_t)((q_at / C::kQSlots) & 1));
+        ok = warp_wait(q_full, (uint32_t)(mine_q.turn & 1));
         if (!ok) break;
       }
 #pragma unroll
@@ -1202,7 +1213,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         } else if (real) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int64_t at = (slot * (D / 4) + q * 8 + i) * BQ + r;
+            const int64_t at = (state * (D / 4) + q * 8 + i) * BQ + r;
             if (RF_IN(p.err, at, (int64_t)4 * gridDim.x * (D / 4) * BQ))
               p.ws_o[at] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                        __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
@@ -1227,10 +1238,10 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->q_empty[q_at % C::kQSlots]));
+        if (lane == 0) mbar_arrive(smem_u32(&bars->q_empty[slot]));
       }
-      if (!all && real && RF_IN(p.err, slot * BQ + r, (int64_t)4 * gridDim.x * BQ))
-        p.ws_st[slot * BQ + r] = make_float4(kF8 ? M_ref : m_ref, m_ref, l_run, 0.f);
+      if (!all && real && RF_IN(p.err, state * BQ + r, (int64_t)4 * gridDim.x * BQ))
+        p.ws_st[state * BQ + r] = make_float4(kF8 ? M_ref : m_ref, m_ref, l_run, 0.f);
       tc_fence_before();                              // O is read before the next product writes it
     }
     if (!ok) {
@@ -1475,7 +1486,9 @@ cudaError_t launch_masked_rows(const PagedKV& c, const Mask& mask, const void* Q
 //   4 the merge counts a cut item's pieces and finds their slots, in key order;
 //   5 every row with tokens lies in one tile of one item;
 //   6 every key that a row reads lies in exactly one half of a key tile that its tile
-//     takes.
+//     takes;
+//   7 over a cache whose queries are converted in place, a query tile's place is never
+//     the other's, and its loads are counted one by one.
 int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k, int B, int Hkv,
                           int G, int max_q, int total_q, int total_k, int window, int sinks,
                           int tree, int sms) {
@@ -1557,12 +1570,22 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
     at = r[1];
     Walk walk(start[0], start[1], start[2], r[1] - r[0]);
     Piece pc;
+    QTurns<2, true> q2(p);
+    QTurns<4, true> q4(p);
+    int turns[2][2][4] = {};                          // of 2 and 4 places, by tile and place
+    auto in_turn = [&](int (&n)[2][4], int x, QPlace q) {
+      return n[1 - x][q.slot] == 0 && q.turn == n[x][q.slot]++;
+    };
     int cuts = 0;
     int64_t s0 = r[0] - (r[1] > r[0] ? start[2] : 0);
     while (walk.next(p, pc, &err)) {
       if (err & kDevErrBounds) return 1;
       const int64_t item0 = s0;
       s0 += pc.w.n;
+      for (int x = 0; seq_lens && x < 2; ++x)
+        if (tile_of(p, pc.w, x).has() &&
+            !(in_turn(turns[0], x, q2.next(x)) && in_turn(turns[1], x, q4.next(x))))
+          return 7;
       for (int j = pc.j0; j < pc.j1; ++j) {
         if (wj == wn) {                               // on to the next item
           wj = 0;

@@ -242,6 +242,31 @@ __host__ __device__ __forceinline__ Whole whole_of(const Geo& p, const Group& w)
   return a;
 }
 
+// Where a query tile is loaded: the place, and how many were there before.  Tiles come
+// piece by piece, a before b, and not every piece has a b.  With kOwn each of the two
+// has places of its own (where no piece has a b, a has all): whoever waits for the tiles
+// of one of them only waits for every load of a place, in turn.  In places that both
+// share it would pass over the other's loads, and a wait for the load behind one that has
+// not ended yet goes by the same parity as the load before that, and returns at once.
+struct QPlace {
+  int slot, turn;
+};
+template <int S, bool kOwn>
+struct QTurns {
+  int na, nb;               // tiles so far: a's and b's, or (not kOwn) both in na
+  bool pairs;
+  __host__ __device__ __forceinline__ explicit QTurns(const Geo& p)
+      : na(0), nb(0), pairs(p.max_q > p.tpt) {}
+  __host__ __device__ __forceinline__ int places() const { return kOwn && pairs ? S / 2 : S; }
+  __host__ __device__ __forceinline__ QPlace at(int x, int n) const {
+    if (!kOwn || !pairs) return {n % S, n / S};
+    return {x * (S / 2) + n % (S / 2), n / (S / 2)};
+  }
+  __host__ __device__ __forceinline__ QPlace next(int x) {
+    return at(x, kOwn && x ? nb++ : na++);
+  }
+};
+
 // The workspace slot of CTA c's piece of an item that begins at tile s0 (in the
 // order of all tiles), of which the CTA's range begins at x0: only its first and
 // its last item can be cut.

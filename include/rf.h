@@ -746,10 +746,11 @@ int rf_selftest_decode_paged_ex_plan(const int32_t* seq_lens, int B, int tiles, 
  * longest sequence it can hold (total_q and the cumulative lengths are ignored),
  * tree 1 for a tree of drafted tokens.  For a device of `sms` SMs it checks that all
  * tiles of all items are taken once, in order, that only a cache's items are cut, into
- * workspace slots that the merge finds again, that every row lies in one tile and that
- * its keys lie in the tiles loaded for it, once.  Returns 0 when all of that holds, -1
- * for refused sizes (also: more than 2^24 rows or keys, or no memory for the walk),
- * else the number (1..6) of the first check that fails.
+ * workspace slots that the merge finds again, that every row lies in one tile, that
+ * its keys lie in the tiles loaded for it, once, and (cache) that a query tile is loaded
+ * where only its own reader waits, for one load after the other.  Returns 0 when all of
+ * that holds, -1 for refused sizes (also: more than 2^24 rows or keys, or no memory for
+ * the walk), else the number (1..7) of the first check that fails.
  */
 int rf_selftest_masked_plan(const int32_t* seq_lens, const int32_t* cu_seqlens_q,
                             const int32_t* cu_seqlens_k, int B, int Hkv, int G, int max_q,

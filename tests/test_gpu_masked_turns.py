@@ -1,0 +1,61 @@
+"""Masked attention on the GPU where the kernel's warps wait for one another in an order
+that not every piece of work has all of: query tiles that are missing, sequences that
+read nothing.  Against the fp64 oracle, and again and again with the same bits.
+
+Tolerances as in tests/test_gpu_masked_values.py."""
+import numpy as np
+import pytest
+import torch
+
+from tests.helpers import to64
+from tests.test_gpu_masked import masked_reference, rf, run, tree_of  # noqa: F401
+from tests.test_gpu_masked_values import MANY
+from tests.test_gpu_paged import BF16, Batch, _gen
+
+pytestmark = pytest.mark.gpu
+
+
+def again_and_again(rf, bt, q, scale, what, window=0, sinks=0, parents=None, calls=25):  # noqa: F811
+    """The oracle's result, and the same bits in every call, with L2 full of other data or not."""
+    got, status = run(rf, bt, q, scale, window, sinks, parents)
+    assert status == rf.RF_OK, what
+    ref, tol = masked_reference(q, bt, scale, window, sinks, parents, **MANY)
+    err = np.abs(to64(got) - ref)
+    assert (err <= tol).all(), f"{what}: worst {np.nanmax(err / tol):.2f} of the tolerance"
+    cache, qd = bt.device(rf), q.cuda()
+    B, Tq, Hq, d = q.shape
+    ws = torch.empty(rf.rf_attn_decode_paged_ex_workspace_size(B, Hq, bt.Hkv, Tq, d), dtype=torch.uint8,
+                     device="cuda")
+    mask = rf.rf_attn_mask(window, sinks, None if parents is None else
+                           torch.tensor(parents, dtype=torch.int32).cuda())
+    other = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(calls):
+        if i % 2:
+            other.fill_(i)
+        o = torch.full_like(qd, 7.0)
+        rf.rf_attn_decode_paged_ex(cache, qd, o, scale, mask, ws)
+        assert torch.equal(o, got), f"{what}: call {i} gives other bits"
+    assert rf.rf_get_device_status() == rf.RF_OK
+
+
+LAST_ALONE = [
+    # kind, d, Hkv, group, query tokens, tree, window, sinks, lens
+    ("e4m3", 128, 4, 8, 40, True, 0, 0, [40 + 37 * i % 260 for i in range(12)]),
+    ("e4m3", 128, 4, 8, 40, False, 90, 4, [40 + 53 * i % 900 for i in range(40)]),
+    ("e4m3", 128, 2, 8, 33, True, 0, 0, [33, 3000, 300, 60, 9000, 170, 40, 41]),
+    ("e4m3", 128, 2, 5, 60, True, 0, 0, [60 + 91 * i % 700 for i in range(50)]),
+    ("e4m3", 64, 2, 8, 40, True, 0, 0, [40 + 37 * i % 500 for i in range(50)]),
+    ("e4m3", 64, 1, 5, 60, False, 200, 3, [60, 5000, 90, 1200] * 4),
+    ("bf16", 128, 4, 8, 40, True, 0, 0, [40 + 53 * i % 700 for i in range(24)]),
+    ("bf16", 64, 2, 5, 60, False, 64, 3, [60 + 91 * i % 900 for i in range(50)]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LAST_ALONE)))
+def test_last_pairs_of_one_tile(rf, case):  # noqa: F811
+    kind, d, Hkv, G_, Tq, tree, window, sinks, lens = LAST_ALONE[case]
+    assert 0 < Tq % (2 * (128 // G_)) <= 128 // G_
+    bt = Batch(kind, lens, Hkv, d, 64, seed=1100 + case).garbage()
+    q = torch.randn(len(lens), Tq, Hkv * G_, d, generator=_gen(1120 + case)).to(BF16)
+    parents = [tree_of(_gen(1140 + b), Tq) for b in range(len(lens))] if tree else None
+    again_and_again(rf, bt, q, d ** -0.5, LAST_ALONE[case][:8], window, sinks, parents)
