@@ -833,7 +833,6 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       }
       if (!t.has()) continue;
       const int slot = mine_q.slot;
-      const uint32_t q_full = smem_u32(&bars->q_full[slot]);
       const int tok = t.t0 + my_t;
       const bool real = my_t < geo.tpt && tok < t.t1;
       const int ctx = c.w.lk - c.w.lq;
@@ -858,7 +857,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       if (kF8) {
         // The row's queries as f16, scaled by a power of two to a largest element in
         // [2^14, 2^15): exact down to 2^-28 of it.
-        if (!warp_wait(q_full, (uint32_t)(mine_q.turn & 1))) {
+        if (!warp_wait(smem_u32(&bars->q_full[slot]), (uint32_t)(mine_q.turn & 1))) {
           ok = false;
           break;
         }
@@ -1162,7 +1161,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       if (*abort_flag) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      // the piece's last product (a tile may have no unit in it)
+      // the piece's last product (over a cache, a tile may have no unit in it)
       if (cnt > cnt0 &&
           !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->pv_done[x]), (uint32_t)((cnt - 1) & 1)) && !*abort_flag)) {
         ok = false;
@@ -1179,11 +1178,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       // E4M3: 2^(M - m) / l in two factors, since 2^(M - m) itself may underflow
       const float half = kF8 ? ex2(0.5f * (M_ref - m_ref)) : 1.f;
       const float inv = l_run == 0.f ? 0.f : half / l_run;
-      uint8_t* stage = smem + slot * C::kTile;
-      if (C::kStaged) {                               // (a tile may have had no event)
-        ok = warp_wait(q_full, (uint32_t)(mine_q.turn & 1));
-        if (!ok) break;
-      }
+      uint8_t* stage = smem + slot * C::kTile;        // (its queries came before their scores)
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
         uint32_t o[32];
@@ -1488,7 +1483,8 @@ cudaError_t launch_masked_rows(const PagedKV& c, const Mask& mask, const void* Q
 //   6 every key that a row reads lies in exactly one half of a key tile that its tile
 //     takes;
 //   7 over a cache whose queries are converted in place, a query tile's place is never
-//     the other's, and its loads are counted one by one.
+//     the other's, and its loads are counted one by one; a prompt's query tiles all take
+//     something of their item.
 int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k, int B, int Hkv,
                           int G, int max_q, int total_q, int total_k, int window, int sinks,
                           int tree, int sms) {
@@ -1518,6 +1514,9 @@ int masked_plan_selfcheck(const int* seq_lens, const int* cu_q, const int* cu_k,
       const Tile t = tile_of(p, w, x);
       if (!t.has()) continue;
       if (t.t1 - t.t0 > p.tpt) return 5;
+      bool takes = seq_lens != nullptr;
+      for (int u = 0; u < 2 * w.n; ++u) takes |= t.takes(u);
+      if (!takes) return 7;
       for (int i = t.t0; i < t.t1; ++i) {
         // a tree's node may be at any position from its first on, and reads no other key
         const int at[2] = {p.tree ? w.lk - w.lq : w.lk - w.lq + i, p.tree ? w.lk - 1 : w.lk - w.lq + i};

@@ -199,7 +199,10 @@ struct Walk {
 };
 
 // Tile x (0, 1) of a piece: its tokens, and which units it takes (unit u: the keys of
-// half u & 1 of the item's key tile u / 2): those in which some row may read a key.
+// half u & 1 of the item's key tile u / 2): those in which some row may read a key.  A
+// prompt's tile that reads no key takes the first all the same: its scores tell the
+// softmax warps, which write their output where the queries were loaded, that the load
+// has ended (each waits for the scores of its own tiles only, every one in turn).
 constexpr int kUnit = BK / 2;
 struct Tile {
   int t0, t1;               // its tokens; t0 >= t1: it has no rows
@@ -217,7 +220,7 @@ __host__ __device__ __forceinline__ Tile tile_of(const Geo& p, const Group& w, i
   const int hi = p.tree ? w.lk - 1 : imin(w.lk - 1, ctx + t.t1 - 1);     // its last row's position
   const int lo = p.window > 0 ? (p.tree ? ctx : ctx + t.t0) - p.window + 1 : 0;
   t.sink = t.first = 0;
-  t.last = -1;
+  t.last = t.has() && !p.seq_lens ? 0 : -1;
   if (hi < 0 || !t.has()) return t;
   t.first = 2 * w.lead + (lo > w.start ? (lo - w.start) / kUnit : 0);
   t.last = 2 * w.lead + (hi - w.start) / kUnit;

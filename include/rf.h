@@ -747,8 +747,9 @@ int rf_selftest_decode_paged_ex_plan(const int32_t* seq_lens, int B, int tiles, 
  * tree 1 for a tree of drafted tokens.  For a device of `sms` SMs it checks that all
  * tiles of all items are taken once, in order, that only a cache's items are cut, into
  * workspace slots that the merge finds again, that every row lies in one tile, that
- * its keys lie in the tiles loaded for it, once, and (cache) that a query tile is loaded
- * where only its own reader waits, for one load after the other.  Returns 0 when all of
+ * its keys lie in the tiles loaded for it, once, and that who reads a query tile waits
+ * for its load and no other (cache: loaded where only its own reader waits, for one load
+ * after the other; prompts: by scores that each query tile has).  Returns 0 when all of
  * that holds, -1 for refused sizes (also: more than 2^24 rows or keys, or no memory for
  * the walk), else the number (1..7) of the first check that fails.
  */

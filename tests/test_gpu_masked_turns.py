@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from tests import test_gpu_window as W
 from tests.helpers import to64
 from tests.test_gpu_masked import masked_reference, rf, run, tree_of  # noqa: F401
 from tests.test_gpu_masked_values import MANY
@@ -59,3 +60,37 @@ def test_last_pairs_of_one_tile(rf, case):  # noqa: F811
     q = torch.randn(len(lens), Tq, Hkv * G_, d, generator=_gen(1120 + case)).to(BF16)
     parents = [tree_of(_gen(1140 + b), Tq) for b in range(len(lens))] if tree else None
     again_and_again(rf, bt, q, d ** -0.5, LAST_ALONE[case][:8], window, sinks, parents)
+
+
+NO_KEYS = [
+    # d, Hq, Hkv, window, sinks, new tokens, keys: prompts of one and two query tiles, some
+    # of which read nothing, several to a CTA
+    (128, 4, 1, 16, 2, [300, 1, 30, 33, 40, 300], [0, 1, 0, 10, 0, 300]),
+    (64, 8, 8, 0, 0, [300, 1, 128, 129, 40, 300, 77] * 6, [0, 1, 0, 10, 0, 300, 500] * 6),
+    (128, 32, 8, 100, 4, [32, 64, 1, 70, 32, 0, 60, 33] * 6, [0, 0, 0, 90, 0, 0, 0, 300] * 6),
+    (128, 40, 8, 0, 0, [51, 20, 1, 25, 26] * 9, [0, 0, 3, 0, 400] * 9),
+    (64, 16, 16, 200, 130, [400, 128, 128, 1, 500], [250, 0, 0, 0, 3]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(NO_KEYS)))
+def test_prompts_whose_rows_read_nothing(rf, case):  # noqa: F811
+    d, Hq, Hkv, window, sinks, new, keys = NO_KEYS[case]
+    q, k, v = W.inputs(new, keys, Hq, Hkv, d, 1200 + case)
+    ref, tol = W.reference(q, k, v, new, keys, d ** -0.5, window, sinks)
+    q, k, v, cq, ck = (t.cuda() for t in (q, k, v, W._cu(new), W._cu(keys)))
+    other = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    first = None
+    for i in range(25):
+        if i % 2:
+            other.fill_(i)
+        o = torch.full_like(q, 7.0)
+        rf.rf_attn_fwd_window(q, k, v, o, d ** -0.5, window, sinks, cq, ck, max(new))
+        if first is None:
+            W.assert_close(o, ref, tol, NO_KEYS[case])
+            first = o
+        assert torch.equal(o, first), f"call {i} gives other bits"
+        a = q.clone()                                  # in place
+        rf.rf_attn_fwd_window(a, k, v, a, d ** -0.5, window, sinks, cq, ck, max(new))
+        assert torch.equal(a, first), f"call {i} in place gives other bits"
+    assert rf.rf_get_device_status() == rf.RF_OK
