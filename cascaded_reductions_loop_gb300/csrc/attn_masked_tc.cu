@@ -126,6 +126,7 @@ struct Bars {
   // of tile m - 1 - kVs is done and what was 8 tiles ago is not looked at any more.
   unsigned rec[8];
   unsigned bad[4][4];                                 // per V stage: values that are not finite
+  int looked[4][2];                                   // halves of it: 1 + the key tile bad is of
   // E4M3: codes have come, are widened; queries are; per key tile, the pages' scales as
   // they come, and per 16 keys the key scale and log2 of the value scale
   uint64_t raw_full[2][5], raw_empty[2][5], q_ok[4];
@@ -140,7 +141,7 @@ struct Bars {
     };
     Piece piece[kPieces];                             // j0 < 0: there are no more
   };
-  int64_t x[2], total;                                // the CTA's range, all tiles
+  int64_t x[2];                                       // the CTA's range
   int g, h, j;                                        // where it begins
   uint32_t tmem;
   int abort;
@@ -174,6 +175,28 @@ __device__ __forceinline__ bool elect_one() {
 // mbar_wait of a whole warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+// mbar_wait of a whole warp, for the count at `at` (of set_count) to reach n: for what only
+// some events wait for.  A barrier's parity takes a phase that has not begun for the one
+// two before it; a count does not.
+__device__ __forceinline__ bool warp_wait_count(uint32_t at, int n) {
+  auto there = [&]() {
+    int v;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return __all_sync(0xffffffffu, v >= n) != 0;
+  };
+  if (there()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (there()) return true;
+    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kDefaultWaitNs)) return false;
+  }
+}
+// What this thread wrote before is there for who finds the count.
+__device__ __forceinline__ void set_count(uint32_t at, int n) {
+  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(at), "r"(n) : "memory");
 }
 // One column of this thread's lane (waits for it).
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
@@ -286,6 +309,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         mbar_init(smem_u32(&bars->raw_empty[1][i]), 2);
       }
     }
+    for (int i = 0; i < 4; ++i) bars->looked[i][0] = bars->looked[i][1] = 0;
     bars->abort = 0;
     bars->x[0] = bars->x[1] = 0;
     bars->g = bars->h = bars->j = 0;
@@ -716,12 +740,11 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
           if (lane == 0) {
             bars->bad[pr][2 * h] = bad[0];
             bars->bad[pr][2 * h + 1] = bad[1];
+            set_count(smem_u32(&bars->looked[pr][h]), nt + 1);
           }
         }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&bars->v_ok[pr]));
-        }
+        if (lane == 0) mbar_arrive(smem_u32(&bars->v_ok[pr]));
         if (*abort_flag) ok = false;
         ok = __all_sync(0xffffffffu, ok);
       }
@@ -790,6 +813,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
+        if (v == 1) set_count(smem_u32(&bars->looked[pr][h]), nt + 1);
         mbar_arrive(smem_u32(&bars->raw_empty[v][rp]));
         mbar_arrive(smem_u32(v ? &bars->v_ok[pr] : &bars->full[pr]));
       }
@@ -1076,7 +1100,10 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         tmem_st_wait();
         if (part) {
           const int pr = tile % C::kVs;
-          if (!warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((tile / C::kVs) & 1))) return false;
+          // (Not v_ok: neither tile may have had an event for some key tiles, and those'
+          // phases of it may still be to come.)
+          for (int h = 0; h < 2; ++h)
+            if (!warp_wait_count(smem_u32(&bars->looked[pr][h]), tile + 1)) return false;
           const unsigned* bad = bars->bad[pr];
           if (((halves & 1u) && (bad[0] | bad[1])) || ((halves & 2u) && (bad[2] | bad[3]))) {
             // values that are not finite, for the rows that read them: P times value

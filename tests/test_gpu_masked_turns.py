@@ -94,3 +94,56 @@ def test_prompts_whose_rows_read_nothing(rf, case):  # noqa: F811
         rf.rf_attn_fwd_window(a, k, v, a, d ** -0.5, window, sinks, cq, ck, max(new))
         assert torch.equal(a, first), f"call {i} in place gives other bits"
     assert rf.rf_get_device_status() == rf.RF_OK
+
+
+def empties(n, of, times):
+    """n sequences without tokens in front of each of the others."""
+    return ([x for i in of for x in [0] * n + [i]]) * times
+
+
+EMPTIES = [
+    # kind, d, Hkv, group, query tokens, tree, window, sinks, lens: what lies behind a
+    # sequence's last token in its last page is not finite
+    ("bf16", 128, 4, 4, 16, True, 0, 0, empties(3, [37, 20, 300], 24)),
+    ("bf16", 128, 2, 8, 40, True, 0, 0, empties(2, [41, 700], 30)),
+    ("bf16", 64, 4, 4, 16, False, 50, 3, empties(5, [17, 130, 40], 16)),
+    ("bf16", 128, 1, 4, 40, False, 60, 0, [5, 1, 39, 70, 3, 0, 2, 200] * 24),
+    ("e4m3", 128, 4, 4, 16, True, 0, 0, empties(3, [37, 20, 300], 24)),
+    ("e4m3", 128, 2, 8, 40, True, 0, 0, empties(2, [41, 700], 30)),
+    ("e4m3", 64, 4, 8, 16, False, 50, 3, empties(5, [17, 130, 40], 16)),
+    ("e4m3", 128, 1, 4, 40, False, 60, 0, [5, 1, 39, 70, 3, 0, 2, 200] * 24),
+]
+
+
+@pytest.mark.parametrize("case", range(len(EMPTIES)))
+def test_sequences_that_read_nothing_in_front_of_unread_nans(rf, case):  # noqa: F811
+    kind, d, Hkv, G_, Tq, tree, window, sinks, lens = EMPTIES[case]
+    bt = Batch(kind, lens, Hkv, d, 64, seed=1300 + case).garbage()
+    q = torch.randn(len(lens), Tq, Hkv * G_, d, generator=_gen(1320 + case)).to(BF16)
+    parents = [tree_of(_gen(1340 + b), Tq) for b in range(len(lens))] if tree else None
+    again_and_again(rf, bt, q, d ** -0.5, EMPTIES[case][:8], window, sinks, parents)
+
+
+def test_prompts_that_read_nothing_in_front_of_unread_nans(rf):  # noqa: F811
+    """Infinities and NaN in values that no row reads: of the next sequence, behind a
+    prompt's last key in its last key tile, and between the sinks and the window."""
+    new, keys = [300, 33, 32, 32, 40, 7] * 8, [10, 0, 0, 5, 140, 60] * 8
+    window, sinks, scale = 30, 4, 128 ** -0.5
+    q, k, v = W.inputs(new, keys, 8, 2, 128, 1400)
+    ref, tol = W.reference(q, k, v, new, keys, scale, window, sinks)
+    at = 0
+    for i, (n, nk) in enumerate(zip(new, keys)):
+        if nk == 60:
+            v[at + sinks:at + nk - n + 1 - window] = float("nan") if i % 4 == 1 else float("inf")
+        at += nk
+    assert not torch.isfinite(v).all()
+    q, k, v, cq, ck = (t.cuda() for t in (q, k, v, W._cu(new), W._cu(keys)))
+    first = None
+    for i in range(25):
+        o = torch.full_like(q, 7.0)
+        rf.rf_attn_fwd_window(q, k, v, o, scale, window, sinks, cq, ck, max(new))
+        if first is None:
+            W.assert_close(o, ref, tol, "unread")
+            first = o
+        assert torch.equal(o, first), f"call {i} gives other bits"
+    assert rf.rf_get_device_status() == rf.RF_OK
