@@ -89,6 +89,8 @@ struct Cfg {
   static constexpr uint32_t kIdescHalf = make_idesc(BQ, kUnit, kF8 ? 0 : 1, 0, 0);
   static constexpr uint32_t kIdescO = make_idesc(BQ, D, kF8 ? 0 : 1, 0, 1);
   static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(1 + kVs + (kF8 ? kRawPairs : 0) <= 8 && 1 + kKs + (kF8 ? kRawPairs : 0) <= 8,
+                "records");
 };
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;                         // 128 columns
@@ -118,13 +120,18 @@ struct Bars {
   uint64_t q_full[4], q_empty[4];
   uint64_t full[8], empty[8];                         // of K's places, from 4 on V's
   uint64_t v_ok[4];                                   // a V tile is looked over
-  uint64_t rec_ok[8];                                 // over a cache: rec is set, for the softmax
   uint64_t s_full[2], p_full[2], pv_done[2];          // of a query tile's events
   uint64_t s_read;                                    // of all events: S is in registers
   uint64_t drain[2];
-  // Per key tile.  That of tile m is written once V of tile m - 1 has a stage, so the P.V
-  // of tile m - 1 - kVs is done and what was 8 tiles ago is not looked at any more.
+  // Per key tile, like scale and its parts below: tile m's takes the place of tile m - 8's.
+  // It is written once V of tile m - 1 has a place to be copied to: the one of tile
+  // m - 1 - kVs, whose P.V is done, or (E4M3) the codes' of tile m - 1 - kRawPairs, which are
+  // widened, so that V's place of tile m - 1 - kRawPairs - kVs had been left by its P.V.  And
+  // K of tile m - 1 has one, by the same count with kKs: S of tile m - 1 - kRawPairs - kKs is
+  // done.  Cfg asserts that both are tile m - 8 or later.  The softmax warps of a query tile
+  // look at those of key tiles that it takes only, which P.V does not pass without them.
   unsigned rec[8];
+  int rec_of[8];                                      // over a cache: 1 + its tile, for the softmax
   unsigned bad[4][4];                                 // per V stage: values that are not finite
   int looked[4][2];                                   // halves of it: 1 + the key tile bad is of
   // E4M3: codes have come, are widened; queries are; per key tile, the pages' scales as
@@ -286,8 +293,8 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&bars->full[i]), kF8 ? 2 : 1);       // a copy, or the widening warps
-      mbar_init(smem_u32(&bars->rec_ok[i]), 1);
       mbar_init(smem_u32(&bars->empty[i]), 1);
+      bars->rec_of[i] = 0;
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->s_full[i]), 1);
@@ -533,7 +540,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
               if (lane == 0) {
                 if (v == 0) {
                   bars->rec[nt % 8] = rec;
-                  if (!kF8) mbar_arrive(smem_u32(&bars->rec_ok[nt % 8]));
+                  if (!kF8) set_count(smem_u32(&bars->rec_of[nt % 8]), nt + 1);
                 }
                 mbar_arrive_expect_tx(bar, (uint32_t)(__popc(pages) * p.page_size * D * (kF8 ? 1 : 2)));
               }
@@ -774,7 +781,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
                                                   in ? __log2f(bars->sc_v[nt % 8][page]) : 0.f);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->rec_ok[nt % 8]));
+        if (lane == 0) set_count(smem_u32(&bars->rec_of[nt % 8]), nt + 1);
       }
       ok = nt < ks || warp_wait(smem_u32(&bars->empty[4 * v + pr]), (uint32_t)((nt / ks - 1) & 1));
       if (!ok) break;
@@ -1161,11 +1168,15 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       const int full1 = (max(whole.end, over) - over) / BK;
 #pragma unroll 1
       for (int j = c.j0; j < c.j1; ++j) {
-        unsigned pages = 0xFFu;
+        unsigned pages = 0xFFu, halves = 3u, part = 0u;
         bool fast = j >= full0 && j < full1;
+        if (!fast) {
+          halves = (t.takes(2 * j) ? 1u : 0u) | (t.takes(2 * j + 1) ? 2u : 0u);
+          if (!halves) continue;                      // (its record may be another's by now)
+        }
         if (kPaged) {
           const int tile = j_base + j;
-          if (!warp_wait(smem_u32(&bars->rec_ok[tile % 8]), (uint32_t)((tile / 8) & 1))) {
+          if (!warp_wait_count(smem_u32(&bars->rec_of[tile % 8]), tile + 1)) {
             ok = false;
             break;
           }
@@ -1173,10 +1184,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
           fast = fast && pages == 0xFFu;
         }
         int key0 = 0;
-        unsigned halves = 3u, part = 0u;
         if (!fast) {
-          halves = (t.takes(2 * j) ? 1u : 0u) | (t.takes(2 * j + 1) ? 2u : 0u);
-          if (!halves) continue;
           key0 = key0_of(c.w, j);
           part = (whole.partly(geo, key0, kUnit) ? 1u : 0u) |
                  (whole.partly(geo, key0 + kUnit, kUnit) ? 2u : 0u);

@@ -147,3 +147,22 @@ def test_prompts_that_read_nothing_in_front_of_unread_nans(rf):  # noqa: F811
             first = o
         assert torch.equal(o, first), f"call {i} gives other bits"
     assert rf.rf_get_device_status() == rf.RF_OK
+
+
+SKIPPED = [
+    # kind, d, Hkv, group, query tokens, window, sinks, lens: key tiles that one of a pair's
+    # query tiles takes and the other does not, at either end and behind the sinks
+    ("e4m3", 64, 2, 1, 256, 128, 0, [256 + 331 * i % 3000 for i in range(12)]),
+    ("e4m3", 64, 2, 2, 130, 1, 300, [130 + 331 * i % 3000 for i in range(24)]),
+    ("e4m3", 128, 2, 1, 256, 200, 1, [256 + 331 * i % 2000 for i in range(12)]),
+    ("bf16", 64, 2, 1, 256, 128, 130, [256 + 331 * i % 3000 for i in range(12)]),
+    ("bf16", 128, 1, 2, 128, 64, 0, [128 + 331 * i % 2000 for i in range(24)]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SKIPPED)))
+def test_key_tiles_that_one_of_two_query_tiles_takes(rf, case):  # noqa: F811
+    kind, d, Hkv, G_, Tq, window, sinks, lens = SKIPPED[case]
+    bt = Batch(kind, lens, Hkv, d, 32, seed=1500 + case).garbage()
+    q = torch.randn(len(lens), Tq, Hkv * G_, d, generator=_gen(1520 + case)).to(BF16)
+    again_and_again(rf, bt, q, d ** -0.5, SKIPPED[case][:7], window, sinks)
