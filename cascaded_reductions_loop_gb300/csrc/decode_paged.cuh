@@ -532,12 +532,11 @@ __device__ __forceinline__ unsigned bits_below(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
 }
 
-// Whether any value of keys [lo, hi) of the chunk that are `in` is an infinity or NaN.
-template <bool kF8, int D, typename In>
-__device__ __forceinline__ bool any_nonfinite(uint32_t base, int lane, int lo, int hi, In in) {
+// Whether any value of keys [lo, hi) of the chunk is an infinity or NaN.
+template <bool kF8, int D>
+__device__ __forceinline__ bool any_nonfinite(uint32_t base, int lane, int lo, int hi) {
   bool bad = false;
   for (int key = lo; key < hi; ++key) {
-    if (!in(key)) continue;
     if (kF8) {
       if (lane < D / 16) {
         uint32_t w[4];
@@ -1267,7 +1266,7 @@ __global__ void __launch_bounds__(Cfg<kF8, D, NT>::kThreads, 1)
 #pragma unroll
       for (int h2 = 0; h2 < 2; ++h2) end[h2] = ((valid >> h2) & 1) ? cur_len - key0 : 0;
       const int lo = max(cur_len - p.Tq + 1 - key0, 0), hi = min(cur_len - key0, kChunk);
-      if (p.Tq > 1 && any_nonfinite<kF8, D>(vb, lane, lo, hi, Below{kChunk})) {
+      if (p.Tq > 1 && any_nonfinite<kF8, D>(vb, lane, lo, hi)) {
 #pragma unroll 1
         for (int t = 0; t < p.Tq; ++t) {       // the rows of one query token at a time
           unsigned rows = 0;
