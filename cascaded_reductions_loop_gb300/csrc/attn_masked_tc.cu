@@ -119,7 +119,10 @@ constexpr int kPieces = 3;
 struct Bars {
   uint64_t q_full[4], q_empty[4];
   uint64_t full[8], empty[8];                         // of K's places, from 4 on V's
-  uint64_t v_ok[4];                                   // a V tile is looked over
+  // A V tile is looked over.  By the key tile's number, not by V's place: a query tile's
+  // softmax waits for tiles that it takes only, and a parity tells tile m's phase where the
+  // one before is complete; with the scores of tile m there, that of tile m - 8 is (see rec).
+  uint64_t v_ok[8];
   uint64_t s_full[2], p_full[2], pv_done[2];          // of a query tile's events
   uint64_t s_read;                                    // of all events: S is in registers
   uint64_t drain[2];
@@ -131,9 +134,7 @@ struct Bars {
   // done.  Cfg asserts that both are tile m - 8 or later.  The softmax warps of a query tile
   // look at those of key tiles that it takes only, which P.V does not pass without them.
   unsigned rec[8];
-  int rec_of[8];                                      // over a cache: 1 + its tile, for the softmax
   unsigned bad[4][4];                                 // per V stage: values that are not finite
-  int looked[4][2];                                   // halves of it: 1 + the key tile bad is of
   // E4M3: codes have come, are widened; queries are; per key tile, the pages' scales as
   // they come, and per 16 keys the key scale and log2 of the value scale
   uint64_t raw_full[2][5], raw_empty[2][5], q_ok[4];
@@ -182,28 +183,6 @@ __device__ __forceinline__ bool elect_one() {
 // mbar_wait of a whole warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-}
-// mbar_wait of a whole warp, for the count at `at` (of set_count) to reach n: for what only
-// some events wait for.  A barrier's parity takes a phase that has not begun for the one
-// two before it; a count does not.
-__device__ __forceinline__ bool warp_wait_count(uint32_t at, int n) {
-  auto there = [&]() {
-    int v;
-    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return __all_sync(0xffffffffu, v >= n) != 0;
-  };
-  if (there()) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (there()) return true;
-    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kDefaultWaitNs)) return false;
-  }
-}
-// What this thread wrote before is there for who finds the count.
-__device__ __forceinline__ void set_count(uint32_t at, int n) {
-  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(at), "r"(n) : "memory");
 }
 // One column of this thread's lane (waits for it).
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
@@ -288,16 +267,15 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 1);
       mbar_init(smem_u32(&bars->q_empty[i]), C::kStaged ? 1 + 4 : 1);
-      mbar_init(smem_u32(&bars->v_ok[i]), kF8 ? 2 : 1);
       mbar_init(smem_u32(&bars->q_ok[i]), BQ);
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&bars->full[i]), kF8 ? 2 : 1);       // a copy, or the widening warps
+      mbar_init(smem_u32(&bars->v_ok[i]), kF8 ? 2 : 1);
       mbar_init(smem_u32(&bars->empty[i]), 1);
-      bars->rec_of[i] = 0;
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars->s_full[i]), 1);
+      mbar_init(smem_u32(&bars->s_full[i]), kPaged ? 2 : 1);  // the product; over a cache, rec
       mbar_init(smem_u32(&bars->p_full[i]), BQ);
       mbar_init(smem_u32(&bars->pv_done[i]), 1);
     }
@@ -316,7 +294,6 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         mbar_init(smem_u32(&bars->raw_empty[1][i]), 2);
       }
     }
-    for (int i = 0; i < 4; ++i) bars->looked[i][0] = bars->looked[i][1] = 0;
     bars->abort = 0;
     bars->x[0] = bars->x[1] = 0;
     bars->g = bars->h = bars->j = 0;
@@ -538,10 +515,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
             const CUtensorMap* tm = v ? &tmV : &tmK;
             if (kPaged) {
               if (lane == 0) {
-                if (v == 0) {
-                  bars->rec[nt % 8] = rec;
-                  if (!kF8) set_count(smem_u32(&bars->rec_of[nt % 8]), nt + 1);
-                }
+                if (v == 0) bars->rec[nt % 8] = rec;
                 mbar_arrive_expect_tx(bar, (uint32_t)(__popc(pages) * p.page_size * D * (kF8 ? 1 : 2)));
               }
               __syncwarp();
@@ -637,6 +611,8 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
                   mma_bf16_ss(tmem + kColS + h * kUnit, a + off, b + off, idesc, k != 0);
                 }
                 mma_commit(smem_u32(&bars->s_full[x]));
+                // the softmax may read rec (and scale), which came with the keys
+                if (kPaged) mbar_arrive(smem_u32(&bars->s_full[x]));
               }
             }
             if (ok && (rec & kLast) && leader) mma_commit(smem_u32(&bars->q_empty[slot]));
@@ -651,7 +627,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         constexpr int kPolls = 24;
         for (int nt = 0; ok && more; ++nt) {
           const int pr = nt % C::kVs;
-          ok = warp_wait(smem_u32(&bars->v_ok[pr]), (uint32_t)((nt / C::kVs) & 1));
+          ok = warp_wait(smem_u32(&bars->v_ok[nt % 8]), (uint32_t)((nt / 8) & 1));
           if (!ok) break;
           const unsigned rec = (unsigned)uniform((int)bars->rec[nt % 8]);
           more = !(rec & kEnd);
@@ -747,11 +723,10 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
           if (lane == 0) {
             bars->bad[pr][2 * h] = bad[0];
             bars->bad[pr][2 * h + 1] = bad[1];
-            set_count(smem_u32(&bars->looked[pr][h]), nt + 1);
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->v_ok[pr]));
+        if (lane == 0) mbar_arrive(smem_u32(&bars->v_ok[nt % 8]));
         if (*abort_flag) ok = false;
         ok = __all_sync(0xffffffffu, ok);
       }
@@ -780,8 +755,6 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
           bars->scale[nt % 8][lane] = make_float2(in ? bars->sc_k[nt % 8][page] : 1.f,
                                                   in ? __log2f(bars->sc_v[nt % 8][page]) : 0.f);
         }
-        __syncwarp();
-        if (lane == 0) set_count(smem_u32(&bars->rec_of[nt % 8]), nt + 1);
       }
       ok = nt < ks || warp_wait(smem_u32(&bars->empty[4 * v + pr]), (uint32_t)((nt / ks - 1) & 1));
       if (!ok) break;
@@ -820,9 +793,8 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if (v == 1) set_count(smem_u32(&bars->looked[pr][h]), nt + 1);
         mbar_arrive(smem_u32(&bars->raw_empty[v][rp]));
-        mbar_arrive(smem_u32(v ? &bars->v_ok[pr] : &bars->full[pr]));
+        mbar_arrive(smem_u32(v ? &bars->v_ok[nt % 8] : &bars->full[pr]));
       }
       if (*abort_flag) ok = false;
       ok = __all_sync(0xffffffffu, ok);
@@ -926,9 +898,9 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         mbar_arrive(smem_u32(&bars->q_ok[slot]));
       }
       const int cnt0 = cnt;
-      // one event: halves (bits) of the key tile at key0, in V stage pr; part: of which
+      // one event: halves (bits) of the CTA's key tile `tile`, at key0; part: of which
       // halves some row may not read all keys
-      auto event = [&](int key0, int tile, unsigned halves, unsigned part, unsigned pages) -> bool {
+      auto event = [&](int key0, int tile, unsigned halves, unsigned part) -> bool {
         unsigned w[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};   // keys it reads
         if (part) {
           const int hi = geo.tree ? min(ctx, pos + 1) : pos + 1;
@@ -953,15 +925,10 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
               u = up < u ? up : -1;
             }
           }
-          if (kPaged) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              w[q] &= ((pages >> (2 * q)) & 1u ? 0xFFFFu : 0u) |
-                      ((pages >> (2 * q + 1)) & 1u ? 0xFFFF0000u : 0u);
-          }
         }
         if (!warp_wait(smem_u32(&bars->s_full[x]), (uint32_t)(cnt & 1))) return false;
         tc_fence_after();
+        const unsigned pages = kPaged ? (bars->rec[tile % 8] >> kPages) & 0xFFu : 0xFFu;
         uint32_t v[4][32];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -973,6 +940,13 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         tc_fence_before();                            // S may be overwritten
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->s_read));
+        if (pages != 0xFFu) {                         // keys whose pages are not there
+          part = 3u;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            w[q] &= ((pages >> (2 * q)) & 1u ? 0xFFFFu : 0u) |
+                    ((pages >> (2 * q + 1)) & 1u ? 0xFFFF0000u : 0u);
+        }
         if (part)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -1107,10 +1081,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         tmem_st_wait();
         if (part) {
           const int pr = tile % C::kVs;
-          // (Not v_ok: neither tile may have had an event for some key tiles, and those'
-          // phases of it may still be to come.)
-          for (int h = 0; h < 2; ++h)
-            if (!warp_wait_count(smem_u32(&bars->looked[pr][h]), tile + 1)) return false;
+          if (!warp_wait(smem_u32(&bars->v_ok[tile % 8]), (uint32_t)((tile / 8) & 1))) return false;
           const unsigned* bad = bars->bad[pr];
           if (((halves & 1u) && (bad[0] | bad[1])) || ((halves & 2u) && (bad[2] | bad[3]))) {
             // values that are not finite, for the rows that read them: P times value
@@ -1168,29 +1139,16 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       const int full1 = (max(whole.end, over) - over) / BK;
 #pragma unroll 1
       for (int j = c.j0; j < c.j1; ++j) {
-        unsigned pages = 0xFFu, halves = 3u, part = 0u;
-        bool fast = j >= full0 && j < full1;
-        if (!fast) {
-          halves = (t.takes(2 * j) ? 1u : 0u) | (t.takes(2 * j + 1) ? 2u : 0u);
-          if (!halves) continue;                      // (its record may be another's by now)
-        }
-        if (kPaged) {
-          const int tile = j_base + j;
-          if (!warp_wait_count(smem_u32(&bars->rec_of[tile % 8]), tile + 1)) {
-            ok = false;
-            break;
-          }
-          pages = (bars->rec[tile % 8] >> kPages) & 0xFFu;
-          fast = fast && pages == 0xFFu;
-        }
         int key0 = 0;
-        if (!fast) {
-          key0 = key0_of(c.w, j);
+        unsigned halves = 3u, part = 0u;
+        if (j < full0 || j >= full1 || kPaged) key0 = key0_of(c.w, j);
+        if (j < full0 || j >= full1) {
+          halves = (t.takes(2 * j) ? 1u : 0u) | (t.takes(2 * j + 1) ? 2u : 0u);
+          if (!halves) continue;
           part = (whole.partly(geo, key0, kUnit) ? 1u : 0u) |
                  (whole.partly(geo, key0 + kUnit, kUnit) ? 2u : 0u);
-          if (pages != 0xFFu) part = 3u;
         }
-        ok = event(key0, j_base + j, halves, part, pages);
+        ok = event(key0, j_base + j, halves, part);
         if (!ok) break;
       }
       if (*abort_flag) ok = false;
