@@ -147,7 +147,10 @@ struct Bars {
       int64_t warp_sum[16];
       int warp_items[16], warp_most[16];
     };
-    Piece piece[kPieces];                             // j0 < 0: there are no more
+    struct {
+      Piece piece[kPieces];                           // j0 < 0: there are no more
+      QPlace q[kPieces][2];                           // where its query tiles are
+    };
   };
   int64_t x[2];                                       // the CTA's range
   int g, h, j;                                        // where it begins
@@ -433,14 +436,18 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         ok = np < kPieces ||
              warp_wait(smem_u32(&bars->piece_empty[pc]), (uint32_t)((np / kPieces - 1) & 1));
         if (!ok) break;
+        const Tile ta = tile_of(geo, c.w, 0), tb = tile_of(geo, c.w, 1);
+        QPlace qa = {0, 0}, qb = {0, 0};
+        if (!last) qa = queries.next(0);
+        if (!last && tb.has()) qb = queries.next(1);
         if (lane == 0) {
           bars->piece[pc] = c;
+          bars->q[pc][0] = qa;
+          bars->q[pc][1] = qb;
           mbar_arrive(smem_u32(&bars->piece_full[pc]));
         }
         if (last) break;
-        const Tile ta = tile_of(geo, c.w, 0), tb = tile_of(geo, c.w, 1);
-        auto load_q = [&](int x, const Tile& t) {
-          const QPlace at = queries.next(x);
+        auto load_q = [&](const QPlace& at, const Tile& t) {
           ok = at.turn == 0 ||
                warp_wait(smem_u32(&bars->q_empty[at.slot]), (uint32_t)((at.turn - 1) & 1));
           if (!ok) return;
@@ -453,9 +460,9 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
               tma_load_3d_hint(dst + i * kHalf, &tmQ, bar, 64 * i, c.h * geo.G, c.w.q0 + t.t0, pol_q);
           }
         };
-        load_q(0, ta);
+        load_q(qa, ta);
         // Q_b behind the first keys: its place may still have an output in it
-        if (!C::kStaged && ok && tb.has()) load_q(1, tb);
+        if (!C::kStaged && ok && tb.has()) load_q(qb, tb);
         const Whole whole = whole_of(geo, c.w);
         for (int j = c.j0; ok && j < c.j1; ++j, ++nt) {
           const int key0 = key0_of(c.w, j);
@@ -543,7 +550,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
             }
             ++in_flight;
           }
-          if (C::kStaged && ok && j == c.j0 && tb.has()) load_q(1, tb);
+          if (C::kStaged && ok && j == c.j0 && tb.has()) load_q(qb, tb);
         }
         if (*abort_flag) ok = false;
         ok = __all_sync(0xffffffffu, ok);
@@ -554,7 +561,8 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         // copies in flight land before shared memory is released
         for (int x = 0; x < 2; ++x) {
           const int n = x ? queries.nb : queries.na;
-          for (int i = max(0, n - queries.places()); i < n; ++i) {
+          // (the piece's own may not have been issued: two more)
+          for (int i = max(0, n - queries.places() - 2); i < n; ++i) {
             const QPlace at = queries.at(x, i);
             (void)mbar_wait(smem_u32(&bars->q_full[at.slot]), (uint32_t)(at.turn & 1), 1000000ull);
           }
@@ -814,13 +822,13 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
     const uint64_t c2 = f2(p.c_log2, p.c_log2);
     const int my_t = r / geo.G, my_g = r - my_t * geo.G;
     int nt = 0, cnt = 0;                              // key tiles; events of this warpgroup
-    typename C::Queries queries(geo);
     int64_t s0 = x0 - (x1 > x0 ? bars->j : 0);        // first tile of the piece's item
     for (int np = 0; ok; ++np) {
       const int pc = np % kPieces;
       ok = warp_wait(smem_u32(&bars->piece_full[pc]), (uint32_t)((np / kPieces) & 1));
       if (!ok) break;
       c = bars->piece[pc];
+      const QPlace place = bars->q[pc][x];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->piece_empty[pc]));
       if (c.j0 < 0) break;
@@ -829,13 +837,8 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       s0 += c.w.n;
       const int j_base = nt - c.j0;                   // key tile j is the CTA's j_base + j th
       nt += c.j1 - c.j0;
-      QPlace mine_q = queries.next(0);
-      if (tile_of(geo, c.w, 1).has()) {
-        const QPlace qb = queries.next(1);
-        if (x == 1) mine_q = qb;
-      }
       if (!t.has()) continue;
-      const int slot = mine_q.slot;
+      const int slot = place.slot;
       const int tok = t.t0 + my_t;
       const bool real = my_t < geo.tpt && tok < t.t1;
       const int ctx = c.w.lk - c.w.lq;
@@ -860,7 +863,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
       if (kF8) {
         // The row's queries as f16, scaled by a power of two to a largest element in
         // [2^14, 2^15): exact down to 2^-28 of it.
-        if (!warp_wait(smem_u32(&bars->q_full[slot]), (uint32_t)(mine_q.turn & 1))) {
+        if (!warp_wait(smem_u32(&bars->q_full[slot]), (uint32_t)(place.turn & 1))) {
           ok = false;
           break;
         }
