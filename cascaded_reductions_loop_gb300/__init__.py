@@ -572,6 +572,14 @@ def rf_kv_append_paged(cache, k, v, norm_rope=None, cu_seqlens=None, q=None, q_o
                                   Hq, _stream(stream)), "rf_kv_append_paged")
 
 
+def _c_int(x, name):
+    """x as the library's int (ctypes keeps the low 32 bits of a larger one)."""
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} must be below 2^31")
+    return x
+
+
 def rf_attn_fwd_window(q, k, v, o, scale: float, window: int, sinks: int = 0, cu_seqlens_q=None,
                        cu_seqlens_k=None, max_seqlen_q=None, batch: int = 1, stream=None) -> None:
     """Attention of prompts with a sliding window of `window` keys (0: none) and
@@ -580,6 +588,9 @@ def rf_attn_fwd_window(q, k, v, o, scale: float, window: int, sinks: int = 0, cu
     a token contiguous; cu_seqlens_q/k: int32 [B+1] cumulative lengths (not read
     on the host; max_seqlen_q is then needed with cu_seqlens_q), or None: `batch`
     sequences of equal lengths."""
+    window, sinks, B = _c_int(window, "window"), _c_int(sinks, "sinks"), _c_int(batch, "batch")
+    if max_seqlen_q is not None:
+        max_seqlen_q = _c_int(max_seqlen_q, "max_seqlen_q")
     dev, bf16 = torch.cuda.current_device(), torch.bfloat16
     if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(k, torch.Tensor) or \
             k.dim() != 3:
@@ -590,7 +601,7 @@ def rf_attn_fwd_window(q, k, v, o, scale: float, window: int, sinks: int = 0, cu
     kp, ldk = _rows(k, dev, bf16, total_k, Hkv, d, "k")
     vp, ldv = _rows(v, dev, bf16, total_k, Hkv, d, "v")
     op, ldo = _rows(o, dev, bf16, total_q, Hq, d, "o")
-    B, cq, ck = int(batch), None, None
+    cq = ck = None
     for cu in (cu_seqlens_q, cu_seqlens_k):
         if cu is not None:
             if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.numel() < 2:
@@ -605,8 +616,8 @@ def rf_attn_fwd_window(q, k, v, o, scale: float, window: int, sinks: int = 0, cu
     if max_seqlen_q is None:
         max_seqlen_q = -(-total_q // B) if B > 0 else 0
     _check(lib.rf_attn_fwd_window(qp, ldq, kp, ldk, vp, ldv, op, ldo, cq, ck, B, Hq, Hkv,
-                                  int(max_seqlen_q), total_q, total_k, d, scale, int(window),
-                                  int(sinks), _stream(stream)), "rf_attn_fwd_window")
+                                  max_seqlen_q, total_q, total_k, d, scale, window, sinks,
+                                  _stream(stream)), "rf_attn_fwd_window")
 
 
 def rf_attn_decode_paged_workspace_size(B, Hq, Hkv, Tq=1, d=128) -> int:
