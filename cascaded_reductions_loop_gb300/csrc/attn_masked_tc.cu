@@ -436,10 +436,11 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
         ok = np < kPieces ||
              warp_wait(smem_u32(&bars->piece_empty[pc]), (uint32_t)((np / kPieces - 1) & 1));
         if (!ok) break;
-        const Tile ta = tile_of(geo, c.w, 0), tb = tile_of(geo, c.w, 1);
         QPlace qa = {0, 0}, qb = {0, 0};
-        if (!last) qa = queries.next(0);
-        if (!last && tb.has()) qb = queries.next(1);
+        if (!last) {
+          qa = queries.next(0);
+          if (tile_of(geo, c.w, 1).has()) qb = queries.next(1);
+        }
         if (lane == 0) {
           bars->piece[pc] = c;
           bars->q[pc][0] = qa;
@@ -447,6 +448,7 @@ __global__ void __launch_bounds__((Cfg<D, kPaged, kF8>::kThreads), 1)
           mbar_arrive(smem_u32(&bars->piece_full[pc]));
         }
         if (last) break;
+        const Tile ta = tile_of(geo, c.w, 0), tb = tile_of(geo, c.w, 1);
         auto load_q = [&](const QPlace& at, const Tile& t) {
           ok = at.turn == 0 ||
                warp_wait(smem_u32(&bars->q_empty[at.slot]), (uint32_t)((at.turn - 1) & 1));
