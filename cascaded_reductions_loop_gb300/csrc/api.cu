@@ -542,16 +542,19 @@ size_t rf_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Tq, int d
 
 // With a mask and more query rows a kv head than this, the tensor-core kernel with tiles
 // of 128 rows takes the call; the kernel with tiles of 16 rows reads (and, in E4M3, widens)
-// the keys again for every 16 of them.  128-row tiles against 16-row tiles, us, trees over
-// caches of 500 to 8000 tokens (16 sequences where nothing else is said), cold L2:
-//   d = 128, 8 kv heads, bf16: 16 rows 74 against 67, 20 rows 77 against 104, 64 rows 75
-//     against 176; one sequence of 16000 tokens: 20 rows 52 against 44, 64 rows 46 against 61
-//   d = 128, 8 kv heads, E4M3: 32 rows 120 against 85, 48 rows 124 against 110, 52 rows 118
-//     against 136; 64 sequences: 48 rows 437 against 401, 64 rows 421 against 528; one
-//     sequence of 16000 tokens: 64 rows 62 against 52, 80 rows 61 against 61
-//   d = 64, 8 kv heads, bf16: 32 rows 69 against 67, 48 rows 70 against 85
-//   d = 64, 8 kv heads, E4M3: 64 rows 108 against 102, 80 rows 118 against 116, 96 rows 114
-//     against 137
+// the keys again for every 16 of them.  128-row tiles against 16-row tiles, us, 8 kv heads,
+// trees over caches of 500 to 8000 tokens, cold L2, for batches of 16 and of 64 and for one
+// sequence of 16000 tokens.  The border is where full batches cross:
+//   d = 128, bf16: 16 rows 72 against 66, 232 against 203, 40 against 42; 20 rows 73 against
+//     101, 237 against 375, 44 against 44
+//   d = 128, E4M3: 32 rows 116 against 86, 420 against 269, 50 against 42; 48 rows 117 against
+//     111, 426 against 398, 52 against 46; 52 rows 114 against 138, 426 against 514, 54 against
+//     50; 80 rows 117 against 163, 439 against 647, 52 against 58
+//   d = 64, bf16: 32 rows 60 against 65, 207 against 202, 35 against 32; 48 rows 60 against 84,
+//     213 against 293, 36 against 35
+//   d = 64, E4M3: 64 rows 108 against 97, 377 against 353, 46 against 39; 80 rows 105 against
+//     113, 396 against 429, 48 against 42; 96 rows 106 against 130, 387 against 509, 48 against
+//     46
 static int few_rows(int d, bool f8) { return d == 64 ? (f8 ? 80 : 32) : (f8 ? 48 : 16); }
 static bool many_rows(int R, int G, int d, bool f8) { return R > few_rows(d, f8) && G <= 128; }
 

@@ -29,14 +29,15 @@
 // each) then follow one another; 2800 to 3000 as it is.
 //
 // Measured (heads 32 / 8 of 128; calls among others):
-//   prompt of 16384, window 4096              742 us   1.30 PFLOP/s (69 % of cuBLAS)
-//   6 prompts of 100-4000, window 1024        216 us   0.72 PFLOP/s: ten key tiles an
+//   prompt of 16384, window 4096              740 us   1.30 PFLOP/s (69 % of cuBLAS)
+//   6 prompts of 100-4000, window 1024        217 us   0.71 PFLOP/s: ten key tiles an
 //     item at 1.47 us, and 6.5 us beside them (1 start, 3.5 more in three masked tiles,
 //     0.35 the last product, 1.7 the output)
 //   8 trees of 64 nodes, 2-16k tokens, bf16   92 us    3.3 TB/s
-//   16 trees of 16 nodes, 0.5-8k, E4M3        105 us   1.4 TB/s: one tile an item (64 of
+//   16 trees of 16 nodes, 0.5-8k, E4M3        122 us   1.2 TB/s: one tile an item (64 of
 //     its rows are there), so S, softmax and P.V follow one another, and the widening
-//     shares issue slots and the conversion unit with the softmax; bf16 75 us, 3.4 TB/s
+//     shares issue slots and the conversion unit with the softmax (whose registers spill
+//     there: 172 bytes of stores, 388 of loads); bf16 77 us, 3.8 TB/s (means of six batches)
 // Counters (8192 tokens, window 4096): tensor pipe 49 % of the time, DRAM 4 %, stalls an
 // issue: wait 1.6, long scoreboard 1.5, no instruction 0.6.
 //

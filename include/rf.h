@@ -614,8 +614,10 @@ size_t rf_attn_decode_paged_ex_workspace_size(int B, int Hq, int Hkv, int Tq, in
 
 /*
  * rf_attn_decode_paged with a mask: the same cascade, arguments, layouts, limits
- * and errors, over the keys that `mask` gives each row (NULL: the same call as
- * rf_attn_decode_paged).  Pages in which no row reads a key (between the sinks and
+ * and errors, over the keys that `mask` gives each row (NULL, or neither a window
+ * nor parents: the same call as rf_attn_decode_paged, whose keys are read again for
+ * every 16 query rows of a kv head; a window of 2^30 gives every row the same keys,
+ * and with many rows, below, reads them again for every 256).  Pages in which no row reads a key (between the sinks and
  * the window of the first of the Tq tokens) are not looked at: their entries of
  * block_table may be anything, and a page may have gone to another sequence.  A
  * value that a row does not read has no effect on it, whatever it is.
